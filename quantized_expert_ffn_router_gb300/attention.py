@@ -1,0 +1,245 @@
+"""Attention operators next to the expert layer: rotary positions, the paged
+key-value cache (16-, 8- and 4-bit rows) and the attention of one new token a
+row over it.
+
+Argument marshalling over the C ABI declared in include/ft_attn.h, which says
+what each call computes; errors raise FtError.  Tensors may be strided views
+(channels contiguous); calls enqueue on the current stream (or `stream`).
+
+    cache = KvCache(FT_KV_E4M3, Hkv=8, D=128, page_size=64, n_pages=4096)
+    spin = Rope(128, base=5e5)
+    ws = torch.zeros(attn_decode_workspace(T, Hq, 8, 128), dtype=torch.uint8, device="cuda")
+    # every step, for T sequences: pos[t] = tokens already cached, lens[t] = pos[t] + 1
+    kv_append(cache, k, v, pages, pos, rope=spin, q=q, q_out=q)
+    attn_decode(cache, q, pages, lens, out, ws)
+"""
+
+from __future__ import annotations
+
+import ctypes
+import struct
+
+import torch
+
+from . import FT_ERR_INVALID, FT_OK, FtError, load
+
+FT_KV_BF16, FT_KV_F16, FT_KV_E4M3, FT_KV_NVFP4 = range(4)
+FT_DT_BF16, FT_DT_F16, FT_DT_F32 = range(3)
+(FT_ROPE_PLAIN, FT_ROPE_LINEAR, FT_ROPE_BASE, FT_ROPE_PARTS_BY_TURNS, FT_ROPE_PARTS_BY_INDEX) = range(5)
+
+_DT = {torch.bfloat16: FT_DT_BF16, torch.float16: FT_DT_F16, torch.float32: FT_DT_F32}
+
+_V, _I32, _F, _D, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_double, ctypes.c_size_t
+_SIGS = {
+    "ft_rope_freqs": (_I32, [_I32, _D, _I32, _D, _D, _D, _I32, _V]),
+    "ft_rope": (_I32, [_V, _I32, _I32, _I32, _I32, _V, _V, _V, _V]),
+    "ft_kv_row_bytes": (ctypes.c_uint64, [_I32, _I32]),
+    "ft_kv_append": (_I32, [_V, _V, _V, _I32, _I32, _V, _V, _V, _V, _V, _V, _I32, _V, _V, _V]),
+    "ft_kv_gather": (_I32, [_V, _V, _V, _V, _I32, _V, _V, _I32, _V, _V]),
+    "ft_attn_decode_workspace": (_SZ, [_I32, _I32, _I32, _I32]),
+    "ft_attn_decode": (_I32, [_V, _V, _I32, _I32, _I32, _V, _V, _V, _F, _I32, _V, _I32, _V, _V, _SZ, _V, _V]),
+}
+_lib = None
+
+# The descriptors of ft_attn.h as packed bytes (cheaper to build for each call than ctypes structures).
+_ROWS = struct.Struct("=Qqq")
+_TABLE = struct.Struct("=Qqii")
+
+
+class FtKvCache(ctypes.Structure):
+    _fields_ = [("fmt", _I32), ("Hkv", _I32), ("D", _I32), ("page_size", _I32), ("n_pages", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64),
+                ("k", _V), ("v", _V), ("k_scale", _V), ("v_scale", _V), ("k_block", _V), ("v_block", _V)]
+
+
+class FtRopeTable(ctypes.Structure):
+    _fields_ = [("freqs", _V), ("rot_dim", _I32), ("interleaved", _I32), ("mscale", _F)]
+
+
+def _bind():
+    global _lib
+    if _lib is None:
+        lib = load()
+        for name, (res, args) in _SIGS.items():
+            fn = getattr(lib, name)
+            fn.restype = res
+            fn.argtypes = args
+        _lib = lib
+    return _lib
+
+
+def _need(ok, message):
+    if not ok:
+        raise FtError(FT_ERR_INVALID, message)
+
+
+def _check(status):
+    if status != FT_OK:
+        raise FtError(status, _lib.ft_last_error().decode())
+
+
+def _stream(t, stream):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(t.device.index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _rows(t, name, T, D, dtype=None):
+    """[T, heads, D] as an ft_rows."""
+    _need(t.dim() == 3 and t.shape[0] == T and t.shape[2] == D, f"{name}: shape {tuple(t.shape)}, expected [{T}, *, {D}]")
+    _need(t.stride(2) == 1 or D == 1, f"{name}: channels must be contiguous")
+    _need(dtype is None or t.dtype == dtype, f"{name}: dtype {t.dtype}, expected {dtype}")
+    # a dimension of one place may carry any stride
+    return _ROWS.pack(t.data_ptr(), t.stride(0) if T > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0)
+
+
+def _ints(t, name, T):
+    if t is None:
+        return None
+    _need(t.dtype == torch.int32 and t.dim() == 1 and t.shape[0] == T and t.is_contiguous(),
+          f"{name}: a contiguous int32 [{T}] is needed")
+    return t.data_ptr()
+
+
+def _table(pages):
+    _need(pages.dtype == torch.int32 and pages.dim() == 2 and pages.stride(1) == 1,
+          "pages: an int32 [sequences, pages] is needed")
+    return _TABLE.pack(pages.data_ptr(), pages.stride(0), pages.shape[1], pages.shape[0])
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def kv_row_bytes(fmt: int, D: int) -> int:
+    return int(_bind().ft_kv_row_bytes(fmt, D))
+
+
+class KvCache:
+    """One layer's paged cache: rows [n_pages, Hkv, page_size] of D values.
+
+    Arrays: k, v (16-bit values; float8_e4m3fn codes; uint8 pairs of E2M1
+    codes), k_scale, v_scale (uint8 exponents + 127), k_block, v_block (uint8
+    E4M3 block scales).  `KvCache.over` describes arrays that the caller has,
+    in any order of pages, heads and slots (the rows' last dimension contiguous
+    and the same row strides for all arrays)."""
+
+    def __init__(self, fmt: int, Hkv: int, D: int, page_size: int, n_pages: int, device="cuda"):
+        shape, z = (n_pages, Hkv, page_size), dict(device=device)
+        arrays = {}
+        for n in ("k", "v"):
+            if fmt in (FT_KV_BF16, FT_KV_F16):
+                arrays[n] = torch.zeros(*shape, D, dtype=torch.bfloat16 if fmt == FT_KV_BF16 else torch.float16, **z)
+                continue
+            if fmt == FT_KV_E4M3:
+                arrays[n] = torch.zeros(*shape, D, dtype=torch.float8_e4m3fn, **z)
+            else:
+                arrays[n] = torch.zeros(*shape, D // 2, dtype=torch.uint8, **z)
+                arrays[n + "_block"] = torch.zeros(*shape, D // 16, dtype=torch.uint8, **z)
+            arrays[n + "_scale"] = torch.full(shape, 127, dtype=torch.uint8, **z)
+        self._describe(fmt, D, arrays)
+
+    @classmethod
+    def over(cls, fmt: int, D: int, k, v, k_scale=None, v_scale=None, k_block=None, v_block=None) -> "KvCache":
+        self = cls.__new__(cls)
+        self._describe(fmt, D, dict(k=k, v=v, k_scale=k_scale, v_scale=v_scale, k_block=k_block, v_block=v_block))
+        return self
+
+    def _describe(self, fmt, D, arrays):
+        width = {FT_KV_BF16: D, FT_KV_F16: D, FT_KV_E4M3: D, FT_KV_NVFP4: D // 2}.get(fmt)
+        _need(width is not None, f"cache format {fmt}")
+        k = arrays["k"]
+        _need(k.dim() == 4, "cache arrays are [pages, heads, slots, ...]")
+        n_pages, Hkv, page_size = k.shape[:3]
+        strides = None
+        for name in ("k", "v", "k_scale", "v_scale", "k_block", "v_block"):
+            t = arrays.get(name)
+            setattr(self, name, t)
+            if t is None:
+                continue
+            w = width if name in ("k", "v") else D // 16 if name.endswith("_block") else 1
+            shape = (n_pages, Hkv, page_size) + (() if name.endswith("_scale") else (w,))
+            size = 2 if fmt in (FT_KV_BF16, FT_KV_F16) and name in ("k", "v") else 1
+            _need(tuple(t.shape) == shape and t.element_size() == size, f"cache {name}: {tuple(t.shape)} {t.dtype}")
+            _need(t.dim() == 3 or t.stride(3) == 1, f"cache {name}: rows must be contiguous")
+            _need(all(s % w == 0 for s in t.stride()[:3]), f"cache {name}: strides must be whole rows")
+            # a dimension of one place has no stride of its own
+            rows = [s // w if n > 1 else 0 for s, n in zip(t.stride()[:3], shape)]
+            _need(strides is None or rows == strides, f"cache {name}: row strides {rows}, the keys' are {strides}")
+            strides = rows
+        self.fmt, self.Hkv, self.D, self.page_size, self.n_pages = fmt, Hkv, D, page_size, n_pages
+        self.desc = FtKvCache(fmt, Hkv, D, page_size, n_pages, *strides, *(
+            _ptr(arrays.get(n)) for n in ("k", "v", "k_scale", "v_scale", "k_block", "v_block")))
+        self._ref = ctypes.addressof(self.desc)
+
+
+class Rope:
+    """A rotary table (ft_rope_freqs on the host, kept on the device)."""
+
+    def __init__(self, rot_dim: int, base: float = 10000.0, interleaved: bool = False, scaling: int = FT_ROPE_PLAIN,
+                 factor: float = 1.0, low: float = 1.0, high: float = 32.0, orig_len: int = 8192,
+                 mscale: float = 1.0, device="cuda"):
+        host = torch.empty(max(rot_dim, 0) // 2, dtype=torch.int64)
+        lib = _bind()
+        _check(lib.ft_rope_freqs(rot_dim, base, scaling, factor, low, high, orig_len, host.data_ptr()))
+        self.rot_dim, self.interleaved, self.mscale = rot_dim, bool(interleaved), float(mscale)
+        self.freqs = host.to(device)
+        self.desc = FtRopeTable(self.freqs.data_ptr(), rot_dim, int(self.interleaved), self.mscale)
+        self._ref = ctypes.addressof(self.desc)
+
+
+def rope(x, pos, table: Rope, out, stream=None):
+    """out[t, h] = x[t, h] rotated to pos[t] (ft_rope); out may be x."""
+    T, heads, D = x.shape
+    _need(out.shape == x.shape and out.dtype == x.dtype, "rope: out must be like x")
+    _check(_bind().ft_rope(_rows(x, "x", T, D), T, heads, D, _DT.get(x.dtype, -1), _ints(pos, "pos", T), table._ref,
+                           _rows(out, "out", T, D), _stream(x, stream)))
+
+
+def kv_append(cache: KvCache, k, v, pages, pos, seq=None, rope: Rope | None = None, rope_pos=None, q=None, q_out=None,
+              dev_status=None, stream=None):
+    """Write k and v [T, Hkv, D] to position pos[t] of sequence seq[t] (default t); with `rope`, k is rotated first
+    and q into q_out in the same launch (ft_kv_append)."""
+    T, D = k.shape[0], cache.D
+    _need(k.shape == v.shape and k.shape[1] == cache.Hkv, "kv_append: k and v must be [T, Hkv, D]")
+    _need(q is None or (q_out is not None and q.shape == q_out.shape), "kv_append: q_out must be like q")
+    _check(_bind().ft_kv_append(
+        cache._ref, _rows(k, "k", T, D), _rows(v, "v", T, D, k.dtype), T, _DT.get(k.dtype, -1), _table(pages),
+        _ints(seq, "seq", T), _ints(pos, "pos", T), None if rope is None else rope._ref,
+        _ints(rope_pos, "rope_pos", T), None if q is None else _rows(q, "q", T, D, k.dtype),
+        0 if q is None else q.shape[1], None if q_out is None else _rows(q_out, "q_out", T, D, k.dtype),
+        _ptr(dev_status), _stream(k, stream)))
+
+
+def kv_gather(cache: KvCache, pages, pos, k_out, v_out, seq=None, dev_status=None, stream=None):
+    """k_out, v_out [T, Hkv, D] (either may be None) = the cached rows of position pos[t] of sequence seq[t]
+    (ft_kv_gather)."""
+    some = k_out if k_out is not None else v_out
+    _need(some is not None, "kv_gather: no output")
+    T, D = some.shape[0], cache.D
+    for t in (k_out, v_out):
+        _need(t is None or t.shape[1] == cache.Hkv, "kv_gather: outputs must be [T, Hkv, D]")
+    _check(_bind().ft_kv_gather(
+        cache._ref, _table(pages), _ints(seq, "seq", T), _ints(pos, "pos", T), T,
+        None if k_out is None else _rows(k_out, "k_out", T, D, some.dtype),
+        None if v_out is None else _rows(v_out, "v_out", T, D, some.dtype),
+        _DT.get(some.dtype, -1), _ptr(dev_status), _stream(some, stream)))
+
+
+def attn_decode_workspace(T: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(_bind().ft_attn_decode_workspace(T, Hq, Hkv, D))
+
+
+def attn_decode(cache: KvCache, q, pages, lens, out, ws, seq=None, scale: float | None = None, window: int = 0,
+                lse=None, dev_status=None, stream=None):
+    """out [T, Hq, D] = attention of q [T, Hq, D] over the first lens[t] (with `window`: the last `window` of them)
+    cached tokens of sequence seq[t] (ft_attn_decode).  scale defaults to 1 / sqrt(D)."""
+    T, Hq, D = q.shape
+    _need(D == cache.D and out.shape == q.shape, "attn_decode: q and out must be [T, Hq, D]")
+    _need(lse is None or (lse.dtype == torch.float32 and lse.shape == q.shape[:2] and lse.is_contiguous()),
+          "attn_decode: lse must be a contiguous float32 [T, Hq]")
+    _check(_bind().ft_attn_decode(
+        cache._ref, _rows(q, "q", T, D), T, Hq, _DT.get(q.dtype, -1), _table(pages), _ints(seq, "seq", T),
+        _ints(lens, "lens", T), D ** -0.5 if scale is None else scale, window, _rows(out, "out", T, D),
+        _DT.get(out.dtype, -1), _ptr(lse), ws.data_ptr(), ws.numel() * ws.element_size(), _ptr(dev_status),
+        _stream(q, stream)))

@@ -1,0 +1,76 @@
+// ft_kv_index.h -- the index arithmetic of the paged key-value cache and of
+// the decode attention's work split, as plain C++ that the kernels and a host
+// test both compile.
+#pragma once
+
+#include <stdint.h>
+
+#ifdef __CUDACC__
+#define FT_HD __host__ __device__ __forceinline__
+#else
+#define FT_HD inline
+#endif
+
+namespace ft {
+
+// Unsigned division of n < 2^31 by a fixed d >= 1: (n * mul) >> shift with
+// mul = ceil(2^(31 + s) / d), s = ceil(log2 d).  mul * d - 2^(31+s) < d <= 2^s,
+// so the quotient's error n * (mul * d - 2^(31+s)) / (d * 2^(31+s)) stays below
+// 1 / d and the floor is exact.
+struct FastDiv {
+  uint32_t mul;
+  uint32_t shift;
+};
+
+FT_HD FastDiv make_fast_div(uint32_t d) {
+  uint32_t s = 0;
+  while ((uint64_t(1) << s) < d) ++s;
+  const uint64_t p = uint64_t(1) << (31 + s);
+  return FastDiv{static_cast<uint32_t>((p + d - 1) / d), 31 + s};
+}
+
+FT_HD uint32_t fast_div(uint32_t n, FastDiv f) { return static_cast<uint32_t>((static_cast<uint64_t>(n) * f.mul) >> f.shift); }
+
+constexpr uint32_t kNoRow = 0xffffffffu;
+
+// The cache's row numbering, as the kernels take it: every row index is below
+// kNoRow (checked by the entry points), so rows and strides fit 32 bits.
+struct KvIndex {
+  uint32_t page_size;
+  FastDiv by_page;
+  uint32_t n_pages;
+  uint32_t page_stride, head_stride, slot_stride;
+};
+
+// Row of head 0 of a token at `slot` of `page`; kNoRow for a page outside the cache.
+FT_HD uint32_t kv_row(const KvIndex& x, int32_t page, uint32_t slot) {
+  if (static_cast<uint32_t>(page) >= x.n_pages) return kNoRow;
+  return static_cast<uint32_t>(page) * x.page_stride + slot * x.slot_stride;
+}
+
+// ---- the split of ft_attn_decode -------------------------------------------
+// A row's tokens first..len-1 are cut into tiles of `tile` tokens from the
+// multiple of 16 at or below `first`.  All tiles of all (row, head block) units
+// are numbered row by row, head block by head block; worker c of n takes the
+// numbers [c * share, (c + 1) * share).
+struct RowSpan {
+  int32_t begin;  // the first tile's first token (a multiple of 16)
+  int32_t first;  // the first token that counts
+  int32_t len;    // one past the last
+  int32_t tiles;
+};
+
+FT_HD RowSpan row_span(int32_t len, int32_t window, int64_t most, int32_t tile) {
+  RowSpan r;
+  if (len > most) len = static_cast<int32_t>(most);
+  if (len < 0) len = 0;
+  r.len = len;
+  r.first = (window > 0 && len > window) ? len - window : 0;
+  r.begin = r.first & ~15;
+  r.tiles = (len - r.begin + tile - 1) / tile;
+  return r;
+}
+
+FT_HD int64_t split_share(int64_t total, int64_t workers) { return total > workers ? (total + workers - 1) / workers : 1; }
+
+}  // namespace ft
