@@ -56,7 +56,7 @@ enum { FT_KV_BF16 = 0, FT_KV_F16 = 1, FT_KV_E4M3 = 2, FT_KV_NVFP4 = 3 };
  * exponent byte at k_scale + r, its block scales at k_block + r * (D / 16).
  * Arrays 16-byte aligned; scale and block arrays NULL where the format has
  * none.  Limits: D a multiple of 16 (FT_KV_NVFP4: of 32), at most 256; every
- * row index below 2^32 - 1.
+ * row index below 2^31 - 1.
  */
 typedef struct {
   int32_t fmt;

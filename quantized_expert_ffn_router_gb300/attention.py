@@ -84,27 +84,39 @@ def _stream(t, stream):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _rows(t, name, T, D, dtype=None):
-    """[T, heads, D] as an ft_rows."""
-    _need(t.dim() == 3 and t.shape[0] == T and t.shape[2] == D, f"{name}: shape {tuple(t.shape)}, expected [{T}, *, {D}]")
-    _need(t.stride(2) == 1 or D == 1, f"{name}: channels must be contiguous")
-    _need(dtype is None or t.dtype == dtype, f"{name}: dtype {t.dtype}, expected {dtype}")
+def _bad(message):
+    raise FtError(FT_ERR_INVALID, message)
+
+
+# The checks below build their messages only when they fail: a decode step calls these functions once a layer, and
+# formatting them costs more than the launch.
+def _rows(t, name, shape, dtype):
+    """A tensor of this [T, heads, D] and type as an ft_rows."""
+    if t.shape != shape:
+        _bad(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype is not dtype:
+        _bad(f"{name}: dtype {t.dtype}, expected {dtype}")
+    s0, s1, s2 = t.stride()
+    if s2 != 1:
+        _bad(f"{name}: channels must be contiguous")
     # a dimension of one place may carry any stride
-    return _ROWS.pack(t.data_ptr(), t.stride(0) if T > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0)
+    return _ROWS.pack(t.data_ptr(), s0 if shape[0] > 1 else 0, s1 if shape[1] > 1 else 0)
 
 
 def _ints(t, name, T):
     if t is None:
         return None
-    _need(t.dtype == torch.int32 and t.dim() == 1 and t.shape[0] == T and t.is_contiguous(),
-          f"{name}: a contiguous int32 [{T}] is needed")
+    if t.dtype is not torch.int32 or t.numel() != T or not t.is_contiguous():
+        _bad(f"{name}: a contiguous int32 [{T}] is needed")
     return t.data_ptr()
 
 
 def _table(pages):
-    _need(pages.dtype == torch.int32 and pages.dim() == 2 and pages.stride(1) == 1,
-          "pages: an int32 [sequences, pages] is needed")
-    return _TABLE.pack(pages.data_ptr(), pages.stride(0), pages.shape[1], pages.shape[0])
+    s0, s1 = pages.stride() if pages.dim() == 2 else (0, 0)
+    if pages.dtype != torch.int32 or s1 != 1:
+        _bad("pages: an int32 [sequences, pages] is needed")
+    n, most = pages.shape
+    return _TABLE.pack(pages.data_ptr(), s0, most, n)
 
 
 def _ptr(t):
@@ -188,42 +200,66 @@ class Rope:
         self._ref = ctypes.addressof(self.desc)
 
 
+def _shape3(t, name, heads, D):
+    """t's [T, heads, D] with these heads and channels (None: any)."""
+    shape = t.shape
+    if len(shape) != 3 or (heads is not None and shape[1] != heads) or (D is not None and shape[2] != D):
+        _bad(f"{name}: shape {tuple(shape)}, expected [T, {'*' if heads is None else heads}, {'*' if D is None else D}]")
+    return shape
+
+
 def rope(x, pos, table: Rope, out, stream=None):
     """out[t, h] = x[t, h] rotated to pos[t] (ft_rope); out may be x."""
-    T, heads, D = x.shape
-    _need(out.shape == x.shape and out.dtype == x.dtype, "rope: out must be like x")
-    _check(_bind().ft_rope(_rows(x, "x", T, D), T, heads, D, _DT.get(x.dtype, -1), _ints(pos, "pos", T), table._ref,
-                           _rows(out, "out", T, D), _stream(x, stream)))
+    lib = _lib or _bind()
+    dtype = x.dtype
+    T, heads, D = shape = _shape3(x, "x", None, None)
+    status = lib.ft_rope(_rows(x, "x", shape, dtype), T, heads, D, _DT.get(dtype, -1), _ints(pos, "pos", T),
+                         table._ref, _rows(out, "out", shape, dtype), _stream(x, stream))
+    if status:
+        _check(status)
 
 
 def kv_append(cache: KvCache, k, v, pages, pos, seq=None, rope: Rope | None = None, rope_pos=None, q=None, q_out=None,
               dev_status=None, stream=None):
     """Write k and v [T, Hkv, D] to position pos[t] of sequence seq[t] (default t); with `rope`, k is rotated first
     and q into q_out in the same launch (ft_kv_append)."""
-    T, D = k.shape[0], cache.D
-    _need(k.shape == v.shape and k.shape[1] == cache.Hkv, "kv_append: k and v must be [T, Hkv, D]")
-    _need(q is None or (q_out is not None and q.shape == q_out.shape), "kv_append: q_out must be like q")
-    _check(_bind().ft_kv_append(
-        cache._ref, _rows(k, "k", T, D), _rows(v, "v", T, D, k.dtype), T, _DT.get(k.dtype, -1), _table(pages),
-        _ints(seq, "seq", T), _ints(pos, "pos", T), None if rope is None else rope._ref,
-        _ints(rope_pos, "rope_pos", T), None if q is None else _rows(q, "q", T, D, k.dtype),
-        0 if q is None else q.shape[1], None if q_out is None else _rows(q_out, "q_out", T, D, k.dtype),
-        _ptr(dev_status), _stream(k, stream)))
+    lib = _lib or _bind()
+    dtype = k.dtype
+    shape = _shape3(k, "k", cache.Hkv, cache.D)
+    T = shape[0]
+    Hq, q_rows, q_out_rows = 0, None, None
+    if q is not None:
+        q_shape = _shape3(q, "q", None, cache.D)
+        Hq = q_shape[1]
+        if q_shape[0] != T or q_out is None:
+            _bad("kv_append: q has k's tokens, and needs q_out")
+        q_rows, q_out_rows = _rows(q, "q", q_shape, dtype), _rows(q_out, "q_out", q_shape, dtype)
+    status = lib.ft_kv_append(
+        cache._ref, _rows(k, "k", shape, dtype), _rows(v, "v", shape, dtype), T, _DT.get(dtype, -1), _table(pages),
+        None if seq is None else _ints(seq, "seq", T), _ints(pos, "pos", T), None if rope is None else rope._ref,
+        None if rope_pos is None else _ints(rope_pos, "rope_pos", T), q_rows, Hq, q_out_rows,
+        None if dev_status is None else dev_status.data_ptr(), _stream(k, stream))
+    if status:
+        _check(status)
 
 
 def kv_gather(cache: KvCache, pages, pos, k_out, v_out, seq=None, dev_status=None, stream=None):
     """k_out, v_out [T, Hkv, D] (either may be None) = the cached rows of position pos[t] of sequence seq[t]
     (ft_kv_gather)."""
+    lib = _lib or _bind()
     some = k_out if k_out is not None else v_out
-    _need(some is not None, "kv_gather: no output")
-    T, D = some.shape[0], cache.D
-    for t in (k_out, v_out):
-        _need(t is None or t.shape[1] == cache.Hkv, "kv_gather: outputs must be [T, Hkv, D]")
-    _check(_bind().ft_kv_gather(
-        cache._ref, _table(pages), _ints(seq, "seq", T), _ints(pos, "pos", T), T,
-        None if k_out is None else _rows(k_out, "k_out", T, D, some.dtype),
-        None if v_out is None else _rows(v_out, "v_out", T, D, some.dtype),
-        _DT.get(some.dtype, -1), _ptr(dev_status), _stream(some, stream)))
+    if some is None:
+        _bad("kv_gather: no output")
+    dtype = some.dtype
+    shape = _shape3(some, "output", cache.Hkv, cache.D)
+    T = shape[0]
+    status = lib.ft_kv_gather(
+        cache._ref, _table(pages), None if seq is None else _ints(seq, "seq", T), _ints(pos, "pos", T), T,
+        None if k_out is None else _rows(k_out, "k_out", shape, dtype),
+        None if v_out is None else _rows(v_out, "v_out", shape, dtype), _DT.get(dtype, -1),
+        None if dev_status is None else dev_status.data_ptr(), _stream(some, stream))
+    if status:
+        _check(status)
 
 
 def attn_decode_workspace(T: int, Hq: int, Hkv: int, D: int) -> int:
@@ -234,12 +270,15 @@ def attn_decode(cache: KvCache, q, pages, lens, out, ws, seq=None, scale: float 
                 lse=None, dev_status=None, stream=None):
     """out [T, Hq, D] = attention of q [T, Hq, D] over the first lens[t] (with `window`: the last `window` of them)
     cached tokens of sequence seq[t] (ft_attn_decode).  scale defaults to 1 / sqrt(D)."""
-    T, Hq, D = q.shape
-    _need(D == cache.D and out.shape == q.shape, "attn_decode: q and out must be [T, Hq, D]")
-    _need(lse is None or (lse.dtype == torch.float32 and lse.shape == q.shape[:2] and lse.is_contiguous()),
-          "attn_decode: lse must be a contiguous float32 [T, Hq]")
-    _check(_bind().ft_attn_decode(
-        cache._ref, _rows(q, "q", T, D), T, Hq, _DT.get(q.dtype, -1), _table(pages), _ints(seq, "seq", T),
-        _ints(lens, "lens", T), D ** -0.5 if scale is None else scale, window, _rows(out, "out", T, D),
-        _DT.get(out.dtype, -1), _ptr(lse), ws.data_ptr(), ws.numel() * ws.element_size(), _ptr(dev_status),
-        _stream(q, stream)))
+    lib = _lib or _bind()
+    T, Hq, D = shape = _shape3(q, "q", None, cache.D)
+    dtype, out_dtype = q.dtype, out.dtype
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (T, Hq) or not lse.is_contiguous()):
+        _bad("attn_decode: lse must be a contiguous float32 [T, Hq]")
+    status = lib.ft_attn_decode(
+        cache._ref, _rows(q, "q", shape, dtype), T, Hq, _DT.get(dtype, -1), _table(pages),
+        None if seq is None else _ints(seq, "seq", T), _ints(lens, "lens", T), D ** -0.5 if scale is None else scale,
+        window, _rows(out, "out", shape, out_dtype), _DT.get(out_dtype, -1), None if lse is None else lse.data_ptr(),
+        ws.data_ptr(), ws.nbytes, None if dev_status is None else dev_status.data_ptr(), _stream(q, stream))
+    if status:
+        _check(status)

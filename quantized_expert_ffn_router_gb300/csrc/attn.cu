@@ -6,19 +6,31 @@
 // 4 G flops a byte pair, far below the tensor cores' ridge, so the kernel is
 // bound by HBM and everything is arranged around loads in flight.
 //
-// Layout of the work in a warp.  Keys go straight from global memory into the
-// A operand of mma.m16n8k16 (16 tokens x 16 channels, S^T = K Q^T) and values
-// into the A operand of the second product (16 channels x 16 tokens,
-// O^T = V^T P^T), without passing through shared memory: the order of the
-// contracted index is free as long as both operands agree, so each lane loads
-// 16 contiguous bytes of a row and its elements are dealt to the fragments'
-// places by renaming registers (keys) or by one byte permute a register
-// (values, whose contracted index runs over tokens).  With tokens and channels
-// on the 16-row side, 8 query heads fill the 8-column side: no row of the
-// instruction is wasted at G = 8.  P^T changes from accumulator to operand
-// layout by movmatrix.  mma.sync and not tcgen05: operands that arrive in
-// registers need no staging, no barrier and no TMEM round trip, and the
-// tensor work is a small part of the time (each warp has 30 mma per 8 KB).
+// Layout of the work in a warp.  A warp works alone on steps of 16 or 32
+// tokens: one lane a token looks its page up, and 16-byte asynchronous copies
+// (any pages and strides; masked tokens become zeros) bring the rows into the
+// warp's own ring in shared memory, several steps ahead and across the ends of
+// units, so that loads stay in flight while the warp computes.  Keys become
+// the A operand of mma.m16n8k16 (16 tokens x 16 channels, S^T = K Q^T) and
+// values that of the second product (16 channels x 16 tokens, O^T = V^T P^T):
+// the order of a contracted index is free as long as both operands agree, so a
+// lane reads 16 contiguous bytes of a row and its elements are dealt to the
+// fragments' places by renaming registers (keys) or by one byte permute a
+// register (values, whose contracted index runs over tokens).  With tokens and
+// channels on the 16-row side, 8 query heads fill the 8-column side.  P^T goes
+// from accumulator to operand layout by movmatrix.  mma.sync and not tcgen05:
+// 8- and 4-bit rows have to pass through registers to become 16-bit operands,
+// and the tensor work is a small part of the time.  Copies by lanes and not by
+// TMA: row gathers and bulk copies take their operands from uniform registers,
+// so a warp that starts one for every four rows runs a loop of some 15
+// instructions for each; measured, that cost more than it saved (4-bit rows,
+// 64 rows up to 16384 tokens: 231 us against 186 us with loads into registers).
+//
+// Order of tokens.  Place r = 0..7 of the contracted index holds token r / 2
+// (r even) or 4 + r / 2 (r odd) of its 8, so that a lane quarter's value rows
+// are q, q + 4, q + 8, q + 12 and the swizzles below keep every read of shared
+// memory free of bank conflicts.  Key rows and notes lie in the places' order,
+// value rows in the tokens'.
 //
 // 8- and 4-bit rows: a key's power-of-two scale multiplies its score; a
 // value's enters the running maximum, so that the weight that is rounded to
@@ -43,6 +55,16 @@ namespace ft {
 namespace {
 
 constexpr int kWarps = 4;
+#ifndef FT_TS_MIN
+#define FT_TS_MIN 128
+#endif
+#ifndef FT_S3
+#define FT_S3 3
+#endif
+#ifndef FT_C4
+#define FT_C4 1
+#endif
+constexpr int kSmemSm = 227 * 1024;  // of an SM, for its CTAs' dynamic shared memory
 constexpr int kMaxWorkers = 1024;  // CTAs of one call (sizes the workspace)
 constexpr uint32_t kAll = 0xffffffffu;
 
@@ -56,6 +78,7 @@ struct AttnArgs {
   const int32_t* lens;
   float* part_o;   // [worker][2][heads of a block][D padded]
   float2* part_ml;  // [worker][2][heads of a block] (maximum, sum)
+  int4* begun;      // [worker] the unit that the worker began and others went on with: row, unit, last worker, 1 (or 0)
   float scale_log2;
   int32_t window, T, Hq, G;
   int32_t units;         // head blocks of a row: Hkv * blocks
@@ -117,21 +140,32 @@ __device__ __forceinline__ float2 unpack16(uint32_t w) {
   return make_float2(bf16_lo(w), bf16_hi(w));
 }
 
-// N words (1, 2 or 4) of a cached row: read once, kept out of L1.
+// N words (1, 2 or 4) of shared memory.
 template <int N>
-__device__ __forceinline__ void load_row(const uint8_t* p, uint32_t (&w)[N]) {
+__device__ __forceinline__ void load_words(uint32_t p, uint32_t (&w)[N]) {
   if constexpr (N == 4)
-    asm("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(p));
   else if constexpr (N == 2)
-    asm("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(p));
   else
-    asm("ld.global.nc.u32 %0, [%1];" : "=r"(w[0]) : "l"(p));
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(p));
 }
 
-// How a format's rows are dealt to lanes, for heads padded to DP channels.
-// Keys: piece p of a row gives lane quarter q the EK channels p*4*EK + q*EK..;
-// values: piece p gives lane group g the EV channels p*8*EV + g*EV...
-template <int FMT, int DP>
+// 16 bytes from global to shared memory, past L1; `bytes` (16 or 0) of them read, the rest zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy16_or_zero(uint32_t dst, const uint8_t* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+constexpr int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
+
+// How a format's rows are cut, for heads padded to DP channels (channels past
+// D read zeros).  Keys: piece p of a row gives lane quarter q the EK channels
+// p*4*EK + q*EK..; values: piece p gives lane group g the EV channels
+// p*8*EV + g*EV...
+template <int FMT, int DP, int NT>
 struct Deal {
   static constexpr bool kQuant = FMT == FT_KV_E4M3 || FMT == FT_KV_NVFP4;
   static constexpr bool kBlocks = FMT == FT_KV_NVFP4;
@@ -139,203 +173,47 @@ struct Deal {
   static constexpr int EK = !kQuant ? 8 : !kBlocks ? 16 : DP % 128 == 0 ? 32 : 16;
   static constexpr int EV = !kQuant ? 8 : !kBlocks ? (DP % 128 == 0 ? 16 : 8) : DP % 256 == 0 ? 32 : DP % 128 == 0 ? 16 : 8;
   static constexpr int NK = DP / (4 * EK), NV = DP / (8 * EV);
-  static constexpr int per = !kQuant ? 2 : kBlocks ? 8 : 4;  // elements of a word
-  static constexpr int WK = EK / per, WV = EV / per;         // words of a piece
-  static constexpr int row_bits = !kQuant ? 16 : kBlocks ? 4 : 8;
-  // 16-token tiles that a warp has in flight at once: about 4 KB of keys
-  static constexpr int kKeyBytes = 16 * DP * row_bits / 8;
-  static constexpr int U = kKeyBytes >= 4096 ? 1 : kKeyBytes >= 2048 ? 2 : 4;
-};
-
-template <int FMT, int DP, int NT>
-struct Warp {
-  using X = Deal<FMT, DP>;
-  static constexpr int U = X::U;
-  static constexpr int R = (16 * U + 31) / 32;  // tokens of a step held by a lane
-  static constexpr int MT = DP / 16;
-
-  // ---- a step's rows: lane i holds those of tokens base + i (+ 32)
-  __device__ static __forceinline__ void pages_of(const AttnArgs& a, const int32_t* table, int base, int first, int end,
-                                                  int lane, int32_t (&page)[R]) {
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const int tok = base + lane + 32 * i;
-      page[i] = -1;
-      if ((U > 1 || lane < 16) && tok >= first && tok < end) page[i] = table[fast_div(tok, a.kv.at.by_page)];
-    }
+  static constexpr int bits = !kQuant ? 16 : kBlocks ? 4 : 8;
+  static constexpr int WK = EK * bits / 32, WV = EV * bits / 32;  // words of a piece
+  static constexpr int MT = DP / 16, H = 8 * NT;
+  static constexpr int RB = DP * bits / 8;          // bytes of a row in shared memory
+  static constexpr int PK = WK * 4, PV = WV * 4;    // bytes of a piece
+  static constexpr bool kSwap = RB % 128 == 0;      // keys: odd places have 64-byte halves swapped
+  static constexpr int KP = kSwap ? 2 : 1;
+  static_assert(!kSwap || PK == 16, "");
+  __device__ static int key_swizzle(int place) { return kSwap ? (place & 1) << 6 : 0; }
+  __device__ static int value_swizzle(int token) {
+    return PV == 16 ? (token & 3) << 5 : PV == 8 ? ((token >> 1) & 1) << 5 : 0;
   }
-  __device__ static __forceinline__ void rows_of(const AttnArgs& a, uint32_t head_row, int base, int first, int end,
-                                                 int lane, const int32_t (&page)[R], uint32_t (&row)[R]) {
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const int tok = base + lane + 32 * i;
-      row[i] = kNoRow;
-      if ((U > 1 || lane < 16) && tok >= first && tok < end) {
-        row[i] = kv_row(a.kv.at, page[i], tok - fast_div(tok, a.kv.at.by_page) * a.kv.at.page_size);
-        if (row[i] == kNoRow)
-          record_status(a.status, FT_ERR_BAD_ID);
-        else
-          row[i] += head_row;
-      }
-    }
+  // A step: TS tokens.
+  static constexpr int TS = RB >= FT_TS_MIN ? 16 : 32;
+  static constexpr int U = TS / 16;
+  static constexpr int kSide = TS * RB;          // keys, or values, of a step
+  // The copies of a step: chunk i = 32 c + lane of a side is row i / CPR, bytes 16 (i % CPR)..;
+  // both repeat every CY copies, CR rows further on.
+  static constexpr int CPR = RB / 16, kCopies = TS * CPR / 32;
+  static constexpr int CY = CPR / gcd(32, CPR), CR = 32 * CY / CPR;
+  static_assert(kCopies % CY == 0, "");
+  // Beside the rows: per token (key factor, value exponent, 2^-value exponent),
+  // the block scales as f16 (keys [place][block], values [block][place]), and
+  // the mask of tokens that count.
+  static constexpr int kTok = kQuant ? TS * 16 : 0;
+  static constexpr int NBK = DP / 16, VS = TS + 4, DPW = DP / 64;
+  static constexpr int kKeyBlk = kBlocks ? TS * NBK * 2 : 0, kValBlk = kBlocks ? NBK * VS * 2 : 0;
+  static constexpr int kNotes = kTok + kKeyBlk + kValBlk + 16;
+  static constexpr uint32_t kFull = TS == 32 ? 0xffffffffu : (1u << (TS & 31)) - 1;
+  // The merge of the warps takes two warps' sums at a time.
+  static constexpr int kMerge = (MT * NT * 4 + NT * 4) * 32 * 4;
+  // Slots of a warp's ring with so many CTAs an SM, and the choice of both.
+  static constexpr int slots(int ctas) {
+    const int n = (kSmemSm / ctas - 1152 - 2 * kMerge) / kWarps / (2 * kSide + kNotes);
+    return n < 8 ? n : 8;
   }
-
-  // ---- keys and values of a step
-  uint32_t k[U][2][X::NK][X::WK];
-  uint32_t kb[X::kBlocks ? U : 1][2][X::NK];
-  uint32_t v[U][4][X::NV][X::WV];
-  uint32_t vb[X::kBlocks ? U : 1][4][X::NV];
-  uint32_t sc[R];    // the lane's tokens' scale bytes: key | value << 8
-  uint32_t valid;    // bit 2u + r: token 16u + g + 8r counts
-
-  __device__ __forceinline__ void load_keys(const AttnArgs& a, const uint32_t (&row)[R], int g, int q) {
-    valid = 0;
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const uint32_t n = __shfl_sync(kAll, row[u >> 1], ((16 * u) & 31) + g + 8 * r);
-        const bool ok = n != kNoRow;
-        if (ok) valid |= 1u << (2 * u + r);
-        const uint8_t* src = a.kv.data[0] + static_cast<uint64_t>(n) * a.kv.row_bytes;
-#pragma unroll
-        for (int p = 0; p < X::NK; ++p) {
-          const int d = p * 4 * X::EK + q * X::EK;
-#pragma unroll
-          for (int w = 0; w < X::WK; ++w) k[u][r][p][w] = 0;
-          if (X::kBlocks) kb[u][r][p] = 0;
-          if (ok && (p * 4 * X::EK + 4 * X::EK <= DP - 64 || d < a.kv.D)) {
-            load_row(src + d * X::row_bits / 8, k[u][r][p]);
-            if constexpr (X::kBlocks) {
-              const uint8_t* bp = a.kv.block[0] + static_cast<uint64_t>(n) * (a.kv.D >> 4) + (d >> 4);
-              kb[u][r][p] = X::EK == 32 ? *reinterpret_cast<const uint16_t*>(bp) : *bp;
-            }
-          }
-        }
-      }
-    if constexpr (X::kQuant) {
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        sc[i] = 0x7f7f;
-        if (row[i] != kNoRow) sc[i] = a.kv.scale[0][row[i]] | (a.kv.scale[1][row[i]] << 8);
-      }
-    }
-  }
-
-  __device__ __forceinline__ void load_values(const AttnArgs& a, const uint32_t (&row)[R], int g, int q) {
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const uint32_t n = __shfl_sync(kAll, row[u >> 1], ((16 * u) & 31) + 2 * q + (r & 1) + 8 * (r >> 1));
-        const bool ok = n != kNoRow;
-        const uint8_t* src = a.kv.data[1] + static_cast<uint64_t>(n) * a.kv.row_bytes;
-#pragma unroll
-        for (int p = 0; p < X::NV; ++p) {
-          const int d = p * 8 * X::EV + g * X::EV;
-#pragma unroll
-          for (int w = 0; w < X::WV; ++w) v[u][r][p][w] = 0;
-          if (X::kBlocks) vb[u][r][p] = 0;
-          if (ok && (p * 8 * X::EV + 8 * X::EV <= DP - 64 || d < a.kv.D)) {
-            load_row(src + d * X::row_bits / 8, v[u][r][p]);
-            if constexpr (X::kBlocks) {
-              const uint8_t* bp = a.kv.block[1] + static_cast<uint64_t>(n) * (a.kv.D >> 4) + (d >> 4);
-              vb[u][r][p] = X::EV == 32 ? *reinterpret_cast<const uint16_t*>(bp) : *bp;
-            }
-          }
-        }
-      }
-  }
-
-  // s[u][nt] = S^T of tile u: (token g | g + 8) x (head 2q | 2q + 1)
-  __device__ __forceinline__ void scores(const uint32_t (&qb)[MT][NT][2], float (&s)[U][NT][4]) {
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[u][n][i] = 0.f;
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int p = 0; p < X::NK; ++p) {
-        uint32_t f[2][X::EK / 2];  // 16-bit pairs of rows g and g + 8
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          if constexpr (!X::kQuant) {
-#pragma unroll
-            for (int w = 0; w < X::WK; ++w) f[r][w] = k[u][r][p][w];
-          } else if constexpr (!X::kBlocks) {
-#pragma unroll
-            for (int w = 0; w < X::WK; ++w) {
-              f[r][2 * w] = cvt_e4m3x2(k[u][r][p][w]);
-              f[r][2 * w + 1] = cvt_e4m3x2(k[u][r][p][w] >> 16);
-            }
-          } else {
-            const uint32_t b2 = cvt_e4m3x2(kb[u][r][p]);  // the block scales (one or two)
-#pragma unroll
-            for (int w = 0; w < X::WK; ++w) {
-              uint32_t h[4];
-              e2m1x8(k[u][r][p][w], h);
-              const uint32_t b = __byte_perm(b2, 0, w < 2 ? 0x1010 : 0x3232);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) f[r][4 * w + i] = mul_f16x2(h[i], b);
-            }
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < X::EK / 4; ++i)
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const int st = p * (X::EK / 4) + i;
-            mma<X::kF16>(s[u][n], f[0][2 * i], f[1][2 * i], f[0][2 * i + 1], f[1][2 * i + 1], qb[st][n][0], qb[st][n][1]);
-          }
-      }
-  }
-
-  // acc += V^T P^T of tile u; hi and lo: P^T as operand (tokens 0..7, 8..15)
-  __device__ __forceinline__ void add_values(int u, const uint32_t (&hi)[NT][2], const uint32_t (&lo)[NT][2], bool two,
-                                             float (&acc)[MT][NT][4]) {
-    const auto step = [&](int mt, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        mma<X::kF16>(acc[mt][n], a0, a1, a2, a3, hi[n][0], hi[n][1]);
-        if (two) mma<X::kF16>(acc[mt][n], a0, a1, a2, a3, lo[n][0], lo[n][1]);
-      }
-    };
-#pragma unroll
-    for (int p = 0; p < X::NV; ++p) {
-      const int m0 = p * (X::EV / 2);
-#pragma unroll
-      for (int w = 0; w < X::WV; ++w) {
-        const uint32_t t0 = v[u][0][p][w], t1 = v[u][1][p][w], t2 = v[u][2][p][w], t3 = v[u][3][p][w];
-        if constexpr (!X::kQuant) {
-          step(m0 + w, __byte_perm(t0, t1, 0x5410), __byte_perm(t0, t1, 0x7632), __byte_perm(t2, t3, 0x5410),
-               __byte_perm(t2, t3, 0x7632));
-        } else if constexpr (!X::kBlocks) {
-          // bytes of two tokens side by side, then two conversions a word
-          const uint32_t x0 = __byte_perm(t0, t1, 0x5140), x1 = __byte_perm(t0, t1, 0x7362);
-          const uint32_t y0 = __byte_perm(t2, t3, 0x5140), y1 = __byte_perm(t2, t3, 0x7362);
-          step(m0 + 2 * w, cvt_e4m3x2(x0), cvt_e4m3x2(x0 >> 16), cvt_e4m3x2(y0), cvt_e4m3x2(y0 >> 16));
-          step(m0 + 2 * w + 1, cvt_e4m3x2(x1), cvt_e4m3x2(x1 >> 16), cvt_e4m3x2(y1), cvt_e4m3x2(y1 >> 16));
-        } else {
-          // nibbles of two tokens side by side: even elements, odd elements
-          const uint32_t m = 0x0f0f0f0fu;
-          uint32_t e0[4], o0[4], e1[4], o1[4];
-          e2m1x8((t0 & m) | ((t1 & m) << 4), e0);
-          e2m1x8(((t0 >> 4) & m) | (t1 & ~m), o0);
-          e2m1x8((t2 & m) | ((t3 & m) << 4), e1);
-          e2m1x8(((t2 >> 4) & m) | (t3 & ~m), o1);
-          const int sh = (X::EV == 32 && w >= 2) ? 8 : 0;
-          const uint32_t b0 = cvt_e4m3x2(((vb[u][0][p] >> sh) & 0xffu) | (((vb[u][1][p] >> sh) & 0xffu) << 8));
-          const uint32_t b1 = cvt_e4m3x2(((vb[u][2][p] >> sh) & 0xffu) | (((vb[u][3][p] >> sh) & 0xffu) << 8));
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            step(m0 + 4 * w + i, mul_f16x2(e0[i], b0), mul_f16x2(o0[i], b0), mul_f16x2(e1[i], b1), mul_f16x2(o1[i], b1));
-        }
-      }
-    }
-  }
+  static constexpr int kCtas = FT_C4 && kQuant && NT == 1 && DP <= 128 && slots(4) >= 2 ? 4 : slots(3) >= FT_S3 ? 3 : slots(2) >= 2 ? 2 : 1;
+  static constexpr int S = slots(kCtas);
+  static_assert(S >= 2, "");
+  static constexpr int kRing = kWarps * S * 2 * kSide;
+  static constexpr int kSmem = 128 + kRing + kWarps * S * kNotes + 2 * kMerge;
 };
 
 // Tiles of row t; the line's length over all rows, by one warp.
@@ -380,73 +258,322 @@ __device__ __forceinline__ void store_lse(const AttnArgs& a, int t, int h, float
 // 2^(m - M), 0 where nothing was seen (m = -inf); M = -inf only with every m.
 __device__ __forceinline__ float weight_of(float m, float M) { return m == -INFINITY ? 0.f : exp2_approx(m - M); }
 
+// The place of a token among its step's (see the order of tokens above), and the token of a place.
+__device__ __forceinline__ int place_of(int t) { return (t & ~7) + 2 * (t & 3) + ((t >> 2) & 1); }
+__device__ __forceinline__ int token_at(int r) { return (r & ~7) + 4 * (r & 1) + ((r >> 1) & 3); }
+
+// A warp's way through its CTA's share of the line, unit by unit.
+struct Walk {
+  int t, at, left;   // row, place in the row's line, tiles left in the share
+  int unit, tile0;   // the unit, and its first tile in this share
+  int seq;           // the row's sequence
+  int first, base, stop;  // tokens: the first that counts, this warp's next step's, the end
+  bool whole;        // the share holds all of the unit
+  int rest;          // the unit's tiles past the share
+
+  // The next unit that the share touches; false at the share's end.  A row of
+  // a bad sequence has no steps.
+  __device__ __forceinline__ bool next(const AttnArgs& a, int offset) {
+    if (left == 0) return false;
+    RowSpan s = span_of(a, t);
+    while (at >= s.tiles * a.units) {
+      at -= s.tiles * a.units;
+      s = span_of(a, ++t);
+    }
+    unit = at / s.tiles;
+    tile0 = at - unit * s.tiles;
+    const int n = min(s.tiles - tile0, left);
+    at += n;
+    left -= n;
+    whole = n == s.tiles;
+    rest = s.tiles - tile0 - n;
+    seq = kv_seq(a.kv, t);
+    first = s.first;
+    base = s.begin + tile0 * a.tile + offset;
+    stop = min(s.len, s.begin + (tile0 + n) * a.tile);
+    if (static_cast<uint32_t>(seq) >= a.kv.n_seqs) {
+      record_status(a.status, FT_ERR_BAD_ID);
+      stop = 0;
+    }
+    return true;
+  }
+};
+
+// The side of a warp that fills its ring, ahead of the side that computes.
+// What is read for a step is used one step later: a page at the step's issue,
+// the scales (which reach the notes beside the rows) at the next one's.
+template <typename X>
+struct Feeder {
+  static constexpr int BW = X::kBlocks ? X::DPW : 1;
+  Walk walk;
+  bool more, live;          // a step is prepared; the lane's token counts
+  int32_t page;             // the token's page
+  uint32_t place;           // and its place in it
+  int slot;                 // the step's
+  bool late, late_ok;       // the step before has scales under way; the token had a row
+  uint32_t scales;          // key | value << 8
+  uint32_t blk[2][BW];      // its block scales
+
+  __device__ __forceinline__ void prepare(const AttnArgs& a, int offset, int step, int lane) {
+    while (walk.base >= walk.stop)
+      if (!walk.next(a, offset)) {
+        more = false;
+        return;
+      }
+    more = true;
+    const int tok = walk.base + lane;
+    live = lane < X::TS && tok >= walk.first && tok < walk.stop;
+    if (live) {
+      const uint32_t p = fast_div(tok, a.kv.at.by_page);
+      place = tok - p * a.kv.at.page_size;
+      page = a.kv.pages[walk.seq * a.kv.table_stride + p];
+    }
+    walk.base += step;
+  }
+
+  __device__ __forceinline__ void put_notes(uint32_t at, int lane) {
+    if constexpr (X::kQuant) {
+      if (late && lane < X::TS) {
+        // exponent bytes as writers store them; others are held to 2^-100 .. 2^123
+        const uint32_t kb = min(max(scales & 0xffu, 27u), 250u), vb = min(max(scales >> 8, 27u), 250u);
+        const float ks = late_ok ? __uint_as_float(kb << 23) : 0.f;
+        const float ev = late_ok ? static_cast<float>(static_cast<int>(vb) - 127) : -INFINITY;
+        const float iv = late_ok ? __uint_as_float((254u - vb) << 23) : 0.f;
+        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at + place_of(lane) * 16), "f"(ks), "f"(ev), "f"(iv), "f"(0.f)
+                     : "memory");
+        if constexpr (X::kBlocks) {
+          const uint32_t ka = at + X::kTok + place_of(lane) * (X::NBK * 2);
+          const uint32_t va = at + X::kTok + X::kKeyBlk + place_of(lane) * 2;
+#pragma unroll
+          for (int w = 0; w < BW; ++w)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t k2 = cvt_e4m3x2(blk[0][w] >> (16 * i)), v2 = cvt_e4m3x2(blk[1][w] >> (16 * i));
+              asm volatile("st.shared.u32 [%0], %1;" ::"r"(ka + (2 * w + i) * 4), "r"(k2) : "memory");
+              asm volatile("st.shared.u16 [%0], %1;" ::"r"(va + (4 * w + 2 * i) * (X::VS * 2)),
+                           "h"(static_cast<uint16_t>(v2))
+                           : "memory");
+              asm volatile("st.shared.u16 [%0], %1;" ::"r"(va + (4 * w + 2 * i + 1) * (X::VS * 2)),
+                           "h"(static_cast<uint16_t>(v2 >> 16))
+                           : "memory");
+            }
+        }
+      }
+    }
+  }
+
+  __device__ __forceinline__ void read_blocks(const AttnArgs& a, uint32_t row) {
+    if constexpr (X::kBlocks) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint8_t* src = a.kv.block[j] + static_cast<uint64_t>(row) * (a.kv.D >> 4);
+        if ((a.kv.D & 63) == 0) {
+#pragma unroll
+          for (int w = 0; w < BW; ++w)
+            blk[j][w] = 64 * w < a.kv.D ? *reinterpret_cast<const uint32_t*>(src + 4 * w) : 0;
+        } else {  // rows of an odd number of pairs
+#pragma unroll
+          for (int w = 0; w < BW; ++w) {
+            blk[j][w] = 64 * w < a.kv.D ? *reinterpret_cast<const uint16_t*>(src + 4 * w) : 0;
+            if (64 * w + 32 < a.kv.D) blk[j][w] |= *reinterpret_cast<const uint16_t*>(src + 4 * w + 2) << 16;
+          }
+        }
+      }
+    }
+  }
+
+  // Starts the prepared step's copies into its slot and finishes the notes of
+  // the step before.  One group of copies a call, whether it has any or not.
+  __device__ __forceinline__ void issue(const AttnArgs& a, uint32_t ring, uint32_t notes, int lane) {
+    const int before = slot == 0 ? X::S - 1 : slot - 1;
+    put_notes(notes + before * X::kNotes, lane);
+    late = false;
+    __syncwarp();  // every lane has finished reading the slot
+    if (more) {
+      uint32_t row = kNoRow;
+      if (live) {
+        row = kv_row(a.kv.at, page, place);
+        if (row == kNoRow)
+          record_status(a.status, FT_ERR_BAD_ID);
+        else
+          row += static_cast<uint32_t>(walk.unit / a.blocks) * a.kv.at.head_stride;
+      }
+      late_ok = row != kNoRow;
+      const uint32_t mask = __ballot_sync(kAll, late_ok);
+      if (!X::kQuant && lane == 0)
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(notes + slot * X::kNotes), "r"(mask) : "memory");
+      const uint32_t keys = ring + slot * (2 * X::kSide), values = keys + X::kSide;
+      const bool plain = mask == X::kFull && a.kv.row_bytes == X::RB;
+#pragma unroll
+      for (int c = 0; c < X::kCopies; ++c) {
+        const int cy = c % X::CY, more_rows = c / X::CY * X::CR;
+        const int r0 = (cy * 32 + lane) / X::CPR, chunk = (cy * 32 + lane) % X::CPR;
+        const int tok = r0 + more_rows;
+        const uint32_t n = __shfl_sync(kAll, row, tok);
+        const int pl = place_of(tok);
+        const uint32_t kd = keys + pl * X::RB + ((chunk * 16) ^ X::key_swizzle(pl));
+        const uint32_t vd = values + tok * X::RB + ((chunk * 16) ^ X::value_swizzle(tok));
+        if (plain) {
+          const uint64_t off = static_cast<uint64_t>(n) * X::RB + chunk * 16;
+          copy16(kd, a.kv.data[0] + off);
+          copy16(vd, a.kv.data[1] + off);
+        } else {
+          const bool ok = n != kNoRow && chunk * 16 < a.kv.row_bytes;
+          const uint64_t off = ok ? static_cast<uint64_t>(n) * a.kv.row_bytes + chunk * 16 : 0;
+          copy16_or_zero(kd, a.kv.data[0] + off, ok ? 16 : 0);
+          copy16_or_zero(vd, a.kv.data[1] + off, ok ? 16 : 0);
+        }
+      }
+      if constexpr (X::kQuant) {
+        late = true;
+        scales = 0;
+#pragma unroll
+        for (int w = 0; w < BW; ++w) blk[0][w] = blk[1][w] = 0;
+        if (late_ok) {
+          scales = a.kv.scale[0][row] | (a.kv.scale[1][row] << 8);
+          read_blocks(a, row);
+        }
+      }
+      slot = slot + 1 == X::S ? 0 : slot + 1;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+};
+
 // The weights are rescaled when a score exceeds the running reference by this
 // much (in powers of two), not at every new maximum: 2^4 leaves p far inside f16.
 constexpr float kSlack = 4.f;
 
+template <typename X, bool TWO, int NT>
+__device__ __forceinline__ void add_values(uint32_t at, uint32_t vnotes, int u, int g, int q,
+                                           const uint32_t (&hi)[NT][2], const uint32_t (&lo)[NT][2],
+                                           float (&acc)[X::MT][NT][4]) {
+  const auto step = [&](int mt, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      mma<X::kF16>(acc[mt][n], a0, a1, a2, a3, hi[n][0], hi[n][1]);
+      if (TWO) mma<X::kF16>(acc[mt][n], a0, a1, a2, a3, lo[n][0], lo[n][1]);
+    }
+  };
+#pragma unroll
+  for (int p = 0; p < X::NV; ++p) {
+    uint32_t v[4][X::WV];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      load_words(at + p * (8 * X::PV) + (16 * u + 4 * r) * X::RB, v[r]);
+    const int m0 = p * (X::EV / 2);
+    uint32_t b0 = 0, b1 = 0;  // block scales of the tokens q, q + 4 and q + 8, q + 12
+#pragma unroll
+    for (int w = 0; w < X::WV; ++w) {
+      const uint32_t t0 = v[0][w], t1 = v[1][w], t2 = v[2][w], t3 = v[3][w];
+      if constexpr (!X::kQuant) {
+        step(m0 + w, __byte_perm(t0, t1, 0x5410), __byte_perm(t0, t1, 0x7632), __byte_perm(t2, t3, 0x5410),
+             __byte_perm(t2, t3, 0x7632));
+      } else if constexpr (!X::kBlocks) {
+        // bytes of two tokens side by side, then two conversions a word
+        const uint32_t x0 = __byte_perm(t0, t1, 0x5140), x1 = __byte_perm(t0, t1, 0x7362);
+        const uint32_t y0 = __byte_perm(t2, t3, 0x5140), y1 = __byte_perm(t2, t3, 0x7362);
+        step(m0 + 2 * w, cvt_e4m3x2(x0), cvt_e4m3x2(x0 >> 16), cvt_e4m3x2(y0), cvt_e4m3x2(y0 >> 16));
+        step(m0 + 2 * w + 1, cvt_e4m3x2(x1), cvt_e4m3x2(x1 >> 16), cvt_e4m3x2(y1), cvt_e4m3x2(y1 >> 16));
+      } else {
+        if (w % 2 == 0) {
+          const int block = X::EV >= 16 ? p * (X::EV / 2) + g * (X::EV / 16) + w / 2 : p * 4 + (g >> 1);
+          const uint32_t na = vnotes + block * (X::VS * 2) + (16 * u + 2 * q) * 2;
+          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(b0) : "r"(na));
+          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(b1) : "r"(na + 16));
+        }
+        // nibbles of two tokens side by side: even elements, odd elements
+        const uint32_t m = 0x0f0f0f0fu;
+        uint32_t e0[4], o0[4], e1[4], o1[4];
+        e2m1x8((t0 & m) | ((t1 & m) << 4), e0);
+        e2m1x8(((t0 >> 4) & m) | (t1 & ~m), o0);
+        e2m1x8((t2 & m) | ((t3 & m) << 4), e1);
+        e2m1x8(((t2 >> 4) & m) | (t3 & ~m), o1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          step(m0 + 4 * w + i, mul_f16x2(e0[i], b0), mul_f16x2(o0[i], b0), mul_f16x2(e1[i], b1), mul_f16x2(o1[i], b1));
+      }
+    }
+  }
+}
+
 template <int FMT, int DP, int NT>
-__global__ void __launch_bounds__(kWarps * 32) attend_kernel(const AttnArgs a) {
-  using X = Deal<FMT, DP>;
-  using W = Warp<FMT, DP, NT>;
-  constexpr int U = X::U, R = W::R, MT = DP / 16, H = 8 * NT, DS = DP + 8;
-  __shared__ float red[kWarps][H][DS];
-  __shared__ float2 red_ml[kWarps][H];
+__global__ void __launch_bounds__(kWarps * 32, Deal<FMT, DP, NT>::kCtas)
+    attend_kernel(const __grid_constant__ AttnArgs a) {
+  using X = Deal<FMT, DP, NT>;
+  constexpr int U = X::U, MT = X::MT, H = X::H, S = X::S;
+  extern __shared__ uint8_t smem_raw[];
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int wh = warp & ((1 << a.warps_h_log2) - 1), wt = warp >> a.warps_h_log2;
   const int warps_t = kWarps >> a.warps_h_log2;
 
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  const uint32_t ring = smem_u32(smem) + warp * (S * 2 * X::kSide);
+  const uint32_t notes = smem_u32(smem) + X::kRing + warp * (S * X::kNotes);
+  float* merge = reinterpret_cast<float*>(smem + X::kRing + kWarps * S * X::kNotes);
+
   // this CTA's share of the line, and the row it begins in
   const int64_t total = tiles_before(a, a.T, lane) * a.units;
   const int64_t share = split_share(total, a.workers);
-  int64_t at = blockIdx.x * share;
-  if (at >= total) return;
-  const int64_t end = at + share < total ? at + share : total;
-  int t = 0;
-  int64_t row_at = 0;  // the row's first number
-  for (int t0 = 0;; t0 += 32) {
-    int64_t n = t0 + lane < a.T ? static_cast<int64_t>(span_of(a, t0 + lane).tiles) * a.units : 0;
-    int64_t upto = n;
+  const int64_t from = blockIdx.x * share;
+  if (threadIdx.x == 0) a.begun[blockIdx.x] = make_int4(0, 0, 0, 0);
+  // rows that see nothing
+  for (int t = blockIdx.x; t < a.T; t += gridDim.x)
+    if (span_of(a, t).tiles == 0)
+      for (int i = threadIdx.x; i < a.Hq * (a.kv.D / 2); i += kWarps * 32) {
+        const int h = i / (a.kv.D / 2), d = 2 * (i - h * (a.kv.D / 2));
+        store_out(a, t, h, d, 0.f, 0.f);
+        if (d == 0) store_lse(a, t, h, -INFINITY, 0.f);
+      }
+  if (from >= total) return;
+  Walk walk;
+  walk.left = static_cast<int>(from + share < total ? share : total - from);
+  {
+    int64_t row_at = 0;  // the row's first number
+    for (int t0 = 0;; t0 += 32) {
+      const int64_t n = t0 + lane < a.T ? static_cast<int64_t>(span_of(a, t0 + lane).tiles) * a.units : 0;
+      int64_t upto = n;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(kAll, upto, o);
-      if (lane >= o) upto += y;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(kAll, upto, o);
+        if (lane >= o) upto += y;
+      }
+      const uint32_t past = __ballot_sync(kAll, row_at + upto > from);
+      if (past) {
+        const int i = __ffs(past) - 1;
+        walk.t = t0 + i;
+        walk.at = static_cast<int>(from - row_at - __shfl_sync(kAll, upto - n, i));
+        break;
+      }
+      row_at += __shfl_sync(kAll, upto, 31);
     }
-    const uint32_t past = __ballot_sync(kAll, row_at + upto > at);
-    if (past) {
-      const int i = __ffs(past) - 1;
-      t = t0 + i;
-      row_at += __shfl_sync(kAll, upto - n, i);
-      break;
-    }
-    row_at += __shfl_sync(kAll, upto, 31);
+  }
+  walk.base = walk.stop = 0;
+  const int offset = wt * X::TS, step = X::TS * warps_t;
+
+  Feeder<X> feed;
+  feed.walk = walk;
+  feed.slot = 0;
+  feed.late = false;
+  feed.prepare(a, offset, step, lane);
+#pragma unroll 1
+  for (int i = 0; i < S; ++i) {
+    feed.issue(a, ring, notes, lane);
+    if (feed.more) feed.prepare(a, offset, step, lane);
   }
 
-  while (at < end) {
-    RowSpan span = span_of(a, t);
-    while (span.tiles == 0) span = span_of(a, ++t);
-    const int unit = static_cast<int>((at - row_at) / span.tiles);
-    const int tile0 = static_cast<int>(at - row_at - static_cast<int64_t>(unit) * span.tiles);
-    const int tile1 = end - at < span.tiles - tile0 ? tile0 + static_cast<int>(end - at) : span.tiles;
-    const int kv_head = unit / a.blocks;
-    const int head0 = (unit - kv_head * a.blocks) * a.block_heads;  // of the key head's group
+  // places of the lane's pieces in a step's rows
+  uint32_t koff[X::KP];
+#pragma unroll
+  for (int p = 0; p < X::KP; ++p) koff[p] = g * X::RB + ((p * 4 + q) * X::PK ^ X::key_swizzle(g));
+  const uint32_t voff = q * X::RB + (g * X::PV ^ X::value_swizzle(q));
 
-    const int32_t seq = kv_seq(a.kv, t);
-    const bool bad_seq = static_cast<uint32_t>(seq) >= a.kv.n_seqs;
-    if (bad_seq) record_status(a.status, FT_ERR_BAD_ID);
-    const int32_t* table = a.kv.pages + static_cast<int64_t>(bad_seq ? 0 : seq) * a.kv.table_stride;
-    const uint32_t head_row = static_cast<uint32_t>(kv_head) * a.kv.at.head_stride;
-    const int first = span.first;
-    const int stop = span.begin + tile1 * a.tile < span.len ? span.begin + tile1 * a.tile : span.len;
-    const int tok_end = bad_seq ? 0 : stop;
-    const int step = 16 * U * warps_t;
-    int base = span.begin + tile0 * a.tile + wt * 16 * U;
-
-    // the first rows' loads go out before the queries are prepared
-    W w;
-    int32_t page[R];
-    uint32_t row[R];
-    W::pages_of(a, table, base, first, tok_end, lane, page);
+  int slot = 0;
+  while (walk.next(a, offset)) {
+    const int t = walk.t;
+    const int kv_head = walk.unit / a.blocks;
+    const int head0 = (walk.unit - kv_head * a.blocks) * a.block_heads;  // of the key head's group
 
     // queries: B operand (head g of each tile), power-of-two scaled into f16 where the products are f16
     uint32_t qb[MT][NT][2];
@@ -458,8 +585,8 @@ __global__ void __launch_bounds__(kWarps * 32) attend_kernel(const AttnArgs a) {
       uint2 raw[MT];
 #pragma unroll
       for (int st = 0; st < MT; ++st) {
-        constexpr int S = X::EK / 4;
-        const int d = (st / S) * 4 * X::EK + q * X::EK + (st % S) * 4;
+        constexpr int E = X::EK / 4;
+        const int d = (st / E) * 4 * X::EK + q * X::EK + (st % E) * 4;
         raw[st] = make_uint2(0, 0);
         if (h < a.G && d < a.kv.D) raw[st] = *reinterpret_cast<const uint2*>(src + d);
       }
@@ -510,45 +637,91 @@ __global__ void __launch_bounds__(kWarps * 32) attend_kernel(const AttnArgs a) {
         for (int i = 0; i < 4; ++i) acc[mt][n][i] = 0.f;
     }
 
-    W::rows_of(a, head_row, base, first, tok_end, lane, page, row);
-    w.load_keys(a, row, g, q);
-    w.load_values(a, row, g, q);
-    W::pages_of(a, table, base + step, first, tok_end, lane, page);
-    while (base < tok_end) {
+#pragma unroll 1
+    for (; walk.base < walk.stop; walk.base += step) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+      __syncwarp();
+      const uint32_t at = ring + slot * (2 * X::kSide), note = notes + slot * X::kNotes;
+
+      // s[u][n] = S^T of 16 tokens: (token g | g + 8) x (head 2q | 2q + 1)
       float s[U][NT][4];
-      w.scores(qb, s);
-      const uint32_t valid = w.valid;
-      uint32_t scale_bytes[R];
 #pragma unroll
-      for (int i = 0; i < R; ++i) scale_bytes[i] = X::kQuant ? w.sc[i] : 0;
-      base += step;
-      W::rows_of(a, head_row, base, first, tok_end, lane, page, row);
-      w.load_keys(a, row, g, q);  // of the next step: in flight during this one's weights and values
+      for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[u][n][i] = 0.f;
+#pragma unroll
+        for (int p = 0; p < X::NK; ++p) {
+          uint32_t f[2][X::EK / 2];  // 16-bit pairs of rows g and g + 8
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            uint32_t k[X::WK];
+            load_words(at + (p / X::KP) * (X::KP * 4 * X::PK) + koff[p % X::KP] + (16 * u + 8 * r) * X::RB, k);
+            if constexpr (!X::kQuant) {
+#pragma unroll
+              for (int w = 0; w < X::WK; ++w) f[r][w] = k[w];
+            } else if constexpr (!X::kBlocks) {
+#pragma unroll
+              for (int w = 0; w < X::WK; ++w) {
+                f[r][2 * w] = cvt_e4m3x2(k[w]);
+                f[r][2 * w + 1] = cvt_e4m3x2(k[w] >> 16);
+              }
+            } else {
+              uint32_t b2;  // the lane's block scales: one or two
+              const uint32_t na = note + X::kTok + (16 * u + 8 * r + g) * (X::NBK * 2) + (p * 4 + q) * (X::EK / 8);
+              if (X::EK == 32) {
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(b2) : "r"(na));
+              } else {
+                uint16_t b1;
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(b1) : "r"(na));
+                b2 = b1;
+              }
+#pragma unroll
+              for (int w = 0; w < X::WK; ++w) {
+                uint32_t h[4];
+                e2m1x8(k[w], h);
+                const uint32_t b = __byte_perm(b2, 0, w < 2 ? 0x1010 : 0x3232);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[r][4 * w + i] = mul_f16x2(h[i], b);
+              }
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < X::EK / 4; ++i)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              const int st = p * (X::EK / 4) + i;
+              mma<X::kF16>(s[u][n], f[0][2 * i], f[1][2 * i], f[0][2 * i + 1], f[1][2 * i + 1], qb[st][n][0],
+                           qb[st][n][1]);
+            }
+        }
+      }
 
       // scores in powers of two, with the value's exponent; masked tokens -inf
       float iv[U][2];
       bool more = false;
+      uint32_t mask = 0;
+      if constexpr (!X::kQuant) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(mask) : "r"(note));
+      const bool part = !X::kQuant && mask != X::kFull;
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          float ks = 1.f, ev = 0.f;
+          float ks = 1.f, ev = 0.f, none;
           iv[u][r] = 1.f;
-          if (X::kQuant) {
-            const uint32_t b = __shfl_sync(kAll, scale_bytes[u >> 1], ((16 * u) & 31) + g + 8 * r);
-            const uint32_t kb = max(b & 0xffu, 27u), vb = max(b >> 8, 27u);  // 2^-100: a byte that no writer stores
-            ks = __uint_as_float(kb << 23);
-            ev = static_cast<float>(static_cast<int>(vb) - 127);
-            iv[u][r] = __uint_as_float((254u - vb) << 23);
-          }
-          const bool ok = (valid >> (2 * u + r)) & 1;
+          if constexpr (X::kQuant)
+            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(ks), "=f"(ev), "=f"(iv[u][r]), "=f"(none)
+                         : "r"(note + (16 * u + 8 * r + g) * 16));
+          const bool ok = (mask >> token_at(16 * u + 8 * r + g)) & 1;
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               float& x = s[u][n][2 * r + i];
               x = X::kQuant ? fmaf(x * ks, mul[n][i], ev) : x * mul[n][i];
-              x = ok ? x : -INFINITY;
+              if (part) x = ok ? x : -INFINITY;
               more |= x > m[n][i] + kSlack;
             }
         }
@@ -573,19 +746,16 @@ __global__ void __launch_bounds__(kWarps * 32) attend_kernel(const AttnArgs a) {
             }
           }
       }
-      float ref[NT][2];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) ref[n][i] = m[n][i] == -INFINITY ? 0.f : m[n][i];
+      const bool two = !X::kF16 || a.two_terms;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         uint32_t hi[NT][2], lo[NT][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n) {
+          const float r0 = m[n][0] == -INFINITY ? 0.f : m[n][0], r1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const float p0 = exp2_approx(s[u][n][2 * r] - ref[n][0]), p1 = exp2_approx(s[u][n][2 * r + 1] - ref[n][1]);
+            const float p0 = exp2_approx(s[u][n][2 * r] - r0), p1 = exp2_approx(s[u][n][2 * r + 1] - r1);
             if (X::kQuant) {
               l[n][0] = fmaf(p0, iv[u][r], l[n][0]);
               l[n][1] = fmaf(p1, iv[u][r], l[n][1]);
@@ -596,18 +766,25 @@ __global__ void __launch_bounds__(kWarps * 32) attend_kernel(const AttnArgs a) {
             const uint32_t h = pack16<X::kF16>(p0, p1);
             hi[n][r] = transpose8x8(h);
             lo[n][r] = 0;
-            if (!X::kF16 || a.two_terms) {
+            if (two) {
               const float2 back = unpack16<X::kF16>(h);
               lo[n][r] = transpose8x8(pack16<X::kF16>(p0 - back.x, p1 - back.y));
             }
           }
-        w.add_values(u, hi, lo, !X::kF16 || a.two_terms, acc);
+        }
+        const uint32_t vnotes = note + X::kTok + X::kKeyBlk;
+        if (two)
+          add_values<X, true, NT>(at + X::kSide + voff, vnotes, u, g, q, hi, lo, acc);
+        else if constexpr (X::kF16)
+          add_values<X, false, NT>(at + X::kSide + voff, vnotes, u, g, q, hi, lo, acc);
       }
-      w.load_values(a, row, g, q);
-      W::pages_of(a, table, base + step, first, tok_end, lane, page);
+      feed.issue(a, ring, notes, lane);  // refills this slot
+      if (feed.more) feed.prepare(a, offset, step, lane);
+      slot = slot + 1 == S ? 0 : slot + 1;
     }
 
-    // the warps' sums meet in shared memory
+    // The warps' sums meet in shared memory, half of them handing over at a
+    // time.  A warp hands over in the place that it took over from before.
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -615,112 +792,168 @@ __global__ void __launch_bounds__(kWarps * 32) attend_kernel(const AttnArgs a) {
         l[n][i] += __shfl_xor_sync(kAll, l[n][i], 4);
         l[n][i] += __shfl_xor_sync(kAll, l[n][i], 8);
         l[n][i] += __shfl_xor_sync(kAll, l[n][i], 16);
-        if (g == 0) red_ml[warp][n * 8 + 2 * q + i] = make_float2(m[n][i], l[n][i]);
+      }
+    if (warps_t > 1) __syncthreads();  // the places are free of the unit before
+    for (int half = warps_t >> 1; half > 0; half >>= 1) {
+      float* place = merge + (half == 2 ? wt & 1 : a.warps_h_log2 ? wh : 1) * (X::kMerge / 4) + lane;
+      if (wt >= half && wt < 2 * half) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          const int d = (mt / (X::EV / 2)) * 8 * X::EV + g * X::EV + 2 * (mt % (X::EV / 2));
-          *reinterpret_cast<float2*>(&red[warp][n * 8 + 2 * q + i][d]) = make_float2(acc[mt][n][i], acc[mt][n][2 + i]);
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            place[(n * 4 + i) * 32] = m[n][i];
+            place[(n * 4 + 2 + i) * 32] = l[n][i];
+          }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) place[(NT * 4 + (mt * NT + n) * 4 + i) * 32] = acc[mt][n][i];
         }
       }
-    __syncthreads();
-    const bool whole = tile0 == 0 && tile1 == span.tiles;
-    const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (tile0 == 0 ? 1 : 0);
-    const int heads = a.block_heads < a.G - head0 ? a.block_heads : a.G - head0;
-    for (int i = threadIdx.x; i < heads * (DP / 2); i += kWarps * 32) {
-      const int h = i / (DP / 2), d = 2 * (i - h * (DP / 2));
-      const int x = h / H, hh = h - x * H;  // warp column and head in it
-      float M = -INFINITY;
-      for (int y = 0; y < warps_t; ++y) M = fmaxf(M, red_ml[(y << a.warps_h_log2) + x][hh].x);
-      float L = 0.f, o0 = 0.f, o1 = 0.f;
-      for (int y = 0; y < warps_t; ++y) {
-        const int wi = (y << a.warps_h_log2) + x;
-        const float2 ml = red_ml[wi][hh];
-        const float c = weight_of(ml.x, M);
-        const float2 o = *reinterpret_cast<const float2*>(&red[wi][hh][d]);
-        L += c * ml.y;
-        o0 += c * o.x;
-        o1 += c * o.y;
-      }
-      if (whole) {
-        const int hq = kv_head * a.G + head0 + h;
-        const float inv = L == 0.f ? 0.f : 1.f / L;
-        if (d < a.kv.D) store_out(a, t, hq, d, o0 * inv, o1 * inv);
-        if (d == 0) store_lse(a, t, hq, M, L);
-      } else {
-        *reinterpret_cast<float2*>(a.part_o + (slot * a.block_heads + h) * DP + d) = make_float2(o0, o1);
-        if (d == 0) a.part_ml[slot * a.block_heads + h] = make_float2(M, L);
+      __syncthreads();
+      if (wt < half) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float om = place[(n * 4 + i) * 32], ol = place[(n * 4 + 2 + i) * 32];
+            const float top = fmaxf(m[n][i], om);
+            const float x = weight_of(m[n][i], top), y = weight_of(om, top);
+            m[n][i] = top;
+            l[n][i] = l[n][i] * x + ol * y;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              float* o = place + (NT * 4 + (mt * NT + n) * 4) * 32;
+              acc[mt][n][i] = acc[mt][n][i] * x + o[i * 32] * y;
+              acc[mt][n][2 + i] = acc[mt][n][2 + i] * x + o[(2 + i) * 32] * y;
+            }
+          }
       }
     }
-    __syncthreads();  // red is free for the next unit
-    at += tile1 - tile0;
-    if (tile1 == span.tiles && unit == a.units - 1) {
-      row_at += static_cast<int64_t>(span.tiles) * a.units;
-      ++t;
+    if (threadIdx.x == 0 && walk.tile0 == 0 && !walk.whole)
+      a.begun[blockIdx.x] = make_int4(
+          t, walk.unit, static_cast<int>(blockIdx.x) + static_cast<int>((walk.rest + share - 1) / share), 1);
+    if (wt == 0) {
+      const int64_t part = static_cast<int64_t>(blockIdx.x) * 2 + (walk.tile0 == 0 ? 1 : 0);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int h = wh * H + n * 8 + 2 * q + i;  // in the block
+          if (h >= a.block_heads || head0 + h >= a.G) continue;
+          const float M = m[n][i], L = l[n][i];
+          const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            const int d = (mt / (X::EV / 2)) * 8 * X::EV + g * X::EV + 2 * (mt % (X::EV / 2));
+            if (!walk.whole)
+              *reinterpret_cast<float2*>(a.part_o + (part * a.block_heads + h) * DP + d) =
+                  make_float2(acc[mt][n][i], acc[mt][n][2 + i]);
+            else if (d < a.kv.D)
+              store_out(a, t, kv_head * a.G + head0 + h, d, acc[mt][n][i] * inv, acc[mt][n][2 + i] * inv);
+          }
+          if (g == 0) {
+            if (walk.whole)
+              store_lse(a, t, kv_head * a.G + head0 + h, M, L);
+            else
+              a.part_ml[part * a.block_heads + h] = make_float2(M, L);
+          }
+        }
     }
   }
 }
 
-// Adds the partial sums of units that crossed shares, in the shares' order,
-// and answers rows that see nothing.  One CTA a (row, query head); its warps
-// take every fourth partial.
-template <int DP>
-__global__ void __launch_bounds__(128) join_kernel(const AttnArgs a) {
-  constexpr int N = DP / 32;  // channels of a lane
-  __shared__ float acc_s[4][DP];
-  __shared__ float2 ml_s[4];
-  const int t = blockIdx.x / a.Hq, hq = blockIdx.x - t * a.Hq;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// Adds the partial sums of the unit that worker blockIdx.x began, if it went
+// past its share, in the workers' order.  A CTA takes kHeads heads of the
+// block, 8 / kHeads warps a head (each every so-many-th partial): one head
+// where few units have many partials each (one long row), eight otherwise.
+template <int DP, int kHeads>
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnArgs a) {
+  constexpr int N = DP / 64;           // channel pairs of a lane: 2 * lane + 64 i
+  constexpr int kSpread = 8 / kHeads;  // warps of a head
+  constexpr int kBatch = 4;            // partials in flight
+  __shared__ float2 acc_s[kSpread > 1 ? 8 : 1][DP / 2];
+  __shared__ float2 ml_s[8];
   // every CTA waits, whether it has something to add or not: work after this
   // grid must also come after attend_kernel
   pdl_wait();
-  const RowSpan span = span_of(a, t);
-  if (span.tiles == 0) {
-    for (int d = 2 * threadIdx.x; d < a.kv.D; d += 256) store_out(a, t, hq, d, 0.f, 0.f);
-    if (threadIdx.x == 0) store_lse(a, t, hq, -INFINITY, 0.f);
-    return;
-  }
-  const int64_t before = tiles_before(a, t, lane);
-  const int64_t total = tiles_before(a, a.T, lane) * a.units;
-  const int64_t share = split_share(total, a.workers);
-  const int kv_head = hq / a.G, hg = hq - kv_head * a.G;
-  const int block = hg / a.block_heads, h = hg - block * a.block_heads;
-  const int64_t from = before * a.units + static_cast<int64_t>(kv_head * a.blocks + block) * span.tiles;
-  const int64_t c0 = from / share, c1 = (from + span.tiles - 1) / share;
-  if (c0 == c1) return;
-  float m = -INFINITY, l = 0.f, acc[N];
+  const int4 unit = a.begun[blockIdx.x];
+  if (unit.w == 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = blockIdx.y * kHeads + warp / kSpread;
+  const int kv_head = unit.y / a.blocks;
+  const int hg = (unit.y - kv_head * a.blocks) * a.block_heads + h;  // in the key head's group
+  const bool live = h < a.block_heads && hg < a.G;
+  const int c0 = blockIdx.x, c1 = unit.z;
+  float m = -INFINITY, l = 0.f;
+  float2 acc[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) acc[i] = 0.f;
-  for (int64_t c = c0 + warp; c <= c1; c += 4) {
-    const int64_t slot = (c * 2 + (c == c0 ? 1 : 0)) * a.block_heads + h;
-    const float2 ml = a.part_ml[slot];
-    float o[N];
+  for (int i = 0; i < N; ++i) acc[i] = make_float2(0.f, 0.f);
+  for (int c = c0 + warp % kSpread; live && c <= c1; c += kBatch * kSpread) {
+    float2 ml[kBatch], o[kBatch][N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) o[i] = a.part_o[slot * DP + lane + 32 * i];
-    const float top = fmaxf(m, ml.x);
-    const float x = weight_of(m, top), y = weight_of(ml.x, top);
-    m = top;
-    l = l * x + ml.y * y;
+    for (int k = 0; k < kBatch; ++k) {
+      const int ck = c + k * kSpread;
+      ml[k] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] = acc[i] * x + o[i] * y;
-  }
-  if (lane == 0) ml_s[warp] = make_float2(m, l);
+      for (int i = 0; i < N; ++i) o[k][i] = make_float2(0.f, 0.f);
+      if (ck <= c1) {
+        const int64_t slot = (static_cast<int64_t>(ck) * 2 + (ck == c0 ? 1 : 0)) * a.block_heads + h;
+        ml[k] = a.part_ml[slot];
 #pragma unroll
-  for (int i = 0; i < N; ++i) acc_s[warp][lane + 32 * i] = acc[i];
-  __syncthreads();
-  float M = -INFINITY, L = 0.f;
-  for (int y = 0; y < 4; ++y) M = fmaxf(M, ml_s[y].x);
-  for (int y = 0; y < 4; ++y) L += weight_of(ml_s[y].x, M) * ml_s[y].y;
-  const float inv = L == 0.f ? 0.f : 1.f / L;
-  for (int d = 2 * threadIdx.x; d < a.kv.D; d += 256) {
-    float o0 = 0.f, o1 = 0.f;
-    for (int y = 0; y < 4; ++y) {
-      const float c = weight_of(ml_s[y].x, M);
-      o0 += c * acc_s[y][d];
-      o1 += c * acc_s[y][d + 1];
+        for (int i = 0; i < N; ++i) o[k][i] = *reinterpret_cast<const float2*>(a.part_o + slot * DP + 2 * lane + 64 * i);
+      }
     }
-    store_out(a, t, hq, d, o0 * inv, o1 * inv);
+    float top = m;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) top = fmaxf(top, ml[k].x);
+    const float x = weight_of(m, top);
+    m = top;
+    l *= x;
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] = make_float2(acc[i].x * x, acc[i].y * x);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const float y = weight_of(ml[k].x, top);
+      l += ml[k].y * y;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        acc[i].x += o[k][i].x * y;
+        acc[i].y += o[k][i].y * y;
+      }
+    }
   }
-  if (threadIdx.x == 0) store_lse(a, t, hq, M, L);
+  if (kSpread > 1) {
+    if (lane == 0) ml_s[warp] = make_float2(m, l);
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc_s[warp][lane + 32 * i] = acc[i];
+    __syncthreads();
+    if (warp % kSpread != 0) return;
+    const float own = m;
+#pragma unroll
+    for (int y = 0; y < kSpread; ++y) m = fmaxf(m, ml_s[warp + y].x);
+    const float x = weight_of(own, m);
+    l *= x;
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] = make_float2(acc[i].x * x, acc[i].y * x);
+#pragma unroll
+    for (int y = 1; y < kSpread; ++y) {
+      const float w = weight_of(ml_s[warp + y].x, m);
+      l += w * ml_s[warp + y].y;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        acc[i].x += w * acc_s[warp + y][lane + 32 * i].x;
+        acc[i].y += w * acc_s[warp + y][lane + 32 * i].y;
+      }
+    }
+  }
+  if (!live) return;
+  const int hq = kv_head * a.G + hg;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (2 * lane + 64 * i < a.kv.D) store_out(a, unit.x, hq, 2 * lane + 64 * i, acc[i].x * inv, acc[i].y * inv);
+  if (lane == 0) store_lse(a, unit.x, hq, m, l);
 }
 
 // ------------------------------------------------------------------ host side ---
@@ -749,34 +982,41 @@ size_t part_ml_bytes(const Shape& s) { return static_cast<size_t>(kMaxWorkers) *
 
 template <int FMT, int DP, int NT>
 ft_status launch(AttnArgs& a, cudaStream_t s) {
-  using X = Deal<FMT, DP>;
+  using X = Deal<FMT, DP, NT>;
+  ft_status st = ensure_dyn_smem(reinterpret_cast<const void*>(attend_kernel<FMT, DP, NT>), X::kSmem, "attn_decode");
+  if (st != FT_OK) return st;
   static std::atomic<int> resident{0};  // CTAs an SM holds
   int r = resident.load(std::memory_order_relaxed);
   if (r == 0) {
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&r, attend_kernel<FMT, DP, NT>, kWarps * 32, 0) != cudaSuccess || r < 1)
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&r, attend_kernel<FMT, DP, NT>, kWarps * 32, X::kSmem) != cudaSuccess ||
+        r < 1)
       return fail(FT_ERR_CUDA, "attn_decode: %s", cudaGetErrorString(cudaGetLastError()));
     resident.store(r, std::memory_order_relaxed);
   }
-  a.tile = 16 * X::U * (kWarps >> a.warps_h_log2);
+  a.tile = X::TS * (kWarps >> a.warps_h_log2);
   const int64_t longest = a.window > 0 && a.window < a.most ? a.window + 15 : a.most;
   const int64_t most_tiles = (longest + a.tile - 1) / a.tile * a.units * a.T;
   int64_t workers = static_cast<int64_t>(device_sm_count()) * r;
   if (workers > kMaxWorkers) workers = kMaxWorkers;
   if (workers > most_tiles) workers = most_tiles;
+  // positions in a row's line, and in a share, are 32-bit in the kernel
+  if (most_tiles / a.T >= (1ll << 31) || most_tiles / workers >= (1ll << 31))
+    return fail(FT_ERR_UNSUPPORTED, "attn_decode: page table too large");
   a.workers = static_cast<int>(workers);
-  attend_kernel<FMT, DP, NT><<<a.workers, kWarps * 32, 0, s>>>(a);
-  ft_status st = launch_check("attn_decode");
+  attend_kernel<FMT, DP, NT><<<a.workers, kWarps * 32, X::kSmem, s>>>(a);
+  st = launch_check("attn_decode");
   if (st != FT_OK) return st;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.T) * a.Hq);
-  cfg.blockDim = dim3(128);
+  const bool long_rows = workers > 8ll * a.T * a.units;  // more than eight partials a unit on average
+  cfg.gridDim = dim3(a.workers, long_rows ? a.block_heads : a.block_heads / 8);
+  cfg.blockDim = dim3(256);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, join_kernel<DP>, a);
+  cudaLaunchKernelEx(&cfg, long_rows ? join_kernel<DP, 1> : join_kernel<DP, 8>, a);
   return launch_check("attn_decode join");
 }
 
@@ -805,7 +1045,7 @@ extern "C" {
 size_t ft_attn_decode_workspace(int32_t T, int32_t Hq, int32_t Hkv, int32_t D) {
   if (!attn_shape_ok(T, Hq, Hkv, D)) return 0;
   const Shape s = shape_of(D, Hq / Hkv);
-  return part_o_bytes(s) + part_ml_bytes(s);
+  return part_o_bytes(s) + part_ml_bytes(s) + kMaxWorkers * sizeof(int4);
 }
 
 ft_status ft_attn_decode(const ft_kv_cache* cache_host, const ft_rows* q_host, int32_t T, int32_t Hq, int32_t dtype,
@@ -842,6 +1082,7 @@ ft_status ft_attn_decode(const ft_kv_cache* cache_host, const ft_rows* q_host, i
   a.lens = lens;
   a.part_o = static_cast<float*>(ws);
   a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + part_o_bytes(sh));
+  a.begun = reinterpret_cast<int4*>(static_cast<uint8_t*>(ws) + part_o_bytes(sh) + part_ml_bytes(sh));
   a.scale_log2 = scale * 1.4426950408889634f;
   a.window = window;
   a.T = T;

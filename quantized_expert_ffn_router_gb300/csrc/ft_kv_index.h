@@ -34,7 +34,7 @@ FT_HD uint32_t fast_div(uint32_t n, FastDiv f) { return static_cast<uint32_t>((s
 constexpr uint32_t kNoRow = 0xffffffffu;
 
 // The cache's row numbering, as the kernels take it: every row index is below
-// kNoRow (checked by the entry points), so rows and strides fit 32 bits.
+// 2^31 - 1 (checked by the entry points), so rows and strides fit 32 bits.
 struct KvIndex {
   uint32_t page_size;
   FastDiv by_page;

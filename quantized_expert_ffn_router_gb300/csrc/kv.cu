@@ -581,9 +581,9 @@ ft_status kv_view(const char* what, const ft_kv_cache* c, const ft_page_table* p
   const double last = static_cast<double>(c->n_pages - 1) * c->page_stride +
                       static_cast<double>(c->Hkv - 1) * c->head_stride +
                       static_cast<double>(c->page_size - 1) * c->slot_stride;
-  if (!(last < 4294967295.0) || c->n_pages >= (1ll << 31) || c->page_stride >= (1ll << 32) ||
+  if (!(last < 2147483647.0) || c->n_pages >= (1ll << 31) || c->page_stride >= (1ll << 32) ||
       c->head_stride >= (1ll << 32) || c->slot_stride >= (1ll << 32))
-    return fail(FT_ERR_UNSUPPORTED, "%s: cache rows beyond 2^32", what);
+    return fail(FT_ERR_UNSUPPORTED, "%s: cache rows beyond 2^31", what);
   const bool quant = c->fmt == FT_KV_E4M3 || c->fmt == FT_KV_NVFP4;
   FT_REQUIRE(c->k != nullptr && c->v != nullptr, "%s: cache k or v is NULL", what);
   FT_REQUIRE(!quant || (c->k_scale != nullptr && c->v_scale != nullptr), "%s: the format needs scale arrays", what);
