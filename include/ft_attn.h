@@ -54,7 +54,8 @@ enum { FT_KV_BF16 = 0, FT_KV_F16 = 1, FT_KV_E4M3 = 2, FT_KV_NVFP4 = 3 };
  * and layers interleaved in one allocation, can be described), the same for
  * keys and values; its codes start at k + r * row bytes (ft_kv_row_bytes), its
  * exponent byte at k_scale + r, its block scales at k_block + r * (D / 16).
- * Arrays 16-byte aligned; scale and block arrays NULL where the format has
+ * Arrays 16-byte aligned, the scale arrays allocated in whole 4-byte words
+ * (they are read as words); scale and block arrays NULL where the format has
  * none.  Limits: D a multiple of 16 (FT_KV_NVFP4: of 32), at most 256; every
  * row index below 2^31 - 1.
  */

@@ -78,7 +78,7 @@ struct AttnArgs {
   const int32_t* lens;
   float* part_o;   // [worker][2][heads of a block][D padded]
   float2* part_ml;  // [worker][2][heads of a block] (maximum, sum)
-  int4* begun;      // [worker] the unit that the worker began and others went on with: row, unit, last worker, 1 (or 0)
+  int2* shared_by;  // [row][unit] the first and the last worker of a unit that crossed shares; (1, 0) of any other
   float scale_log2;
   int32_t window, T, Hq, G;
   int32_t units;         // head blocks of a row: Hkv * blocks
@@ -140,6 +140,13 @@ __device__ __forceinline__ float2 unpack16(uint32_t w) {
   return make_float2(bf16_lo(w), bf16_hi(w));
 }
 
+// The four E4M3 codes of a word as two f16 pairs.
+__device__ __forceinline__ void e4m3x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+
 // N words (1, 2 or 4) of shared memory.
 template <int N>
 __device__ __forceinline__ void load_words(uint32_t p, uint32_t (&w)[N]) {
@@ -181,8 +188,8 @@ struct Deal {
   static constexpr bool kSwap = RB % 128 == 0;      // keys: odd places have 64-byte halves swapped
   static constexpr int KP = kSwap ? 2 : 1;
   static_assert(!kSwap || PK == 16, "");
-  __device__ static int key_swizzle(int place) { return kSwap ? (place & 1) << 6 : 0; }
-  __device__ static int value_swizzle(int token) {
+  __device__ static constexpr int key_swizzle(int place) { return kSwap ? (place & 1) << 6 : 0; }
+  __device__ static constexpr int value_swizzle(int token) {
     return PV == 16 ? (token & 3) << 5 : PV == 8 ? ((token >> 1) & 1) << 5 : 0;
   }
   // A step: TS tokens.
@@ -194,26 +201,32 @@ struct Deal {
   static constexpr int CPR = RB / 16, kCopies = TS * CPR / 32;
   static constexpr int CY = CPR / gcd(32, CPR), CR = 32 * CY / CPR;
   static_assert(kCopies % CY == 0, "");
-  // Beside the rows: per token (key factor, value exponent, 2^-value exponent),
-  // the block scales as f16 (keys [place][block], values [block][place]), and
-  // the mask of tokens that count.
+  // Beside a slot's rows, as copied: the words that hold the tokens' exponent
+  // bytes (keys, then values), and the block scales (keys, then values).
+  static constexpr int NBK = DP / 16, VS = TS + 4;
+  static constexpr int kRawBlk = kBlocks ? TS * NBK : 0;
+  static constexpr int kRaw = kQuant ? 2 * TS * 4 + 2 * kRawBlk : 0;
+  // Once a warp, worked out when the step's turn comes: per place (key factor,
+  // value exponent, 2^-value exponent, -), and the block scales as f16 (keys
+  // [place][block], values [block][place]).
   static constexpr int kTok = kQuant ? TS * 16 : 0;
-  static constexpr int NBK = DP / 16, VS = TS + 4, DPW = DP / 64;
   static constexpr int kKeyBlk = kBlocks ? TS * NBK * 2 : 0, kValBlk = kBlocks ? NBK * VS * 2 : 0;
-  static constexpr int kNotes = kTok + kKeyBlk + kValBlk + 16;
+  static constexpr int kNotes = kTok + kKeyBlk + kValBlk;
   static constexpr uint32_t kFull = TS == 32 ? 0xffffffffu : (1u << (TS & 31)) - 1;
   // The merge of the warps takes two warps' sums at a time.
   static constexpr int kMerge = (MT * NT * 4 + NT * 4) * 32 * 4;
   // Slots of a warp's ring with so many CTAs an SM, and the choice of both.
   static constexpr int slots(int ctas) {
-    const int n = (kSmemSm / ctas - 1152 - 2 * kMerge) / kWarps / (2 * kSide + kNotes);
+    const int n = ((kSmemSm / ctas - 1152 - 2 * kMerge) / kWarps - kNotes) / (2 * kSide + kRaw);
     return n < 8 ? n : 8;
   }
   static constexpr int kCtas = FT_C4 && kQuant && NT == 1 && DP <= 128 && slots(4) >= 2 ? 4 : slots(3) >= FT_S3 ? 3 : slots(2) >= 2 ? 2 : 1;
   static constexpr int S = slots(kCtas);
   static_assert(S >= 2, "");
-  static constexpr int kRing = kWarps * S * 2 * kSide;
-  static constexpr int kSmem = 128 + kRing + kWarps * S * kNotes + 2 * kMerge;
+  static constexpr int kSlot = 2 * kSide + kRaw;
+  static constexpr int kRing = kWarps * S * kSlot;
+  static constexpr int kSmem = 128 + kRing + kWarps * kNotes + 2 * kMerge;
+  static_assert(kSlot % 128 == 0 && kNotes % 16 == 0 && 3 * S <= 32, "");
 };
 
 // Tiles of row t; the line's length over all rows, by one warp.
@@ -255,12 +268,13 @@ __device__ __forceinline__ void store_lse(const AttnArgs& a, int t, int h, float
   if (a.lse) a.lse[static_cast<int64_t>(t) * a.Hq + h] = l > 0.f || l != l ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
-// 2^(m - M), 0 where nothing was seen (m = -inf); M = -inf only with every m.
-__device__ __forceinline__ float weight_of(float m, float M) { return m == -INFINITY ? 0.f : exp2_approx(m - M); }
+// A maximum over nothing: finite, so that 2^(-inf - kLowest) and 2^(kLowest - m) are 0 and not NaN.
+constexpr float kLowest = -3.0e38f;
+__device__ __forceinline__ float weight_of(float m, float M) { return exp2_approx(m - M); }
 
 // The place of a token among its step's (see the order of tokens above), and the token of a place.
-__device__ __forceinline__ int place_of(int t) { return (t & ~7) + 2 * (t & 3) + ((t >> 2) & 1); }
-__device__ __forceinline__ int token_at(int r) { return (r & ~7) + 4 * (r & 1) + ((r >> 1) & 3); }
+__device__ __forceinline__ constexpr int place_of(int t) { return (t & ~7) + 2 * (t & 3) + ((t >> 2) & 1); }
+__device__ __forceinline__ constexpr int token_at(int r) { return (r & ~7) + 4 * (r & 1) + ((r >> 1) & 3); }
 
 // A warp's way through its CTA's share of the line, unit by unit.
 struct Walk {
@@ -299,96 +313,136 @@ struct Walk {
   }
 };
 
-// The side of a warp that fills its ring, ahead of the side that computes.
-// What is read for a step is used one step later: a page at the step's issue,
-// the scales (which reach the notes beside the rows) at the next one's.
+// The side of a warp that fills its ring, ahead of the side that computes.  A
+// page is read one step before its use.
 template <typename X>
 struct Feeder {
-  static constexpr int BW = X::kBlocks ? X::DPW : 1;
   Walk walk;
   bool more, live;          // a step is prepared; the lane's token counts
   int32_t page;             // the token's page
   uint32_t place;           // and its place in it
-  int slot;                 // the step's
-  bool late, late_ok;       // the step before has scales under way; the token had a row
-  uint32_t scales;          // key | value << 8
-  uint32_t blk[2][BW];      // its block scales
+  const int32_t* table;     // the unit's sequence's pages
+  uint32_t head_row;        // the unit's key head
+  uint32_t at;              // the slot to fill next
+  uint32_t past;            // of the last steps, three bits each: the lane's token had a row, and that modulo 4
+  // the lane's part of the copies, the same in every step (see Deal): source
+  // chunk, and places in the keys' and the values' side of a slot
+  const uint8_t* src[2][X::CY];
+  uint32_t kdst[X::CY], vdst[X::CY];
+
+  __device__ __forceinline__ void init(const AttnArgs& a, uint32_t ring, int lane) {
+#pragma unroll
+    for (int c = 0; c < X::CY; ++c) {
+      const int row = (c * 32 + lane) / X::CPR, chunk = (c * 32 + lane) % X::CPR;
+      src[0][c] = a.kv.data[0] + chunk * 16;
+      src[1][c] = a.kv.data[1] + chunk * 16;
+      kdst[c] = place_of(row) * X::RB + ((chunk * 16) ^ X::key_swizzle(place_of(row)));
+      vdst[c] = X::kSide + row * X::RB + ((chunk * 16) ^ X::value_swizzle(row));
+    }
+    at = ring;
+    past = 0;
+  }
 
   __device__ __forceinline__ void prepare(const AttnArgs& a, int offset, int step, int lane) {
-    while (walk.base >= walk.stop)
+    while (walk.base >= walk.stop) {
       if (!walk.next(a, offset)) {
         more = false;
         return;
       }
+      table = a.kv.pages + walk.seq * a.kv.table_stride;
+      head_row = static_cast<uint32_t>(walk.unit / a.blocks) * a.kv.at.head_stride;
+    }
     more = true;
     const int tok = walk.base + lane;
     live = lane < X::TS && tok >= walk.first && tok < walk.stop;
     if (live) {
       const uint32_t p = fast_div(tok, a.kv.at.by_page);
       place = tok - p * a.kv.at.page_size;
-      page = a.kv.pages[walk.seq * a.kv.table_stride + p];
+      page = table[p];
     }
     walk.base += step;
   }
 
-  __device__ __forceinline__ void put_notes(uint32_t at, int lane) {
-    if constexpr (X::kQuant) {
-      if (late && lane < X::TS) {
-        // exponent bytes as writers store them; others are held to 2^-100 .. 2^123
-        const uint32_t kb = min(max(scales & 0xffu, 27u), 250u), vb = min(max(scales >> 8, 27u), 250u);
-        const float ks = late_ok ? __uint_as_float(kb << 23) : 0.f;
-        const float ev = late_ok ? static_cast<float>(static_cast<int>(vb) - 127) : -INFINITY;
-        const float iv = late_ok ? __uint_as_float((254u - vb) << 23) : 0.f;
-        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at + place_of(lane) * 16), "f"(ks), "f"(ev), "f"(iv), "f"(0.f)
-                     : "memory");
-        if constexpr (X::kBlocks) {
-          const uint32_t ka = at + X::kTok + place_of(lane) * (X::NBK * 2);
-          const uint32_t va = at + X::kTok + X::kKeyBlk + place_of(lane) * 2;
-#pragma unroll
-          for (int w = 0; w < BW; ++w)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t k2 = cvt_e4m3x2(blk[0][w] >> (16 * i)), v2 = cvt_e4m3x2(blk[1][w] >> (16 * i));
-              asm volatile("st.shared.u32 [%0], %1;" ::"r"(ka + (2 * w + i) * 4), "r"(k2) : "memory");
-              asm volatile("st.shared.u16 [%0], %1;" ::"r"(va + (4 * w + 2 * i) * (X::VS * 2)),
-                           "h"(static_cast<uint16_t>(v2))
-                           : "memory");
-              asm volatile("st.shared.u16 [%0], %1;" ::"r"(va + (4 * w + 2 * i + 1) * (X::VS * 2)),
-                           "h"(static_cast<uint16_t>(v2 >> 16))
-                           : "memory");
-            }
-        }
-      }
-    }
-  }
-
-  __device__ __forceinline__ void read_blocks(const AttnArgs& a, uint32_t row) {
+  // The block scales of the lane's token into the slot.  Rows of an odd number
+  // of byte pairs are not word-aligned: read and stored.
+  __device__ __forceinline__ void copy_blocks(const AttnArgs& a, uint32_t row, int lane) {
     if constexpr (X::kBlocks) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const uint8_t* src = a.kv.block[j] + static_cast<uint64_t>(row) * (a.kv.D >> 4);
-        if ((a.kv.D & 63) == 0) {
+        const uint8_t* from = a.kv.block[j] + static_cast<uint64_t>(row) * (a.kv.D >> 4);
+        const uint32_t to = at + 2 * X::kSide + 2 * X::TS * 4 + j * X::kRawBlk + lane * X::NBK;
+        if (a.kv.D == X::NBK * 16) {
+          if constexpr (X::NBK == 16) {
+            copy16(to, from);
+          } else if constexpr (X::NBK == 8) {
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
+          } else {
 #pragma unroll
-          for (int w = 0; w < BW; ++w)
-            blk[j][w] = 64 * w < a.kv.D ? *reinterpret_cast<const uint32_t*>(src + 4 * w) : 0;
-        } else {  // rows of an odd number of pairs
+            for (int w = 0; w < X::NBK / 4; ++w)
+              asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + 4 * w), "l"(from + 4 * w) : "memory");
+          }
+        } else {
 #pragma unroll
-          for (int w = 0; w < BW; ++w) {
-            blk[j][w] = 64 * w < a.kv.D ? *reinterpret_cast<const uint16_t*>(src + 4 * w) : 0;
-            if (64 * w + 32 < a.kv.D) blk[j][w] |= *reinterpret_cast<const uint16_t*>(src + 4 * w + 2) << 16;
+          for (int w = 0; w < X::NBK / 2; ++w) {
+            const uint16_t v = 32 * w < a.kv.D ? *reinterpret_cast<const uint16_t*>(from + 2 * w) : 0;
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + 2 * w), "h"(v) : "memory");
           }
         }
       }
     }
   }
 
-  // Starts the prepared step's copies into its slot and finishes the notes of
-  // the step before.  One group of copies a call, whether it has any or not.
-  __device__ __forceinline__ void issue(const AttnArgs& a, uint32_t ring, uint32_t notes, int lane) {
-    const int before = slot == 0 ? X::S - 1 : slot - 1;
-    put_notes(notes + before * X::kNotes, lane);
-    late = false;
+  // The notes of the step in slot `slot`, S steps after its issue: one lane a token.
+  __device__ __forceinline__ void put_notes(uint32_t slot, uint32_t notes, int lane) const {
+    if constexpr (X::kQuant) {
+      if (lane < X::TS) {
+        const uint32_t was = past >> (3 * (X::S - 1));
+        const bool ok = (was & 4) != 0;
+        const uint32_t raw = slot + 2 * X::kSide, sh = (was & 3) * 8;
+        uint32_t kw, vw;
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(kw) : "r"(raw + lane * 4));
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vw) : "r"(raw + X::TS * 4 + lane * 4));
+        // exponent bytes as writers store them; others are held to 2^-100 .. 2^123
+        const uint32_t kb = min(max((kw >> sh) & 0xffu, 27u), 250u), vb = min(max((vw >> sh) & 0xffu, 27u), 250u);
+        const float ks = ok ? __uint_as_float(kb << 23) : 0.f;
+        const float ev = ok ? static_cast<float>(static_cast<int>(vb) - 127) : -INFINITY;
+        const float iv = ok ? __uint_as_float((254u - vb) << 23) : 0.f;
+        const uint32_t pl = place_of(lane);
+        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(notes + pl * 16), "f"(ks), "f"(ev), "f"(iv), "f"(0.f)
+                     : "memory");
+        if constexpr (X::kBlocks) {
+          const uint32_t ka = notes + X::kTok + pl * (X::NBK * 2);
+          const uint32_t va = notes + X::kTok + X::kKeyBlk + pl * 2;
+#pragma unroll
+          for (int w = 0; w < X::NBK / 4; ++w) {
+            uint32_t kq, vq;
+            const uint32_t from = raw + 2 * X::TS * 4 + lane * X::NBK + w * 4;
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(kq) : "r"(from));
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vq) : "r"(from + X::kRawBlk));
+            uint32_t k2[2], v2[2];
+            e4m3x4(ok ? kq : 0, k2[0], k2[1]);
+            e4m3x4(ok ? vq : 0, v2[0], v2[1]);
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(ka + w * 8), "r"(k2[0]), "r"(k2[1]) : "memory");
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              asm volatile("st.shared.u16 [%0], %1;" ::"r"(va + (4 * w + i) * (X::VS * 2)),
+                           "h"(static_cast<uint16_t>(v2[i >> 1] >> (16 * (i & 1))))
+                           : "memory");
+          }
+        }
+      }
+      __syncwarp();
+    }
+  }
+
+  // The tokens of the oldest step that counts, one bit each.
+  __device__ __forceinline__ uint32_t mask() const { return __ballot_sync(kAll, (past >> (3 * (X::S - 1)) & 4) != 0); }
+
+  // Starts the prepared step's copies into its slot.  One group of copies a
+  // call, whether it has any or not.
+  __device__ __forceinline__ void issue(const AttnArgs& a, uint32_t ring, int lane) {
     __syncwarp();  // every lane has finished reading the slot
+    past <<= 3;
     if (more) {
       uint32_t row = kNoRow;
       if (live) {
@@ -396,45 +450,48 @@ struct Feeder {
         if (row == kNoRow)
           record_status(a.status, FT_ERR_BAD_ID);
         else
-          row += static_cast<uint32_t>(walk.unit / a.blocks) * a.kv.at.head_stride;
+          row += head_row;
       }
-      late_ok = row != kNoRow;
-      const uint32_t mask = __ballot_sync(kAll, late_ok);
-      if (!X::kQuant && lane == 0)
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(notes + slot * X::kNotes), "r"(mask) : "memory");
-      const uint32_t keys = ring + slot * (2 * X::kSide), values = keys + X::kSide;
-      const bool plain = mask == X::kFull && a.kv.row_bytes == X::RB;
+      const bool has_row = row != kNoRow;
+      if (has_row) past |= 4 | (row & 3);
+      const uint32_t counts = __ballot_sync(kAll, has_row);
+      // Rows (c / CY) * CR further on move a lane's places by constants: the
+      // order of places and the swizzles only rearrange and join bits, and the
+      // rows of one period are the low bits.
+      if (counts == X::kFull && a.kv.row_bytes == X::RB) {
 #pragma unroll
-      for (int c = 0; c < X::kCopies; ++c) {
-        const int cy = c % X::CY, more_rows = c / X::CY * X::CR;
-        const int r0 = (cy * 32 + lane) / X::CPR, chunk = (cy * 32 + lane) % X::CPR;
-        const int tok = r0 + more_rows;
-        const uint32_t n = __shfl_sync(kAll, row, tok);
-        const int pl = place_of(tok);
-        const uint32_t kd = keys + pl * X::RB + ((chunk * 16) ^ X::key_swizzle(pl));
-        const uint32_t vd = values + tok * X::RB + ((chunk * 16) ^ X::value_swizzle(tok));
-        if (plain) {
-          const uint64_t off = static_cast<uint64_t>(n) * X::RB + chunk * 16;
-          copy16(kd, a.kv.data[0] + off);
-          copy16(vd, a.kv.data[1] + off);
-        } else {
-          const bool ok = n != kNoRow && chunk * 16 < a.kv.row_bytes;
-          const uint64_t off = ok ? static_cast<uint64_t>(n) * a.kv.row_bytes + chunk * 16 : 0;
-          copy16_or_zero(kd, a.kv.data[0] + off, ok ? 16 : 0);
-          copy16_or_zero(vd, a.kv.data[1] + off, ok ? 16 : 0);
+        for (int c = 0; c < X::kCopies; ++c) {
+          const int cy = c % X::CY, on = c / X::CY * X::CR;
+          const uint32_t n = __shfl_sync(kAll, row, (cy * 32 + lane) / X::CPR + on);
+          copy16(at + (kdst[cy] ^ X::key_swizzle(place_of(on))) + place_of(on) * X::RB,
+                 src[0][cy] + static_cast<uint64_t>(n) * X::RB);
+          copy16(at + (vdst[cy] ^ X::value_swizzle(on)) + on * X::RB, src[1][cy] + static_cast<uint64_t>(n) * X::RB);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < X::kCopies; ++c) {
+          const int cy = c % X::CY, on = c / X::CY * X::CR;
+          const uint32_t n = __shfl_sync(kAll, row, (cy * 32 + lane) / X::CPR + on);
+          const bool ok = n != kNoRow && (cy * 32 + lane) % X::CPR * 16 < a.kv.row_bytes;
+          const uint64_t off = ok ? static_cast<uint64_t>(n) * a.kv.row_bytes : 0;
+          copy16_or_zero(at + (kdst[cy] ^ X::key_swizzle(place_of(on))) + place_of(on) * X::RB,
+                         ok ? src[0][cy] + off : a.kv.data[0], ok ? 16 : 0);
+          copy16_or_zero(at + (vdst[cy] ^ X::value_swizzle(on)) + on * X::RB, ok ? src[1][cy] + off : a.kv.data[1],
+                         ok ? 16 : 0);
         }
       }
       if constexpr (X::kQuant) {
-        late = true;
-        scales = 0;
-#pragma unroll
-        for (int w = 0; w < BW; ++w) blk[0][w] = blk[1][w] = 0;
-        if (late_ok) {
-          scales = a.kv.scale[0][row] | (a.kv.scale[1][row] << 8);
-          read_blocks(a, row);
+        if (has_row) {
+          // the aligned words around the exponent bytes
+          const uint32_t to = at + 2 * X::kSide + lane * 4;
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(a.kv.scale[0] + (row & ~3u)) : "memory");
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + X::TS * 4), "l"(a.kv.scale[1] + (row & ~3u))
+                       : "memory");
+          copy_blocks(a, row, lane);
         }
       }
-      slot = slot + 1 == X::S ? 0 : slot + 1;
+      at += X::kSlot;
+      if (at == ring + X::S * X::kSlot) at = ring;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
@@ -471,10 +528,13 @@ __device__ __forceinline__ void add_values(uint32_t at, uint32_t vnotes, int u, 
              __byte_perm(t2, t3, 0x7632));
       } else if constexpr (!X::kBlocks) {
         // bytes of two tokens side by side, then two conversions a word
-        const uint32_t x0 = __byte_perm(t0, t1, 0x5140), x1 = __byte_perm(t0, t1, 0x7362);
-        const uint32_t y0 = __byte_perm(t2, t3, 0x5140), y1 = __byte_perm(t2, t3, 0x7362);
-        step(m0 + 2 * w, cvt_e4m3x2(x0), cvt_e4m3x2(x0 >> 16), cvt_e4m3x2(y0), cvt_e4m3x2(y0 >> 16));
-        step(m0 + 2 * w + 1, cvt_e4m3x2(x1), cvt_e4m3x2(x1 >> 16), cvt_e4m3x2(y1), cvt_e4m3x2(y1 >> 16));
+        uint32_t f[8];
+        e4m3x4(__byte_perm(t0, t1, 0x5140), f[0], f[1]);
+        e4m3x4(__byte_perm(t2, t3, 0x5140), f[2], f[3]);
+        e4m3x4(__byte_perm(t0, t1, 0x7362), f[4], f[5]);
+        e4m3x4(__byte_perm(t2, t3, 0x7362), f[6], f[7]);
+        step(m0 + 2 * w, f[0], f[1], f[2], f[3]);
+        step(m0 + 2 * w + 1, f[4], f[5], f[6], f[7]);
       } else {
         if (w % 2 == 0) {
           const int block = X::EV >= 16 ? p * (X::EV / 2) + g * (X::EV / 16) + w / 2 : p * 4 + (g >> 1);
@@ -509,23 +569,24 @@ __global__ void __launch_bounds__(kWarps * 32, Deal<FMT, DP, NT>::kCtas)
   const int warps_t = kWarps >> a.warps_h_log2;
 
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
-  const uint32_t ring = smem_u32(smem) + warp * (S * 2 * X::kSide);
-  const uint32_t notes = smem_u32(smem) + X::kRing + warp * (S * X::kNotes);
-  float* merge = reinterpret_cast<float*>(smem + X::kRing + kWarps * S * X::kNotes);
+  const uint32_t ring = smem_u32(smem) + warp * (S * X::kSlot);
+  const uint32_t note = smem_u32(smem) + X::kRing + warp * X::kNotes;
+  float* merge = reinterpret_cast<float*>(smem + X::kRing + kWarps * X::kNotes);
 
   // this CTA's share of the line, and the row it begins in
   const int64_t total = tiles_before(a, a.T, lane) * a.units;
   const int64_t share = split_share(total, a.workers);
   const int64_t from = blockIdx.x * share;
-  if (threadIdx.x == 0) a.begun[blockIdx.x] = make_int4(0, 0, 0, 0);
   // rows that see nothing
   for (int t = blockIdx.x; t < a.T; t += gridDim.x)
-    if (span_of(a, t).tiles == 0)
+    if (span_of(a, t).tiles == 0) {
       for (int i = threadIdx.x; i < a.Hq * (a.kv.D / 2); i += kWarps * 32) {
         const int h = i / (a.kv.D / 2), d = 2 * (i - h * (a.kv.D / 2));
         store_out(a, t, h, d, 0.f, 0.f);
         if (d == 0) store_lse(a, t, h, -INFINITY, 0.f);
       }
+      for (int i = threadIdx.x; i < a.units; i += kWarps * 32) a.shared_by[t * a.units + i] = make_int2(1, 0);
+    }
   if (from >= total) return;
   Walk walk;
   walk.left = static_cast<int>(from + share < total ? share : total - from);
@@ -554,12 +615,11 @@ __global__ void __launch_bounds__(kWarps * 32, Deal<FMT, DP, NT>::kCtas)
 
   Feeder<X> feed;
   feed.walk = walk;
-  feed.slot = 0;
-  feed.late = false;
+  feed.init(a, ring, lane);
   feed.prepare(a, offset, step, lane);
 #pragma unroll 1
   for (int i = 0; i < S; ++i) {
-    feed.issue(a, ring, notes, lane);
+    feed.issue(a, ring, lane);
     if (feed.more) feed.prepare(a, offset, step, lane);
   }
 
@@ -569,7 +629,7 @@ __global__ void __launch_bounds__(kWarps * 32, Deal<FMT, DP, NT>::kCtas)
   for (int p = 0; p < X::KP; ++p) koff[p] = g * X::RB + ((p * 4 + q) * X::PK ^ X::key_swizzle(g));
   const uint32_t voff = q * X::RB + (g * X::PV ^ X::value_swizzle(q));
 
-  int slot = 0;
+  uint32_t at = ring;  // the slot to read next
   while (walk.next(a, offset)) {
     const int t = walk.t;
     const int kv_head = walk.unit / a.blocks;
@@ -628,7 +688,7 @@ __global__ void __launch_bounds__(kWarps * 32, Deal<FMT, DP, NT>::kCtas)
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        m[n][i] = -INFINITY;
+        m[n][i] = kLowest;
         l[n][i] = 0.f;
       }
 #pragma unroll
@@ -641,7 +701,7 @@ __global__ void __launch_bounds__(kWarps * 32, Deal<FMT, DP, NT>::kCtas)
     for (; walk.base < walk.stop; walk.base += step) {
       asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
       __syncwarp();
-      const uint32_t at = ring + slot * (2 * X::kSide), note = notes + slot * X::kNotes;
+      feed.put_notes(at, note, lane);
 
       // s[u][n] = S^T of 16 tokens: (token g | g + 8) x (head 2q | 2q + 1)
       float s[U][NT][4];
@@ -663,10 +723,7 @@ __global__ void __launch_bounds__(kWarps * 32, Deal<FMT, DP, NT>::kCtas)
               for (int w = 0; w < X::WK; ++w) f[r][w] = k[w];
             } else if constexpr (!X::kBlocks) {
 #pragma unroll
-              for (int w = 0; w < X::WK; ++w) {
-                f[r][2 * w] = cvt_e4m3x2(k[w]);
-                f[r][2 * w + 1] = cvt_e4m3x2(k[w] >> 16);
-              }
+              for (int w = 0; w < X::WK; ++w) e4m3x4(k[w], f[r][2 * w], f[r][2 * w + 1]);
             } else {
               uint32_t b2;  // the lane's block scales: one or two
               const uint32_t na = note + X::kTok + (16 * u + 8 * r + g) * (X::NBK * 2) + (p * 4 + q) * (X::EK / 8);
@@ -701,8 +758,7 @@ __global__ void __launch_bounds__(kWarps * 32, Deal<FMT, DP, NT>::kCtas)
       // scores in powers of two, with the value's exponent; masked tokens -inf
       float iv[U][2];
       bool more = false;
-      uint32_t mask = 0;
-      if constexpr (!X::kQuant) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(mask) : "r"(note));
+      const uint32_t mask = X::kQuant ? 0 : feed.mask();
       const bool part = !X::kQuant && mask != X::kFull;
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -752,10 +808,9 @@ __global__ void __launch_bounds__(kWarps * 32, Deal<FMT, DP, NT>::kCtas)
         uint32_t hi[NT][2], lo[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const float r0 = m[n][0] == -INFINITY ? 0.f : m[n][0], r1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const float p0 = exp2_approx(s[u][n][2 * r] - r0), p1 = exp2_approx(s[u][n][2 * r + 1] - r1);
+            const float p0 = exp2_approx(s[u][n][2 * r] - m[n][0]), p1 = exp2_approx(s[u][n][2 * r + 1] - m[n][1]);
             if (X::kQuant) {
               l[n][0] = fmaf(p0, iv[u][r], l[n][0]);
               l[n][1] = fmaf(p1, iv[u][r], l[n][1]);
@@ -778,9 +833,10 @@ __global__ void __launch_bounds__(kWarps * 32, Deal<FMT, DP, NT>::kCtas)
         else if constexpr (X::kF16)
           add_values<X, false, NT>(at + X::kSide + voff, vnotes, u, g, q, hi, lo, acc);
       }
-      feed.issue(a, ring, notes, lane);  // refills this slot
+      feed.issue(a, ring, lane);  // refills this slot
       if (feed.more) feed.prepare(a, offset, step, lane);
-      slot = slot + 1 == S ? 0 : slot + 1;
+      at += X::kSlot;
+      if (at == ring + S * X::kSlot) at = ring;
     }
 
     // The warps' sums meet in shared memory, half of them handing over at a
@@ -830,9 +886,10 @@ __global__ void __launch_bounds__(kWarps * 32, Deal<FMT, DP, NT>::kCtas)
           }
       }
     }
-    if (threadIdx.x == 0 && walk.tile0 == 0 && !walk.whole)
-      a.begun[blockIdx.x] = make_int4(
-          t, walk.unit, static_cast<int>(blockIdx.x) + static_cast<int>((walk.rest + share - 1) / share), 1);
+    if (threadIdx.x == 0 && walk.tile0 == 0) {
+      const int first = blockIdx.x, last = first + static_cast<int>((walk.rest + share - 1) / share);
+      a.shared_by[t * a.units + walk.unit] = walk.whole ? make_int2(1, 0) : make_int2(first, last);
+    }
     if (wt == 0) {
       const int64_t part = static_cast<int64_t>(blockIdx.x) * 2 + (walk.tile0 == 0 ? 1 : 0);
 #pragma unroll
@@ -863,29 +920,30 @@ __global__ void __launch_bounds__(kWarps * 32, Deal<FMT, DP, NT>::kCtas)
   }
 }
 
-// Adds the partial sums of the unit that worker blockIdx.x began, if it went
-// past its share, in the workers' order.  A CTA takes kHeads heads of the
-// block, 8 / kHeads warps a head (each every so-many-th partial): one head
-// where few units have many partials each (one long row), eight otherwise.
+// Adds the partial sums of unit blockIdx.x, if it crossed shares, in the
+// workers' order.  A CTA takes kHeads heads of the block, 8 / kHeads warps a
+// head (each every so-many-th partial): one head where few units have many
+// partials each (one long row), eight otherwise.
 template <int DP, int kHeads>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int N = DP / 64;           // channel pairs of a lane: 2 * lane + 64 i
   constexpr int kSpread = 8 / kHeads;  // warps of a head
-  constexpr int kBatch = 4;            // partials in flight
+  constexpr int kBatch = kHeads == 1 ? 8 : 2;  // partials in flight
   __shared__ float2 acc_s[kSpread > 1 ? 8 : 1][DP / 2];
   __shared__ float2 ml_s[8];
   // every CTA waits, whether it has something to add or not: work after this
   // grid must also come after attend_kernel
   pdl_wait();
-  const int4 unit = a.begun[blockIdx.x];
-  if (unit.w == 0) return;
+  const int2 workers = a.shared_by[blockIdx.x];
+  if (workers.y <= workers.x) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int h = blockIdx.y * kHeads + warp / kSpread;
-  const int kv_head = unit.y / a.blocks;
-  const int hg = (unit.y - kv_head * a.blocks) * a.block_heads + h;  // in the key head's group
+  const int t = blockIdx.x / a.units, unit = blockIdx.x - t * a.units;
+  const int kv_head = unit / a.blocks;
+  const int hg = (unit - kv_head * a.blocks) * a.block_heads + h;  // in the key head's group
   const bool live = h < a.block_heads && hg < a.G;
-  const int c0 = blockIdx.x, c1 = unit.z;
-  float m = -INFINITY, l = 0.f;
+  const int c0 = workers.x, c1 = workers.y;
+  float m = kLowest, l = 0.f;
   float2 acc[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) acc[i] = make_float2(0.f, 0.f);
@@ -894,7 +952,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnA
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const int ck = c + k * kSpread;
-      ml[k] = make_float2(-INFINITY, 0.f);
+      ml[k] = make_float2(kLowest, 0.f);
 #pragma unroll
       for (int i = 0; i < N; ++i) o[k][i] = make_float2(0.f, 0.f);
       if (ck <= c1) {
@@ -952,8 +1010,8 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnA
   const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
   for (int i = 0; i < N; ++i)
-    if (2 * lane + 64 * i < a.kv.D) store_out(a, unit.x, hq, 2 * lane + 64 * i, acc[i].x * inv, acc[i].y * inv);
-  if (lane == 0) store_lse(a, unit.x, hq, m, l);
+    if (2 * lane + 64 * i < a.kv.D) store_out(a, t, hq, 2 * lane + 64 * i, acc[i].x * inv, acc[i].y * inv);
+  if (lane == 0) store_lse(a, t, hq, m, l);
 }
 
 // ------------------------------------------------------------------ host side ---
@@ -1008,7 +1066,7 @@ ft_status launch(AttnArgs& a, cudaStream_t s) {
   if (st != FT_OK) return st;
   cudaLaunchConfig_t cfg = {};
   const bool long_rows = workers > 8ll * a.T * a.units;  // more than eight partials a unit on average
-  cfg.gridDim = dim3(a.workers, long_rows ? a.block_heads : a.block_heads / 8);
+  cfg.gridDim = dim3(a.T * a.units, long_rows ? a.block_heads : a.block_heads / 8);
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
@@ -1045,7 +1103,7 @@ extern "C" {
 size_t ft_attn_decode_workspace(int32_t T, int32_t Hq, int32_t Hkv, int32_t D) {
   if (!attn_shape_ok(T, Hq, Hkv, D)) return 0;
   const Shape s = shape_of(D, Hq / Hkv);
-  return part_o_bytes(s) + part_ml_bytes(s) + kMaxWorkers * sizeof(int4);
+  return part_o_bytes(s) + part_ml_bytes(s) + static_cast<size_t>(T) * Hkv * s.blocks * sizeof(int2);
 }
 
 ft_status ft_attn_decode(const ft_kv_cache* cache_host, const ft_rows* q_host, int32_t T, int32_t Hq, int32_t dtype,
@@ -1082,7 +1140,7 @@ ft_status ft_attn_decode(const ft_kv_cache* cache_host, const ft_rows* q_host, i
   a.lens = lens;
   a.part_o = static_cast<float*>(ws);
   a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + part_o_bytes(sh));
-  a.begun = reinterpret_cast<int4*>(static_cast<uint8_t*>(ws) + part_o_bytes(sh) + part_ml_bytes(sh));
+  a.shared_by = reinterpret_cast<int2*>(static_cast<uint8_t*>(ws) + part_o_bytes(sh) + part_ml_bytes(sh));
   a.scale_log2 = scale * 1.4426950408889634f;
   a.window = window;
   a.T = T;

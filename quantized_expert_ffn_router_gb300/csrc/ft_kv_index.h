@@ -13,23 +13,30 @@
 
 namespace ft {
 
-// Unsigned division of n < 2^31 by a fixed d >= 1: (n * mul) >> shift with
-// mul = ceil(2^(31 + s) / d), s = ceil(log2 d).  mul * d - 2^(31+s) < d <= 2^s,
-// so the quotient's error n * (mul * d - 2^(31+s)) / (d * 2^(31+s)) stays below
-// 1 / d and the floor is exact.
+// Unsigned division of n < 2^31 by a fixed d in 1 .. 2^31: (n * mul) >> (31 + s)
+// with mul = ceil(2^(31 + s) / d), s = ceil(log2 d), taken as the high word of
+// 2 n * mul.  mul * d - 2^(31+s) < d <= 2^s, so the quotient's error
+// n * (mul * d - 2^(31+s)) / (d * 2^(31+s)) stays below 1 / d and the floor is
+// exact.
 struct FastDiv {
   uint32_t mul;
-  uint32_t shift;
+  uint32_t shift;  // s
 };
 
 FT_HD FastDiv make_fast_div(uint32_t d) {
   uint32_t s = 0;
   while ((uint64_t(1) << s) < d) ++s;
   const uint64_t p = uint64_t(1) << (31 + s);
-  return FastDiv{static_cast<uint32_t>((p + d - 1) / d), 31 + s};
+  return FastDiv{static_cast<uint32_t>((p + d - 1) / d), s};
 }
 
-FT_HD uint32_t fast_div(uint32_t n, FastDiv f) { return static_cast<uint32_t>((static_cast<uint64_t>(n) * f.mul) >> f.shift); }
+FT_HD uint32_t fast_div(uint32_t n, FastDiv f) {
+#ifdef __CUDA_ARCH__
+  return __umulhi(n + n, f.mul) >> f.shift;
+#else
+  return static_cast<uint32_t>((static_cast<uint64_t>(n + n) * f.mul) >> 32) >> f.shift;
+#endif
+}
 
 constexpr uint32_t kNoRow = 0xffffffffu;
 
