@@ -182,6 +182,13 @@ __device__ __forceinline__ float finite_abs(float x) {
 
 // ------------------------------------------------------------ rotate, write ---
 enum { kPairs, kHalves, kAny };
+constexpr int kMaxBatch = 8;
+#ifndef FT_FILL
+#define FT_FILL 8
+#endif
+#ifndef FT_BATCH
+#define FT_BATCH 4
+#endif
 
 struct WriteArgs {
   KvView kv;
@@ -197,12 +204,64 @@ struct WriteArgs {
   int32_t T, Hq, Hkv, D;
   int32_t lanes_log2;       // lanes of one row
   int32_t parts;            // CTAs of one token
+  int32_t batch;            // tokens of a CTA
   int32_t* status;
 };
 
-// One CTA takes (a part of) one token: its threads first request their rows,
-// then put the token's rot/2 cosines and sines into shared memory once for
-// all heads, then rotate, quantise and store.
+// Where frequency f's cosine (or sine) lies among `half`: 16-byte chunks in an
+// order that lets 8 lanes read every other chunk without a bank conflict.
+__device__ __forceinline__ int turn_at(int f) {
+  const int j = f >> 2;
+  return ((j ^ ((j >> 3) & 1)) << 2) | (f & 3);
+}
+
+// One lane's 16 channels of one row, as loaded: two chunks of 8, and the other
+// sides of their rotations where the lane does not hold them (kAny).
+template <int LAY>
+struct Chunks {
+  uint4 own[2];
+  uint4 other[LAY == kAny ? 2 : 1];
+};
+
+// The codes of a quantised row's 16 channels.
+struct Codes {
+  uint32_t w[4];   // E4M3: four words; NVFP4: two
+  uint32_t block;  // NVFP4: the block's scale
+};
+
+// x[16] to codes, given the row's exponent; d[16] is added first (the check of
+// rotated keys quantises both ends of their uncertainty).
+template <int FMT>
+__device__ __forceinline__ Codes encode(const float (&x)[16], const float (&d)[16], float sign, float block_max, int e) {
+  Codes c;
+  const float inv = pow2f(-e);
+  if (FMT == FT_KV_E4M3) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      c.w[i] = to_e4m3x2(fmaf(sign, d[4 * i], x[4 * i]) * inv, fmaf(sign, d[4 * i + 1], x[4 * i + 1]) * inv) |
+               (to_e4m3x2(fmaf(sign, d[4 * i + 2], x[4 * i + 2]) * inv, fmaf(sign, d[4 * i + 3], x[4 * i + 3]) * inv) << 16);
+    c.block = 0;
+  } else {
+    float nan = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) nan = isnan(x[i]) ? x[i] : nan;
+    c.block = to_e4m3x2(isnan(nan) ? nan : block_max * inv / 6.f, 0.f) & 0xffu;
+    const float bs = __half2float(__ushort_as_half(static_cast<uint16_t>(cvt_e4m3x2(c.block))));
+    c.w[0] = c.w[1] = c.w[2] = c.w[3] = 0;
+    if (bs > 0.f) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        c.w[i >> 2] |= to_e2m1x2(fmaf(sign, d[2 * i], x[2 * i]) * inv / bs, fmaf(sign, d[2 * i + 1], x[2 * i + 1]) * inv / bs)
+                       << (8 * (i & 3));
+    }
+  }
+  return c;
+}
+
+// A CTA takes (a part of the rows of) `batch` tokens, one after the other,
+// loading the next rows while it works on these.  Before the first, its
+// threads share out the work of looking up the tokens' rows in the cache and
+// of the tokens' rot/2 cosines and sines, which all heads use.
 //
 // A lane holds two chunks of 8 channels.
 //   kPairs   neighbouring chunks; interleaved rotations (or none) stay inside.
@@ -211,12 +270,22 @@ struct WriteArgs {
 //   kAny     neighbouring chunks, half layout: the other side is loaded as
 //            well (it is in L1, another lane's own).
 //
-// FMT: a cache format, or -1 to rotate q only.  EXACT: keys are rotated in
-// two-float arithmetic (rotated and quantised).
-template <bool F16, int FMT, int LAY, bool EXACT>
-__global__ void __launch_bounds__(512) write_kernel(const WriteArgs a) {
-  extern __shared__ float2 turn[];  // [half] (cos, sin), then with EXACT [half] what they round away
-  const uint32_t t = blockIdx.x / a.parts, part = blockIdx.x - t * a.parts;
+// FMT: a cache format, or -1 to rotate q only.
+//
+// Rotated keys that are quantised.  A code has to be that of the exact
+// rotation, but fp32 is good to d = 2^-20.5 (|u| + |v|) m of it (angle 2^-24
+// turn and sincospif 2 ulp: 2^-21.8; two products and a sum: 2^-22.4).  So both
+// ends x - d and x + d are quantised: where they agree, that is the code;
+// where a border lies between (about one element in 2^16), its lane rotates it
+// again in two-float arithmetic.
+template <bool F16, int FMT, int LAY>
+__global__ void __launch_bounds__(512) write_kernel(const __grid_constant__ WriteArgs a) {
+  constexpr bool kQuant = FMT == FT_KV_E4M3 || FMT == FT_KV_NVFP4;
+  extern __shared__ __align__(16) float turns[];  // [batch][cosines, sines][half, rounded up to whole chunk pairs]
+  __shared__ uint32_t rows_s[kMaxBatch];          // head 0's row of each token's place
+  const int half_up = (a.half + 31) & ~31;
+  const uint32_t group = blockIdx.x / a.parts, part = blockIdx.x - group * a.parts;
+  const int t0 = group * a.batch, tokens = min(a.batch, a.T - t0);
   const int lanes = 1 << a.lanes_log2;
   const int rows = a.Hq + (FMT >= 0 ? 2 * a.Hkv : 0);
   const int step = (a.parts * blockDim.x) >> a.lanes_log2;
@@ -231,164 +300,201 @@ __global__ void __launch_bounds__(512) write_kernel(const WriteArgs a) {
     c1 = 2 * l + 1;
   }
   const bool has0 = c0 * 8 < a.D, has1 = c1 * 8 < a.D;
+  const bool vec = (a.half & 7) == 0;
   const int r_cta = (part * blockDim.x) >> a.lanes_log2;
   const int rounds = (rows - r_cta + step - 1) / step;  // the same for every thread of the CTA
+  const int r_first = r_cta + (threadIdx.x >> a.lanes_log2);
 
-  uint32_t row0 = kNoRow;  // head 0's row of the token's place
-  int32_t place = -1;
-  if (FMT >= 0) place = a.pos[t];
-  for (int round = 0; round < rounds; ++round) {
-    const int r = r_cta + (threadIdx.x >> a.lanes_log2) + round * step;
+  const auto source = [&](int token, int r) {
+    const int kind = r < a.Hq ? 0 : r < a.Hq + a.Hkv ? 1 : 2;
+    const int h = kind == 0 ? r : kind == 1 ? r - a.Hq : r - a.Hq - a.Hkv;
+    return a.in[kind] + static_cast<int64_t>(t0 + token) * a.in_tok[kind] + h * a.in_head[kind];
+  };
+  const auto load = [&](int token, int r, Chunks<LAY>& c) {
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    c.own[0] = c.own[1] = c.other[0] = zero;
+    if (LAY == kAny) c.other[LAY == kAny ? 1 : 0] = zero;
+    if (r >= rows || token >= tokens) return;
+    const uint16_t* src = source(token, r);
+    if (has0) c.own[0] = *reinterpret_cast<const uint4*>(src + c0 * 8);
+    if (has1) c.own[1] = *reinterpret_cast<const uint4*>(src + c1 * 8);
+    if (LAY == kAny && vec && (FMT < 0 || r < a.Hq + a.Hkv)) {
+      if (c0 < 2 * hc) c.other[0] = *reinterpret_cast<const uint4*>(src + (c0 < hc ? c0 + hc : c0 - hc) * 8);
+      if (c1 < 2 * hc) c.other[LAY == kAny ? 1 : 0] = *reinterpret_cast<const uint4*>(src + (c1 < hc ? c1 + hc : c1 - hc) * 8);
+    }
+  };
+
+  Chunks<LAY> next;
+  load(0, r_first, next);
+
+  if (FMT >= 0 && threadIdx.x < tokens) {
+    const int32_t place = a.pos[t0 + threadIdx.x];
+    rows_s[threadIdx.x] = place < 0 ? kNoRow : kv_token_row(a.kv, kv_seq(a.kv, t0 + threadIdx.x), place, a.status);
+  }
+  if (a.rot > 0) {
+    for (int i = threadIdx.x; i < tokens * a.half; i += blockDim.x) {
+      const int token = i / a.half, f = i - token * a.half;
+      const int64_t p = a.rope_pos[t0 + token];
+      const float2 cs = turn_f32(static_cast<int64_t>(static_cast<uint64_t>(p) * static_cast<uint64_t>(a.freqs[f])), a.mscale);
+      turns[token * 2 * half_up + turn_at(f)] = cs.x;
+      turns[token * 2 * half_up + half_up + turn_at(f)] = cs.y;
+    }
+  }
+  __syncthreads();
+
+  for (int token = 0, round = 0; token < tokens;) {
+    const Chunks<LAY> now = next;
+    const int tk = token, r = r_first + round * step;
+    if (++round == rounds) {
+      round = 0;
+      ++token;
+    }
+    load(token, r_first + round * step, next);
+
     const bool live = r < rows;
     const int kind = r < a.Hq ? 0 : r < a.Hq + a.Hkv ? 1 : 2;
     const int h = kind == 0 ? r : kind == 1 ? r - a.Hq : r - a.Hq - a.Hkv;
-    const uint16_t* src = a.in[kind] + static_cast<int64_t>(t) * a.in_tok[kind] + h * a.in_head[kind];
     const bool spin = a.rot > 0 && kind < 2;
-    uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0, o0 = w0, o1 = w0;
-    const bool load0 = live && has0, load1 = live && has1;
-    if (load0) w0 = *reinterpret_cast<const uint4*>(src + c0 * 8);
-    if (load1) w1 = *reinterpret_cast<const uint4*>(src + c1 * 8);
-    // the other side of half-layout rotations that this lane does not hold
-    const bool other = LAY == kAny && spin;
-    const bool vec = (a.half & 7) == 0;
-    float y[16];
-    if (other && vec) {
-      if (load0 && c0 < 2 * hc) o0 = *reinterpret_cast<const uint4*>(src + (c0 < hc ? c0 + hc : c0 - hc) * 8);
-      if (load1 && c1 < 2 * hc) o1 = *reinterpret_cast<const uint4*>(src + (c1 < hc ? c1 + hc : c1 - hc) * 8);
-    } else if (other) {
+    const float* cosines = turns + tk * 2 * half_up;
+    const float* sines = cosines + half_up;
+    float x[16], d[16];  // the channels; what they may be off by (quantised keys)
+    unpack8<F16>(now.own[0], x);
+    unpack8<F16>(now.own[1], x + 8);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int d = (i < 8 ? c0 : c1) * 8 + (i & 7);
-        y[i] = (live && d < a.rot) ? load_one<F16>(src + (d < a.half ? d + a.half : d - a.half)) : 0.f;
-      }
-    }
-    if (round == 0) {
-      if (FMT >= 0 && place >= 0) row0 = kv_token_row(a.kv, kv_seq(a.kv, t), place, a.status);
-      if (a.rot > 0) {
-        const int64_t p = a.rope_pos[t];
-        for (int i = threadIdx.x; i < a.half; i += blockDim.x) {
-          const int64_t turns = static_cast<int64_t>(static_cast<uint64_t>(p) * static_cast<uint64_t>(a.freqs[i]));
-          if (EXACT)
-            turn_pair(turns, a.mscale, &turn[i], &turn[a.half + i]);
-          else
-            turn[i] = turn_f32(turns, a.mscale);
-        }
-        __syncthreads();
-      }
-    }
-    float x[16];
-    unpack8<F16>(w0, x);
-    unpack8<F16>(w1, x + 8);
+    for (int i = 0; i < 16; ++i) d[i] = 0.f;
+    const bool exact = kQuant && kind == 1 && spin;
+    const float off = 6.7434956e-7f * fabsf(a.mscale);  // 2^-20.5
     if (spin) {
-      const bool exact = EXACT && kind == 1;
-      if (LAY == kPairs) {
+      if (LAY == kPairs || LAY == kHalves) {
+        // 8 rotations: channels (2i, 2i + 1), or (i, i + 8)
+        const int f0 = LAY == kPairs ? 8 * l : 8 * c0;
+        const int turning = LAY == kPairs ? min(8, a.half - f0) : l < hc ? 8 : 0;
+        if (turning > 0) {
+          float cs[8], sn[8];
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-          const int d = (i < 8 ? c0 : c1) * 8 + (i & 7);
-          if (d < a.rot) {
-            const float2 cs = turn[d >> 1];
-            const float u = x[i], v = x[i + 1];
-            if (exact) {
-              const float2 lo = turn[a.half + (d >> 1)];
-              x[i] = rotate_odd(u, v, cs.x, lo.x, cs.y, lo.y);
-              x[i + 1] = rotate_odd(v, -u, cs.x, lo.x, cs.y, lo.y);
-            } else {
-              x[i] = u * cs.x - v * cs.y;
-              x[i + 1] = v * cs.x + u * cs.y;
-            }
+          for (int i = 0; i < 8; i += 4) {
+            const int at = turn_at(f0 + i);
+            *reinterpret_cast<float4*>(cs + i) = *reinterpret_cast<const float4*>(cosines + at);
+            *reinterpret_cast<float4*>(sn + i) = *reinterpret_cast<const float4*>(sines + at);
           }
-        }
-      } else if (LAY == kHalves) {
-        if (l < hc) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float2 cs = turn[c0 * 8 + i];
-            const float u = x[i], v = x[i + 8];
-            if (exact) {
-              const float2 lo = turn[a.half + c0 * 8 + i];
-              x[i] = rotate_odd(u, v, cs.x, lo.x, cs.y, lo.y);
-              x[i + 8] = rotate_odd(v, -u, cs.x, lo.x, cs.y, lo.y);
-            } else {
-              x[i] = u * cs.x - v * cs.y;
-              x[i + 8] = v * cs.x + u * cs.y;
+            const int iu = LAY == kPairs ? 2 * i : i, iv = LAY == kPairs ? 2 * i + 1 : i + 8;
+            if (LAY == kHalves || i < turning) {
+              const float u = x[iu], v = x[iv];
+              x[iu] = u * cs[i] - v * sn[i];
+              x[iv] = v * cs[i] + u * sn[i];
+              if (kQuant) d[iu] = d[iv] = exact ? (fabsf(u) + fabsf(v)) * off : 0.f;
             }
           }
         }
       } else {
+        float y[16];
         if (vec) {
-          unpack8<F16>(o0, y);
-          unpack8<F16>(o1, y + 8);
+          unpack8<F16>(now.other[0], y);
+          unpack8<F16>(now.other[LAY == kAny ? 1 : 0], y + 8);
+        } else {
+          const uint16_t* src = source(tk, live ? r : 0);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int c = (i < 8 ? c0 : c1) * 8 + (i & 7);
+            y[i] = (live && c < a.rot) ? load_one<F16>(src + (c < a.half ? c + a.half : c - a.half)) : 0.f;
+          }
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const int d = (i < 8 ? c0 : c1) * 8 + (i & 7);
-          if (d < a.rot) {
-            const bool left = d < a.half;
-            const int f = left ? d : d - a.half;
-            const float2 cs = turn[f];
-            const float o = left ? y[i] : -y[i];
-            if (exact) {
-              const float2 lo = turn[a.half + f];
-              x[i] = rotate_odd(x[i], o, cs.x, lo.x, cs.y, lo.y);
-            } else {
-              x[i] = x[i] * cs.x - o * cs.y;
-            }
+          const int c = (i < 8 ? c0 : c1) * 8 + (i & 7);
+          if (c < a.rot) {
+            const bool left = c < a.half;
+            const int at = turn_at(left ? c : c - a.half);
+            if (kQuant) d[i] = exact ? (fabsf(x[i]) + fabsf(y[i])) * off : 0.f;
+            x[i] = x[i] * cosines[at] - (left ? y[i] : -y[i]) * sines[at];
           }
         }
       }
     }
     __syncwarp();  // in place: the row's lanes have loaded both sides before any of them stores
     if (kind == 0 || FMT < 0) {
-      uint16_t* dst = a.q_out + static_cast<int64_t>(t) * a.out_tok + h * a.out_head;
-      if (load0) *reinterpret_cast<uint4*>(dst + c0 * 8) = pack8<F16>(x);
-      if (load1) *reinterpret_cast<uint4*>(dst + c1 * 8) = pack8<F16>(x + 8);
+      uint16_t* dst = a.q_out + static_cast<int64_t>(t0 + tk) * a.out_tok + h * a.out_head;
+      if (live && has0) *reinterpret_cast<uint4*>(dst + c0 * 8) = pack8<F16>(x);
+      if (live && has1) *reinterpret_cast<uint4*>(dst + c1 * 8) = pack8<F16>(x + 8);
     }
     if (FMT < 0) continue;
+    const uint32_t row0 = rows_s[tk];
     const bool put = live && kind > 0 && row0 != kNoRow;
+    if (!__any_sync(0xffffffffu, put)) continue;
     const int w = kind == 2 ? 1 : 0;
     const uint32_t row = row0 + static_cast<uint32_t>(h) * a.kv.at.head_stride;
     uint8_t* dst = a.kv.data[w] + static_cast<uint64_t>(row) * a.kv.row_bytes;
-    if (FMT == FT_KV_BF16 || FMT == FT_KV_F16) {
+    if (!kQuant) {
       if (put && has0) *reinterpret_cast<uint4*>(dst + c0 * 16) = pack8<F16>(x);
       if (put && has1) *reinterpret_cast<uint4*>(dst + c1 * 16) = pack8<F16>(x + 8);
-    } else {
-      float m0 = 0.f;
+      continue;
+    }
+    constexpr int top = FMT == FT_KV_E4M3 ? 8 : 11;                              // 448 = 1.75 * 2^8,
+    constexpr uint32_t top_bits = FMT == FT_KV_E4M3 ? 0x600000u : 0x280000u;     // 2688 = 1.3125 * 2^11
+    const auto maxima = [&](float& block_max, float& amax) {
+      block_max = 0.f;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) m0 = fmaxf(m0, finite_abs(x[i]));
-      float amax = m0;
+      for (int i = 0; i < 16; ++i) block_max = fmaxf(block_max, finite_abs(x[i]));
+      amax = block_max;
       for (int o = lanes >> 1; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      if (FMT == FT_KV_E4M3) {
-        const int e = row_exponent(amax, 8, 0x600000u);  // 448 = 1.75 * 2^8
-        const float inv = pow2f(-e);
-        uint32_t c[4];
+    };
+    float block_max, amax;
+    maxima(block_max, amax);
+    int e = row_exponent(amax, top, top_bits);
+    Codes code = encode<FMT>(x, d, -1.f, block_max, e);
+    if (__any_sync(0xffffffffu, exact)) {
+      // Both ends, and the row's and block's largest: the row's is at least
+      // the largest pair's size / sqrt 2, so off by at most 2^-19 of itself.
+      const float part = amax * 0x1p-19f;
+      float far = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          c[i] = to_e4m3x2(x[4 * i] * inv, x[4 * i + 1] * inv) |
-                 (to_e4m3x2(x[4 * i + 2] * inv, x[4 * i + 3] * inv) << 16);
-        if (put && has0) *reinterpret_cast<uint2*>(dst + c0 * 8) = make_uint2(c[0], c[1]);
-        if (put && has1) *reinterpret_cast<uint2*>(dst + c1 * 8) = make_uint2(c[2], c[3]);
-        if (put && l == 0) a.kv.scale[w][row] = static_cast<uint8_t>(e + 127);
-      } else {  // NVFP4: neighbouring chunks, so that a lane holds one block of 16
-        const int e = row_exponent(amax, 11, 0x280000u);  // 2688 = 1.3125 * 2^11
-        const float inv = pow2f(-e);
-        float nan = 0.f;
+      for (int i = 0; i < 16; ++i) far = fmaxf(far, d[i]);
+      const Codes up = encode<FMT>(x, d, 1.f, block_max + far, e);
+      bool all = row_exponent(amax - part, top, top_bits) != row_exponent(amax + part, top, top_bits);
+      if (FMT == FT_KV_NVFP4) all |= (to_e4m3x2((block_max - far) * pow2f(-e) / 6.f, 0.f) & 0xffu) != up.block;
+      uint32_t unsure = all ? 0xffffu : 0;  // one bit a channel
 #pragma unroll
-        for (int i = 0; i < 16; ++i) nan = isnan(x[i]) ? x[i] : nan;
-        const uint32_t b = to_e4m3x2(isnan(nan) ? nan : m0 * inv / 6.f, 0.f) & 0xffu;
-        const float bs = __half2float(__ushort_as_half(static_cast<uint16_t>(cvt_e4m3x2(b))));
-        uint32_t c[2] = {0u, 0u};
-        if (bs > 0.f) {
+      for (int i = 0; i < 16; ++i) {
+        constexpr int per = FMT == FT_KV_E4M3 ? 4 : 8, bits = 32 / per;
+        if (((code.w[i / per] ^ up.w[i / per]) >> (bits * (i % per))) & ((1u << bits) - 1)) unsure |= 1u << i;
+      }
+      if (!exact || !live) unsure = 0;
+      if (__any_sync(0xffffffffu, unsure != 0)) {
+        const int64_t p = a.rope_pos[t0 + tk];
+        const uint16_t* src = source(tk, live ? r : 0);
+        while (unsure != 0) {
+          const int i = __ffs(unsure) - 1;
+          unsure &= unsure - 1;
+          const int c = (i < 8 ? c0 : c1) * 8 + (i & 7);
+          if (c >= a.rot) continue;
+          const bool left = LAY == kPairs ? (c & 1) == 0 : c < a.half;
+          const int f = LAY == kPairs ? c >> 1 : left ? c : c - a.half;
+          const int o = LAY == kPairs ? c ^ 1 : left ? c + a.half : c - a.half;
+          float2 hi, lo;
+          turn_pair(static_cast<int64_t>(static_cast<uint64_t>(p) * static_cast<uint64_t>(a.freqs[f])), a.mscale, &hi, &lo);
+          const float u = load_one<F16>(src + c), v = load_one<F16>(src + o);
+          const float y = rotate_odd(u, left ? v : -v, hi.x, lo.x, hi.y, lo.y);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            c[i >> 2] |= to_e2m1x2(x[2 * i] * inv / bs, x[2 * i + 1] * inv / bs) << (8 * (i & 3));
+          for (int j = 0; j < 16; ++j) x[j] = j == i ? y : x[j];
         }
-        if (put && has0) {
-          *reinterpret_cast<uint2*>(dst + l * 8) = make_uint2(c[0], c[1]);
-          a.kv.block[w][static_cast<uint64_t>(row) * (a.D / 16) + l] = static_cast<uint8_t>(b);
-        }
-        if (put && l == 0) a.kv.scale[w][row] = static_cast<uint8_t>(e + 127);
+        __syncwarp();
+        maxima(block_max, amax);
+        e = row_exponent(amax, top, top_bits);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) d[i] = 0.f;
+        code = encode<FMT>(x, d, 0.f, block_max, e);
       }
     }
+    if (FMT == FT_KV_E4M3) {
+      if (put && has0) *reinterpret_cast<uint2*>(dst + c0 * 8) = make_uint2(code.w[0], code.w[1]);
+      if (put && has1) *reinterpret_cast<uint2*>(dst + c1 * 8) = make_uint2(code.w[2], code.w[3]);
+    } else if (put && has0) {  // neighbouring chunks, so that a lane holds one block of 16
+      *reinterpret_cast<uint2*>(dst + l * 8) = make_uint2(code.w[0], code.w[1]);
+      a.kv.block[w][static_cast<uint64_t>(row) * (a.D / 16) + l] = static_cast<uint8_t>(code.block);
+    }
+    if (put && l == 0) a.kv.scale[w][row] = static_cast<uint8_t>(e + 127);
   }
 }
 
@@ -404,86 +510,101 @@ struct ReadArgs {
   int32_t* status;
 };
 
+#ifndef FT_NI
+#define FT_NI 1
+#endif
+constexpr int kItems = FT_NI;
+
 // A lane reads 16 elements of a (token, head)'s key row and of its value row
 // (they share the place in the cache, so the dependent loads of position, page
-// and row are paid once for both) and writes them out dense.
+// and row are paid once for both) and writes them out dense; kItems of them,
+// whose loads are all under way together.
 template <int FMT, int DT>
-__global__ void __launch_bounds__(256) read_kernel(const ReadArgs a) {
-  const uint32_t i = (blockIdx.x * 256u + threadIdx.x) >> a.lanes_log2;
+__global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadArgs a) {
+  constexpr int W = FMT == FT_KV_NVFP4 ? 2 : FMT == FT_KV_E4M3 ? 4 : 8;  // words of 16 elements
   const int l = threadIdx.x & ((1 << a.lanes_log2) - 1);
-  if (i >= a.rows || l * 16 >= a.kv.D) return;
-  const uint32_t t = fast_div(i, a.by_heads), h = i - t * a.kv.Hkv;
-  const int32_t pos = a.pos[t];
-  uint32_t row = kNoRow;
-  if (pos >= 0) row = kv_token_row(a.kv, kv_seq(a.kv, t), pos, l == 0 ? a.status : nullptr);
-  uint32_t w[2][8];  // the codes; 16-bit formats fill all eight words
-  uint32_t b[2] = {0, 0};
-  float scale[2] = {1.f, 1.f};
+  if (l * 16 >= a.kv.D) return;
+  uint32_t at[kItems], token[kItems], head[kItems];
+  uint32_t row[kItems];
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-#pragma unroll
-    for (int n = 0; n < 8; ++n) w[j][n] = 0;
-    if (row == kNoRow || a.out[j] == nullptr) continue;
-    const uint64_t r = row + h * a.kv.at.head_stride;
-    const uint8_t* src = a.kv.data[j] + r * a.kv.row_bytes;
-    if (FMT == FT_KV_NVFP4) {
-      const uint2 v = *reinterpret_cast<const uint2*>(src + l * 8);
-      w[j][0] = v.x;
-      w[j][1] = v.y;
-      b[j] = a.kv.block[j][r * (a.kv.D / 16) + l];
-    } else {
-      const uint4 v = *reinterpret_cast<const uint4*>(src + l * (FMT == FT_KV_E4M3 ? 16 : 32));
-      w[j][0] = v.x, w[j][1] = v.y, w[j][2] = v.z, w[j][3] = v.w;
-      if (FMT != FT_KV_E4M3) {
-        const uint4 u = *reinterpret_cast<const uint4*>(src + l * 32 + 16);
-        w[j][4] = u.x, w[j][5] = u.y, w[j][6] = u.z, w[j][7] = u.w;
-      }
-    }
-    if (FMT == FT_KV_E4M3 || FMT == FT_KV_NVFP4) scale[j] = pow2f(static_cast<int>(a.kv.scale[j][r]) - 127);
+  for (int n = 0; n < kItems; ++n) {
+    at[n] = ((blockIdx.x * kItems + n) * 256u + threadIdx.x) >> a.lanes_log2;
+    token[n] = fast_div(at[n] < a.rows ? at[n] : 0, a.by_heads);
+    head[n] = at[n] - token[n] * a.kv.Hkv;
+    row[n] = kNoRow;
+    const int32_t pos = at[n] < a.rows ? a.pos[token[n]] : -1;
+    if (pos >= 0) row[n] = kv_token_row(a.kv, kv_seq(a.kv, token[n]), pos, l == 0 ? a.status : nullptr);
   }
+  uint32_t w[kItems][2][W], b[kItems][2], e[kItems][2];
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    if (a.out[j] == nullptr) continue;
-    float x[16];
-    if (FMT == FT_KV_BF16 || FMT == FT_KV_F16) {
+  for (int n = 0; n < kItems; ++n)
 #pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        const float2 v = unpack2<FMT == FT_KV_F16>(w[j][n]);
-        x[2 * n] = v.x;
-        x[2 * n + 1] = v.y;
+    for (int j = 0; j < 2; ++j) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) w[n][j][i] = 0;
+      b[n][j] = 0;
+      e[n][j] = 127;
+      if (row[n] == kNoRow || a.out[j] == nullptr) continue;
+      const uint64_t r = row[n] + head[n] * a.kv.at.head_stride;
+      const uint8_t* src = a.kv.data[j] + r * a.kv.row_bytes + l * (W * 4);
+      if constexpr (W == 2) {
+        const uint2 v = *reinterpret_cast<const uint2*>(src);
+        w[n][j][0] = v.x, w[n][j][1] = v.y;
+        b[n][j] = a.kv.block[j][r * (a.kv.D / 16) + l];
+      } else {
+#pragma unroll
+        for (int i = 0; i < W / 4; ++i) {
+          const uint4 v = *reinterpret_cast<const uint4*>(src + 16 * i);
+          w[n][j][4 * i] = v.x, w[n][j][4 * i + 1] = v.y, w[n][j][4 * i + 2] = v.z, w[n][j][4 * i + 3] = v.w;
+        }
       }
-    } else {
-      uint32_t f[8];  // f16 pairs; code * block scale is exact in f16
-      if (FMT == FT_KV_E4M3) {
+      if (W < 8) e[n][j] = a.kv.scale[j][r];
+    }
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          f[2 * n] = cvt_e4m3x2(w[j][n]);
-          f[2 * n + 1] = cvt_e4m3x2(w[j][n] >> 16);
+  for (int n = 0; n < kItems; ++n)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if (at[n] >= a.rows || a.out[j] == nullptr) continue;
+      float x[16];
+      if constexpr (W == 8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 v = unpack2<FMT == FT_KV_F16>(w[n][j][i]);
+          x[2 * i] = v.x;
+          x[2 * i + 1] = v.y;
         }
       } else {
-        e2m1x8(w[j][0], f);
-        e2m1x8(w[j][1], f + 4);
-        const float bs = unpack2<true>(cvt_e4m3x2(b[j])).x;
-        scale[j] *= bs;
-      }
+        uint32_t f[8];  // f16 pairs; code * block scale is exact in fp32
+        float scale = pow2f(static_cast<int>(e[n][j]) - 127);
+        if constexpr (W == 4) {
 #pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        const float2 v = unpack2<true>(f[n]);
-        x[2 * n] = v.x * scale[j];
-        x[2 * n + 1] = v.y * scale[j];
+          for (int i = 0; i < 4; ++i) {
+            f[2 * i] = cvt_e4m3x2(w[n][j][i]);
+            f[2 * i + 1] = cvt_e4m3x2(w[n][j][i] >> 16);
+          }
+        } else {
+          e2m1x8(w[n][j][0], f);
+          e2m1x8(w[n][j][1], f + 4);
+          scale *= unpack2<true>(cvt_e4m3x2(b[n][j])).x;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 v = unpack2<true>(f[i]);
+          x[2 * i] = v.x * scale;
+          x[2 * i + 1] = v.y * scale;
+        }
+      }
+      const int64_t to = static_cast<int64_t>(token[n]) * a.tok[j] + head[n] * a.head[j] + l * 16;
+      if (DT == FT_DT_F32) {
+        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out[j]) + to);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+      } else {
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out[j]) + to);
+        dst[0] = pack8<DT == FT_DT_F16>(x);
+        dst[1] = pack8<DT == FT_DT_F16>(x + 8);
       }
     }
-    const int64_t at = static_cast<int64_t>(t) * a.tok[j] + h * a.head[j] + l * 16;
-    if (DT == FT_DT_F32) {
-      float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out[j]) + at);
-#pragma unroll
-      for (int n = 0; n < 4; ++n) dst[n] = make_float4(x[4 * n], x[4 * n + 1], x[4 * n + 2], x[4 * n + 3]);
-    } else {
-      uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out[j]) + at);
-      dst[0] = pack8<DT == FT_DT_F16>(x);
-      dst[1] = pack8<DT == FT_DT_F16>(x + 8);
-    }
-  }
 }
 
 int ceil_log2(int n) {
@@ -499,38 +620,41 @@ bool rows_overlap_partly(const ft_rows* a, const ft_rows* b) {
 // Shape of a write launch and the launch itself.
 template <bool F16, int FMT>
 ft_status launch_write(WriteArgs& a, bool interleaved, const char* what, cudaStream_t s) {
-  const bool quant = FMT == FT_KV_E4M3 || FMT == FT_KV_NVFP4;
   a.half = a.rot / 2;
   constexpr bool kBlocks = FMT == FT_KV_NVFP4;  // a lane has to hold whole blocks of 16
   const bool halves = !kBlocks && a.half % 8 == 0 && (a.D - a.rot) % 16 == 0;
   a.lanes_log2 = ceil_log2((a.D + 15) / 16);
   const int64_t items = static_cast<int64_t>(a.Hq + (FMT >= 0 ? 2 * a.Hkv : 0)) << a.lanes_log2;
+  const int sms = device_sm_count();
   // Few tokens: a token's rows over several CTAs, so that each lane has one row.
-  const int64_t fill = device_sm_count() / a.T;
   int64_t parts = (items + 127) / 128;
-  if (parts > fill) parts = fill > 1 ? fill : 1;
+  if (parts > sms / a.T) parts = sms / a.T > 1 ? sms / a.T : 1;
   const int64_t per = (items + parts - 1) / parts;
   const int64_t rounds = (per + 511) / 512;
   const int block = static_cast<int>(((per + rounds - 1) / rounds + 31) / 32 * 32);
   // Parts that would begin past the last row are not launched.
   a.parts = static_cast<int>(parts);
   while (a.parts > 1 && static_cast<int64_t>(a.parts - 1) * block >= items) --a.parts;
-  FT_REQUIRE(static_cast<int64_t>(a.T) * a.parts < (1ll << 31), "%s: too many rows", what);
-  const unsigned grid = static_cast<unsigned>(a.T) * a.parts;
-  const size_t smem = static_cast<size_t>(a.half) * sizeof(float2) * (quant ? 2 : 1);
+  // Many tokens: several a CTA, while the SMs stay full.
+  const int fill = a.T / (FT_FILL * sms);
+  a.batch = fill < 1 ? 1 : fill > FT_BATCH ? FT_BATCH : fill;
+  const int64_t groups = (a.T + a.batch - 1) / a.batch;
+  FT_REQUIRE(groups * a.parts < (1ll << 31), "%s: too many rows", what);
+  const unsigned grid = static_cast<unsigned>(groups) * a.parts;
+  const size_t smem = static_cast<size_t>(a.batch) * 2 * ((a.half + 31) / 32 * 32) * sizeof(float);
   if (interleaved || a.rot == 0)
-    write_kernel<F16, FMT, kPairs, quant><<<grid, block, smem, s>>>(a);
+    write_kernel<F16, FMT, kPairs><<<grid, block, smem, s>>>(a);
   else if (halves)
-    write_kernel<F16, FMT, kBlocks ? kAny : kHalves, quant><<<grid, block, smem, s>>>(a);
+    write_kernel<F16, FMT, kBlocks ? kAny : kHalves><<<grid, block, smem, s>>>(a);
   else
-    write_kernel<F16, FMT, kAny, quant><<<grid, block, smem, s>>>(a);
+    write_kernel<F16, FMT, kAny><<<grid, block, smem, s>>>(a);
   return launch_check(what);
 }
 
 template <int FMT, int DT>
 void launch_read(const ReadArgs& a, cudaStream_t s) {
   const uint64_t threads = static_cast<uint64_t>(a.rows) << a.lanes_log2;
-  read_kernel<FMT, DT><<<static_cast<unsigned>((threads + 255) / 256), 256, 0, s>>>(a);
+  read_kernel<FMT, DT><<<static_cast<unsigned>((threads + 256 * kItems - 1) / (256 * kItems)), 256, 0, s>>>(a);
 }
 
 template <int FMT>
