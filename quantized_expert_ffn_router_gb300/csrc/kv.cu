@@ -150,6 +150,30 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
   return make_uint4(pack2<F16>(f[0], f[1]), pack2<F16>(f[2], f[3]), pack2<F16>(f[4], f[5]), pack2<F16>(f[6], f[7]));
 }
 
+// 32 bytes to or from two places of 16, in one access where they are one
+// 32-byte place: two would each touch half of every sector.
+__device__ __forceinline__ void store32(void* p, uint4 a, uint4 b, bool whole) {
+  if (whole) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z),
+                 "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+  } else {
+    static_cast<uint4*>(p)[0] = a;
+    static_cast<uint4*>(p)[1] = b;
+  }
+}
+
+__device__ __forceinline__ void load32(const void* p, uint4& a, uint4& b, bool whole) {
+  if (whole) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+                 : "l"(p));
+  } else {
+    a = static_cast<const uint4*>(p)[0];
+    b = static_cast<const uint4*>(p)[1];
+  }
+}
+
 // --------------------------------------------------------------- quantising ---
 // The smallest e >= kMinExponent with amax <= top * 2^e, where top = 1.t * 2^x
 // and t_bits are top's fraction bits: exact, from the bits of amax.
@@ -183,13 +207,6 @@ __device__ __forceinline__ float finite_abs(float x) {
 // ------------------------------------------------------------ rotate, write ---
 enum { kPairs, kHalves, kAny };
 constexpr int kMaxBatch = 8;
-#ifndef FT_FILL
-#define FT_FILL 8
-#endif
-#ifndef FT_BATCH
-#define FT_BATCH 4
-#endif
-
 struct WriteArgs {
   KvView kv;
   const uint16_t* in[3];  // q, k, v
@@ -205,6 +222,7 @@ struct WriteArgs {
   int32_t lanes_log2;       // lanes of one row
   int32_t parts;            // CTAs of one token
   int32_t batch;            // tokens of a CTA
+  int32_t wide_in, wide_out;  // inputs, q_out: every 16 channels are a 32-byte place
   int32_t* status;
 };
 
@@ -229,17 +247,15 @@ struct Codes {
   uint32_t block;  // NVFP4: the block's scale
 };
 
-// x[16] to codes, given the row's exponent; d[16] is added first (the check of
-// rotated keys quantises both ends of their uncertainty).
+// x[16] to codes, given the row's exponent and the block's largest magnitude.
 template <int FMT>
-__device__ __forceinline__ Codes encode(const float (&x)[16], const float (&d)[16], float sign, float block_max, int e) {
+__device__ __forceinline__ Codes encode(const float (&x)[16], float block_max, int e) {
   Codes c;
   const float inv = pow2f(-e);
   if (FMT == FT_KV_E4M3) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      c.w[i] = to_e4m3x2(fmaf(sign, d[4 * i], x[4 * i]) * inv, fmaf(sign, d[4 * i + 1], x[4 * i + 1]) * inv) |
-               (to_e4m3x2(fmaf(sign, d[4 * i + 2], x[4 * i + 2]) * inv, fmaf(sign, d[4 * i + 3], x[4 * i + 3]) * inv) << 16);
+      c.w[i] = to_e4m3x2(x[4 * i] * inv, x[4 * i + 1] * inv) | (to_e4m3x2(x[4 * i + 2] * inv, x[4 * i + 3] * inv) << 16);
     c.block = 0;
   } else {
     float nan = 0.f;
@@ -250,12 +266,23 @@ __device__ __forceinline__ Codes encode(const float (&x)[16], const float (&d)[1
     c.w[0] = c.w[1] = c.w[2] = c.w[3] = 0;
     if (bs > 0.f) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        c.w[i >> 2] |= to_e2m1x2(fmaf(sign, d[2 * i], x[2 * i]) * inv / bs, fmaf(sign, d[2 * i + 1], x[2 * i + 1]) * inv / bs)
-                       << (8 * (i & 3));
+      for (int i = 0; i < 8; ++i) c.w[i >> 2] |= to_e2m1x2(x[2 * i] * inv / bs, x[2 * i + 1] * inv / bs) << (8 * (i & 3));
     }
   }
   return c;
+}
+
+// The largest finite magnitude of x[16].
+__device__ __forceinline__ float largest(const float (&x)[16]) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(x[i]));  // NaN is passed over
+  if (m > 3.4028235e38f) {
+    m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = fmaxf(m, finite_abs(x[i]));
+  }
+  return m;
 }
 
 // A CTA takes (a part of the rows of) `batch` tokens, one after the other,
@@ -279,7 +306,7 @@ __device__ __forceinline__ Codes encode(const float (&x)[16], const float (&d)[1
 // where a border lies between (about one element in 2^16), its lane rotates it
 // again in two-float arithmetic.
 template <bool F16, int FMT, int LAY>
-__global__ void __launch_bounds__(512) write_kernel(const __grid_constant__ WriteArgs a) {
+__global__ void __launch_bounds__(512, LAY == kAny ? 1 : 2) write_kernel(const __grid_constant__ WriteArgs a) {
   constexpr bool kQuant = FMT == FT_KV_E4M3 || FMT == FT_KV_NVFP4;
   extern __shared__ __align__(16) float turns[];  // [batch][cosines, sines][half, rounded up to whole chunk pairs]
   __shared__ uint32_t rows_s[kMaxBatch];          // head 0's row of each token's place
@@ -305,27 +332,35 @@ __global__ void __launch_bounds__(512) write_kernel(const __grid_constant__ Writ
   const int rounds = (rows - r_cta + step - 1) / step;  // the same for every thread of the CTA
   const int r_first = r_cta + (threadIdx.x >> a.lanes_log2);
 
-  const auto source = [&](int token, int r) {
-    const int kind = r < a.Hq ? 0 : r < a.Hq + a.Hkv ? 1 : 2;
-    const int h = kind == 0 ? r : kind == 1 ? r - a.Hq : r - a.Hq - a.Hkv;
-    return a.in[kind] + static_cast<int64_t>(t0 + token) * a.in_tok[kind] + h * a.in_head[kind];
+  // the row of this round: what it is, and where its first token's channels are
+  int r = r_first, kind, h;
+  const uint16_t* src;
+  const auto turn_to = [&](int row) {
+    r = row;
+    kind = r < a.Hq ? 0 : r < a.Hq + a.Hkv ? 1 : 2;
+    h = kind == 0 ? r : kind == 1 ? r - a.Hq : r - a.Hq - a.Hkv;
+    src = a.in[kind] + static_cast<int64_t>(t0) * a.in_tok[kind] + h * a.in_head[kind];
   };
-  const auto load = [&](int token, int r, Chunks<LAY>& c) {
+  const auto load = [&](const uint16_t* from, bool any, Chunks<LAY>& c) {
     const uint4 zero = make_uint4(0, 0, 0, 0);
     c.own[0] = c.own[1] = c.other[0] = zero;
     if (LAY == kAny) c.other[LAY == kAny ? 1 : 0] = zero;
-    if (r >= rows || token >= tokens) return;
-    const uint16_t* src = source(token, r);
-    if (has0) c.own[0] = *reinterpret_cast<const uint4*>(src + c0 * 8);
-    if (has1) c.own[1] = *reinterpret_cast<const uint4*>(src + c1 * 8);
-    if (LAY == kAny && vec && (FMT < 0 || r < a.Hq + a.Hkv)) {
-      if (c0 < 2 * hc) c.other[0] = *reinterpret_cast<const uint4*>(src + (c0 < hc ? c0 + hc : c0 - hc) * 8);
-      if (c1 < 2 * hc) c.other[LAY == kAny ? 1 : 0] = *reinterpret_cast<const uint4*>(src + (c1 < hc ? c1 + hc : c1 - hc) * 8);
+    if (!any || r >= rows) return;
+    if (LAY != kHalves && has1) {
+      load32(from + c0 * 8, c.own[0], c.own[1], a.wide_in != 0);
+    } else {
+      if (has0) c.own[0] = *reinterpret_cast<const uint4*>(from + c0 * 8);
+      if (has1) c.own[1] = *reinterpret_cast<const uint4*>(from + c1 * 8);
+    }
+    if (LAY == kAny && vec && kind < 2) {
+      if (c0 < 2 * hc) c.other[0] = *reinterpret_cast<const uint4*>(from + (c0 < hc ? c0 + hc : c0 - hc) * 8);
+      if (c1 < 2 * hc) c.other[LAY == kAny ? 1 : 0] = *reinterpret_cast<const uint4*>(from + (c1 < hc ? c1 + hc : c1 - hc) * 8);
     }
   };
 
   Chunks<LAY> next;
-  load(0, r_first, next);
+  turn_to(r_first);
+  load(src, true, next);
 
   if (FMT >= 0 && threadIdx.x < tokens) {
     const int32_t place = a.pos[t0 + threadIdx.x];
@@ -342,28 +377,61 @@ __global__ void __launch_bounds__(512) write_kernel(const __grid_constant__ Writ
   }
   __syncthreads();
 
-  for (int token = 0, round = 0; token < tokens;) {
-    const Chunks<LAY> now = next;
-    const int tk = token, r = r_first + round * step;
-    if (++round == rounds) {
-      round = 0;
-      ++token;
+  // kAny: the other sides of the lane's rotations
+  const auto other_sides = [&](const Chunks<LAY>& c, const uint16_t* from, float (&y)[16]) {
+    if (vec) {
+      unpack8<F16>(c.other[0], y);
+      unpack8<F16>(c.other[LAY == kAny ? 1 : 0], y + 8);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int ch = (i < 8 ? c0 : c1) * 8 + (i & 7);
+        y[i] = (r < rows && ch < a.rot) ? load_one<F16>(from + (ch < a.half ? ch + a.half : ch - a.half)) : 0.f;
+      }
     }
-    load(token, r_first + round * step, next);
+  };
+  // what fp32's rotation of the lane's channels may be off by
+  const auto uncertainty = [&](const Chunks<LAY>& c, const uint16_t* from, bool any, float (&d)[16]) {
+    const float off = any ? 6.7434956e-7f * fabsf(a.mscale) : 0.f;  // 2^-20.5
+    float u[16];
+    unpack8<F16>(c.own[0], u);
+    unpack8<F16>(c.own[1], u + 8);
+    if (LAY == kAny) {
+      float y[16];
+      other_sides(c, from, y);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) d[i] = (i < 8 ? c0 : c1) * 8 + (i & 7) < a.rot ? (fabsf(u[i]) + fabsf(y[i])) * off : 0.f;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int iu = LAY == kPairs ? 2 * i : i, iv = LAY == kPairs ? 2 * i + 1 : i + 8;
+        const bool turns_too = LAY == kPairs ? 8 * l + i < a.half : l < hc;
+        d[iu] = d[iv] = turns_too ? (fabsf(u[iu]) + fabsf(u[iv])) * off : 0.f;
+      }
+    }
+  };
 
-    const bool live = r < rows;
-    const int kind = r < a.Hq ? 0 : r < a.Hq + a.Hkv ? 1 : 2;
-    const int h = kind == 0 ? r : kind == 1 ? r - a.Hq : r - a.Hq - a.Hkv;
-    const bool spin = a.rot > 0 && kind < 2;
+  for (int round = 0; round < rounds; ++round) {
+  if (round > 0) {
+    turn_to(r_first + round * step);
+    load(src, true, next);
+  }
+  const bool live = r < rows;
+  const bool spin = a.rot > 0 && kind < 2;
+  const bool exact = kQuant && kind == 1 && spin;
+  const int64_t stride = a.in_tok[kind];
+  const int w = kind == 2 ? 1 : 0;
+  uint16_t* dst_q = a.q_out + static_cast<int64_t>(t0) * a.out_tok + h * a.out_head;
+#pragma unroll 1
+  for (int tk = 0; tk < tokens; ++tk, src += stride, dst_q += a.out_tok) {
+    const Chunks<LAY> now = next;
+    load(src + stride, tk + 1 < tokens, next);
+
     const float* cosines = turns + tk * 2 * half_up;
     const float* sines = cosines + half_up;
-    float x[16], d[16];  // the channels; what they may be off by (quantised keys)
+    float x[16];
     unpack8<F16>(now.own[0], x);
     unpack8<F16>(now.own[1], x + 8);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) d[i] = 0.f;
-    const bool exact = kQuant && kind == 1 && spin;
-    const float off = 6.7434956e-7f * fabsf(a.mscale);  // 2^-20.5
     if (spin) {
       if (LAY == kPairs || LAY == kHalves) {
         // 8 rotations: channels (2i, 2i + 1), or (i, i + 8)
@@ -384,30 +452,18 @@ __global__ void __launch_bounds__(512) write_kernel(const __grid_constant__ Writ
               const float u = x[iu], v = x[iv];
               x[iu] = u * cs[i] - v * sn[i];
               x[iv] = v * cs[i] + u * sn[i];
-              if (kQuant) d[iu] = d[iv] = exact ? (fabsf(u) + fabsf(v)) * off : 0.f;
             }
           }
         }
       } else {
         float y[16];
-        if (vec) {
-          unpack8<F16>(now.other[0], y);
-          unpack8<F16>(now.other[LAY == kAny ? 1 : 0], y + 8);
-        } else {
-          const uint16_t* src = source(tk, live ? r : 0);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int c = (i < 8 ? c0 : c1) * 8 + (i & 7);
-            y[i] = (live && c < a.rot) ? load_one<F16>(src + (c < a.half ? c + a.half : c - a.half)) : 0.f;
-          }
-        }
+        other_sides(now, src, y);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int c = (i < 8 ? c0 : c1) * 8 + (i & 7);
           if (c < a.rot) {
             const bool left = c < a.half;
             const int at = turn_at(left ? c : c - a.half);
-            if (kQuant) d[i] = exact ? (fabsf(x[i]) + fabsf(y[i])) * off : 0.f;
             x[i] = x[i] * cosines[at] - (left ? y[i] : -y[i]) * sines[at];
           }
         }
@@ -415,15 +471,17 @@ __global__ void __launch_bounds__(512) write_kernel(const __grid_constant__ Writ
     }
     __syncwarp();  // in place: the row's lanes have loaded both sides before any of them stores
     if (kind == 0 || FMT < 0) {
-      uint16_t* dst = a.q_out + static_cast<int64_t>(t0 + tk) * a.out_tok + h * a.out_head;
-      if (live && has0) *reinterpret_cast<uint4*>(dst + c0 * 8) = pack8<F16>(x);
-      if (live && has1) *reinterpret_cast<uint4*>(dst + c1 * 8) = pack8<F16>(x + 8);
+      if (LAY != kHalves && live && has1) {
+        store32(dst_q + c0 * 8, pack8<F16>(x), pack8<F16>(x + 8), a.wide_out != 0);
+      } else {
+        if (live && has0) *reinterpret_cast<uint4*>(dst_q + c0 * 8) = pack8<F16>(x);
+        if (live && has1) *reinterpret_cast<uint4*>(dst_q + c1 * 8) = pack8<F16>(x + 8);
+      }
     }
     if (FMT < 0) continue;
     const uint32_t row0 = rows_s[tk];
     const bool put = live && kind > 0 && row0 != kNoRow;
     if (!__any_sync(0xffffffffu, put)) continue;
-    const int w = kind == 2 ? 1 : 0;
     const uint32_t row = row0 + static_cast<uint32_t>(h) * a.kv.at.head_stride;
     uint8_t* dst = a.kv.data[w] + static_cast<uint64_t>(row) * a.kv.row_bytes;
     if (!kQuant) {
@@ -431,39 +489,43 @@ __global__ void __launch_bounds__(512) write_kernel(const __grid_constant__ Writ
       if (put && has1) *reinterpret_cast<uint4*>(dst + c1 * 16) = pack8<F16>(x + 8);
       continue;
     }
-    constexpr int top = FMT == FT_KV_E4M3 ? 8 : 11;                              // 448 = 1.75 * 2^8,
-    constexpr uint32_t top_bits = FMT == FT_KV_E4M3 ? 0x600000u : 0x280000u;     // 2688 = 1.3125 * 2^11
-    const auto maxima = [&](float& block_max, float& amax) {
-      block_max = 0.f;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) block_max = fmaxf(block_max, finite_abs(x[i]));
-      amax = block_max;
-      for (int o = lanes >> 1; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    constexpr int top = FMT == FT_KV_E4M3 ? 8 : 11;                           // 448 = 1.75 * 2^8,
+    constexpr uint32_t top_bits = FMT == FT_KV_E4M3 ? 0x600000u : 0x280000u;  // 2688 = 1.3125 * 2^11
+    const auto row_largest = [&](float m) {
+      for (int o = lanes >> 1; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      return m;
     };
-    float block_max, amax;
-    maxima(block_max, amax);
+    float block_max = largest(x), amax = row_largest(block_max);
     int e = row_exponent(amax, top, top_bits);
-    Codes code = encode<FMT>(x, d, -1.f, block_max, e);
-    if (__any_sync(0xffffffffu, exact)) {
-      // Both ends, and the row's and block's largest: the row's is at least
-      // the largest pair's size / sqrt 2, so off by at most 2^-19 of itself.
-      const float part = amax * 0x1p-19f;
-      float far = 0.f;
+    Codes code;
+    if (!__any_sync(0xffffffffu, exact)) {
+      code = encode<FMT>(x, block_max, e);
+    } else {
+      // Both ends; the row's largest is at least the largest pair's size /
+      // sqrt 2, so off by at most 2^-19 of itself.
+      float d[16], z[16], far = 0.f;
+      uncertainty(now, src, exact, d);
 #pragma unroll
       for (int i = 0; i < 16; ++i) far = fmaxf(far, d[i]);
-      const Codes up = encode<FMT>(x, d, 1.f, block_max + far, e);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) z[i] = x[i] - d[i];
+      code = encode<FMT>(z, block_max, e);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) z[i] = x[i] + d[i];
+      const Codes up = encode<FMT>(z, block_max + far, e);
+      const float part = amax * 0x1p-19f;
       bool all = row_exponent(amax - part, top, top_bits) != row_exponent(amax + part, top, top_bits);
       if (FMT == FT_KV_NVFP4) all |= (to_e4m3x2((block_max - far) * pow2f(-e) / 6.f, 0.f) & 0xffu) != up.block;
-      uint32_t unsure = all ? 0xffffu : 0;  // one bit a channel
+      const bool differ = code.w[0] != up.w[0] || code.w[1] != up.w[1] || code.w[2] != up.w[2] || code.w[3] != up.w[3];
+      if (__any_sync(0xffffffffu, exact && live && (all || differ))) {
+        uint32_t unsure = all ? 0xffffu : 0;  // one bit a channel
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        constexpr int per = FMT == FT_KV_E4M3 ? 4 : 8, bits = 32 / per;
-        if (((code.w[i / per] ^ up.w[i / per]) >> (bits * (i % per))) & ((1u << bits) - 1)) unsure |= 1u << i;
-      }
-      if (!exact || !live) unsure = 0;
-      if (__any_sync(0xffffffffu, unsure != 0)) {
+        for (int i = 0; i < 16; ++i) {
+          constexpr int per = FMT == FT_KV_E4M3 ? 4 : 8, bits = 32 / per;
+          if (((code.w[i / per] ^ up.w[i / per]) >> (bits * (i % per))) & ((1u << bits) - 1)) unsure |= 1u << i;
+        }
+        if (!exact || !live) unsure = 0;
         const int64_t p = a.rope_pos[t0 + tk];
-        const uint16_t* src = source(tk, live ? r : 0);
         while (unsure != 0) {
           const int i = __ffs(unsure) - 1;
           unsure &= unsure - 1;
@@ -480,11 +542,10 @@ __global__ void __launch_bounds__(512) write_kernel(const __grid_constant__ Writ
           for (int j = 0; j < 16; ++j) x[j] = j == i ? y : x[j];
         }
         __syncwarp();
-        maxima(block_max, amax);
+        block_max = largest(x);
+        amax = row_largest(block_max);
         e = row_exponent(amax, top, top_bits);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) d[i] = 0.f;
-        code = encode<FMT>(x, d, 0.f, block_max, e);
+        code = encode<FMT>(x, block_max, e);
       }
     }
     if (FMT == FT_KV_E4M3) {
@@ -495,6 +556,7 @@ __global__ void __launch_bounds__(512) write_kernel(const __grid_constant__ Writ
       a.kv.block[w][static_cast<uint64_t>(row) * (a.D / 16) + l] = static_cast<uint8_t>(code.block);
     }
     if (put && l == 0) a.kv.scale[w][row] = static_cast<uint8_t>(e + 127);
+  }
   }
 }
 
@@ -507,85 +569,75 @@ struct ReadArgs {
   FastDiv by_heads;
   uint32_t rows;  // T * Hkv
   int32_t lanes_log2;
+  int32_t wide_in, wide_out;  // 16-bit rows of the cache, of the outputs: every 16 elements are a 32-byte place
   int32_t* status;
 };
 
-#ifndef FT_NI
-#define FT_NI 1
-#endif
-constexpr int kItems = FT_NI;
-
 // A lane reads 16 elements of a (token, head)'s key row and of its value row
 // (they share the place in the cache, so the dependent loads of position, page
-// and row are paid once for both) and writes them out dense; kItems of them,
-// whose loads are all under way together.
+// and row are paid once for both) and writes them out dense.  One such pair a
+// lane: with two or four the SMs hold fewer (16384 tokens x 8 heads of 128,
+// E4M3 to bf16: 21.2 us, 23.3 and 28.1).
 template <int FMT, int DT>
 __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadArgs a) {
   constexpr int W = FMT == FT_KV_NVFP4 ? 2 : FMT == FT_KV_E4M3 ? 4 : 8;  // words of 16 elements
   const int l = threadIdx.x & ((1 << a.lanes_log2) - 1);
   if (l * 16 >= a.kv.D) return;
-  uint32_t at[kItems], token[kItems], head[kItems];
-  uint32_t row[kItems];
-#pragma unroll
-  for (int n = 0; n < kItems; ++n) {
-    at[n] = ((blockIdx.x * kItems + n) * 256u + threadIdx.x) >> a.lanes_log2;
-    token[n] = fast_div(at[n] < a.rows ? at[n] : 0, a.by_heads);
-    head[n] = at[n] - token[n] * a.kv.Hkv;
-    row[n] = kNoRow;
-    const int32_t pos = at[n] < a.rows ? a.pos[token[n]] : -1;
-    if (pos >= 0) row[n] = kv_token_row(a.kv, kv_seq(a.kv, token[n]), pos, l == 0 ? a.status : nullptr);
-  }
-  uint32_t w[kItems][2][W], b[kItems][2], e[kItems][2];
-#pragma unroll
-  for (int n = 0; n < kItems; ++n)
+  const uint32_t at = (blockIdx.x * 256u + threadIdx.x) >> a.lanes_log2;
+  if (at >= a.rows) return;
+  const uint32_t token = fast_div(at, a.by_heads), head = at - token * a.kv.Hkv;
+  const int32_t pos = a.pos[token];
+  uint32_t row = kNoRow;
+  if (pos >= 0) row = kv_token_row(a.kv, kv_seq(a.kv, token), pos, l == 0 ? a.status : nullptr);
+  uint32_t w[2][W], b[2], e[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
 #pragma unroll
-      for (int i = 0; i < W; ++i) w[n][j][i] = 0;
-      b[n][j] = 0;
-      e[n][j] = 127;
-      if (row[n] == kNoRow || a.out[j] == nullptr) continue;
-      const uint64_t r = row[n] + head[n] * a.kv.at.head_stride;
+      for (int i = 0; i < W; ++i) w[j][i] = 0;
+      b[j] = 0;
+      e[j] = 127;
+      if (row == kNoRow || a.out[j] == nullptr) continue;
+      const uint64_t r = row + head * a.kv.at.head_stride;
       const uint8_t* src = a.kv.data[j] + r * a.kv.row_bytes + l * (W * 4);
       if constexpr (W == 2) {
         const uint2 v = *reinterpret_cast<const uint2*>(src);
-        w[n][j][0] = v.x, w[n][j][1] = v.y;
-        b[n][j] = a.kv.block[j][r * (a.kv.D / 16) + l];
+        w[j][0] = v.x, w[j][1] = v.y;
+        b[j] = a.kv.block[j][r * (a.kv.D / 16) + l];
       } else {
-#pragma unroll
-        for (int i = 0; i < W / 4; ++i) {
-          const uint4 v = *reinterpret_cast<const uint4*>(src + 16 * i);
-          w[n][j][4 * i] = v.x, w[n][j][4 * i + 1] = v.y, w[n][j][4 * i + 2] = v.z, w[n][j][4 * i + 3] = v.w;
-        }
+        uint4 v, u;
+        if constexpr (W == 8)
+          load32(src, v, u, a.wide_in != 0);
+        else
+          v = *reinterpret_cast<const uint4*>(src);
+        w[j][0] = v.x, w[j][1] = v.y, w[j][2] = v.z, w[j][3] = v.w;
+        if constexpr (W == 8) w[j][4] = u.x, w[j][5] = u.y, w[j][6] = u.z, w[j][7] = u.w;
       }
-      if (W < 8) e[n][j] = a.kv.scale[j][r];
+      if (W < 8) e[j] = a.kv.scale[j][r];
     }
 #pragma unroll
-  for (int n = 0; n < kItems; ++n)
-#pragma unroll
     for (int j = 0; j < 2; ++j) {
-      if (at[n] >= a.rows || a.out[j] == nullptr) continue;
+      if (a.out[j] == nullptr) continue;
       float x[16];
       if constexpr (W == 8) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float2 v = unpack2<FMT == FT_KV_F16>(w[n][j][i]);
+          const float2 v = unpack2<FMT == FT_KV_F16>(w[j][i]);
           x[2 * i] = v.x;
           x[2 * i + 1] = v.y;
         }
       } else {
         uint32_t f[8];  // f16 pairs; code * block scale is exact in fp32
-        float scale = pow2f(static_cast<int>(e[n][j]) - 127);
+        float scale = pow2f(static_cast<int>(e[j]) - 127);
         if constexpr (W == 4) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            f[2 * i] = cvt_e4m3x2(w[n][j][i]);
-            f[2 * i + 1] = cvt_e4m3x2(w[n][j][i] >> 16);
+            f[2 * i] = cvt_e4m3x2(w[j][i]);
+            f[2 * i + 1] = cvt_e4m3x2(w[j][i] >> 16);
           }
         } else {
-          e2m1x8(w[n][j][0], f);
-          e2m1x8(w[n][j][1], f + 4);
-          scale *= unpack2<true>(cvt_e4m3x2(b[n][j])).x;
+          e2m1x8(w[j][0], f);
+          e2m1x8(w[j][1], f + 4);
+          scale *= unpack2<true>(cvt_e4m3x2(b[j])).x;
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -594,15 +646,14 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadA
           x[2 * i + 1] = v.y * scale;
         }
       }
-      const int64_t to = static_cast<int64_t>(token[n]) * a.tok[j] + head[n] * a.head[j] + l * 16;
+      const int64_t to = static_cast<int64_t>(token) * a.tok[j] + head * a.head[j] + l * 16;
       if (DT == FT_DT_F32) {
         float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out[j]) + to);
 #pragma unroll
         for (int i = 0; i < 4; ++i) dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
       } else {
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out[j]) + to);
-        dst[0] = pack8<DT == FT_DT_F16>(x);
-        dst[1] = pack8<DT == FT_DT_F16>(x + 8);
+        store32(static_cast<uint16_t*>(a.out[j]) + to, pack8<DT == FT_DT_F16>(x), pack8<DT == FT_DT_F16>(x + 8),
+                a.wide_out != 0);
       }
     }
 }
@@ -630,14 +681,22 @@ ft_status launch_write(WriteArgs& a, bool interleaved, const char* what, cudaStr
   int64_t parts = (items + 127) / 128;
   if (parts > sms / a.T) parts = sms / a.T > 1 ? sms / a.T : 1;
   const int64_t per = (items + parts - 1) / parts;
-  const int64_t rounds = (per + 511) / 512;
-  const int block = static_cast<int>(((per + rounds - 1) / rounds + 31) / 32 * 32);
+  // As few rounds as leave at least 960 of the 1024 threads that fit an SM (64
+  // registers): 384 lanes in one block of 384 are two blocks an SM and took 46
+  // us where two rounds of 192 took 38 (8192 tokens, 32 + 2 x 8 heads of 128).
+  int64_t rounds = (per + 511) / 512;
+  int block = static_cast<int>(((per + rounds - 1) / rounds + 31) / 32 * 32);
+  while (block > 64 && 1024 / block * block < 960) {
+    ++rounds;
+    block = static_cast<int>(((per + rounds - 1) / rounds + 31) / 32 * 32);
+  }
   // Parts that would begin past the last row are not launched.
   a.parts = static_cast<int>(parts);
   while (a.parts > 1 && static_cast<int64_t>(a.parts - 1) * block >= items) --a.parts;
-  // Many tokens: several a CTA, while the SMs stay full.
-  const int fill = a.T / (FT_FILL * sms);
-  a.batch = fill < 1 ? 1 : fill > FT_BATCH ? FT_BATCH : fill;
+  // Many tokens: several a CTA, so that their loads overlap, while there are
+  // eight CTAs an SM (4099 tokens x 40 heads rotated: 17.7 us, with four 19.4).
+  const int fill = a.T / (8 * sms);
+  a.batch = fill < 1 ? 1 : fill > kMaxBatch ? kMaxBatch : fill;
   const int64_t groups = (a.T + a.batch - 1) / a.batch;
   FT_REQUIRE(groups * a.parts < (1ll << 31), "%s: too many rows", what);
   const unsigned grid = static_cast<unsigned>(groups) * a.parts;
@@ -654,7 +713,7 @@ ft_status launch_write(WriteArgs& a, bool interleaved, const char* what, cudaStr
 template <int FMT, int DT>
 void launch_read(const ReadArgs& a, cudaStream_t s) {
   const uint64_t threads = static_cast<uint64_t>(a.rows) << a.lanes_log2;
-  read_kernel<FMT, DT><<<static_cast<unsigned>((threads + 256 * kItems - 1) / (256 * kItems)), 256, 0, s>>>(a);
+  read_kernel<FMT, DT><<<static_cast<unsigned>((threads + 255) / 256), 256, 0, s>>>(a);
 }
 
 template <int FMT>
@@ -665,6 +724,11 @@ void launch_read_dt(const ReadArgs& a, int32_t dtype, cudaStream_t s) {
     launch_read<FMT, FT_DT_F16>(a, s);
   else
     launch_read<FMT, FT_DT_F32>(a, s);
+}
+
+// Every 16 elements of 16-bit rows (D a multiple of 16) are a 32-byte place.
+bool wide(const ft_rows* r) {
+  return reinterpret_cast<uintptr_t>(r->base) % 32 == 0 && r->token_stride % 16 == 0 && r->head_stride % 16 == 0;
 }
 
 ft_status check_rope(const char* what, const ft_rope_table* r, int32_t D) {
@@ -817,6 +881,8 @@ ft_status ft_rope(const ft_rows* x_host, int32_t T, int32_t heads, int32_t D, in
   a.T = T;
   a.Hq = heads;
   a.D = D;
+  a.wide_in = wide(x_host);
+  a.wide_out = wide(out_host);
   const bool pairs = rope_host->interleaved != 0;
   if (dtype == FT_DT_F16) return launch_write<true, -1>(a, pairs, "rope", as_stream(stream));
   return launch_write<false, -1>(a, pairs, "rope", as_stream(stream));
@@ -855,6 +921,8 @@ ft_status ft_kv_append(const ft_kv_cache* cache_host, const ft_rows* k_host, con
     a.in_tok[i] = in[i]->token_stride;
     a.in_head[i] = in[i]->head_stride;
   }
+  a.wide_in = wide(k_host) && wide(v_host) && (!with_q || wide(q_host));
+  a.wide_out = with_q && wide(q_out_host);
   bool pairs = false;
   if (rope_host != nullptr) {
     if ((st = check_rope("kv_append", rope_host, cache_host->D)) != FT_OK) return st;
@@ -895,6 +963,8 @@ ft_status ft_kv_gather(const ft_kv_cache* cache_host, const ft_page_table* table
   if (T == 0) return FT_OK;
   FT_REQUIRE(pos != nullptr, "kv_gather: pos is NULL");
   const ft_rows* out[2] = {k_out_host, v_out_host};
+  a.wide_out = (!k_out_host || wide(k_out_host)) && (!v_out_host || wide(v_out_host));
+  a.wide_in = reinterpret_cast<uintptr_t>(cache_host->k) % 32 == 0 && reinterpret_cast<uintptr_t>(cache_host->v) % 32 == 0;
   for (int j = 0; j < 2; ++j) {
     if (out[j] == nullptr) continue;
     if ((st = check_rows("kv_gather", j ? "v_out" : "k_out", out[j], dtype == FT_DT_F32 ? 4 : 8)) != FT_OK) return st;
