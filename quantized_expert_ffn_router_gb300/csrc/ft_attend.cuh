@@ -1,0 +1,983 @@
+// ft_attend.cuh -- attention of one new token a row over the paged key-value
+// cache: the kernel, for one cache format a translation unit (attn_*.cu).
+//
+// For each row t and query head h:  x_j = scale q.k_j,  o = sum_j e^(x_j - m) v_j / sum_j e^(x_j - m)
+// over the row's tokens j, in one pass with a running maximum m.  Every cached
+// byte is read once and used by the G = Hq / Hkv query heads of its key head:
+// 4 G flops a byte pair, far below the tensor cores' ridge, so the kernel is
+// bound by HBM and everything is arranged around loads in flight.
+//
+// Layout of the work in a warp.  A warp works alone on steps of 16 or 32
+// tokens: one lane a token looks its page up, and 16-byte asynchronous copies
+// (any pages and strides; masked tokens become zeros) bring the rows into the
+// warp's own ring in shared memory, several steps ahead and across the ends of
+// units, so that loads stay in flight while the warp computes.  Keys become
+// the A operand of mma.m16n8k16 (16 tokens x 16 channels, S^T = K Q^T) and
+// values that of the second product (16 channels x 16 tokens, O^T = V^T P^T):
+// the order of a contracted index is free as long as both operands agree, so a
+// lane reads 16 contiguous bytes of a row and its elements are dealt to the
+// fragments' places by renaming registers (keys) or by one byte permute a
+// register (values, whose contracted index runs over tokens).  With tokens and
+// channels on the 16-row side, 8 query heads fill the 8-column side.  P^T goes
+// from accumulator to operand layout by movmatrix.  mma.sync and not tcgen05:
+// 8- and 4-bit rows have to pass through registers to become 16-bit operands,
+// and the tensor work is a small part of the time.  Copies by lanes and not by
+// TMA: row gathers and bulk copies take their operands from uniform registers,
+// so a warp that starts one for every four rows runs a loop of some 15
+// instructions for each; measured, that cost more than it saved (4-bit rows,
+// 64 rows up to 16384 tokens: 231 us against 186 us with loads into registers).
+//
+// Order of tokens.  Place r = 0..7 of the contracted index holds token r / 2
+// (r even) or 4 + r / 2 (r odd) of its 8, so that a lane quarter's value rows
+// are q, q + 4, q + 8, q + 12 and the swizzles below keep every read of shared
+// memory free of bank conflicts.  Key rows and notes lie in the places' order,
+// value rows in the tokens'.
+//
+// 8- and 4-bit rows: a key's power-of-two scale multiplies its score; a
+// value's enters the running maximum, so that the weight that is rounded to
+// f16 is p_j = 2^(x_j + ev_j - m) <= 1 whatever the scales are, and the sum
+// of the softmax takes p_j 2^-ev_j in fp32.
+//
+// Split.  The tiles of all rows and key heads are numbered in one line and cut
+// into equal shares, one a CTA (lengths are read on the device, so a captured
+// graph serves any lengths).  A unit (row, head block) inside one share is
+// written directly; one that crosses shares leaves partial sums that
+// join_kernel adds in order.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include <atomic>
+
+#include "ft_attn_args.cuh"
+
+namespace ft {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kSmemSm = 227 * 1024;  // of an SM, for its CTAs' dynamic shared memory
+constexpr uint32_t kAll = 0xffffffffu;
+
+// --------------------------------------------------------------- warp helpers ---
+template <bool F16>
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  if (F16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  uint32_t d;
+  if (F16)
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+template <bool F16>
+__device__ __forceinline__ float2 unpack16(uint32_t w) {
+  if (F16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return make_float2(bf16_lo(w), bf16_hi(w));
+}
+
+// The four E4M3 codes of a word as two f16 pairs.
+__device__ __forceinline__ void e4m3x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+
+// N words (1, 2 or 4) of shared memory.
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t p, uint32_t (&w)[N]) {
+  if constexpr (N == 4)
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(p));
+  else if constexpr (N == 2)
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(p));
+  else
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(p));
+}
+
+// 16 bytes from global to shared memory, past L1; `bytes` (16 or 0) of them read, the rest zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy16_or_zero(uint32_t dst, const uint8_t* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+constexpr int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
+
+// How a format's rows are cut, for heads padded to DP channels (channels past
+// D read zeros).  Keys: piece p of a row gives lane quarter q the EK channels
+// p*4*EK + q*EK..; values: piece p gives lane group g the EV channels
+// p*8*EV + g*EV...
+template <int FMT, int DP, int NT>
+struct Deal {
+  static constexpr bool kQuant = FMT == FT_KV_E4M3 || FMT == FT_KV_NVFP4;
+  static constexpr bool kBlocks = FMT == FT_KV_NVFP4;
+  static constexpr bool kF16 = FMT != FT_KV_BF16;  // operand type of the products
+  static constexpr int EK = !kQuant ? 8 : !kBlocks ? 16 : DP % 128 == 0 ? 32 : 16;
+  static constexpr int EV = !kQuant ? 8 : !kBlocks ? (DP % 128 == 0 ? 16 : 8) : DP % 256 == 0 ? 32 : DP % 128 == 0 ? 16 : 8;
+  static constexpr int NK = DP / (4 * EK), NV = DP / (8 * EV);
+  static constexpr int bits = !kQuant ? 16 : kBlocks ? 4 : 8;
+  static constexpr int WK = EK * bits / 32, WV = EV * bits / 32;  // words of a piece
+  static constexpr int MT = DP / 16, H = 8 * NT;
+  static constexpr int RB = DP * bits / 8;          // bytes of a row in shared memory
+  static constexpr int PK = WK * 4, PV = WV * 4;    // bytes of a piece
+  static constexpr bool kSwap = RB % 128 == 0;      // keys: odd places have 64-byte halves swapped
+  static constexpr int KP = kSwap ? 2 : 1;
+  static_assert(!kSwap || PK == 16, "");
+  __device__ static constexpr int key_swizzle(int place) { return kSwap ? (place & 1) << 6 : 0; }
+  __device__ static constexpr int value_swizzle(int token) {
+    return PV == 16 ? (token & 3) << 5 : PV == 8 ? ((token >> 1) & 1) << 5 : 0;
+  }
+  // A step: TS tokens, 2 to 8 KB of keys and values each.
+  static constexpr int TS = RB >= 128 && !kBlocks ? 16 : 32;
+  static constexpr int U = TS / 16;
+  // What a unit costs beside its tiles (queries, merge, output: about 2 us of a
+  // CTA), in tiles.  Without it, shares of many short rows finish last: 64 rows
+  // up to 16384 tokens NVFP4 122 us, with 1, 2, 3, 4 tiles 118, 102, 102, 104
+  // (the last three after other steps); 32 rows up to 8192 bf16 with 1, 2, 3:
+  // 63.7, 63.5, 63.2.
+  static constexpr int kLead = kQuant ? 2 : 3;
+  static constexpr int kSide = TS * RB;          // keys, or values, of a step
+  // The copies of a step: chunk i = 32 c + lane of a side is row i / CPR, bytes 16 (i % CPR)..;
+  // both repeat every CY copies, CR rows further on.
+  static constexpr int CPR = RB / 16, kCopies = TS * CPR / 32;
+  static constexpr int CY = CPR / gcd(32, CPR), CR = 32 * CY / CPR;
+  static_assert(kCopies % CY == 0, "");
+  // Beside a slot's rows, as copied: the words that hold the tokens' exponent
+  // bytes (keys, then values), and the block scales (keys, then values).
+  static constexpr int NBK = DP / 16, VS = TS + 4;
+  static constexpr int kRawBlk = kBlocks ? TS * NBK : 0;
+  static constexpr int kRaw = kQuant ? 2 * TS * 4 + 2 * kRawBlk : 0;
+  // Once a warp, worked out when the step's turn comes: per place (key factor,
+  // value exponent, 2^-value exponent, -), and the block scales as f16 (keys
+  // [place][block], values [block][place]).
+  static constexpr int kTok = kQuant ? TS * 16 : 0;
+  static constexpr int kKeyBlk = kBlocks ? TS * NBK * 2 : 0, kValBlk = kBlocks ? NBK * VS * 2 : 0;
+  static constexpr int kNotes = kTok + kKeyBlk + kValBlk;
+  static constexpr uint32_t kFull = TS == 32 ? 0xffffffffu : (1u << (TS & 31)) - 1;
+  static constexpr int kSlot = 2 * kSide + kRaw;
+  // At a unit's end a warp hands its sums over in the slot that it read last,
+  // kBox head tiles at a time.
+  static constexpr int kBox = 2 * kSide / (MT * 4 * 32 * 4) < NT ? 2 * kSide / (MT * 4 * 32 * 4) : NT;
+  // The queries of a block as operands: a head's row, 16 bytes apart from the next (bank conflicts).
+  static constexpr int kQuery = DP * 2 + 16;
+  // Shared memory beside the ring, for the block_heads of one warp column.
+  static constexpr int kRest = 128 + kWarps * kNotes + kWarps * (H * 8 + 8) + H * (kQuery + 4);
+  // Steps of a warp's ring with so many CTAs an SM.  More CTAs hide more
+  // latency and keep the ALUs of 8- and 4-bit formats busier; the registers of
+  // two head tiles or wide heads allow two or three.
+  static constexpr int slots(int ctas) {
+    const int n = (kSmemSm / ctas - 1024 - kRest) / kWarps / kSlot;
+    return n < 6 ? n : 6;
+  }
+  static constexpr int kMostCtas = DP == 64 ? (NT == 1 ? 4 : 3) : DP * NT <= 128 ? 4 : 2;
+  static constexpr int pick(int ctas) { return ctas == 1 || slots(ctas) >= 2 ? ctas : pick(ctas - 1); }
+  static constexpr int kCtas = pick(kMostCtas);
+  static constexpr int S = slots(kCtas);
+  static constexpr int kRing = kWarps * S * kSlot;
+  static_assert(S >= 2 && 3 * S <= 32 && kBox >= 1 && NT % kBox == 0, "");
+  static_assert(kSlot % 128 == 0 && kNotes % 16 == 0, "");
+};
+
+// The tiles of row t.
+__device__ __forceinline__ RowSpan span_of(const AttnArgs& a, int t) {
+  return row_span(a.lens[t], a.window, a.most, a.tile);
+}
+
+// Two output values in one word.
+__device__ __forceinline__ uint32_t pack_out(const AttnArgs& a, float x, float y) {
+  return a.q_f16 ? pack16<true>(x, y) : pack16<false>(x, y);
+}
+
+__device__ __forceinline__ void store_lse(const AttnArgs& a, int t, int h, float m, float l) {
+  if (a.lse) a.lse[static_cast<int64_t>(t) * a.Hq + h] = l > 0.f || l != l ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
+// A maximum over nothing: finite, so that 2^(-inf - kLowest) and 2^(kLowest - m) are 0 and not NaN.
+constexpr float kLowest = -3.0e38f;
+__device__ __forceinline__ float weight_of(float m, float M) { return exp2_approx(m - M); }
+
+// The place of a token among its step's (see the order of tokens above), and the token of a place.
+__device__ __forceinline__ constexpr int place_of(int t) { return (t & ~7) + 2 * (t & 3) + ((t >> 2) & 1); }
+__device__ __forceinline__ constexpr int token_at(int r) { return (r & ~7) + 4 * (r & 1) + ((r >> 1) & 3); }
+
+// A warp's way through its CTA's share of the line, unit by unit.
+struct Walk {
+  int t, at, left;   // row, place in the row's line, numbers left in the share
+  UnitPart part;     // what the share holds of the unit
+  int seq;           // the row's sequence
+  int first, base, stop;  // tokens: the first that counts, this warp's next step's, the end
+
+  // The next unit of which the share holds tiles; false at the share's end.  A
+  // row of a bad sequence has no steps.
+  __device__ __forceinline__ bool next(const AttnArgs& a, int offset) {
+    RowSpan s;
+    do {
+      if (left == 0) return false;
+      s = span_of(a, t);
+      while (at >= row_numbers(s.tiles, a.lead, a.units)) {
+        at -= row_numbers(s.tiles, a.lead, a.units);
+        s = span_of(a, ++t);
+      }
+      part = unit_part(at, left, s.tiles, a.lead);
+      at += part.used;
+      left -= part.used;
+    } while (part.tiles == 0);
+    seq = kv_seq(a.kv, t);
+    first = s.first;
+    base = s.begin + part.tile0 * a.tile + offset;
+    stop = min(s.len, s.begin + (part.tile0 + part.tiles) * a.tile);
+    if (static_cast<uint32_t>(seq) >= a.kv.n_seqs) {
+      record_status(a.status, FT_ERR_BAD_ID);
+      stop = 0;
+    }
+    return true;
+  }
+};
+
+// The side of a warp that fills its ring, ahead of the side that computes.  A
+// page is read one step before its use.
+template <typename X>
+struct Feeder {
+  Walk walk;
+  bool more, live;          // a step is prepared; the lane's token counts
+  int32_t page;             // the token's page
+  uint32_t place;           // and its place in it
+  const int32_t* table;     // the unit's sequence's pages
+  uint32_t head_row;        // the unit's key head
+  uint32_t at;              // the slot to fill next
+  uint32_t past;            // of the last steps, three bits each: the lane's token had a row, and that modulo 4
+  // the lane's part of the copies, the same in every step (see Deal): source
+  // chunk, and places in the keys' and the values' side of a slot
+  const uint8_t* src[2][X::CY];
+  uint32_t kdst[X::CY], vdst[X::CY];
+
+  __device__ __forceinline__ void init(const AttnArgs& a, uint32_t ring, int lane) {
+#pragma unroll
+    for (int c = 0; c < X::CY; ++c) {
+      const int row = (c * 32 + lane) / X::CPR, chunk = (c * 32 + lane) % X::CPR;
+      src[0][c] = a.kv.data[0] + chunk * 16;
+      src[1][c] = a.kv.data[1] + chunk * 16;
+      kdst[c] = place_of(row) * X::RB + ((chunk * 16) ^ X::key_swizzle(place_of(row)));
+      vdst[c] = X::kSide + row * X::RB + ((chunk * 16) ^ X::value_swizzle(row));
+    }
+    at = ring;
+    past = 0;
+  }
+
+  // What stays the same over the walk's unit.  Its queries are fetched into L2
+  // on the way: the reads of the cache that follow would hold them up.
+  __device__ __forceinline__ void enter(const AttnArgs& a, int lane) {
+    table = a.kv.pages + walk.seq * a.kv.table_stride;
+    const int kv_head = walk.part.unit / a.blocks;
+    head_row = static_cast<uint32_t>(kv_head) * a.kv.at.head_stride;
+    const int h = (walk.part.unit - kv_head * a.blocks) * a.block_heads + lane;
+    if (lane < a.block_heads && h < a.G) {
+      const uint16_t* row = a.q + static_cast<int64_t>(walk.t) * a.q_tok + static_cast<int64_t>(kv_head * a.G + h) * a.q_head;
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(row));
+      if (X::kQuery > 272) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + (a.kv.D > 128 ? 128 : 0)));
+    }
+  }
+
+  __device__ __forceinline__ void prepare(const AttnArgs& a, int offset, int step, int lane) {
+    while (walk.base >= walk.stop) {
+      if (!walk.next(a, offset)) {
+        more = false;
+        return;
+      }
+      enter(a, lane);
+    }
+    more = true;
+    const int tok = walk.base + lane;
+    live = lane < X::TS && tok >= walk.first && tok < walk.stop;
+    if (live) {
+      const uint32_t p = fast_div(tok, a.kv.at.by_page);
+      place = tok - p * a.kv.at.page_size;
+      page = table[p];
+    }
+    walk.base += step;
+  }
+
+  // The block scales of the lane's token into the slot.  Rows of an odd number
+  // of byte pairs are not word-aligned: read and stored.
+  __device__ __forceinline__ void copy_blocks(const AttnArgs& a, uint32_t row, int lane) {
+    if constexpr (X::kBlocks) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint8_t* from = a.kv.block[j] + static_cast<uint64_t>(row) * (a.kv.D >> 4);
+        const uint32_t to = at + 2 * X::kSide + 2 * X::TS * 4 + j * X::kRawBlk + lane * X::NBK;
+        if (a.kv.D == X::NBK * 16) {
+          if constexpr (X::NBK == 16) {
+            copy16(to, from);
+          } else if constexpr (X::NBK == 8) {
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
+          } else {
+#pragma unroll
+            for (int w = 0; w < X::NBK / 4; ++w)
+              asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + 4 * w), "l"(from + 4 * w) : "memory");
+          }
+        } else {
+#pragma unroll
+          for (int w = 0; w < X::NBK / 2; ++w) {
+            const uint16_t v = 32 * w < a.kv.D ? *reinterpret_cast<const uint16_t*>(from + 2 * w) : 0;
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + 2 * w), "h"(v) : "memory");
+          }
+        }
+      }
+    }
+  }
+
+  // The notes of the step in slot `slot`, S steps after its issue: one lane a token.
+  __device__ __forceinline__ void put_notes(uint32_t slot, uint32_t notes, int lane) const {
+    if constexpr (X::kQuant) {
+      if (lane < X::TS) {
+        const uint32_t was = past >> (3 * (X::S - 1));
+        const bool ok = (was & 4) != 0;
+        const uint32_t raw = slot + 2 * X::kSide, sh = (was & 3) * 8;
+        uint32_t kw, vw;
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(kw) : "r"(raw + lane * 4));
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vw) : "r"(raw + X::TS * 4 + lane * 4));
+        // exponent bytes as writers store them; others are held to 2^-100 .. 2^123
+        const uint32_t kb = min(max((kw >> sh) & 0xffu, 27u), 250u), vb = min(max((vw >> sh) & 0xffu, 27u), 250u);
+        const float ks = ok ? __uint_as_float(kb << 23) : 0.f;
+        const float ev = ok ? static_cast<float>(static_cast<int>(vb) - 127) : -INFINITY;
+        const float iv = ok ? __uint_as_float((254u - vb) << 23) : 0.f;
+        const uint32_t pl = place_of(lane);
+        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(notes + pl * 16), "f"(ks), "f"(ev), "f"(iv), "f"(0.f)
+                     : "memory");
+        if constexpr (X::kBlocks) {
+          const uint32_t ka = notes + X::kTok + pl * (X::NBK * 2);
+          const uint32_t va = notes + X::kTok + X::kKeyBlk + pl * 2;
+#pragma unroll
+          for (int w = 0; w < X::NBK / 4; ++w) {
+            uint32_t kq, vq;
+            const uint32_t from = raw + 2 * X::TS * 4 + lane * X::NBK + w * 4;
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(kq) : "r"(from));
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vq) : "r"(from + X::kRawBlk));
+            uint32_t k2[2], v2[2];
+            e4m3x4(ok ? kq : 0, k2[0], k2[1]);
+            e4m3x4(ok ? vq : 0, v2[0], v2[1]);
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(ka + w * 8), "r"(k2[0]), "r"(k2[1]) : "memory");
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              asm volatile("st.shared.u16 [%0], %1;" ::"r"(va + (4 * w + i) * (X::VS * 2)),
+                           "h"(static_cast<uint16_t>(v2[i >> 1] >> (16 * (i & 1))))
+                           : "memory");
+          }
+        }
+      }
+      __syncwarp();
+    }
+  }
+
+  // The tokens of the oldest step that counts, one bit each.
+  __device__ __forceinline__ uint32_t mask() const { return __ballot_sync(kAll, (past >> (3 * (X::S - 1)) & 4) != 0); }
+
+  // Starts the prepared step's copies into its slot.  One group of copies a
+  // call, whether it has any or not.
+  __device__ __forceinline__ void issue(const AttnArgs& a, uint32_t ring, int lane) {
+    __syncwarp();  // every lane has finished reading the slot
+    past <<= 3;
+    if (more) {
+      uint32_t row = kNoRow;
+      if (live) {
+        row = kv_row(a.kv.at, page, place);
+        if (row == kNoRow)
+          record_status(a.status, FT_ERR_BAD_ID);
+        else
+          row += head_row;
+      }
+      const bool has_row = row != kNoRow;
+      if (has_row) past |= 4 | (row & 3);
+      const uint32_t counts = __ballot_sync(kAll, has_row);
+      // Rows (c / CY) * CR further on move a lane's places by constants: the
+      // order of places and the swizzles only rearrange and join bits, and the
+      // rows of one period are the low bits.
+      if (counts == X::kFull && a.kv.row_bytes == X::RB) {
+#pragma unroll
+        for (int c = 0; c < X::kCopies; ++c) {
+          const int cy = c % X::CY, on = c / X::CY * X::CR;
+          const uint32_t n = __shfl_sync(kAll, row, (cy * 32 + lane) / X::CPR + on);
+          copy16(at + (kdst[cy] ^ X::key_swizzle(place_of(on))) + place_of(on) * X::RB,
+                 src[0][cy] + static_cast<uint64_t>(n) * X::RB);
+          copy16(at + (vdst[cy] ^ X::value_swizzle(on)) + on * X::RB, src[1][cy] + static_cast<uint64_t>(n) * X::RB);
+        }
+      } else {
+#pragma unroll 1
+        for (int i = lane; i < X::kCopies * 32; i += 32) {
+          const int tok = i / X::CPR, chunk = i % X::CPR * 16;
+          const uint32_t n = __shfl_sync(kAll, row, tok);
+          const bool ok = n != kNoRow && chunk < a.kv.row_bytes;
+          const uint64_t off = ok ? static_cast<uint64_t>(n) * a.kv.row_bytes + chunk : 0;
+          const int pl = place_of(tok);
+          copy16_or_zero(at + pl * X::RB + (chunk ^ X::key_swizzle(pl)), a.kv.data[0] + off, ok ? 16 : 0);
+          copy16_or_zero(at + X::kSide + tok * X::RB + (chunk ^ X::value_swizzle(tok)), a.kv.data[1] + off, ok ? 16 : 0);
+        }
+      }
+      if constexpr (X::kQuant) {
+        if (has_row) {
+          // the aligned words around the exponent bytes
+          const uint32_t to = at + 2 * X::kSide + lane * 4;
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(a.kv.scale[0] + (row & ~3u)) : "memory");
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + X::TS * 4), "l"(a.kv.scale[1] + (row & ~3u))
+                       : "memory");
+          copy_blocks(a, row, lane);
+        }
+      }
+      at += X::kSlot;
+      if (at == ring + X::S * X::kSlot) at = ring;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+};
+
+// The weights are rescaled when a score exceeds the running reference by this
+// much (in powers of two), not at every new maximum: 2^4 leaves p far inside f16.
+constexpr float kSlack = 4.f;
+
+template <typename X, bool TWO, int NT>
+__device__ __forceinline__ void add_values(uint32_t at, uint32_t vnotes, int u, int g, int q,
+                                           const uint32_t (&hi)[NT][2], const uint32_t (&lo)[NT][2],
+                                           float (&acc)[X::MT][NT][4]) {
+  const auto step = [&](int mt, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      mma<X::kF16>(acc[mt][n], a0, a1, a2, a3, hi[n][0], hi[n][1]);
+      if (TWO) mma<X::kF16>(acc[mt][n], a0, a1, a2, a3, lo[n][0], lo[n][1]);
+    }
+  };
+#pragma unroll
+  for (int p = 0; p < X::NV; ++p) {
+    uint32_t v[4][X::WV];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      load_words(at + p * (8 * X::PV) + (16 * u + 4 * r) * X::RB, v[r]);
+    const int m0 = p * (X::EV / 2);
+    uint32_t b0 = 0, b1 = 0;  // block scales of the tokens q, q + 4 and q + 8, q + 12
+#pragma unroll
+    for (int w = 0; w < X::WV; ++w) {
+      const uint32_t t0 = v[0][w], t1 = v[1][w], t2 = v[2][w], t3 = v[3][w];
+      if constexpr (!X::kQuant) {
+        step(m0 + w, __byte_perm(t0, t1, 0x5410), __byte_perm(t0, t1, 0x7632), __byte_perm(t2, t3, 0x5410),
+             __byte_perm(t2, t3, 0x7632));
+      } else if constexpr (!X::kBlocks) {
+        // bytes of two tokens side by side, then two conversions a word
+        uint32_t f[8];
+        e4m3x4(__byte_perm(t0, t1, 0x5140), f[0], f[1]);
+        e4m3x4(__byte_perm(t2, t3, 0x5140), f[2], f[3]);
+        e4m3x4(__byte_perm(t0, t1, 0x7362), f[4], f[5]);
+        e4m3x4(__byte_perm(t2, t3, 0x7362), f[6], f[7]);
+        step(m0 + 2 * w, f[0], f[1], f[2], f[3]);
+        step(m0 + 2 * w + 1, f[4], f[5], f[6], f[7]);
+      } else {
+        if (w % 2 == 0) {
+          const int block = X::EV >= 16 ? p * (X::EV / 2) + g * (X::EV / 16) + w / 2 : p * 4 + (g >> 1);
+          const uint32_t na = vnotes + block * (X::VS * 2) + (16 * u + 2 * q) * 2;
+          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(b0) : "r"(na));
+          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(b1) : "r"(na + 16));
+        }
+        // nibbles of two tokens side by side: even elements, odd elements
+        const uint32_t m = 0x0f0f0f0fu;
+        uint32_t e0[4], o0[4], e1[4], o1[4];
+        e2m1x8((t0 & m) | ((t1 & m) << 4), e0);
+        e2m1x8(((t0 >> 4) & m) | (t1 & ~m), o0);
+        e2m1x8((t2 & m) | ((t3 & m) << 4), e1);
+        e2m1x8(((t2 >> 4) & m) | (t3 & ~m), o1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          step(m0 + 4 * w + i, mul_f16x2(e0[i], b0), mul_f16x2(o0[i], b0), mul_f16x2(e1[i], b1), mul_f16x2(o1[i], b1));
+      }
+    }
+  }
+}
+
+// A row that sees nothing: zeros and -inf, and no unit to join.
+__device__ __noinline__ void empty_row(const AttnArgs& a, int t) {
+  const bool f32 = a.out_f32 != 0;
+  for (int i = threadIdx.x; i < a.Hq * (a.kv.D / 2); i += kWarps * 32) {
+    const int h = i / (a.kv.D / 2), d = 2 * (i - h * (a.kv.D / 2));
+    const int64_t to = static_cast<int64_t>(t) * a.out_tok + static_cast<int64_t>(h) * a.out_head + d;
+    if (f32)
+      *reinterpret_cast<float2*>(static_cast<float*>(a.out) + to) = make_float2(0.f, 0.f);
+    else
+      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + to) = 0;
+    if (d == 0) store_lse(a, t, h, -INFINITY, 0.f);
+  }
+  for (int i = threadIdx.x; i < a.units; i += kWarps * 32) a.shared_by[t * a.units + i] = make_int2(1, 0);
+}
+
+// TWO: weights as two 16-bit terms (bf16 caches, and fp32 outputs of the others).
+template <int FMT, int DP, int NT, bool TWO>
+__global__ void __launch_bounds__(kWarps * 32, Deal<FMT, DP, NT>::kCtas) attend_kernel(const __grid_constant__ AttnArgs a) {
+  using X = Deal<FMT, DP, NT>;
+  constexpr int U = X::U, MT = X::MT, H = X::H, S = X::S;
+  extern __shared__ uint8_t smem_raw[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int wh = warp & ((1 << a.warps_h_log2) - 1), wt = warp >> a.warps_h_log2;
+  const int warps_t = kWarps >> a.warps_h_log2;
+
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  const uint32_t ring = smem_u32(smem) + warp * (S * X::kSlot);
+  const uint32_t note = smem_u32(smem) + X::kRing + warp * X::kNotes;
+  uint8_t* rest = smem + X::kRing + kWarps * X::kNotes;
+  float2* sums = reinterpret_cast<float2*>(rest);                              // [warp][H] maximum and sum handed over
+  uint32_t* box_of = reinterpret_cast<uint32_t*>(rest + kWarps * H * 8);         // [warp] where its accumulators are
+  uint8_t* queries = rest + kWarps * (H * 8 + 8);                              // [head][kQuery]
+  float* downs = reinterpret_cast<float*>(queries + a.block_heads * X::kQuery);  // [head] undoes the query's scaling
+
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // this CTA's share of the line, and the row it begins in
+  Walk walk;
+  int share;
+  {
+    int total = 0;
+    for (int t = lane; t < a.T; t += 32) total += row_numbers(span_of(a, t).tiles, a.lead, a.units);
+    total = __reduce_add_sync(kAll, total);
+    share = split_share(total, a.workers);
+    const int from = blockIdx.x * share;
+    // rows that see nothing
+    for (int t = blockIdx.x; t < a.T; t += gridDim.x)
+      if (span_of(a, t).tiles == 0) empty_row(a, t);
+    if (from >= total) return;
+    walk.left = min(share, total - from);
+    int row_at = 0;  // the row's first number
+    for (int t0 = 0;; t0 += 32) {
+      const int n = t0 + lane < a.T ? row_numbers(span_of(a, t0 + lane).tiles, a.lead, a.units) : 0;
+      int upto = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kAll, upto, o);
+        if (lane >= o) upto += y;
+      }
+      const uint32_t past = __ballot_sync(kAll, row_at + upto > from);
+      if (past) {
+        const int i = __ffs(past) - 1;
+        walk.t = t0 + i;
+        walk.at = from - row_at - __shfl_sync(kAll, upto - n, i);
+        break;
+      }
+      row_at += __shfl_sync(kAll, upto, 31);
+    }
+  }
+  walk.base = walk.stop = 0;
+  const int offset = wt * X::TS, step = X::TS * warps_t;
+
+  if (!walk.next(a, offset)) return;  // the share is the lead of a unit that begins in the next
+  Feeder<X> feed;
+  feed.walk = walk;
+  feed.init(a, ring, lane);
+  feed.enter(a, lane);
+  feed.prepare(a, offset, step, lane);
+
+  // places of the lane's pieces in a step's rows
+  uint32_t koff[X::KP];
+#pragma unroll
+  for (int p = 0; p < X::KP; ++p) koff[p] = g * X::RB + ((p * 4 + q) * X::PK ^ X::key_swizzle(g));
+  const uint32_t voff = q * X::RB + (g * X::PV ^ X::value_swizzle(q));
+
+  // The queries of a unit, as loaded: the first unit's before the ring is
+  // filled, for the same reason as in enter().
+  int kv_head, head0;  // the key head, and the unit's first query head in its group
+  const auto query = [&](int h) {
+    uint4 raw = make_uint4(0, 0, 0, 0);
+    if (head0 + h < a.G && lane * 8 < a.kv.D)
+      raw = *reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(walk.t) * a.q_tok +
+                                            static_cast<int64_t>(kv_head * a.G + head0 + h) * a.q_head + lane * 8);
+    return raw;
+  };
+  uint4 early[H / kWarps];
+  const auto enter = [&]() {
+    kv_head = walk.part.unit / a.blocks;
+    head0 = (walk.part.unit - kv_head * a.blocks) * a.block_heads;
+#pragma unroll
+    for (int i = 0; i < H / kWarps; ++i) early[i] = query(warp + i * kWarps);
+  };
+  enter();
+#pragma unroll 1
+  for (int i = 0; i < S - 1; ++i) {
+    feed.issue(a, ring, lane);
+    if (feed.more) feed.prepare(a, offset, step, lane);
+  }
+
+  uint32_t at = ring;  // the slot to read next
+  uint32_t qb[MT][NT][2];
+  float mul[NT][2], acc[MT][NT][4], m[NT][2], l[NT][2];
+#pragma unroll 1
+  while (true) {
+    // Queries as B operands.  Where the products are f16, a head's row is
+    // scaled by a power of two, its largest element to [128, 256): exact,
+    // undone in the scores' factor.
+    const auto place = [&](int h, uint4 raw) {
+      if (X::kF16) {
+        float x[8];
+        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+        float amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 v = a.q_f16 ? unpack16<true>(w[i]) : unpack16<false>(w[i]);
+          x[2 * i] = v.x;
+          x[2 * i + 1] = v.y;
+          amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
+        }
+        // positive floats order as their bits do
+        amax = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(amax)));
+        int e = 134 - static_cast<int>(__float_as_uint(amax) >> 23);
+        e = amax > 0.f && amax <= 3.4028235e38f ? min(max(e, -120), 120) : 0;
+        const float up = __uint_as_float((127 + e) << 23);
+        raw = make_uint4(pack16<true>(x[0] * up, x[1] * up), pack16<true>(x[2] * up, x[3] * up),
+                         pack16<true>(x[4] * up, x[5] * up), pack16<true>(x[6] * up, x[7] * up));
+        if (lane == 0) downs[h] = __uint_as_float((127 - e) << 23);
+      }
+      if (lane * 8 < DP) *reinterpret_cast<uint4*>(queries + h * X::kQuery + lane * 16) = raw;
+    };
+#pragma unroll
+    for (int i = 0; i < H / kWarps; ++i) place(warp + i * kWarps, early[i]);
+#pragma unroll 1
+    for (int h = H + warp; h < a.block_heads; h += kWarps) place(h, query(h));
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const uint8_t* row = queries + (wh * H + n * 8 + g) * X::kQuery;
+#pragma unroll
+      for (int st = 0; st < MT; ++st) {
+        constexpr int E = X::EK / 4;
+        const uint2 b = *reinterpret_cast<const uint2*>(row + 2 * ((st / E) * 4 * X::EK + q * X::EK + (st % E) * 4));
+        qb[st][n][0] = b.x;
+        qb[st][n][1] = b.y;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        mul[n][i] = a.scale_log2 * (X::kF16 ? downs[wh * H + n * 8 + 2 * q + i] : 1.f);
+        m[n][i] = kLowest;
+        l[n][i] = 0.f;
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[mt][n][i] = 0.f;
+    }
+
+    uint32_t last = 0;  // the slot that this unit's last step was read from; 0: none yet
+#pragma unroll 1
+    for (; walk.base < walk.stop; walk.base += step) {
+      feed.issue(a, ring, lane);  // fills the slot of the step before
+      if (feed.more) feed.prepare(a, offset, step, lane);
+      asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+      __syncwarp();
+      feed.put_notes(at, note, lane);
+
+      // s[u][n] = S^T of 16 tokens: (token g | g + 8) x (head 2q | 2q + 1)
+      float s[U][NT][4];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[u][n][i] = 0.f;
+#pragma unroll
+        for (int p = 0; p < X::NK; ++p) {
+          uint32_t f[2][X::EK / 2];  // 16-bit pairs of rows g and g + 8
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            uint32_t k[X::WK];
+            load_words(at + (p / X::KP) * (X::KP * 4 * X::PK) + koff[p % X::KP] + (16 * u + 8 * r) * X::RB, k);
+            if constexpr (!X::kQuant) {
+#pragma unroll
+              for (int w = 0; w < X::WK; ++w) f[r][w] = k[w];
+            } else if constexpr (!X::kBlocks) {
+#pragma unroll
+              for (int w = 0; w < X::WK; ++w) e4m3x4(k[w], f[r][2 * w], f[r][2 * w + 1]);
+            } else {
+              uint32_t b2;  // the lane's block scales: one or two
+              const uint32_t na = note + X::kTok + (16 * u + 8 * r + g) * (X::NBK * 2) + (p * 4 + q) * (X::EK / 8);
+              if (X::EK == 32) {
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(b2) : "r"(na));
+              } else {
+                uint16_t b1;
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(b1) : "r"(na));
+                b2 = b1;
+              }
+#pragma unroll
+              for (int w = 0; w < X::WK; ++w) {
+                uint32_t h[4];
+                e2m1x8(k[w], h);
+                const uint32_t b = __byte_perm(b2, 0, w < 2 ? 0x1010 : 0x3232);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[r][4 * w + i] = mul_f16x2(h[i], b);
+              }
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < X::EK / 4; ++i)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              const int st = p * (X::EK / 4) + i;
+              mma<X::kF16>(s[u][n], f[0][2 * i], f[1][2 * i], f[0][2 * i + 1], f[1][2 * i + 1], qb[st][n][0],
+                           qb[st][n][1]);
+            }
+        }
+      }
+
+      // scores in powers of two, with the value's exponent; masked tokens -inf
+      float iv[U][2];
+      bool more = false;
+      const uint32_t mask = X::kQuant ? 0 : feed.mask();
+      const bool part = !X::kQuant && mask != X::kFull;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float ks = 1.f, ev = 0.f, none;
+          iv[u][r] = 1.f;
+          if constexpr (X::kQuant)
+            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(ks), "=f"(ev), "=f"(iv[u][r]), "=f"(none)
+                         : "r"(note + (16 * u + 8 * r + g) * 16));
+          const bool ok = (mask >> token_at(16 * u + 8 * r + g)) & 1;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float& x = s[u][n][2 * r + i];
+              x = X::kQuant ? fmaf(x * ks, mul[n][i], ev) : x * mul[n][i];
+              if (part) x = ok ? x : -INFINITY;
+              more |= x > m[n][i] + kSlack;
+            }
+        }
+      if (__any_sync(kAll, more)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float top = m[n][i];
+#pragma unroll
+            for (int u = 0; u < U; ++u) top = fmaxf(top, fmaxf(s[u][n][i], s[u][n][2 + i]));
+            top = fmaxf(top, __shfl_xor_sync(kAll, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(kAll, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(kAll, top, 16));
+            const float c = weight_of(m[n][i], top);
+            m[n][i] = top;
+            l[n][i] *= c;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              acc[mt][n][i] *= c;
+              acc[mt][n][2 + i] *= c;
+            }
+          }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        uint32_t hi[NT][2], lo[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float p0 = exp2_approx(s[u][n][2 * r] - m[n][0]), p1 = exp2_approx(s[u][n][2 * r + 1] - m[n][1]);
+            if (X::kQuant) {
+              l[n][0] = fmaf(p0, iv[u][r], l[n][0]);
+              l[n][1] = fmaf(p1, iv[u][r], l[n][1]);
+            } else {
+              l[n][0] += p0;
+              l[n][1] += p1;
+            }
+            const uint32_t h = pack16<X::kF16>(p0, p1);
+            hi[n][r] = transpose8x8(h);
+            lo[n][r] = 0;
+            if (TWO) {
+              const float2 back = unpack16<X::kF16>(h);
+              lo[n][r] = transpose8x8(pack16<X::kF16>(p0 - back.x, p1 - back.y));
+            }
+          }
+        }
+        const uint32_t vnotes = note + X::kTok + X::kKeyBlk;
+        add_values<X, TWO, NT>(at + X::kSide + voff, vnotes, u, g, q, hi, lo, acc);
+      }
+
+      last = at;
+      at += X::kSlot;
+      if (at == ring + S * X::kSlot) at = ring;
+    }
+
+    // The unit's end: the warps' sums meet in shared memory, and each warp
+    // joins and writes a part of the channels.  A warp with steps has read a
+    // slot, which is not filled again before the next unit; one without has
+    // nothing to add.
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        l[n][i] += __shfl_xor_sync(kAll, l[n][i], 4);
+        l[n][i] += __shfl_xor_sync(kAll, l[n][i], 8);
+        l[n][i] += __shfl_xor_sync(kAll, l[n][i], 16);
+      }
+      if (g < 2) sums[warp * H + n * 8 + 2 * q + g] = make_float2(g ? m[n][1] : m[n][0], g ? l[n][1] : l[n][0]);
+    }
+    if (lane == 0) box_of[warp] = last;
+    const bool whole = walk.part.rest == 0 && walk.part.tile0 == 0;
+    if (threadIdx.x == 0 && walk.part.tile0 == 0)
+      a.shared_by[walk.t * a.units + walk.part.unit] =
+          whole ? make_int2(1, 0) : make_int2(blockIdx.x, blockIdx.x + (walk.part.rest + share - 1) / share);
+    const int part = blockIdx.x * 2 + (walk.part.tile0 == 0 ? 1 : 0);
+    const bool f32 = !whole || (X::kF16 ? TWO : a.out_f32 != 0);
+#pragma unroll
+    for (int n0 = 0; n0 < NT; n0 += X::kBox) {
+      if (n0 > 0) __syncthreads();  // the tiles before have been read
+      if (last != 0) {
+#pragma unroll
+        for (int n = n0; n < n0 + X::kBox; ++n)
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(last + ((n - n0) * MT + mt) * 512 + lane * 16),
+                         "f"(acc[mt][n][0]), "f"(acc[mt][n][1]), "f"(acc[mt][n][2]), "f"(acc[mt][n][3])
+                         : "memory");
+      }
+      __syncthreads();
+#pragma unroll
+      for (int n = n0; n < n0 + X::kBox; ++n) {
+        // the warps of this column: their weights for the heads 2q and 2q + 1
+        float M[2], L[2] = {0.f, 0.f}, y[kWarps][2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          M[i] = kLowest;
+          for (int w = 0; w < warps_t; ++w) M[i] = fmaxf(M[i], sums[((w << a.warps_h_log2) | wh) * H + n * 8 + 2 * q + i].x);
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            y[w][i] = 0.f;
+            if (w < warps_t) {
+              const float2 o = sums[((w << a.warps_h_log2) | wh) * H + n * 8 + 2 * q + i];
+              y[w][i] = weight_of(o.x, M[i]);
+              L[i] += o.y * y[w][i];
+            }
+          }
+        }
+        const int h0 = wh * H + n * 8 + 2 * q;  // in the block
+        float norm[2];
+        float* out32[2];
+        uint16_t* out16[2];
+        bool live[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int hq = kv_head * a.G + head0 + h0 + i;
+          const int64_t to = static_cast<int64_t>(walk.t) * a.out_tok + static_cast<int64_t>(hq) * a.out_head;
+          live[i] = head0 + h0 + i < a.G;
+          norm[i] = !whole ? 1.f : L[i] == 0.f ? 0.f : 1.f / L[i];
+          out32[i] = whole ? static_cast<float*>(a.out) + to
+                           : a.part_o + (static_cast<int64_t>(part) * a.block_heads + h0 + i) * DP;
+          out16[i] = static_cast<uint16_t*>(a.out) + to;
+          if (g == 0 && wt == 0 && live[i]) {
+            if (whole)
+              store_lse(a, walk.t, hq, M[i], L[i]);
+            else
+              a.part_ml[part * a.block_heads + h0 + i] = make_float2(M[i], L[i]);
+          }
+        }
+#pragma unroll 1
+        for (int mt = wt; mt < MT; mt += warps_t) {
+          float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            const uint32_t box = w < warps_t ? box_of[(w << a.warps_h_log2) | wh] : 0;
+            if (box != 0) {
+              float o[4];
+              asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                           : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3])
+                           : "r"(box + ((n - n0) * MT + mt) * 512 + lane * 16));
+#pragma unroll
+              for (int i = 0; i < 4; ++i) c[i] = fmaf(o[i], y[w][i & 1], c[i]);
+            }
+          }
+          const int d = (mt / (X::EV / 2)) * 8 * X::EV + g * X::EV + 2 * (mt % (X::EV / 2));
+          if (whole && d >= a.kv.D) continue;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (!live[i]) continue;
+            if (f32)
+              *reinterpret_cast<float2*>(out32[i] + d) = make_float2(c[i] * norm[i], c[2 + i] * norm[i]);
+            else
+              *reinterpret_cast<uint32_t*>(out16[i] + d) = pack_out(a, c[i] * norm[i], c[2 + i] * norm[i]);
+          }
+        }
+      }
+    }
+    if (!walk.next(a, offset)) break;
+    enter();
+    __syncthreads();  // the unit has been handed over: its slots and queries are free
+  }
+}
+
+// ------------------------------------------------------------------ host side ---
+template <int FMT, int DP, int NT, bool TWO>
+ft_status launch(AttnArgs& a, cudaStream_t s) {
+  using X = Deal<FMT, DP, NT>;
+  const auto kernel = attend_kernel<FMT, DP, NT, TWO>;
+  // heads past one warp column's: their queries beside the ring
+  const int smem = X::kRing + X::kRest + (a.block_heads - X::H) * (X::kQuery + 4);
+  ft_status st = ensure_dyn_smem(reinterpret_cast<const void*>(kernel), smem, "attn_decode");
+  if (st != FT_OK) return st;
+  static std::atomic<int> resident[3];  // CTAs an SM holds, by warp columns
+  std::atomic<int>& held = resident[a.warps_h_log2];
+  int r = held.load(std::memory_order_relaxed);
+  if (r == 0) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&r, kernel, kWarps * 32, smem) != cudaSuccess || r < 1)
+      return fail(FT_ERR_CUDA, "attn_decode: %s", cudaGetErrorString(cudaGetLastError()));
+    held.store(r, std::memory_order_relaxed);
+  }
+  a.tile = X::TS * (kWarps >> a.warps_h_log2);
+  a.lead = X::kLead;
+  const int64_t longest = a.window > 0 && a.window < a.most ? a.window + 15 : a.most;
+  const int64_t most_tiles = ((longest + a.tile - 1) / a.tile + a.lead) * a.units * a.T;
+  // the line's numbers are 32-bit in the kernel
+  if (most_tiles >= (1ll << 31) - kMaxWorkers) return fail(FT_ERR_UNSUPPORTED, "attn_decode: rows times pages too large");
+  int64_t workers = static_cast<int64_t>(device_sm_count()) * r;
+  if (workers > kMaxWorkers) workers = kMaxWorkers;
+  if (workers > most_tiles) workers = most_tiles;
+  a.workers = static_cast<int>(workers);
+  return launch_pdl(kernel, dim3(a.workers), kWarps * 32, smem, s, a, "attn_decode");
+}
+
+template <int FMT, bool TWO>
+ft_status launch_shape(AttnArgs& a, const AttnShape& sh, cudaStream_t s) {
+  switch (sh.DP) {
+    case 64: return sh.NT == 2 ? launch<FMT, 64, 2, TWO>(a, s) : launch<FMT, 64, 1, TWO>(a, s);
+    case 128: return sh.NT == 2 ? launch<FMT, 128, 2, TWO>(a, s) : launch<FMT, 128, 1, TWO>(a, s);
+    case 192: return launch<FMT, 192, 1, TWO>(a, s);
+    default: return launch<FMT, 256, 1, TWO>(a, s);
+  }
+}
+
+}  // namespace
+}  // namespace ft

@@ -1,0 +1,66 @@
+// ft_attn_args.cuh -- what attn.cu and the attention kernels share: the
+// arguments, the shapes, and the launch of each format's kernel.
+#pragma once
+
+#include "ft_async.cuh"
+#include "ft_kv.cuh"
+
+namespace ft {
+
+constexpr int kMaxWorkers = 1024;  // CTAs of one call (sizes the workspace)
+
+struct AttnArgs {
+  KvView kv;
+  const uint16_t* q;
+  int64_t q_tok, q_head;
+  void* out;
+  int64_t out_tok, out_head;
+  float* lse;
+  const int32_t* lens;
+  float* part_o;   // [worker][2][heads of a block][D padded]
+  float2* part_ml;  // [worker][2][heads of a block] (maximum, sum)
+  int2* shared_by;  // [row][unit] the first and the last worker of a unit that crossed shares; (1, 0) of any other
+  float scale_log2;
+  int32_t window, T, Hq, G;
+  int32_t units;         // head blocks of a row: Hkv * blocks
+  int32_t blocks;        // head blocks of a key head
+  int32_t warps_h_log2;  // warps of a CTA over head tiles; the others over tokens
+  int32_t block_heads;   // heads of a block
+  int32_t tile;          // tokens of a CTA's tile
+  int32_t lead;          // numbers of a unit in the line before those of its tiles
+  int32_t most;          // max_pages * page_size
+  int32_t q_f16, out_f32;
+  int32_t workers;
+  int32_t* status;
+};
+
+struct AttnShape {
+  int DP, NT;        // channels padded to 64s; 8-head column tiles of a warp
+  int warps_h_log2, block_heads, blocks;
+};
+
+// The kernel of each cache format; sets a.tile and a.workers.
+ft_status attend_bf16(AttnArgs& a, const AttnShape& sh, cudaStream_t s);
+ft_status attend_f16(AttnArgs& a, const AttnShape& sh, cudaStream_t s);
+ft_status attend_e4m3(AttnArgs& a, const AttnShape& sh, cudaStream_t s);
+ft_status attend_nvfp4(AttnArgs& a, const AttnShape& sh, cudaStream_t s);
+
+// A launch whose grid may start while the one before it on the stream drains;
+// the kernel waits (pdl_wait) before it touches memory.
+template <typename Kernel, typename Args>
+ft_status launch_pdl(Kernel kernel, dim3 grid, int block, size_t smem, cudaStream_t s, const Args& a, const char* what) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, kernel, a);
+  return launch_check(what);
+}
+
+}  // namespace ft

@@ -57,9 +57,10 @@ FT_HD uint32_t kv_row(const KvIndex& x, int32_t page, uint32_t slot) {
 
 // ---- the split of ft_attn_decode -------------------------------------------
 // A row's tokens first..len-1 are cut into tiles of `tile` tokens from the
-// multiple of 16 at or below `first`.  All tiles of all (row, head block) units
-// are numbered row by row, head block by head block; worker c of n takes the
-// numbers [c * share, (c + 1) * share).
+// multiple of 16 at or below `first`.  All (row, head block) units are numbered
+// row by row, head block by head block, in one line: `lead` numbers that stand
+// for what a unit costs beside its tiles, then one for each tile.  Worker c of
+// n takes the numbers [c * share, (c + 1) * share).
 struct RowSpan {
   int32_t begin;  // the first tile's first token (a multiple of 16)
   int32_t first;  // the first token that counts
@@ -78,6 +79,31 @@ FT_HD RowSpan row_span(int32_t len, int32_t window, int64_t most, int32_t tile) 
   return r;
 }
 
-FT_HD int64_t split_share(int64_t total, int64_t workers) { return total > workers ? (total + workers - 1) / workers : 1; }
+FT_HD int32_t split_share(int32_t total, int32_t workers) { return total > workers ? (total + workers - 1) / workers : 1; }
+
+// Numbers of a row of so many tiles and units.
+FT_HD int32_t row_numbers(int32_t tiles, int32_t lead, int32_t units) { return tiles > 0 ? (tiles + lead) * units : 0; }
+
+// What a share that has `left` numbers, the next at place `at` of a row's line,
+// holds of the unit there.
+struct UnitPart {
+  int32_t unit;
+  int32_t used;          // numbers of the share that go to it
+  int32_t tile0, tiles;  // its tiles in the share (none where the share holds of its lead alone)
+  int32_t rest;          // its tiles past the share
+};
+
+FT_HD UnitPart unit_part(int32_t at, int32_t left, int32_t tiles, int32_t lead) {
+  UnitPart p;
+  const int32_t n = tiles + lead;
+  p.unit = at / n;
+  const int32_t from = at - p.unit * n;
+  p.used = n - from < left ? n - from : left;
+  p.tile0 = from > lead ? from - lead : 0;
+  const int32_t end = from + p.used - lead;  // one past its last tile in the share
+  p.tiles = end > p.tile0 ? end - p.tile0 : 0;
+  p.rest = tiles - (end > 0 ? end : 0);
+  return p;
+}
 
 }  // namespace ft

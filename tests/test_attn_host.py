@@ -182,6 +182,11 @@ void span(int len, int window, long most, int tile, int* out) {
   out[0] = r.begin, out[1] = r.first, out[2] = r.len, out[3] = r.tiles;
 }
 long share(long total, long workers) { return split_share(total, workers); }
+int numbers(int tiles, int lead, int units) { return row_numbers(tiles, lead, units); }
+void part(int at, int left, int tiles, int lead, int* out) {
+  const UnitPart p = unit_part(at, left, tiles, lead);
+  out[0] = p.unit, out[1] = p.used, out[2] = p.tile0, out[3] = p.tiles, out[4] = p.rest;
+}
 }
 """)
     so = d / "index.so"
@@ -230,3 +235,46 @@ def test_spans_and_shares_cover_every_token_once(index, tile):
         assert share >= 1 and share * workers >= total
     index.span(2 ** 31 - 1, 0, 2 ** 31 - 4096, tile, out)
     assert out[2] == 2 ** 31 - 4096 and out[3] > 0
+
+
+@pytest.mark.parametrize("lead", [0, 1, 2, 5])
+def test_unit_parts_cover_every_tile_once(index, lead):
+    """Every worker's walk, as the kernel takes it: each tile of each unit once, in order; the worker that holds a
+    unit's first tile knows the last one that holds any, and those in between hold some."""
+    r = np.random.default_rng(lead)
+    out = (ctypes.c_int * 5)()
+    for _ in range(200):
+        T, units = int(r.integers(1, 12)), int(r.integers(1, 6))
+        tiles = [int(x) for x in r.choice([0, 1, 2, 3, 40], T)]
+        numbers = [index.numbers(n, lead, units) for n in tiles]
+        assert numbers == [(n + lead) * units if n else 0 for n in tiles]
+        total, workers = sum(numbers), int(r.choice([1, 3, 16, 64]))
+        share = index.share(total, workers)
+        held = {}
+        for c in range(workers):
+            at, left = c * share, min(share, total - c * share)
+            t = 0
+            while left > 0:
+                while at >= numbers[t]:
+                    at -= numbers[t]
+                    t += 1
+                index.part(at, left, tiles[t], lead, out)
+                unit, used, tile0, n, rest = out
+                assert 0 < used <= left and 0 <= unit < units
+                at += used
+                left -= used
+                if n:
+                    held.setdefault((t, unit), []).append((c, tile0, n, rest))
+        for t in range(T):
+            for u in range(units):
+                parts = held.get((t, u), [])
+                assert bool(parts) == bool(tiles[t])
+                done = 0
+                for i, (c, tile0, n, rest) in enumerate(parts):
+                    assert tile0 == done and rest == tiles[t] - tile0 - n
+                    done += n
+                    assert c == parts[0][0] + i
+                assert done == tiles[t]
+                if parts:
+                    c, _, n, rest = parts[0]
+                    assert parts[-1][0] == c + -(-rest // share)
