@@ -44,6 +44,13 @@ Stream orchestration only: every step is a call into libft_moe.so.
   allocation or a refused rebuild leaves the running cache untouched
   ("FreeToken 딥다이브", design pattern 7: validate before destroy;
   "FreeToken: 让消费级电脑跑起 284B MoE", sec. 7).
+
+* DecodeAttention runs the attention that stands before a decode layer call:
+  the new tokens' keys and values go into the paged cache (rotated and
+  quantised in the same launch, with their queries), then each token attends
+  over its sequence's pages.  With DecodeLayer it makes up a decoder block's
+  step, captured into one CUDA graph that serves growing sequences
+  (examples/decoder_block.py).
 """
 
 from __future__ import annotations
@@ -124,6 +131,46 @@ class DecodeLayer:
         main.wait_event(self.ev_join)
         merge_partials(self.part_cache, self.part_host, out, stream=main)
         return out
+
+
+class DecodeAttention:
+    """Buffers for the attention of T new tokens a step (allocated once, so that
+    steps can be captured in a CUDA graph): token t belongs to row t of the page
+    table, or to sequence seq[t]."""
+
+    def __init__(self, cache, Hq: int, T: int, rope=None, window: int = 0, scale: float | None = None, dtype=None,
+                 device="cuda"):
+        import torch
+
+        from . import attention as att
+
+        self.cache, self.Hq, self.T, self.rope, self.window, self.scale = cache, Hq, T, rope, window, scale
+        dtype = dtype or torch.bfloat16
+        D = cache.D
+        self.q = torch.empty((T, Hq, D), dtype=dtype, device=device)
+        self.out = torch.empty((T, Hq, D), dtype=dtype, device=device)
+        self.lens = torch.empty(T, dtype=torch.int32, device=device)
+        self.ws = torch.empty(att.attn_decode_workspace(T, Hq, cache.Hkv, D), dtype=torch.uint8, device=device)
+        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+
+    def __call__(self, qkv, pages, pos, seq=None):
+        """qkv [T, (Hq + 2 Hkv) D]: one projection's row of queries, keys, values; pos [T] int32: the new tokens'
+        positions, that is the tokens cached before them -> [T, Hq D], on the current stream."""
+        from . import attention as att
+
+        T, Hq, Hkv, D = self.T, self.Hq, self.cache.Hkv, self.cache.D
+        heads = qkv.view(T, Hq + 2 * Hkv, D)
+        q, k, v = heads[:, :Hq], heads[:, Hq:Hq + Hkv], heads[:, Hq + Hkv:]
+        if self.rope is None:
+            att.kv_append(self.cache, k, v, pages, pos, seq=seq, dev_status=self.status)
+        else:
+            att.kv_append(self.cache, k, v, pages, pos, seq=seq, rope=self.rope, q=q, q_out=self.q,
+                          dev_status=self.status)
+            q = self.q
+        self.lens.copy_(pos).add_(1)
+        att.attn_decode(self.cache, q, pages, self.lens, self.out, self.ws, seq=seq, scale=self.scale,
+                        window=self.window, dev_status=self.status)
+        return self.out.view(T, Hq * D)
 
 
 class SpeculativeDecode:
