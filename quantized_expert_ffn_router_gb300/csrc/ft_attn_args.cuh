@@ -2,7 +2,6 @@
 // arguments, the shapes, and the launch of each format's kernel.
 #pragma once
 
-#include "ft_async.cuh"
 #include "ft_kv.cuh"
 
 namespace ft {
@@ -44,23 +43,5 @@ ft_status attend_bf16(AttnArgs& a, const AttnShape& sh, cudaStream_t s);
 ft_status attend_f16(AttnArgs& a, const AttnShape& sh, cudaStream_t s);
 ft_status attend_e4m3(AttnArgs& a, const AttnShape& sh, cudaStream_t s);
 ft_status attend_nvfp4(AttnArgs& a, const AttnShape& sh, cudaStream_t s);
-
-// A launch whose grid may start while the one before it on the stream drains;
-// the kernel waits (pdl_wait) before it touches memory.
-template <typename Kernel, typename Args>
-ft_status launch_pdl(Kernel kernel, dim3 grid, int block, size_t smem, cudaStream_t s, const Args& a, const char* what) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, kernel, a);
-  return launch_check(what);
-}
 
 }  // namespace ft

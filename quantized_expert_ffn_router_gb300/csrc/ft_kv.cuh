@@ -3,6 +3,7 @@
 // conversions of cached rows.
 #pragma once
 
+#include "ft_async.cuh"
 #include "ft_attn.h"
 #include "ft_common.cuh"
 #include "ft_dequant.cuh"
@@ -46,5 +47,23 @@ ft_status kv_view(const char* what, const ft_kv_cache* c, const ft_page_table* p
                   KvView* out);
 // Strides multiples of `grain` elements, base 16-byte aligned.
 ft_status check_rows(const char* what, const char* name, const ft_rows* r, int64_t grain);
+
+// A launch whose grid may start while the one before it on the stream drains;
+// the kernel waits (pdl_wait) before it touches memory.
+template <typename Kernel, typename Args>
+ft_status launch_pdl(Kernel kernel, dim3 grid, int block, size_t smem, cudaStream_t s, const Args& a, const char* what) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, kernel, a);
+  return launch_check(what);
+}
 
 }  // namespace ft

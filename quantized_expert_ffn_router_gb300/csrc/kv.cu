@@ -358,6 +358,7 @@ __global__ void __launch_bounds__(512, LAY == kAny ? 1 : 2) write_kernel(const _
     }
   };
 
+  pdl_wait();
   Chunks<LAY> next;
   turn_to(r_first);
   load(src, true, next);
@@ -582,9 +583,9 @@ template <int FMT, int DT>
 __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadArgs a) {
   constexpr int W = FMT == FT_KV_NVFP4 ? 2 : FMT == FT_KV_E4M3 ? 4 : 8;  // words of 16 elements
   const int l = threadIdx.x & ((1 << a.lanes_log2) - 1);
-  if (l * 16 >= a.kv.D) return;
   const uint32_t at = (blockIdx.x * 256u + threadIdx.x) >> a.lanes_log2;
-  if (at >= a.rows) return;
+  pdl_wait();
+  if (at >= a.rows || l * 16 >= a.kv.D) return;
   const uint32_t token = fast_div(at, a.by_heads), head = at - token * a.kv.Hkv;
   const int32_t pos = a.pos[token];
   uint32_t row = kNoRow;
@@ -701,29 +702,19 @@ ft_status launch_write(WriteArgs& a, bool interleaved, const char* what, cudaStr
   FT_REQUIRE(groups * a.parts < (1ll << 31), "%s: too many rows", what);
   const unsigned grid = static_cast<unsigned>(groups) * a.parts;
   const size_t smem = static_cast<size_t>(a.batch) * 2 * ((a.half + 31) / 32 * 32) * sizeof(float);
-  if (interleaved || a.rot == 0)
-    write_kernel<F16, FMT, kPairs><<<grid, block, smem, s>>>(a);
-  else if (halves)
-    write_kernel<F16, FMT, kBlocks ? kAny : kHalves><<<grid, block, smem, s>>>(a);
-  else
-    write_kernel<F16, FMT, kAny><<<grid, block, smem, s>>>(a);
-  return launch_check(what);
-}
-
-template <int FMT, int DT>
-void launch_read(const ReadArgs& a, cudaStream_t s) {
-  const uint64_t threads = static_cast<uint64_t>(a.rows) << a.lanes_log2;
-  read_kernel<FMT, DT><<<static_cast<unsigned>((threads + 255) / 256), 256, 0, s>>>(a);
+  const auto kernel = interleaved || a.rot == 0 ? write_kernel<F16, FMT, kPairs>
+                      : halves                  ? write_kernel<F16, FMT, kBlocks ? kAny : kHalves>
+                                                : write_kernel<F16, FMT, kAny>;
+  return launch_pdl(kernel, dim3(grid), block, smem, s, a, what);
 }
 
 template <int FMT>
-void launch_read_dt(const ReadArgs& a, int32_t dtype, cudaStream_t s) {
-  if (dtype == FT_DT_BF16)
-    launch_read<FMT, FT_DT_BF16>(a, s);
-  else if (dtype == FT_DT_F16)
-    launch_read<FMT, FT_DT_F16>(a, s);
-  else
-    launch_read<FMT, FT_DT_F32>(a, s);
+ft_status launch_read(const ReadArgs& a, int32_t dtype, cudaStream_t s) {
+  const uint64_t threads = static_cast<uint64_t>(a.rows) << a.lanes_log2;
+  const auto kernel = dtype == FT_DT_BF16  ? read_kernel<FMT, FT_DT_BF16>
+                      : dtype == FT_DT_F16 ? read_kernel<FMT, FT_DT_F16>
+                                           : read_kernel<FMT, FT_DT_F32>;
+  return launch_pdl(kernel, dim3(static_cast<unsigned>((threads + 255) / 256)), 256, 0, s, a, "kv_gather");
 }
 
 // Every 16 elements of 16-bit rows (D a multiple of 16) are a 32-byte place.
@@ -980,12 +971,11 @@ ft_status ft_kv_gather(const ft_kv_cache* cache_host, const ft_page_table* table
   a.status = dev_status;
   cudaStream_t s = as_stream(stream);
   switch (cache_host->fmt) {
-    case FT_KV_BF16: launch_read_dt<FT_KV_BF16>(a, dtype, s); break;
-    case FT_KV_F16: launch_read_dt<FT_KV_F16>(a, dtype, s); break;
-    case FT_KV_E4M3: launch_read_dt<FT_KV_E4M3>(a, dtype, s); break;
-    default: launch_read_dt<FT_KV_NVFP4>(a, dtype, s); break;
+    case FT_KV_BF16: return launch_read<FT_KV_BF16>(a, dtype, s);
+    case FT_KV_F16: return launch_read<FT_KV_F16>(a, dtype, s);
+    case FT_KV_E4M3: return launch_read<FT_KV_E4M3>(a, dtype, s);
+    default: return launch_read<FT_KV_NVFP4>(a, dtype, s);
   }
-  return launch_check("kv_gather");
 }
 
 }  // extern "C"
