@@ -832,10 +832,17 @@ __global__ void __launch_bounds__(kWarps * 32, Deal<FMT, DP, NT>::kCtas) attend_
       if (at == ring + S * X::kSlot) at = ring;
     }
 
+    // The next unit's queries are requested before this one is handed over.
+    const int t = walk.t, hq0 = kv_head * a.G + head0, heads = min(a.block_heads, a.G - head0);
+    const UnitPart unit = walk.part;
+    const bool more = walk.next(a, offset);
+    if (more) enter();
+
     // The unit's end: the warps' sums meet in shared memory, and each warp
     // joins and writes a part of the channels.  A warp with steps has read a
-    // slot, which is not filled again before the next unit; one without has
-    // nothing to add.
+    // slot, which is not filled again before the next unit.  One without has
+    // nothing to add; then warps after it have no steps either, and its sums
+    // are those of nothing.
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -847,11 +854,8 @@ __global__ void __launch_bounds__(kWarps * 32, Deal<FMT, DP, NT>::kCtas) attend_
       if (g < 2) sums[warp * H + n * 8 + 2 * q + g] = make_float2(g ? m[n][1] : m[n][0], g ? l[n][1] : l[n][0]);
     }
     if (lane == 0) box_of[warp] = last;
-    const bool whole = walk.part.rest == 0 && walk.part.tile0 == 0;
-    if (threadIdx.x == 0 && walk.part.tile0 == 0)
-      a.shared_by[walk.t * a.units + walk.part.unit] =
-          whole ? make_int2(1, 0) : make_int2(blockIdx.x, blockIdx.x + (walk.part.rest + share - 1) / share);
-    const int part = blockIdx.x * 2 + (walk.part.tile0 == 0 ? 1 : 0);
+    const bool whole = unit.rest == 0 && unit.tile0 == 0;
+    const int part = blockIdx.x * 2 + (unit.tile0 == 0 ? 1 : 0);
     const bool f32 = !whole || (X::kF16 ? TWO : a.out_f32 != 0);
 #pragma unroll
     for (int n0 = 0; n0 < NT; n0 += X::kBox) {
@@ -866,75 +870,84 @@ __global__ void __launch_bounds__(kWarps * 32, Deal<FMT, DP, NT>::kCtas) attend_
                          : "memory");
       }
       __syncthreads();
+      // where the column's warps' sums are; the first's in the place of one
+      // that has none (whose weight is 0, or all that there is is zeros)
+      uint32_t box[kWarps];
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const uint32_t own = box_of[(min(w, warps_t - 1) << a.warps_h_log2) | wh], first = box_of[wh];
+        box[w] = (own != 0 && w < warps_t ? own : first) + lane * 16;
+      }
+      const bool any = box_of[wh] != 0;
 #pragma unroll
       for (int n = n0; n < n0 + X::kBox; ++n) {
-        // the warps of this column: their weights for the heads 2q and 2q + 1
-        float M[2], L[2] = {0.f, 0.f}, y[kWarps][2];
+        // the weights of the column's warps for the heads 2q and 2q + 1
+        float M[2], L[2], y[kWarps][2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          M[i] = kLowest;
-          for (int w = 0; w < warps_t; ++w) M[i] = fmaxf(M[i], sums[((w << a.warps_h_log2) | wh) * H + n * 8 + 2 * q + i].x);
+          float2 o[kWarps];
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w)
+            o[w] = sums[((min(w, warps_t - 1) << a.warps_h_log2) | wh) * H + n * 8 + 2 * q + i];
+          M[i] = fmaxf(fmaxf(o[0].x, o[1].x), fmaxf(o[2].x, o[3].x));
+          L[i] = 0.f;
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) {
-            y[w][i] = 0.f;
-            if (w < warps_t) {
-              const float2 o = sums[((w << a.warps_h_log2) | wh) * H + n * 8 + 2 * q + i];
-              y[w][i] = weight_of(o.x, M[i]);
-              L[i] += o.y * y[w][i];
-            }
+            y[w][i] = w < warps_t ? weight_of(o[w].x, M[i]) : 0.f;
+            L[i] = w < warps_t ? fmaf(o[w].y, y[w][i], L[i]) : L[i];
           }
         }
-        const int h0 = wh * H + n * 8 + 2 * q;  // in the block
-        float norm[2];
-        float* out32[2];
-        uint16_t* out16[2];
-        bool live[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int hq = kv_head * a.G + head0 + h0 + i;
-          const int64_t to = static_cast<int64_t>(walk.t) * a.out_tok + static_cast<int64_t>(hq) * a.out_head;
-          live[i] = head0 + h0 + i < a.G;
-          norm[i] = !whole ? 1.f : L[i] == 0.f ? 0.f : 1.f / L[i];
-          out32[i] = whole ? static_cast<float*>(a.out) + to
-                           : a.part_o + (static_cast<int64_t>(part) * a.block_heads + h0 + i) * DP;
-          out16[i] = static_cast<uint16_t*>(a.out) + to;
-          if (g == 0 && wt == 0 && live[i]) {
-            if (whole)
-              store_lse(a, walk.t, hq, M[i], L[i]);
-            else
-              a.part_ml[part * a.block_heads + h0 + i] = make_float2(M[i], L[i]);
-          }
+        const int h = wh * H + n * 8 + 2 * q;  // in the block
+        float norm[2] = {1.f, 1.f};
+        if (whole) {
+          norm[0] = L[0] == 0.f ? 0.f : 1.f / L[0];
+          norm[1] = L[1] == 0.f ? 0.f : 1.f / L[1];
         }
-#pragma unroll 1
+        const int64_t to = whole ? static_cast<int64_t>(t) * a.out_tok + static_cast<int64_t>(hq0 + h) * a.out_head
+                                 : (static_cast<int64_t>(part) * a.block_heads + h) * DP;
+        const int64_t on = whole ? a.out_head : DP;  // to the next head
+        float* out32 = (whole ? static_cast<float*>(a.out) : a.part_o) + to;
+        uint16_t* out16 = static_cast<uint16_t*>(a.out) + to;
+        if (g < 2 && wt == 0 && h + g < heads) {
+          const float mg = g ? M[1] : M[0], lg = g ? L[1] : L[0];
+          if (whole)
+            store_lse(a, t, hq0 + h + g, mg, lg);
+          else
+            a.part_ml[part * a.block_heads + h + g] = make_float2(mg, lg);
+        }
+#pragma unroll 2
         for (int mt = wt; mt < MT; mt += warps_t) {
           float c[4] = {0.f, 0.f, 0.f, 0.f};
+          if (any) {
+            float o[kWarps][4];
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            const uint32_t box = w < warps_t ? box_of[(w << a.warps_h_log2) | wh] : 0;
-            if (box != 0) {
-              float o[4];
+            for (int w = 0; w < kWarps; ++w)
               asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                           : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3])
-                           : "r"(box + ((n - n0) * MT + mt) * 512 + lane * 16));
+                           : "=f"(o[w][0]), "=f"(o[w][1]), "=f"(o[w][2]), "=f"(o[w][3])
+                           : "r"(box[w] + ((n - n0) * MT + mt) * 512));
 #pragma unroll
-              for (int i = 0; i < 4; ++i) c[i] = fmaf(o[i], y[w][i & 1], c[i]);
-            }
+            for (int w = 0; w < kWarps; ++w)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (w < warps_t) c[i] = fmaf(o[w][i], y[w][i & 1], c[i]);
           }
           const int d = (mt / (X::EV / 2)) * 8 * X::EV + g * X::EV + 2 * (mt % (X::EV / 2));
           if (whole && d >= a.kv.D) continue;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            if (!live[i]) continue;
+            if (h + i >= heads) continue;
             if (f32)
-              *reinterpret_cast<float2*>(out32[i] + d) = make_float2(c[i] * norm[i], c[2 + i] * norm[i]);
+              *reinterpret_cast<float2*>(out32 + i * on + d) = make_float2(c[i] * norm[i], c[2 + i] * norm[i]);
             else
-              *reinterpret_cast<uint32_t*>(out16[i] + d) = pack_out(a, c[i] * norm[i], c[2 + i] * norm[i]);
+              *reinterpret_cast<uint32_t*>(out16 + i * on + d) = pack_out(a, c[i] * norm[i], c[2 + i] * norm[i]);
           }
         }
       }
     }
-    if (!walk.next(a, offset)) break;
-    enter();
+    if (threadIdx.x == 0 && unit.tile0 == 0)
+      a.shared_by[t * a.units + unit.unit] =
+          whole ? make_int2(1, 0) : make_int2(blockIdx.x, blockIdx.x + (unit.rest + share - 1) / share);
+    if (!more) break;
     __syncthreads();  // the unit has been handed over: its slots and queries are free
   }
 }
