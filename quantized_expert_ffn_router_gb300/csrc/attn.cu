@@ -43,18 +43,22 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnA
   constexpr int kBatch = kHeads == 1 ? 8 : 2;  // partials in flight
   __shared__ float2 acc_s[kSpread > 1 ? 8 : 1][DP / 2];
   __shared__ float2 ml_s[8];
-  // every CTA waits, whether it has something to add or not: work after this
-  // grid must also come after attend_kernel
-  pdl_wait();
-  const int2 workers = a.shared_by[blockIdx.x];
-  if (workers.y <= workers.x) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int h = blockIdx.y * kHeads + warp / kSpread;
   const int t = blockIdx.x / a.units, unit = blockIdx.x - t * a.units;
   const int kv_head = unit / a.blocks;
   const int hg = (unit - kv_head * a.blocks) * a.block_heads + h;  // in the key head's group
   const bool live = h < a.block_heads && hg < a.G;
-  const int c0 = workers.x, c1 = workers.y;
+  // The workers of the unit, worked out while they are at it: this grid starts
+  // when attend_kernel's CTAs are past their own wait, so the lengths are there.
+  const int tiles = span_of(a, t).tiles;
+  const int share = split_share(numbers_before(a, a.T, lane), a.workers);
+  const int from = numbers_before(a, t, lane) + unit * (tiles + a.lead) + a.lead;  // of its first tile
+  const int c0 = from / share, c1 = (from + tiles - 1) / share;
+  // every CTA waits, whether it has something to add or not: work after this
+  // grid must also come after attend_kernel
+  pdl_wait();
+  if (tiles == 0 || c0 == c1) return;
   float m = kLowest, l = 0.f;
   float2 acc[N];
 #pragma unroll
@@ -174,7 +178,7 @@ extern "C" {
 size_t ft_attn_decode_workspace(int32_t T, int32_t Hq, int32_t Hkv, int32_t D) {
   if (!attn_shape_ok(T, Hq, Hkv, D)) return 0;
   const AttnShape s = shape_of(D, Hq / Hkv);
-  return part_o_bytes(s) + part_ml_bytes(s) + static_cast<size_t>(T) * Hkv * s.blocks * sizeof(int2);
+  return part_o_bytes(s) + part_ml_bytes(s);
 }
 
 ft_status ft_attn_decode(const ft_kv_cache* cache_host, const ft_rows* q_host, int32_t T, int32_t Hq, int32_t dtype,
@@ -211,7 +215,6 @@ ft_status ft_attn_decode(const ft_kv_cache* cache_host, const ft_rows* q_host, i
   a.lens = lens;
   a.part_o = static_cast<float*>(ws);
   a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + part_o_bytes(sh));
-  a.shared_by = reinterpret_cast<int2*>(static_cast<uint8_t*>(ws) + part_o_bytes(sh) + part_ml_bytes(sh));
   a.scale_log2 = scale * 1.4426950408889634f;
   a.window = window;
   a.T = T;

@@ -211,11 +211,6 @@ struct Deal {
   static_assert(kSlot % 128 == 0 && kNotes % 16 == 0, "");
 };
 
-// The tiles of row t.
-__device__ __forceinline__ RowSpan span_of(const AttnArgs& a, int t) {
-  return row_span(a.lens[t], a.window, a.most, a.tile);
-}
-
 // Two output values in one word.
 __device__ __forceinline__ uint32_t pack_out(const AttnArgs& a, float x, float y) {
   return a.q_f16 ? pack16<true>(x, y) : pack16<false>(x, y);
@@ -523,7 +518,7 @@ __device__ __forceinline__ void add_values(uint32_t at, uint32_t vnotes, int u, 
   }
 }
 
-// A row that sees nothing: zeros and -inf, and no unit to join.
+// A row that sees nothing: zeros and -inf.
 __device__ __noinline__ void empty_row(const AttnArgs& a, int t) {
   const bool f32 = a.out_f32 != 0;
   for (int i = threadIdx.x; i < a.Hq * (a.kv.D / 2); i += kWarps * 32) {
@@ -535,7 +530,6 @@ __device__ __noinline__ void empty_row(const AttnArgs& a, int t) {
       *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + to) = 0;
     if (d == 0) store_lse(a, t, h, -INFINITY, 0.f);
   }
-  for (int i = threadIdx.x; i < a.units; i += kWarps * 32) a.shared_by[t * a.units + i] = make_int2(1, 0);
 }
 
 // TWO: weights as two 16-bit terms (bf16 caches, and fp32 outputs of the others).
@@ -562,12 +556,9 @@ __global__ void __launch_bounds__(kWarps * 32, Deal<FMT, DP, NT>::kCtas) attend_
 
   // this CTA's share of the line, and the row it begins in
   Walk walk;
-  int share;
   {
-    int total = 0;
-    for (int t = lane; t < a.T; t += 32) total += row_numbers(span_of(a, t).tiles, a.lead, a.units);
-    total = __reduce_add_sync(kAll, total);
-    share = split_share(total, a.workers);
+    const int total = numbers_before(a, a.T, lane);
+    const int share = split_share(total, a.workers);
     const int from = blockIdx.x * share;
     // rows that see nothing
     for (int t = blockIdx.x; t < a.T; t += gridDim.x)
@@ -944,9 +935,6 @@ __global__ void __launch_bounds__(kWarps * 32, Deal<FMT, DP, NT>::kCtas) attend_
         }
       }
     }
-    if (threadIdx.x == 0 && unit.tile0 == 0)
-      a.shared_by[t * a.units + unit.unit] =
-          whole ? make_int2(1, 0) : make_int2(blockIdx.x, blockIdx.x + (unit.rest + share - 1) / share);
     if (!more) break;
     __syncthreads();  // the unit has been handed over: its slots and queries are free
   }

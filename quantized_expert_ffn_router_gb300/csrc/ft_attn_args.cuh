@@ -18,7 +18,6 @@ struct AttnArgs {
   const int32_t* lens;
   float* part_o;   // [worker][2][heads of a block][D padded]
   float2* part_ml;  // [worker][2][heads of a block] (maximum, sum)
-  int2* shared_by;  // [row][unit] the first and the last worker of a unit that crossed shares; (1, 0) of any other
   float scale_log2;
   int32_t window, T, Hq, G;
   int32_t units;         // head blocks of a row: Hkv * blocks
@@ -32,6 +31,17 @@ struct AttnArgs {
   int32_t workers;
   int32_t* status;
 };
+
+__device__ __forceinline__ RowSpan span_of(const AttnArgs& a, int t) {
+  return row_span(a.lens[t], a.window, a.most, a.tile);
+}
+
+// Numbers of the line that the rows before `rows` take, by one warp.
+__device__ __forceinline__ int numbers_before(const AttnArgs& a, int rows, int lane) {
+  int n = 0;
+  for (int t = lane; t < rows; t += 32) n += row_numbers(span_of(a, t).tiles, a.lead, a.units);
+  return __reduce_add_sync(0xffffffffu, n);
+}
 
 struct AttnShape {
   int DP, NT;        // channels padded to 64s; 8-head column tiles of a warp
