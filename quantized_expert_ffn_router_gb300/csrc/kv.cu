@@ -332,36 +332,40 @@ __global__ void __launch_bounds__(512, LAY == kAny ? 1 : 2) write_kernel(const _
   const int rounds = (rows - r_cta + step - 1) / step;  // the same for every thread of the CTA
   const int r_first = r_cta + (threadIdx.x >> a.lanes_log2);
 
-  // the row of this round: what it is, and where its first token's channels are
-  int r = r_first, kind, h;
+  // The row of this round: what it is, and where its channels are at the
+  // present token.  Lanes past the last row, or past the last channel, load
+  // others again: valid reads, whose results are not stored.
+  int kind, h;
   const uint16_t* src;
   const auto turn_to = [&](int row) {
-    r = row;
+    const int r = min(row, rows - 1);
     kind = r < a.Hq ? 0 : r < a.Hq + a.Hkv ? 1 : 2;
     h = kind == 0 ? r : kind == 1 ? r - a.Hq : r - a.Hq - a.Hkv;
     src = a.in[kind] + static_cast<int64_t>(t0) * a.in_tok[kind] + h * a.in_head[kind];
   };
-  const auto load = [&](const uint16_t* from, bool any, Chunks<LAY>& c) {
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    c.own[0] = c.own[1] = c.other[0] = zero;
-    if (LAY == kAny) c.other[LAY == kAny ? 1 : 0] = zero;
-    if (!any || r >= rows) return;
-    if (LAY != kHalves && has1) {
-      load32(from + c0 * 8, c.own[0], c.own[1], a.wide_in != 0);
+  const int l0 = has0 ? c0 * 8 : 0, l1 = has1 ? c1 * 8 : 0;
+  const int o0 = has0 && c0 < 2 * hc ? (c0 < hc ? c0 + hc : c0 - hc) * 8 : 0;  // the other sides
+  const int o1 = has1 && c1 < 2 * hc ? (c1 < hc ? c1 + hc : c1 - hc) * 8 : 0;
+  const auto load = [&](const uint16_t* from, Chunks<LAY>& c) {
+    if (LAY != kHalves && a.wide_in) {
+      load32(from + l0, c.own[0], c.own[1], true);
     } else {
-      if (has0) c.own[0] = *reinterpret_cast<const uint4*>(from + c0 * 8);
-      if (has1) c.own[1] = *reinterpret_cast<const uint4*>(from + c1 * 8);
+      c.own[0] = *reinterpret_cast<const uint4*>(from + l0);
+      c.own[1] = *reinterpret_cast<const uint4*>(from + l1);
     }
-    if (LAY == kAny && vec && kind < 2) {
-      if (c0 < 2 * hc) c.other[0] = *reinterpret_cast<const uint4*>(from + (c0 < hc ? c0 + hc : c0 - hc) * 8);
-      if (c1 < 2 * hc) c.other[LAY == kAny ? 1 : 0] = *reinterpret_cast<const uint4*>(from + (c1 < hc ? c1 + hc : c1 - hc) * 8);
+    if constexpr (LAY == kAny) {
+      c.other[0] = c.other[1] = make_uint4(0, 0, 0, 0);
+      if (vec) {
+        c.other[0] = *reinterpret_cast<const uint4*>(from + o0);
+        c.other[1] = *reinterpret_cast<const uint4*>(from + o1);
+      }
     }
   };
 
   pdl_wait();
   Chunks<LAY> next;
   turn_to(r_first);
-  load(src, true, next);
+  load(src, next);
 
   if (FMT >= 0 && threadIdx.x < tokens) {
     const int32_t place = a.pos[t0 + threadIdx.x];
@@ -382,42 +386,48 @@ __global__ void __launch_bounds__(512, LAY == kAny ? 1 : 2) write_kernel(const _
   const auto other_sides = [&](const Chunks<LAY>& c, const uint16_t* from, float (&y)[16]) {
     if (vec) {
       unpack8<F16>(c.other[0], y);
-      unpack8<F16>(c.other[LAY == kAny ? 1 : 0], y + 8);
+      unpack8<F16>(c.other[LAY == kAny ? 1 : 0], y + 8);  // of lanes without rotated channels: not used
     } else {
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int ch = (i < 8 ? c0 : c1) * 8 + (i & 7);
-        y[i] = (r < rows && ch < a.rot) ? load_one<F16>(from + (ch < a.half ? ch + a.half : ch - a.half)) : 0.f;
+        y[i] = ch < a.rot ? load_one<F16>(from + (ch < a.half ? ch + a.half : ch - a.half)) : 0.f;
       }
     }
   };
-  // what fp32's rotation of the lane's channels may be off by
-  const auto uncertainty = [&](const Chunks<LAY>& c, const uint16_t* from, bool any, float (&d)[16]) {
-    const float off = any ? 6.7434956e-7f * fabsf(a.mscale) : 0.f;  // 2^-20.5
-    float u[16];
-    unpack8<F16>(c.own[0], u);
-    unpack8<F16>(c.own[1], u + 8);
+  // What fp32's rotation of the lane's channels may be off by: 2^-20.5 (|u| +
+  // |v|) m; that is at most 2^-20 (|x| + |y|) of the rotated pair.
+  const auto uncertainty = [&](const Chunks<LAY>& c, const uint16_t* from, bool any, const float (&x)[16], float (&d)[16]) {
     if (LAY == kAny) {
-      float y[16];
+      const float off = any ? 6.7434956e-7f * fabsf(a.mscale) : 0.f;
+      float u[16], y[16];
+      unpack8<F16>(c.own[0], u);
+      unpack8<F16>(c.own[1], u + 8);
       other_sides(c, from, y);
 #pragma unroll
       for (int i = 0; i < 16; ++i) d[i] = (i < 8 ? c0 : c1) * 8 + (i & 7) < a.rot ? (fabsf(u[i]) + fabsf(y[i])) * off : 0.f;
     } else {
+      const float off = any ? 0x1p-20f : 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int iu = LAY == kPairs ? 2 * i : i, iv = LAY == kPairs ? 2 * i + 1 : i + 8;
         const bool turns_too = LAY == kPairs ? 8 * l + i < a.half : l < hc;
-        d[iu] = d[iv] = turns_too ? (fabsf(u[iu]) + fabsf(u[iv])) * off : 0.f;
+        d[iu] = d[iv] = turns_too ? (fabsf(x[iu]) + fabsf(x[iv])) * off : 0.f;
       }
     }
   };
 
+  const int f0 = LAY == kPairs ? 8 * l : 8 * c0;  // the lane's first frequency, and how many it turns by
+  const int turning = LAY == kPairs ? min(8, a.half - f0) : l < hc ? 8 : 0;
+  const int turn0 = turn_at(f0), turn1 = turn_at(f0 + 4);
+  const bool filled = a.D == (16 << a.lanes_log2);  // every lane has its channels
+
   for (int round = 0; round < rounds; ++round) {
   if (round > 0) {
     turn_to(r_first + round * step);
-    load(src, true, next);
+    load(src, next);
   }
-  const bool live = r < rows;
+  const bool live = r_first + round * step < rows;
   const bool spin = a.rot > 0 && kind < 2;
   const bool exact = kQuant && kind == 1 && spin;
   const int64_t stride = a.in_tok[kind];
@@ -425,35 +435,37 @@ __global__ void __launch_bounds__(512, LAY == kAny ? 1 : 2) write_kernel(const _
   uint16_t* dst_q = a.q_out + static_cast<int64_t>(t0) * a.out_tok + h * a.out_head;
 #pragma unroll 1
   for (int tk = 0; tk < tokens; ++tk, src += stride, dst_q += a.out_tok) {
-    const Chunks<LAY> now = next;
-    load(src + stride, tk + 1 < tokens, next);
-
     const float* cosines = turns + tk * 2 * half_up;
     const float* sines = cosines + half_up;
     float x[16];
-    unpack8<F16>(now.own[0], x);
-    unpack8<F16>(now.own[1], x + 8);
+    unpack8<F16>(next.own[0], x);
+    unpack8<F16>(next.own[1], x + 8);
+    Chunks<LAY> now;  // kAny: the other sides are still to be read
+    if (LAY == kAny) now = next;
+    load(tk + 1 < tokens ? src + stride : src, next);
     if (spin) {
       if (LAY == kPairs || LAY == kHalves) {
         // 8 rotations: channels (2i, 2i + 1), or (i, i + 8)
-        const int f0 = LAY == kPairs ? 8 * l : 8 * c0;
-        const int turning = LAY == kPairs ? min(8, a.half - f0) : l < hc ? 8 : 0;
         if (turning > 0) {
           float cs[8], sn[8];
 #pragma unroll
           for (int i = 0; i < 8; i += 4) {
-            const int at = turn_at(f0 + i);
-            *reinterpret_cast<float4*>(cs + i) = *reinterpret_cast<const float4*>(cosines + at);
-            *reinterpret_cast<float4*>(sn + i) = *reinterpret_cast<const float4*>(sines + at);
+            *reinterpret_cast<float4*>(cs + i) = *reinterpret_cast<const float4*>(cosines + (i ? turn1 : turn0));
+            *reinterpret_cast<float4*>(sn + i) = *reinterpret_cast<const float4*>(sines + (i ? turn1 : turn0));
           }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          const auto spin_one = [&](int i) {
             const int iu = LAY == kPairs ? 2 * i : i, iv = LAY == kPairs ? 2 * i + 1 : i + 8;
-            if (LAY == kHalves || i < turning) {
-              const float u = x[iu], v = x[iv];
-              x[iu] = u * cs[i] - v * sn[i];
-              x[iv] = v * cs[i] + u * sn[i];
-            }
+            const float u = x[iu], v = x[iv];
+            x[iu] = u * cs[i] - v * sn[i];
+            x[iv] = v * cs[i] + u * sn[i];
+          };
+          if (LAY == kHalves || vec) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) spin_one(i);
+          } else {  // the last of the rotated channels
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (i < turning) spin_one(i);
           }
         }
       } else {
@@ -479,7 +491,7 @@ __global__ void __launch_bounds__(512, LAY == kAny ? 1 : 2) write_kernel(const _
         if (live && has1) *reinterpret_cast<uint4*>(dst_q + c1 * 8) = pack8<F16>(x + 8);
       }
     }
-    if (FMT < 0) continue;
+    if (FMT < 0 || __all_sync(0xffffffffu, kind == 0)) continue;
     const uint32_t row0 = rows_s[tk];
     const bool put = live && kind > 0 && row0 != kNoRow;
     if (!__any_sync(0xffffffffu, put)) continue;
@@ -496,6 +508,10 @@ __global__ void __launch_bounds__(512, LAY == kAny ? 1 : 2) write_kernel(const _
       for (int o = lanes >> 1; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       return m;
     };
+    if (!filled) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = (i < 8 ? has0 : has1) ? x[i] : 0.f;
+    }
     float block_max = largest(x), amax = row_largest(block_max);
     int e = row_exponent(amax, top, top_bits);
     Codes code;
@@ -505,7 +521,7 @@ __global__ void __launch_bounds__(512, LAY == kAny ? 1 : 2) write_kernel(const _
       // Both ends; the row's largest is at least the largest pair's size /
       // sqrt 2, so off by at most 2^-19 of itself.
       float d[16], z[16], far = 0.f;
-      uncertainty(now, src, exact, d);
+      uncertainty(now, src, exact, x, d);
 #pragma unroll
       for (int i = 0; i < 16; ++i) far = fmaxf(far, d[i]);
 #pragma unroll
@@ -872,7 +888,7 @@ ft_status ft_rope(const ft_rows* x_host, int32_t T, int32_t heads, int32_t D, in
   a.T = T;
   a.Hq = heads;
   a.D = D;
-  a.wide_in = wide(x_host);
+  a.wide_in = wide(x_host) && D % 16 == 0;
   a.wide_out = wide(out_host);
   const bool pairs = rope_host->interleaved != 0;
   if (dtype == FT_DT_F16) return launch_write<true, -1>(a, pairs, "rope", as_stream(stream));
