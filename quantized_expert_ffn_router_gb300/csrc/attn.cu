@@ -32,10 +32,41 @@ __device__ __forceinline__ void store_lse(const AttnArgs& a, int t, int h, float
   if (a.lse) a.lse[static_cast<int64_t>(t) * a.Hq + h] = l > 0.f || l != l ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
-// Adds the partial sums of unit blockIdx.x, if it crossed shares, in the
-// workers' order.  A CTA takes kHeads heads of the block, 8 / kHeads warps a
-// head (each every so-many-th partial): one head where few units have many
-// partials each (one long row), eight otherwise.
+// Numbers of the line that the rows before `row` take, and all rows, by the
+// whole block.
+struct LineSums {
+  int before, total;
+};
+
+template <int kThreads>
+__device__ __forceinline__ LineSums line_sums(const AttnArgs& a, int row) {
+  __shared__ int2 part_s[kThreads / 32];
+  int before = 0, total = 0;
+  for (int t = threadIdx.x; t < a.T; t += kThreads) {
+    const int n = numbers_of(a, t);
+    total += n;
+    before += t < row ? n : 0;
+  }
+  before = __reduce_add_sync(0xffffffffu, before);
+  total = __reduce_add_sync(0xffffffffu, total);
+  if ((threadIdx.x & 31) == 0) part_s[threadIdx.x >> 5] = make_int2(before, total);
+  __syncthreads();
+  LineSums r = {0, 0};
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    r.before += part_s[w].x;
+    r.total += part_s[w].y;
+  }
+  return r;
+}
+
+// Adds the partial sums of the unit that crosses the end of worker blockIdx.x's
+// share and has its first tile in that share, in the workers' order.  A CTA
+// takes kHeads heads of the block, 8 / kHeads warps a head (each every
+// so-many-th partial): one head where few units have many partials each (one
+// long row), eight otherwise.  Where there are fewer units than workers, CTA
+// (x, y) takes unit x instead: most shares' ends are inside units that began
+// before.
 template <int DP, int kHeads>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int N = DP / 64;           // channel pairs of a lane: 2 * lane + 64 i
@@ -45,20 +76,37 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnA
   __shared__ float2 ml_s[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int h = blockIdx.y * kHeads + warp / kSpread;
-  const int t = blockIdx.x / a.units, unit = blockIdx.x - t * a.units;
+  // Which unit, and its workers, are worked out while they are at it: this grid
+  // starts when attend_kernel's CTAs are past their own wait, so the lengths
+  // are there.
+  int t, unit, c0, c1;
+  if (a.T * a.units <= a.workers) {
+    t = blockIdx.x / a.units;
+    unit = blockIdx.x - t * a.units;
+    const LineSums line = line_sums<256>(a, t);
+    const int tiles = span_of(a, t).tiles, share = split_share(line.total, a.workers);
+    const int from = line.before + unit * (tiles + a.lead) + a.lead;  // of its first tile
+    c0 = from / share;
+    c1 = tiles > 0 ? (from + tiles - 1) / share : c0;
+  } else {
+    const Begin end = begin_of<256>(a, blockIdx.x + 1);
+    t = end.t;
+    c0 = c1 = blockIdx.x;
+    unit = 0;
+    if ((c0 + 1) * end.share < end.total) {
+      const int tiles = span_of(a, t).tiles, n = tiles + a.lead;
+      unit = end.at / n;
+      const int held = end.at - unit * n - a.lead;  // its tiles before the share's end
+      if (held > 0 && held <= end.share) c1 = c0 + (tiles - held + end.share - 1) / end.share;
+    }
+  }
   const int kv_head = unit / a.blocks;
   const int hg = (unit - kv_head * a.blocks) * a.block_heads + h;  // in the key head's group
   const bool live = h < a.block_heads && hg < a.G;
-  // The workers of the unit, worked out while they are at it: this grid starts
-  // when attend_kernel's CTAs are past their own wait, so the lengths are there.
-  const int tiles = span_of(a, t).tiles;
-  const int share = split_share(numbers_before(a, a.T, lane), a.workers);
-  const int from = numbers_before(a, t, lane) + unit * (tiles + a.lead) + a.lead;  // of its first tile
-  const int c0 = from / share, c1 = (from + tiles - 1) / share;
   // every CTA waits, whether it has something to add or not: work after this
   // grid must also come after attend_kernel
   pdl_wait();
-  if (tiles == 0 || c0 == c1) return;
+  if (c0 == c1) return;
   float m = kLowest, l = 0.f;
   float2 acc[N];
 #pragma unroll
@@ -159,7 +207,8 @@ size_t part_ml_bytes(const AttnShape& s) { return static_cast<size_t>(kMaxWorker
 template <int DP>
 ft_status launch_join(const AttnArgs& a, cudaStream_t s) {
   const bool long_rows = a.workers > 8ll * a.T * a.units;  // more than eight partials a unit on average
-  const dim3 grid(a.T * a.units, long_rows ? a.block_heads : a.block_heads / 8);
+  const int units = a.T * a.units;
+  const dim3 grid(units < a.workers ? units : a.workers, long_rows ? a.block_heads : a.block_heads / 8);
   return launch_pdl(long_rows ? join_kernel<DP, 1> : join_kernel<DP, 8>, grid, 256, 0, s, a, "attn_decode join");
 }
 

@@ -557,32 +557,15 @@ __global__ void __launch_bounds__(kWarps * 32, Deal<FMT, DP, NT>::kCtas) attend_
   // this CTA's share of the line, and the row it begins in
   Walk walk;
   {
-    const int total = numbers_before(a, a.T, lane);
-    const int share = split_share(total, a.workers);
-    const int from = blockIdx.x * share;
     // rows that see nothing
     for (int t = blockIdx.x; t < a.T; t += gridDim.x)
       if (span_of(a, t).tiles == 0) empty_row(a, t);
-    if (from >= total) return;
-    walk.left = min(share, total - from);
-    int row_at = 0;  // the row's first number
-    for (int t0 = 0;; t0 += 32) {
-      const int n = t0 + lane < a.T ? row_numbers(span_of(a, t0 + lane).tiles, a.lead, a.units) : 0;
-      int upto = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(kAll, upto, o);
-        if (lane >= o) upto += y;
-      }
-      const uint32_t past = __ballot_sync(kAll, row_at + upto > from);
-      if (past) {
-        const int i = __ffs(past) - 1;
-        walk.t = t0 + i;
-        walk.at = from - row_at - __shfl_sync(kAll, upto - n, i);
-        break;
-      }
-      row_at += __shfl_sync(kAll, upto, 31);
-    }
+    const Begin begin = begin_of<kWarps * 32>(a, blockIdx.x);
+    const int from = blockIdx.x * begin.share;
+    if (from >= begin.total) return;
+    walk.left = min(begin.share, begin.total - from);
+    walk.t = begin.t;
+    walk.at = begin.at;
   }
   walk.base = walk.stop = 0;
   const int offset = wt * X::TS, step = X::TS * warps_t;

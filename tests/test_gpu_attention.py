@@ -110,6 +110,15 @@ def test_many_uneven_rows(att):
     check(att, "bf16", "bf16", "bf16", 64, 2, 4, 16, lens, seed=11)
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_more_units_than_workers(att, fmt):
+    """More (row, key head) units than the grid has CTAs: shares hold many units, and end inside one."""
+    r = np.random.default_rng(5)
+    lens = [int(n) for n in np.exp(r.uniform(0, np.log(90), 700))]
+    lens[10:20], lens[300], lens[699] = [0] * 10, 2500, 0
+    check(att, fmt, "bf16", "bf16", 64, 3, 2, 16, lens, seed=12)
+
+
 @pytest.mark.parametrize("order", ["pshd", "hpsd", "sphd"])
 @pytest.mark.parametrize("fmt", ["f16", "e4m3", "nvfp4"])
 def test_cache_orders(att, fmt, order):
