@@ -178,11 +178,15 @@ FT_API ft_status ft_kv_gather(const ft_kv_cache* cache_host, const ft_page_table
  * natural logarithm of sum_j exp(scale * q . k_j).
  * q: dtype bf16 or f16, equal to the cache's where that is 16-bit; out:
  * out_dtype of q's or FT_DT_F32.  Scores, statistics and sums are fp32; the
- * weights enter the value product as two 16-bit terms (bf16 caches and
+ * weights enter the value product as two 16-bit terms (16-bit caches and
  * fp32 outputs) or one f16 term.
  * ws: device scratch of ft_attn_decode_workspace bytes, 256-byte aligned, of
  * any content; calls that may overlap need separate ones.
- * Limits: Hq a multiple of Hkv, T * Hq < 2^31, T <= 65535.
+ * Limits: Hq a multiple of Hkv, T * Hq < 2^31, T <= 65535.  Work is numbered
+ * in 32 bits: T * Hkv rows of max_pages * page_size tokens (of window + 15 where
+ * that is less; the table's size counts, not the lengths) in tiles of 16 to 128
+ * tokens, for groups of more than 32 query heads once each 32.  From 2^31 tiles
+ * the call is refused with FT_ERR_UNSUPPORTED.
  */
 FT_API size_t ft_attn_decode_workspace(int32_t T, int32_t Hq, int32_t Hkv, int32_t D);
 FT_API ft_status ft_attn_decode(const ft_kv_cache* cache_host, const ft_rows* q_host, int32_t T, int32_t Hq,

@@ -195,8 +195,8 @@ AttnShape shape_of(int D, int G) {
   s.DP = padded(D);
   s.NT = head_tiles(s.DP, G);
   const int H = 8 * s.NT;
-  s.warps_h_log2 = G > 2 * H ? 2 : G > H ? 1 : 0;
-  s.block_heads = H << s.warps_h_log2;
+  s.columns = G > 2 * H ? 4 : G > H ? 2 : 1;
+  s.block_heads = H * s.columns;
   s.blocks = (G + s.block_heads - 1) / s.block_heads;
   return s;
 }
@@ -271,7 +271,6 @@ ft_status ft_attn_decode(const ft_kv_cache* cache_host, const ft_rows* q_host, i
   a.G = Hq / Hkv;
   a.blocks = sh.blocks;
   a.units = Hkv * sh.blocks;
-  a.warps_h_log2 = sh.warps_h_log2;
   a.block_heads = sh.block_heads;
   // token positions stay well inside 31 bits (a tile past the last is computed)
   const int64_t most = static_cast<int64_t>(table_host->max_pages) * cache_host->page_size;

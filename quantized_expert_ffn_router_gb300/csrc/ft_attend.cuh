@@ -67,7 +67,6 @@
 namespace ft {
 namespace {
 
-constexpr int kWarps = 4;
 constexpr int kSmemSm = 227 * 1024;  // of an SM, for its CTAs' dynamic shared memory
 constexpr uint32_t kAll = 0xffffffffu;
 
@@ -151,8 +150,12 @@ constexpr int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
 // D read zeros).  Keys: piece p of a row gives lane quarter q the EK channels
 // p*4*EK + q*EK..; values: piece p gives lane group g the EV channels
 // p*8*EV + g*EV...
-template <int FMT, int DP, int NT>
+// COLS: warps side by side over a block's heads (see the columns above).
+template <int FMT, int DP, int NT, int COLS>
 struct Deal {
+  static constexpr int kWarps = COLS == 1 ? 4 : COLS, kThreads = kWarps * 32;
+  static constexpr int kWarpsT = COLS == 1 ? 4 : 1;  // warps side by side over tokens
+  static constexpr int kRings = kWarpsT, kFill = 32 * COLS;  // threads that fill a ring
   static constexpr bool kQuant = FMT == FT_KV_E4M3 || FMT == FT_KV_NVFP4;
   static constexpr bool kBlocks = FMT == FT_KV_NVFP4;
   static constexpr bool kF16 = FMT != FT_KV_BF16;  // operand type of the products
@@ -181,11 +184,11 @@ struct Deal {
   // 63.7, 63.5, 63.2.
   static constexpr int kLead = kQuant ? 2 : 3;
   static constexpr int kSide = TS * RB;          // keys, or values, of a step
-  // The copies of a step: chunk i = 32 c + lane of a side is row i / CPR, bytes 16 (i % CPR)..;
-  // both repeat every CY copies, CR rows further on.
-  static constexpr int CPR = RB / 16, kCopies = TS * CPR / 32;
-  static constexpr int CY = CPR / gcd(32, CPR), CR = 32 * CY / CPR;
-  static_assert(kCopies % CY == 0, "");
+  // The copies of a step: chunk i = kFill c + filler of a side is row i / CPR, bytes 16 (i % CPR)..;
+  // both repeat every CY copies, CR rows further on.  The last copy may be for some warps only.
+  static constexpr int CPR = RB / 16, kChunks = TS * CPR, kCopies = (kChunks + kFill - 1) / kFill;
+  static constexpr int CY = CPR / gcd(kFill, CPR), CR = kFill * CY / CPR;
+  static_assert(kChunks % 32 == 0 && (kCopies <= CY || (kCopies % CY == 0 && (CR & (CR - 1)) == 0)), "");
   // Beside a slot's rows, as copied: the words that hold the tokens' exponent
   // bytes (keys, then values), and the block scales (keys, then values).
   static constexpr int NBK = DP / 16, VS = TS + 4;
@@ -201,24 +204,27 @@ struct Deal {
   static constexpr int kSlot = 2 * kSide + kRaw;
   // At a unit's end a warp hands its sums over in the slot that it read last,
   // kBox head tiles at a time.
-  static constexpr int kBox = 2 * kSide / (MT * 4 * 32 * 4) < NT ? 2 * kSide / (MT * 4 * 32 * 4) : NT;
+  static constexpr int kBox = COLS > 1 ? NT : 2 * kSide / (MT * 4 * 32 * 4) < NT ? 2 * kSide / (MT * 4 * 32 * 4) : NT;
   // The queries of a block as operands: a head's row, 16 bytes apart from the next (bank conflicts).
   static constexpr int kQuery = DP * 2 + 16;
-  // Shared memory beside the ring, for the block_heads of one warp column.
-  static constexpr int kRest = 128 + kWarps * kNotes + kWarps * (H * 8 + 8) + H * (kQuery + 4);
+  static constexpr int kHeads = COLS * H;  // query heads of a block
+  // Shared memory beside the rings.
+  static constexpr int kRest = 128 + kWarps * kNotes + kWarps * (H * 8 + 8) + kHeads * (kQuery + 4);
   // Steps of a warp's ring with so many CTAs an SM.  More CTAs hide more
   // latency and keep the ALUs of 8- and 4-bit formats busier; the registers of
   // two head tiles or wide heads allow two or three.
+  static constexpr int kMostSlots = COLS == 1 ? 6 : 10, kFewestSlots = COLS == 1 ? 2 : 4;
   static constexpr int slots(int ctas) {
-    const int n = (kSmemSm / ctas - 1024 - kRest) / kWarps / kSlot;
-    return n < 6 ? n : 6;
+    const int n = (kSmemSm / ctas - 1024 - kRest) / kRings / kSlot;
+    return n < kMostSlots ? n : kMostSlots;
   }
-  static constexpr int kMostCtas = DP == 64 ? (NT == 1 ? 4 : 3) : DP * NT <= 128 ? 4 : 2;
-  static constexpr int pick(int ctas) { return ctas == 1 || slots(ctas) >= 2 ? ctas : pick(ctas - 1); }
+  static constexpr int kMostCtas = (DP == 64 ? (NT == 1 ? 4 : 3) : DP * NT <= 128 ? 4 : 2) * 4 / kWarps;
+  static constexpr int pick(int ctas) { return ctas == 1 || slots(ctas) >= kFewestSlots ? ctas : pick(ctas - 1); }
   static constexpr int kCtas = pick(kMostCtas);
   static constexpr int S = slots(kCtas);
-  static constexpr int kRing = kWarps * S * kSlot;
-  static_assert(S >= 2 && 3 * S <= 32 && kBox >= 1 && NT % kBox == 0, "");
+  static constexpr int kRing = kRings * S * kSlot;
+  static_assert(S >= kFewestSlots && 3 * S <= 32 && kBox >= 1 && NT % kBox == 0, "");
+  static constexpr int kEarly = kHeads / kWarps < 4 ? kHeads / kWarps : 4;  // queries that a warp loads at a time
   static_assert(kSlot % 128 == 0 && kNotes % 16 == 0, "");
 };
 
@@ -290,10 +296,10 @@ struct Feeder {
   const uint8_t* src[2][X::CY];
   uint32_t kdst[X::CY], vdst[X::CY];
 
-  __device__ __forceinline__ void init(const AttnArgs& a, uint32_t ring, int lane) {
+  __device__ __forceinline__ void init(const AttnArgs& a, uint32_t ring, int column, int lane) {
 #pragma unroll
     for (int c = 0; c < X::CY; ++c) {
-      const int row = (c * 32 + lane) / X::CPR, chunk = (c * 32 + lane) % X::CPR;
+      const int i = c * X::kFill + column * 32 + lane, row = i / X::CPR, chunk = i % X::CPR;
       src[0][c] = a.kv.data[0] + chunk * 16;
       src[1][c] = a.kv.data[1] + chunk * 16;
       kdst[c] = place_of(row) * X::RB + ((chunk * 16) ^ X::key_swizzle(place_of(row)));
@@ -411,10 +417,10 @@ struct Feeder {
   // The tokens of the oldest step that counts, one bit each.
   __device__ __forceinline__ uint32_t mask() const { return __ballot_sync(kAll, (past >> (3 * (X::S - 1)) & 4) != 0); }
 
-  // Starts the prepared step's copies into its slot.  One group of copies a
-  // call, whether it has any or not.
-  __device__ __forceinline__ void issue(const AttnArgs& a, uint32_t ring, int lane) {
-    __syncwarp();  // every lane has finished reading the slot
+  // Starts the prepared step's copies into its slot, which every thread of the
+  // ring's warps has finished reading.  One group of copies a call, whether it
+  // has any or not.
+  __device__ __forceinline__ void issue(const AttnArgs& a, uint32_t ring, int column, int lane) {
     past <<= 3;
     if (more) {
       uint32_t row = kNoRow;
@@ -434,15 +440,16 @@ struct Feeder {
       if (counts == X::kFull && a.kv.row_bytes == X::RB) {
 #pragma unroll
         for (int c = 0; c < X::kCopies; ++c) {
+          if (X::kCopies * X::kFill > X::kChunks && c * X::kFill + column * 32 >= X::kChunks) break;
           const int cy = c % X::CY, on = c / X::CY * X::CR;
-          const uint32_t n = __shfl_sync(kAll, row, (cy * 32 + lane) / X::CPR + on);
+          const uint32_t n = __shfl_sync(kAll, row, (cy * X::kFill + column * 32 + lane) / X::CPR + on);
           copy16(at + (kdst[cy] ^ X::key_swizzle(place_of(on))) + place_of(on) * X::RB,
                  src[0][cy] + static_cast<uint64_t>(n) * X::RB);
           copy16(at + (vdst[cy] ^ X::value_swizzle(on)) + on * X::RB, src[1][cy] + static_cast<uint64_t>(n) * X::RB);
         }
       } else {
 #pragma unroll 1
-        for (int i = lane; i < X::kCopies * 32; i += 32) {
+        for (int i = column * 32 + lane; i < X::kChunks; i += X::kFill) {
           const int tok = i / X::CPR, chunk = i % X::CPR * 16;
           const uint32_t n = __shfl_sync(kAll, row, tok);
           const bool ok = n != kNoRow && chunk < a.kv.row_bytes;
@@ -453,7 +460,7 @@ struct Feeder {
         }
       }
       if constexpr (X::kQuant) {
-        if (has_row) {
+        if (has_row && column == 0) {
           // the aligned words around the exponent bytes
           const uint32_t to = at + 2 * X::kSide + lane * 4;
           asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(a.kv.scale[0] + (row & ~3u)) : "memory");
@@ -532,7 +539,7 @@ __device__ __forceinline__ void add_values(uint32_t at, uint32_t vnotes, int u, 
 // A row that sees nothing: zeros and -inf.
 __device__ __noinline__ void empty_row(const AttnArgs& a, int t) {
   const bool f32 = a.out_f32 != 0;
-  for (int i = threadIdx.x; i < a.Hq * (a.kv.D / 2); i += kWarps * 32) {
+  for (int i = threadIdx.x; i < a.Hq * (a.kv.D / 2); i += blockDim.x) {
     const int h = i / (a.kv.D / 2), d = 2 * (i - h * (a.kv.D / 2));
     const int64_t to = static_cast<int64_t>(t) * a.out_tok + static_cast<int64_t>(h) * a.out_head + d;
     if (f32)
@@ -543,24 +550,30 @@ __device__ __noinline__ void empty_row(const AttnArgs& a, int t) {
   }
 }
 
-// TWO: weights as two 16-bit terms (bf16 caches, and fp32 outputs of the others).
-template <int FMT, int DP, int NT, bool TWO>
-__global__ void __launch_bounds__(kWarps * 32, Deal<FMT, DP, NT>::kCtas) attend_kernel(const __grid_constant__ AttnArgs a) {
-  using X = Deal<FMT, DP, NT>;
+// TWO: weights as two 16-bit terms.  16-bit caches always: one term would add
+// its rounding to the output's own (f16: 2.4e-4 of the norm where two leave
+// 2.0e-4), and two cost 1% where HBM is the bound (f16, 32 rows up to 8192:
+// 62.5 us against 61.7).  8- and 4-bit caches where the output is fp32: their
+// values are f16 products whose weights, in f16, are eight times finer than a
+// bf16 output.
+template <int FMT, int DP, int NT, int COLS, bool TWO>
+__global__ void __launch_bounds__(Deal<FMT, DP, NT, COLS>::kThreads, Deal<FMT, DP, NT, COLS>::kCtas)
+    attend_kernel(const __grid_constant__ AttnArgs a) {
+  using X = Deal<FMT, DP, NT, COLS>;
+  constexpr int kWarps = X::kWarps, kWarpsT = X::kWarpsT;
   constexpr int U = X::U, MT = X::MT, H = X::H, S = X::S;
   extern __shared__ uint8_t smem_raw[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  const int wh = warp & ((1 << a.warps_h_log2) - 1), wt = warp >> a.warps_h_log2;
-  const int warps_t = kWarps >> a.warps_h_log2;
+  const int wh = COLS > 1 ? warp : 0, wt = COLS > 1 ? 0 : warp;
 
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
-  const uint32_t ring = smem_u32(smem) + warp * (S * X::kSlot);
+  const uint32_t ring = smem_u32(smem) + wt * (S * X::kSlot);
   const uint32_t note = smem_u32(smem) + X::kRing + warp * X::kNotes;
   uint8_t* rest = smem + X::kRing + kWarps * X::kNotes;
   float2* sums = reinterpret_cast<float2*>(rest);                              // [warp][H] maximum and sum handed over
   uint32_t* box_of = reinterpret_cast<uint32_t*>(rest + kWarps * H * 8);         // [warp] where its accumulators are
   uint8_t* queries = rest + kWarps * (H * 8 + 8);                              // [head][kQuery]
-  float* downs = reinterpret_cast<float*>(queries + a.block_heads * X::kQuery);  // [head] undoes the query's scaling
+  float* downs = reinterpret_cast<float*>(queries + X::kHeads * X::kQuery);  // [head] undoes the query's scaling
 
   pdl_wait();
   pdl_launch_dependents();
@@ -571,7 +584,7 @@ __global__ void __launch_bounds__(kWarps * 32, Deal<FMT, DP, NT>::kCtas) attend_
     // rows that see nothing
     for (int t = blockIdx.x; t < a.T; t += gridDim.x)
       if (span_of(a, t).tiles == 0) empty_row(a, t);
-    const Begin begin = begin_of<kWarps * 32>(a, blockIdx.x);
+    const Begin begin = begin_of<X::kThreads>(a, blockIdx.x);
     const int from = blockIdx.x * begin.share;
     if (from >= begin.total) return;
     walk.left = min(begin.share, begin.total - from);
@@ -579,12 +592,12 @@ __global__ void __launch_bounds__(kWarps * 32, Deal<FMT, DP, NT>::kCtas) attend_
     walk.at = begin.at;
   }
   walk.base = walk.stop = 0;
-  const int offset = wt * X::TS, step = X::TS * warps_t;
+  const int offset = wt * X::TS, step = X::TS * kWarpsT;
 
   if (!walk.next(a, offset)) return;  // the share is the lead of a unit that begins in the next
   Feeder<X> feed;
   feed.walk = walk;
-  feed.init(a, ring, lane);
+  feed.init(a, ring, wh, lane);
   feed.enter(a, lane);
   feed.prepare(a, offset, step, lane);
 
@@ -604,17 +617,17 @@ __global__ void __launch_bounds__(kWarps * 32, Deal<FMT, DP, NT>::kCtas) attend_
                                             static_cast<int64_t>(kv_head * a.G + head0 + h) * a.q_head + lane * 8);
     return raw;
   };
-  uint4 early[H / kWarps];
+  uint4 early[X::kEarly];
   const auto enter = [&]() {
     kv_head = walk.part.unit / a.blocks;
     head0 = (walk.part.unit - kv_head * a.blocks) * a.block_heads;
 #pragma unroll
-    for (int i = 0; i < H / kWarps; ++i) early[i] = query(warp + i * kWarps);
+    for (int i = 0; i < X::kEarly; ++i) early[i] = query(warp + i * kWarps);
   };
   enter();
 #pragma unroll 1
   for (int i = 0; i < S - 1; ++i) {
-    feed.issue(a, ring, lane);
+    feed.issue(a, ring, wh, lane);
     if (feed.more) feed.prepare(a, offset, step, lane);
   }
 
@@ -649,10 +662,15 @@ __global__ void __launch_bounds__(kWarps * 32, Deal<FMT, DP, NT>::kCtas) attend_
       }
       if (lane * 8 < DP) *reinterpret_cast<uint4*>(queries + h * X::kQuery + lane * 16) = raw;
     };
-#pragma unroll
-    for (int i = 0; i < H / kWarps; ++i) place(warp + i * kWarps, early[i]);
 #pragma unroll 1
-    for (int h = H + warp; h < a.block_heads; h += kWarps) place(h, query(h));
+    for (int h = warp; h < X::kHeads; h += X::kEarly * kWarps) {
+      if (h > warp) {
+#pragma unroll
+        for (int i = 0; i < X::kEarly; ++i) early[i] = query(h + i * kWarps);
+      }
+#pragma unroll
+      for (int i = 0; i < X::kEarly; ++i) place(h + i * kWarps, early[i]);
+    }
     __syncthreads();
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -679,10 +697,18 @@ __global__ void __launch_bounds__(kWarps * 32, Deal<FMT, DP, NT>::kCtas) attend_
     uint32_t last = 0;  // the slot that this unit's last step was read from; 0: none yet
 #pragma unroll 1
     for (; walk.base < walk.stop; walk.base += step) {
-      feed.issue(a, ring, lane);  // fills the slot of the step before
+      if (COLS > 1) {  // one barrier a step: its copies have landed, and the slot of the step before has been read
+        asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+        __syncthreads();
+      } else {
+        __syncwarp();
+      }
+      feed.issue(a, ring, wh, lane);  // fills the slot of the step before
       if (feed.more) feed.prepare(a, offset, step, lane);
-      asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
-      __syncwarp();
+      if (COLS == 1) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+        __syncwarp();
+      }
       feed.put_notes(at, note, lane);
 
       // s[u][n] = S^T of 16 tokens: (token g | g + 8) x (head 2q | 2q + 1)
@@ -823,108 +849,130 @@ __global__ void __launch_bounds__(kWarps * 32, Deal<FMT, DP, NT>::kCtas) attend_
     const bool more = walk.next(a, offset);
     if (more) enter();
 
-    // The unit's end: the warps' sums meet in shared memory, and each warp
-    // joins and writes a part of the channels.  A warp with steps has read a
-    // slot, which is not filled again before the next unit.  One without has
-    // nothing to add; then warps after it have no steps either, and its sums
-    // are those of nothing.
+    // The unit's end.  A lane has of two heads (8n + 2q, + 1) and 16 channels a
+    // mt the four sums c: (channel d, d + 1) x (head, head + 1).
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         l[n][i] += __shfl_xor_sync(kAll, l[n][i], 4);
         l[n][i] += __shfl_xor_sync(kAll, l[n][i], 8);
         l[n][i] += __shfl_xor_sync(kAll, l[n][i], 16);
       }
-      if (g < 2) sums[warp * H + n * 8 + 2 * q + g] = make_float2(g ? m[n][1] : m[n][0], g ? l[n][1] : l[n][0]);
-    }
-    if (lane == 0) box_of[warp] = last;
     const bool whole = unit.rest == 0 && unit.tile0 == 0;
     const int part = blockIdx.x * 2 + (unit.tile0 == 0 ? 1 : 0);
-    const bool f32 = !whole || (X::kF16 ? TWO : a.out_f32 != 0);
-#pragma unroll
-    for (int n0 = 0; n0 < NT; n0 += X::kBox) {
-      if (n0 > 0) __syncthreads();  // the tiles before have been read
-      if (last != 0) {
-#pragma unroll
-        for (int n = n0; n < n0 + X::kBox; ++n)
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(last + ((n - n0) * MT + mt) * 512 + lane * 16),
-                         "f"(acc[mt][n][0]), "f"(acc[mt][n][1]), "f"(acc[mt][n][2]), "f"(acc[mt][n][3])
-                         : "memory");
+    const bool f32 = !whole || (X::kQuant ? TWO : a.out_f32 != 0);
+    const int64_t on = whole ? a.out_head : DP;  // to the next head
+    const auto place_of_head = [&](int h) {
+      return whole ? static_cast<int64_t>(t) * a.out_tok + static_cast<int64_t>(hq0 + h) * a.out_head
+                   : (static_cast<int64_t>(part) * X::kHeads + h) * DP;
+    };
+    // maxima and sums of the heads h and h + 1; gives what their outputs are multiplied by
+    const auto write_sums = [&](int h, const float (&M)[2], const float (&L)[2], float (&norm)[2]) {
+      norm[0] = !whole ? 1.f : L[0] == 0.f ? 0.f : 1.f / L[0];
+      norm[1] = !whole ? 1.f : L[1] == 0.f ? 0.f : 1.f / L[1];
+      if (g < 2 && wt == 0 && h + g < heads) {
+        const float mg = g ? M[1] : M[0], lg = g ? L[1] : L[0];
+        if (whole)
+          store_lse(a, t, hq0 + h + g, mg, lg);
+        else
+          a.part_ml[part * X::kHeads + h + g] = make_float2(mg, lg);
       }
-      __syncthreads();
-      // where the column's warps' sums are; the first's in the place of one
-      // that has none (whose weight is 0, or all that there is is zeros)
-      uint32_t box[kWarps];
+    };
+    const auto write = [&](int h, int64_t to, int mt, const float (&c)[4], const float (&norm)[2]) {
+      const int d = (mt / (X::EV / 2)) * 8 * X::EV + g * X::EV + 2 * (mt % (X::EV / 2));
+      if (whole && d >= a.kv.D) return;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const uint32_t own = box_of[(min(w, warps_t - 1) << a.warps_h_log2) | wh], first = box_of[wh];
-        box[w] = (own != 0 && w < warps_t ? own : first) + lane * 16;
+      for (int i = 0; i < 2; ++i) {
+        if (h + i >= heads) continue;
+        const int64_t at_d = to + i * on + d;
+        if (f32)
+          *reinterpret_cast<float2*>((whole ? static_cast<float*>(a.out) : a.part_o) + at_d) =
+              make_float2(c[i] * norm[i], c[2 + i] * norm[i]);
+        else
+          *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at_d) = pack_out(a, c[i] * norm[i], c[2 + i] * norm[i]);
       }
-      const bool any = box_of[wh] != 0;
+    };
+    if constexpr (COLS > 1) {  // a warp has its heads' sums
 #pragma unroll
-      for (int n = n0; n < n0 + X::kBox; ++n) {
-        // the weights of the column's warps for the heads 2q and 2q + 1
-        float M[2], L[2], y[kWarps][2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float2 o[kWarps];
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w)
-            o[w] = sums[((min(w, warps_t - 1) << a.warps_h_log2) | wh) * H + n * 8 + 2 * q + i];
-          M[i] = fmaxf(fmaxf(o[0].x, o[1].x), fmaxf(o[2].x, o[3].x));
-          L[i] = 0.f;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            y[w][i] = w < warps_t ? weight_of(o[w].x, M[i]) : 0.f;
-            L[i] = w < warps_t ? fmaf(o[w].y, y[w][i], L[i]) : L[i];
-          }
-        }
+      for (int n = 0; n < NT; ++n) {
         const int h = wh * H + n * 8 + 2 * q;  // in the block
-        float norm[2] = {1.f, 1.f};
-        if (whole) {
-          norm[0] = L[0] == 0.f ? 0.f : 1.f / L[0];
-          norm[1] = L[1] == 0.f ? 0.f : 1.f / L[1];
+        float norm[2];
+        write_sums(h, m[n], l[n], norm);
+        const int64_t to = place_of_head(h);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) write(h, to, mt, acc[mt][n], norm);
+      }
+    } else {
+      // The warps' sums meet in shared memory, and each warp joins and writes a
+      // part of the channels.  A warp with steps has read a slot, which is not
+      // filled again before the next unit.  One without has nothing to add; then
+      // warps after it have no steps either, and its sums are those of nothing.
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        if (g < 2) sums[warp * H + n * 8 + 2 * q + g] = make_float2(g ? m[n][1] : m[n][0], g ? l[n][1] : l[n][0]);
+      if (lane == 0) box_of[warp] = last;
+#pragma unroll
+      for (int n0 = 0; n0 < NT; n0 += X::kBox) {
+        if (n0 > 0) __syncthreads();  // the tiles before have been read
+        if (last != 0) {
+#pragma unroll
+          for (int n = n0; n < n0 + X::kBox; ++n)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+              asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(last + ((n - n0) * MT + mt) * 512 + lane * 16),
+                           "f"(acc[mt][n][0]), "f"(acc[mt][n][1]), "f"(acc[mt][n][2]), "f"(acc[mt][n][3])
+                           : "memory");
         }
-        const int64_t to = whole ? static_cast<int64_t>(t) * a.out_tok + static_cast<int64_t>(hq0 + h) * a.out_head
-                                 : (static_cast<int64_t>(part) * a.block_heads + h) * DP;
-        const int64_t on = whole ? a.out_head : DP;  // to the next head
-        float* out32 = (whole ? static_cast<float*>(a.out) : a.part_o) + to;
-        uint16_t* out16 = static_cast<uint16_t*>(a.out) + to;
-        if (g < 2 && wt == 0 && h + g < heads) {
-          const float mg = g ? M[1] : M[0], lg = g ? L[1] : L[0];
-          if (whole)
-            store_lse(a, t, hq0 + h + g, mg, lg);
-          else
-            a.part_ml[part * a.block_heads + h + g] = make_float2(mg, lg);
+        __syncthreads();
+        // where the warps' sums are; the first's in the place of one that has
+        // none (whose weight is 0, or all that there is is zeros)
+        const uint32_t first = box_of[0];
+        uint32_t box[kWarps];
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const uint32_t own = box_of[w];
+          box[w] = (own != 0 ? own : first) + lane * 16;
         }
-#pragma unroll 2
-        for (int mt = wt; mt < MT; mt += warps_t) {
-          float c[4] = {0.f, 0.f, 0.f, 0.f};
-          if (any) {
-            float o[kWarps][4];
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w)
-              asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                           : "=f"(o[w][0]), "=f"(o[w][1]), "=f"(o[w][2]), "=f"(o[w][3])
-                           : "r"(box[w] + ((n - n0) * MT + mt) * 512));
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w)
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (w < warps_t) c[i] = fmaf(o[w][i], y[w][i & 1], c[i]);
-          }
-          const int d = (mt / (X::EV / 2)) * 8 * X::EV + g * X::EV + 2 * (mt % (X::EV / 2));
-          if (whole && d >= a.kv.D) continue;
+        for (int n = n0; n < n0 + X::kBox; ++n) {
+          // the warps' weights for the heads 2q and 2q + 1
+          float M[2], L[2], y[kWarps][2], norm[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            if (h + i >= heads) continue;
-            if (f32)
-              *reinterpret_cast<float2*>(out32 + i * on + d) = make_float2(c[i] * norm[i], c[2 + i] * norm[i]);
-            else
-              *reinterpret_cast<uint32_t*>(out16 + i * on + d) = pack_out(a, c[i] * norm[i], c[2 + i] * norm[i]);
+            float2 o[kWarps];
+            M[i] = kLowest;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+              o[w] = sums[w * H + n * 8 + 2 * q + i];
+              M[i] = fmaxf(M[i], o[w].x);
+            }
+            L[i] = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+              y[w][i] = weight_of(o[w].x, M[i]);
+              L[i] = fmaf(o[w].y, y[w][i], L[i]);
+            }
+          }
+          const int h = n * 8 + 2 * q;  // in the block
+          write_sums(h, M, L, norm);
+          const int64_t to = place_of_head(h);
+#pragma unroll 2
+          for (int mt = wt; mt < MT; mt += kWarps) {
+            float c[4] = {0.f, 0.f, 0.f, 0.f};
+            if (first != 0) {
+              float o[kWarps][4];
+#pragma unroll
+              for (int w = 0; w < kWarps; ++w)
+                asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                             : "=f"(o[w][0]), "=f"(o[w][1]), "=f"(o[w][2]), "=f"(o[w][3])
+                             : "r"(box[w] + ((n - n0) * MT + mt) * 512));
+#pragma unroll
+              for (int w = 0; w < kWarps; ++w)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) c[i] = fmaf(o[w][i], y[w][i & 1], c[i]);
+            }
+            write(h, to, mt, c, norm);
           }
         }
       }
@@ -935,23 +983,21 @@ __global__ void __launch_bounds__(kWarps * 32, Deal<FMT, DP, NT>::kCtas) attend_
 }
 
 // ------------------------------------------------------------------ host side ---
-template <int FMT, int DP, int NT, bool TWO>
+template <int FMT, int DP, int NT, int COLS, bool TWO>
 ft_status launch(AttnArgs& a, cudaStream_t s) {
-  using X = Deal<FMT, DP, NT>;
-  const auto kernel = attend_kernel<FMT, DP, NT, TWO>;
-  // heads past one warp column's: their queries beside the ring
-  const int smem = X::kRing + X::kRest + (a.block_heads - X::H) * (X::kQuery + 4);
+  using X = Deal<FMT, DP, NT, COLS>;
+  const auto kernel = attend_kernel<FMT, DP, NT, COLS, TWO>;
+  constexpr int smem = X::kRing + X::kRest;
   ft_status st = ensure_dyn_smem(reinterpret_cast<const void*>(kernel), smem, "attn_decode");
   if (st != FT_OK) return st;
-  static std::atomic<int> resident[3];  // CTAs an SM holds, by warp columns
-  std::atomic<int>& held = resident[a.warps_h_log2];
+  static std::atomic<int> held{0};  // CTAs an SM holds
   int r = held.load(std::memory_order_relaxed);
   if (r == 0) {
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&r, kernel, kWarps * 32, smem) != cudaSuccess || r < 1)
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&r, kernel, X::kThreads, smem) != cudaSuccess || r < 1)
       return fail(FT_ERR_CUDA, "attn_decode: %s", cudaGetErrorString(cudaGetLastError()));
     held.store(r, std::memory_order_relaxed);
   }
-  a.tile = X::TS * (kWarps >> a.warps_h_log2);
+  a.tile = X::TS * X::kWarpsT;
   a.lead = X::kLead;
   const int64_t longest = a.window > 0 && a.window < a.most ? a.window + 15 : a.most;
   const int64_t most_tiles = ((longest + a.tile - 1) / a.tile + a.lead) * a.units * a.T;
@@ -961,16 +1007,23 @@ ft_status launch(AttnArgs& a, cudaStream_t s) {
   if (workers > kMaxWorkers) workers = kMaxWorkers;
   if (workers > most_tiles) workers = most_tiles;
   a.workers = static_cast<int>(workers);
-  return launch_pdl(kernel, dim3(a.workers), kWarps * 32, smem, s, a, "attn_decode");
+  return launch_pdl(kernel, dim3(a.workers), X::kThreads, smem, s, a, "attn_decode");
+}
+
+template <int FMT, int DP, int NT, bool TWO>
+ft_status launch_columns(AttnArgs& a, const AttnShape& sh, cudaStream_t s) {
+  if (sh.columns == 4) return launch<FMT, DP, NT, 4, TWO>(a, s);
+  if (sh.columns == 2) return launch<FMT, DP, NT, 2, TWO>(a, s);
+  return launch<FMT, DP, NT, 1, TWO>(a, s);
 }
 
 template <int FMT, bool TWO>
 ft_status launch_shape(AttnArgs& a, const AttnShape& sh, cudaStream_t s) {
   switch (sh.DP) {
-    case 64: return sh.NT == 2 ? launch<FMT, 64, 2, TWO>(a, s) : launch<FMT, 64, 1, TWO>(a, s);
-    case 128: return sh.NT == 2 ? launch<FMT, 128, 2, TWO>(a, s) : launch<FMT, 128, 1, TWO>(a, s);
-    case 192: return launch<FMT, 192, 1, TWO>(a, s);
-    default: return launch<FMT, 256, 1, TWO>(a, s);
+    case 64: return sh.NT == 2 ? launch_columns<FMT, 64, 2, TWO>(a, sh, s) : launch<FMT, 64, 1, 1, TWO>(a, s);
+    case 128: return sh.NT == 2 ? launch_columns<FMT, 128, 2, TWO>(a, sh, s) : launch<FMT, 128, 1, 1, TWO>(a, s);
+    case 192: return launch_columns<FMT, 192, 1, TWO>(a, sh, s);
+    default: return launch_columns<FMT, 256, 1, TWO>(a, sh, s);
   }
 }
 

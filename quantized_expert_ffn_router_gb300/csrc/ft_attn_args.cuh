@@ -22,7 +22,6 @@ struct AttnArgs {
   int32_t window, T, Hq, G;
   int32_t units;         // head blocks of a row: Hkv * blocks
   int32_t blocks;        // head blocks of a key head
-  int32_t warps_h_log2;  // warps of a CTA over head tiles; the others over tokens
   int32_t block_heads;   // heads of a block
   int32_t tile;          // tokens of a CTA's tile
   int32_t lead;          // numbers of a unit in the line before those of its tiles
@@ -88,7 +87,7 @@ __device__ __forceinline__ Begin begin_of(const AttnArgs& a, int c) {
 
 struct AttnShape {
   int DP, NT;        // channels padded to 64s; 8-head column tiles of a warp
-  int warps_h_log2, block_heads, blocks;
+  int columns, block_heads, blocks;  // warps side by side over a block's heads
 };
 
 // The kernel of each cache format; sets a.tile and a.workers.
