@@ -719,6 +719,8 @@ __global__ void __launch_bounds__(Deal<FMT, DP, NT, COLS>::kThreads, Deal<FMT, D
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int i = 0; i < 4; ++i) s[u][n][i] = 0.f;
+        constexpr bool kTwoSums = U == 1;
+        float s2[NT][4] = {};
 #pragma unroll
         for (int p = 0; p < X::NK; ++p) {
           uint32_t f[2][X::EK / 2];  // 16-bit pairs of rows g and g + 8
@@ -757,9 +759,15 @@ __global__ void __launch_bounds__(Deal<FMT, DP, NT, COLS>::kThreads, Deal<FMT, D
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
               const int st = p * (X::EK / 4) + i;
-              mma<X::kF16>(s[u][n], f[0][2 * i], f[1][2 * i], f[0][2 * i + 1], f[1][2 * i + 1], qb[st][n][0],
-                           qb[st][n][1]);
+              mma<X::kF16>(kTwoSums && (i & 1) ? s2[n] : s[u][n], f[0][2 * i], f[1][2 * i], f[0][2 * i + 1], f[1][2 * i + 1],
+                           qb[st][n][0], qb[st][n][1]);
             }
+        }
+        if (kTwoSums) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[u][n][i] += s2[n][i];
         }
       }
 
