@@ -67,13 +67,16 @@ __device__ __forceinline__ LineSums line_sums(const AttnArgs& a, int row) {
 // long row), eight otherwise.  Where there are fewer units than workers, CTA
 // (x, y) takes unit x instead: most shares' ends are inside units that began
 // before.
+template <int kHeads>
+constexpr int kJoinThreads = kHeads == 1 ? 512 : 256;
+
 template <int DP, int kHeads>
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kJoinThreads<kHeads>) join_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int N = DP / 64;           // channel pairs of a lane: 2 * lane + 64 i
-  constexpr int kSpread = 8 / kHeads;  // warps of a head
-  constexpr int kBatch = kHeads == 1 ? 8 : 2;  // partials in flight
-  __shared__ float2 acc_s[kSpread > 1 ? 8 : 1][DP / 2];
-  __shared__ float2 ml_s[8];
+  constexpr int kThreads = kJoinThreads<kHeads>, kSpread = kThreads / 32 / kHeads;  // warps of a head
+  constexpr int kBatch = kHeads == 1 ? (DP <= 128 ? 10 : 6) : 2;  // partials in flight
+  __shared__ float2 acc_s[kSpread > 1 ? kSpread : 1][DP / 2];
+  __shared__ float2 ml_s[kThreads / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int h = blockIdx.y * kHeads + warp / kSpread;
   // Which unit, and its workers, are worked out while they are at it: this grid
@@ -83,13 +86,13 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnA
   if (a.T * a.units <= a.workers) {
     t = blockIdx.x / a.units;
     unit = blockIdx.x - t * a.units;
-    const LineSums line = line_sums<256>(a, t);
+    const LineSums line = line_sums<kThreads>(a, t);
     const int tiles = span_of(a, t).tiles, share = split_share(line.total, a.workers);
     const int from = line.before + unit * (tiles + a.lead) + a.lead;  // of its first tile
     c0 = from / share;
     c1 = tiles > 0 ? (from + tiles - 1) / share : c0;
   } else {
-    const Begin end = begin_of<256>(a, blockIdx.x + 1);
+    const Begin end = begin_of<kThreads>(a, blockIdx.x + 1);
     t = end.t;
     c0 = c1 = blockIdx.x;
     unit = 0;
@@ -209,7 +212,7 @@ ft_status launch_join(const AttnArgs& a, cudaStream_t s) {
   const bool long_rows = a.workers > 8ll * a.T * a.units;  // more than eight partials a unit on average
   const int units = a.T * a.units;
   const dim3 grid(units < a.workers ? units : a.workers, long_rows ? a.block_heads : a.block_heads / 8);
-  return launch_pdl(long_rows ? join_kernel<DP, 1> : join_kernel<DP, 8>, grid, 256, 0, s, a, "attn_decode join");
+  return launch_pdl(long_rows ? join_kernel<DP, 1> : join_kernel<DP, 8>, grid, long_rows ? kJoinThreads<1> : kJoinThreads<8>, 0, s, a, "attn_decode join");
 }
 
 bool attn_shape_ok(int32_t T, int32_t Hq, int32_t Hkv, int32_t D) {
