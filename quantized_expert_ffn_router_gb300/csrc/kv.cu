@@ -1,7 +1,7 @@
 // kv.cu -- rotary positions, and the paged key-value cache's rows written
 // (rotated and quantised on the way) and read back.
 //
-// All three kernels stream: every value is read once and written once, so
+// Both kernels stream: every value is read once and written once, so
 // they are bound by HBM (or, for one token, by the launch and one chain of
 // dependent loads).  A head row is spread over the lanes of part of one warp,
 // 16 elements a lane, so that a row's maximum is a few shuffles and every
@@ -9,10 +9,8 @@
 //
 // What they measured (GPU time in a graph, inputs beyond L2; of 6.70 TB/s):
 //   4099 tokens x 40 heads of 128 rotated, half of each head: 16.2 us (77%);
-//   8192 tokens, 32 + 2 x 8 heads of 128, rotated, into E4M3: 36.5 us (76%),
-//   32 us without the quantising;
-//   16384 tokens x 2 x 8 heads of 128 read back, E4M3 to bf16: 18.5 us (81%);
-//   a torch copy of as many bytes (42 MB each way): 28 us.
+//   8192 tokens, 32 + 2 x 8 heads of 128, rotated, into E4M3: 36.5 us (76%), into bf16 35.6;
+//   16384 tokens x 2 x 8 heads of 128 read back, E4M3 to bf16: 18.3 us (82%).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -213,7 +211,7 @@ __device__ __forceinline__ float finite_abs(float x) {
 
 // ------------------------------------------------------------ rotate, write ---
 enum { kPairs, kHalves, kAny };
-constexpr int kMaxBatch = 8;
+constexpr int kMaxBatch = 16;
 struct WriteArgs {
   KvView kv;
   const uint16_t* in[3];  // q, k, v
@@ -615,71 +613,71 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadA
   if (pos >= 0) row = kv_token_row(a.kv, kv_seq(a.kv, token), pos, l == 0 ? a.status : nullptr);
   uint32_t w[2][W], b[2], e[2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+  for (int j = 0; j < 2; ++j) {
 #pragma unroll
-      for (int i = 0; i < W; ++i) w[j][i] = 0;
-      b[j] = 0;
-      e[j] = 127;
-      if (row == kNoRow || a.out[j] == nullptr) continue;
-      const uint64_t r = row + head * a.kv.at.head_stride;
-      const uint8_t* src = a.kv.data[j] + r * a.kv.row_bytes + l * (W * 4);
-      if constexpr (W == 2) {
-        const uint2 v = *reinterpret_cast<const uint2*>(src);
-        w[j][0] = v.x, w[j][1] = v.y;
-        b[j] = a.kv.block[j][r * (a.kv.D / 16) + l];
-      } else {
-        uint4 v, u;
-        if constexpr (W == 8)
-          load32(src, v, u, a.wide_in != 0);
-        else
-          v = *reinterpret_cast<const uint4*>(src);
-        w[j][0] = v.x, w[j][1] = v.y, w[j][2] = v.z, w[j][3] = v.w;
-        if constexpr (W == 8) w[j][4] = u.x, w[j][5] = u.y, w[j][6] = u.z, w[j][7] = u.w;
-      }
-      if (W < 8) e[j] = a.kv.scale[j][r];
+    for (int i = 0; i < W; ++i) w[j][i] = 0;
+    b[j] = 0;
+    e[j] = 127;
+    if (row == kNoRow || a.out[j] == nullptr) continue;
+    const uint64_t r = row + head * a.kv.at.head_stride;
+    const uint8_t* src = a.kv.data[j] + r * a.kv.row_bytes + l * (W * 4);
+    if constexpr (W == 2) {
+      const uint2 v = *reinterpret_cast<const uint2*>(src);
+      w[j][0] = v.x, w[j][1] = v.y;
+      b[j] = a.kv.block[j][r * (a.kv.D / 16) + l];
+    } else {
+      uint4 v, u;
+      if constexpr (W == 8)
+        load32(src, v, u, a.wide_in != 0);
+      else
+        v = *reinterpret_cast<const uint4*>(src);
+      w[j][0] = v.x, w[j][1] = v.y, w[j][2] = v.z, w[j][3] = v.w;
+      if constexpr (W == 8) w[j][4] = u.x, w[j][5] = u.y, w[j][6] = u.z, w[j][7] = u.w;
     }
+    if (W < 8) e[j] = a.kv.scale[j][r];
+  }
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      if (a.out[j] == nullptr) continue;
-      float x[16];
-      if constexpr (W == 8) {
+  for (int j = 0; j < 2; ++j) {
+    if (a.out[j] == nullptr) continue;
+    float x[16];
+    if constexpr (W == 8) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 v = unpack2<FMT == FT_KV_F16>(w[j][i]);
-          x[2 * i] = v.x;
-          x[2 * i + 1] = v.y;
-        }
-      } else {
-        uint32_t f[8];  // f16 pairs; code * block scale is exact in fp32
-        float scale = pow2f(static_cast<int>(e[j]) - 127);
-        if constexpr (W == 4) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            f[2 * i] = cvt_e4m3x2(w[j][i]);
-            f[2 * i + 1] = cvt_e4m3x2(w[j][i] >> 16);
-          }
-        } else {
-          e2m1x8(w[j][0], f);
-          e2m1x8(w[j][1], f + 4);
-          scale *= unpack2<true>(cvt_e4m3x2(b[j])).x;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 v = unpack2<true>(f[i]);
-          x[2 * i] = v.x * scale;
-          x[2 * i + 1] = v.y * scale;
-        }
+      for (int i = 0; i < 8; ++i) {
+        const float2 v = unpack2<FMT == FT_KV_F16>(w[j][i]);
+        x[2 * i] = v.x;
+        x[2 * i + 1] = v.y;
       }
-      const int64_t to = static_cast<int64_t>(token) * a.tok[j] + head * a.head[j] + l * 16;
-      if (DT == FT_DT_F32) {
-        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out[j]) + to);
+    } else {
+      uint32_t f[8];  // f16 pairs; code * block scale is exact in fp32
+      float scale = pow2f(static_cast<int>(e[j]) - 127);
+      if constexpr (W == 4) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+        for (int i = 0; i < 4; ++i) {
+          f[2 * i] = cvt_e4m3x2(w[j][i]);
+          f[2 * i + 1] = cvt_e4m3x2(w[j][i] >> 16);
+        }
       } else {
-        store32(static_cast<uint16_t*>(a.out[j]) + to, pack8<DT == FT_DT_F16>(x), pack8<DT == FT_DT_F16>(x + 8),
-                a.wide_out != 0);
+        e2m1x8(w[j][0], f);
+        e2m1x8(w[j][1], f + 4);
+        scale *= unpack2<true>(cvt_e4m3x2(b[j])).x;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 v = unpack2<true>(f[i]);
+        x[2 * i] = v.x * scale;
+        x[2 * i + 1] = v.y * scale;
       }
     }
+    const int64_t to = static_cast<int64_t>(token) * a.tok[j] + head * a.head[j] + l * 16;
+    if (DT == FT_DT_F32) {
+      float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out[j]) + to);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+    } else {
+      store32(static_cast<uint16_t*>(a.out[j]) + to, pack8<DT == FT_DT_F16>(x), pack8<DT == FT_DT_F16>(x + 8),
+              a.wide_out != 0);
+    }
+  }
 }
 
 int ceil_log2(int n) {
@@ -717,17 +715,22 @@ ft_status launch_write(WriteArgs& a, bool interleaved, const char* what, cudaStr
   // Parts that would begin past the last row are not launched.
   a.parts = static_cast<int>(parts);
   while (a.parts > 1 && static_cast<int64_t>(a.parts - 1) * block >= items) --a.parts;
-  // Many tokens: several a CTA, so that their loads overlap, while there are
-  // eight CTAs an SM (4099 tokens x 40 heads rotated: 17.7 us, with four 19.4).
-  const int fill = a.T / (8 * sms);
-  a.batch = fill < 1 ? 1 : fill > kMaxBatch ? kMaxBatch : fill;
+  // Many tokens: several a CTA, so that their loads overlap, and so many that
+  // the CTAs fill whole waves of the SMs, as few as the batch allows (4099
+  // tokens x 40 heads rotated, 456 resident CTAs: 9 a CTA 15.5 us, 8 18.7, 3
+  // 16.2; 8192 tokens as above, 760 resident: 11 a CTA 35.7 us, 10 46.6, 6 36.5).
+  const bool any = !(interleaved || a.rot == 0) && !halves;
+  const int64_t resident = (any ? 512 : 1024) / block * sms;
+  const int64_t wave_tokens = (resident > sms ? resident : sms) * kMaxBatch;
+  const int64_t waves = (a.T + wave_tokens - 1) / wave_tokens;
+  a.batch = static_cast<int>((a.T + waves * wave_tokens / kMaxBatch - 1) / (waves * wave_tokens / kMaxBatch));
   const int64_t groups = (a.T + a.batch - 1) / a.batch;
   FT_REQUIRE(groups * a.parts < (1ll << 31), "%s: too many rows", what);
   const unsigned grid = static_cast<unsigned>(groups) * a.parts;
   const size_t smem = static_cast<size_t>(a.batch) * 2 * ((a.half + 31) / 32 * 32) * sizeof(float);
   const auto kernel = interleaved || a.rot == 0 ? write_kernel<F16, FMT, kPairs>
-                      : halves                  ? write_kernel<F16, FMT, kBlocks ? kAny : kHalves>
-                                                : write_kernel<F16, FMT, kAny>;
+                      : any                     ? write_kernel<F16, FMT, kAny>
+                                                : write_kernel<F16, FMT, kBlocks ? kAny : kHalves>;
   return launch_pdl(kernel, dim3(grid), block, smem, s, a, what);
 }
 
