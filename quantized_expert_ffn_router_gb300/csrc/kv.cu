@@ -246,35 +246,26 @@ struct Chunks {
   uint4 other[LAY == kAny ? 2 : 1];
 };
 
-// The codes of a quantised row's 16 channels.
-struct Codes {
-  uint32_t w[4];   // E4M3: four words; NVFP4: two
-  uint32_t block;  // NVFP4: the block's scale
-};
-
-// x[16] to codes, given the row's exponent and the block's largest magnitude.
-template <int FMT>
-__device__ __forceinline__ Codes encode(const float (&x)[16], float block_max, int e) {
-  Codes c;
+// x[16] as E4M3 codes, given the row's exponent.
+__device__ __forceinline__ uint4 codes_e4m3(const float (&x)[16], int e) {
   const float inv = pow2f(-e);
-  if (FMT == FT_KV_E4M3) {
+  uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      c.w[i] = to_e4m3x2(x[4 * i] * inv, x[4 * i + 1] * inv) | (to_e4m3x2(x[4 * i + 2] * inv, x[4 * i + 3] * inv) << 16);
-    c.block = 0;
-  } else {
-    float nan = 0.f;
+  for (int i = 0; i < 4; ++i)
+    w[i] = to_e4m3x2(x[4 * i] * inv, x[4 * i + 1] * inv) | (to_e4m3x2(x[4 * i + 2] * inv, x[4 * i + 3] * inv) << 16);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Half a block's E2M1 codes from values that are scaled already.
+__device__ __forceinline__ uint32_t codes_e2m1(const float (&z)[8]) {
+  uint32_t w = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) nan = isnan(x[i]) ? x[i] : nan;
-    c.block = to_e4m3x2(isnan(nan) ? nan : block_max * inv / 6.f, 0.f) & 0xffu;
-    const float bs = __half2float(__ushort_as_half(static_cast<uint16_t>(cvt_e4m3x2(c.block))));
-    c.w[0] = c.w[1] = c.w[2] = c.w[3] = 0;
-    if (bs > 0.f) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) c.w[i >> 2] |= to_e2m1x2(x[2 * i] * inv / bs, x[2 * i + 1] * inv / bs) << (8 * (i & 3));
-    }
-  }
-  return c;
+  for (int i = 0; i < 4; ++i) w |= to_e2m1x2(z[2 * i], z[2 * i + 1]) << (8 * i);
+  return w;
+}
+
+__device__ __forceinline__ float e4m3_value(uint32_t code) {
+  return __half2float(__ushort_as_half(static_cast<uint16_t>(cvt_e4m3x2(code))));
 }
 
 // The largest finite magnitude of x[16].
@@ -298,7 +289,8 @@ __device__ __forceinline__ float largest(const float (&x)[16]) {
 // A lane holds two chunks of 8 channels.
 //   kPairs   neighbouring chunks; interleaved rotations (or none) stay inside.
 //   kHalves  chunks c and c + half / 8, the two sides of the same 8 rotations
-//            (half layout, halves of whole chunks, rows not in blocks).
+//            (half layout, halves of whole chunks; NVFP4: of whole blocks,
+//            which two neighbouring lanes then share).
 //   kAny     neighbouring chunks, half layout: the other side is loaded as
 //            well (it is in L1, another lane's own).
 //
@@ -517,65 +509,159 @@ __global__ void __launch_bounds__(512, LAY == kAny ? 1 : 2) write_kernel(const _
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = (i < 8 ? has0 : has1) ? x[i] : 0.f;
       }
-      float block_max = largest(x), amax = row_largest(block_max);
-      int e = row_exponent(amax, top, top_bits);
-      Codes code;
-      if (!__any_sync(0xffffffffu, exact)) {
-        code = encode<FMT>(x, block_max, e);
+      // What the exact rotation of the elements in `unsure` (a bit each) gives.
+      const auto rotate_again = [&](uint32_t unsure) {
+        const int64_t p = a.rope_pos[t0 + tk];
+        while (unsure != 0) {
+          const int i = __ffs(unsure) - 1;
+          unsure &= unsure - 1;
+          const int c = (i < 8 ? c0 : c1) * 8 + (i & 7);
+          if (c >= a.rot) continue;
+          const bool left = LAY == kPairs ? (c & 1) == 0 : c < a.half;
+          const int f = LAY == kPairs ? c >> 1 : left ? c : c - a.half;
+          const int o = LAY == kPairs ? c ^ 1 : left ? c + a.half : c - a.half;
+          float2 hi, lo;
+          turn_pair(static_cast<int64_t>(static_cast<uint64_t>(p) * static_cast<uint64_t>(a.freqs[f])), a.mscale, &hi, &lo);
+          const float u = load_one<F16>(src + c), v = load_one<F16>(src + o);
+          const float y = rotate_odd(u, left ? v : -v, hi.x, lo.x, hi.y, lo.y);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) x[j] = j == i ? y : x[j];
+        }
+        __syncwarp();
+      };
+      int e;
+      if constexpr (FMT == FT_KV_E4M3) {
+        float amax = row_largest(largest(x));
+        e = row_exponent(amax, top, top_bits);
+        uint4 code;
+        if (!__any_sync(0xffffffffu, exact)) {
+          code = codes_e4m3(x, e);
+        } else {
+          // Both ends; the row's largest is at least the largest pair's size /
+          // sqrt 2, so off by at most 2^-19 of itself.
+          float d[16], z[16];
+          uncertainty(now, src, exact, x, d);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) z[i] = x[i] - d[i];
+          code = codes_e4m3(z, e);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) z[i] = x[i] + d[i];
+          const uint4 up = codes_e4m3(z, e);
+          const float part = amax * 0x1p-19f;
+          const bool all = row_exponent(amax - part, top, top_bits) != row_exponent(amax + part, top, top_bits);
+          const uint32_t differ[4] = {code.x ^ up.x, code.y ^ up.y, code.z ^ up.z, code.w ^ up.w};
+          if (__any_sync(0xffffffffu, exact && live && (all || (differ[0] | differ[1] | differ[2] | differ[3]) != 0))) {
+            uint32_t unsure = all ? 0xffffu : 0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if ((differ[i >> 2] >> (8 * (i & 3))) & 0xff) unsure |= 1u << i;
+            rotate_again(exact && live ? unsure : 0);
+            amax = row_largest(largest(x));
+            e = row_exponent(amax, top, top_bits);
+            code = codes_e4m3(x, e);
+          }
+        }
+        if (put && has0) *reinterpret_cast<uint2*>(dst + c0 * 8) = make_uint2(code.x, code.y);
+        if (put && has1) *reinterpret_cast<uint2*>(dst + c1 * 8) = make_uint2(code.z, code.w);
       } else {
-        // Both ends; the row's largest is at least the largest pair's size /
-        // sqrt 2, so off by at most 2^-19 of itself.
-        float d[16], z[16], far = 0.f;
-        uncertainty(now, src, exact, x, d);
+        constexpr bool kShared = LAY == kHalves;  // a rotated channel's block is half this lane's, half its neighbour's
+        const bool shared = kShared && l < hc;
+        // of the lane's two chunks, to that of the blocks they are in
+        const auto join = [&](float (&m)[2]) {
+          const float both = fmaxf(m[0], m[1]);
+          if (kShared) {
+            const float n0 = __shfl_xor_sync(0xffffffffu, m[0], 1), n1 = __shfl_xor_sync(0xffffffffu, m[1], 1);
+            m[0] = shared ? fmaxf(m[0], n0) : both;
+            m[1] = shared ? fmaxf(m[1], n1) : both;
+          } else {
+            m[0] = m[1] = both;
+          }
+        };
+        // Codes without divisions: a product with 1 / block scale is good to
+        // 2^-21, which widens d, and values are then treated as keys are (the
+        // divisions of both ends took twice the time).
+        float d[16], m[2] = {0.f, 0.f}, far[2] = {0.f, 0.f};
+        bool odd = false;  // infinities and NaN
+        if (__any_sync(0xffffffffu, exact)) {
+          uncertainty(now, src, exact, x, d);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) far = fmaxf(far, d[i]);
+          for (int i = 0; i < 16; ++i) d[i] = 0.f;
+        }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) z[i] = x[i] - d[i];
-        code = encode<FMT>(z, block_max, e);
+        for (int i = 0; i < 16; ++i) {
+          const float size = fabsf(x[i]);
+          d[i] = fmaf(size, 0x1p-21f, d[i]);
+          m[i >> 3] = fmaxf(m[i >> 3], size);
+          far[i >> 3] = fmaxf(far[i >> 3], d[i]);
+          odd |= !(size <= 3.4028235e38f);
+        }
+        join(m);
+        join(far);
+        const float amax = row_largest(fmaxf(m[0], m[1])), part = amax * 0x1p-19f;
+        e = row_exponent(amax, top, top_bits);
+        const float inv = pow2f(-e);
+        bool all = odd || (exact && row_exponent(amax - part, top, top_bits) != row_exponent(amax + part, top, top_bits));
+        uint32_t code[2], differ[2], block[2];
+        float per = 0.f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) z[i] = x[i] + d[i];
-        const Codes up = encode<FMT>(z, block_max + far, e);
-        const float part = amax * 0x1p-19f;
-        bool all = row_exponent(amax - part, top, top_bits) != row_exponent(amax + part, top, top_bits);
-        if (FMT == FT_KV_NVFP4) all |= (to_e4m3x2((block_max - far) * pow2f(-e) / 6.f, 0.f) & 0xffu) != up.block;
-        const bool differ = code.w[0] != up.w[0] || code.w[1] != up.w[1] || code.w[2] != up.w[2] || code.w[3] != up.w[3];
-        if (__any_sync(0xffffffffu, exact && live && (all || differ))) {
-          uint32_t unsure = all ? 0xffffu : 0;  // one bit a channel
+        for (int c = 0; c < 2; ++c) {
+          if (c == 0 || kShared) {
+            const uint32_t ends = to_e4m3x2((m[c] + far[c]) * (inv * (1.f / 6.f)), (m[c] - far[c]) * (inv * (1.f / 6.f)));
+            block[c] = ends & 0xffu;
+            all |= block[c] != ends >> 8;
+            const float bs = e4m3_value(block[c]);
+            per = bs > 0.f ? __fdividef(inv, bs) : 0.f;
+          } else {
+            block[c] = block[0];
+          }
+          float low[8], high[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            low[i] = (x[8 * c + i] - d[8 * c + i]) * per;
+            high[i] = (x[8 * c + i] + d[8 * c + i]) * per;
+          }
+          code[c] = per > 0.f ? codes_e2m1(low) : 0;
+          differ[c] = per > 0.f ? code[c] ^ codes_e2m1(high) : 0;
+        }
+        if (__any_sync(0xffffffffu, put && (all || (differ[0] | differ[1]) != 0))) {
+          uint32_t unsure = all ? 0xffffu : 0;
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if ((differ[i >> 3] >> (4 * (i & 7))) & 0xf) unsure |= 1u << i;
+          rotate_again(exact && live ? unsure : 0);
+          float nan[2] = {0.f, 0.f};
+          m[0] = m[1] = 0.f;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            constexpr int per = FMT == FT_KV_E4M3 ? 4 : 8, bits = 32 / per;
-            if (((code.w[i / per] ^ up.w[i / per]) >> (bits * (i % per))) & ((1u << bits) - 1)) unsure |= 1u << i;
+            m[i >> 3] = fmaxf(m[i >> 3], finite_abs(x[i]));
+            nan[i >> 3] = isnan(x[i]) ? 1.f : nan[i >> 3];
           }
-          if (!exact || !live) unsure = 0;
-          const int64_t p = a.rope_pos[t0 + tk];
-          while (unsure != 0) {
-            const int i = __ffs(unsure) - 1;
-            unsure &= unsure - 1;
-            const int c = (i < 8 ? c0 : c1) * 8 + (i & 7);
-            if (c >= a.rot) continue;
-            const bool left = LAY == kPairs ? (c & 1) == 0 : c < a.half;
-            const int f = LAY == kPairs ? c >> 1 : left ? c : c - a.half;
-            const int o = LAY == kPairs ? c ^ 1 : left ? c + a.half : c - a.half;
-            float2 hi, lo;
-            turn_pair(static_cast<int64_t>(static_cast<uint64_t>(p) * static_cast<uint64_t>(a.freqs[f])), a.mscale, &hi, &lo);
-            const float u = load_one<F16>(src + c), v = load_one<F16>(src + o);
-            const float y = rotate_odd(u, left ? v : -v, hi.x, lo.x, hi.y, lo.y);
+          join(m);
+          join(nan);
+          e = row_exponent(row_largest(fmaxf(m[0], m[1])), top, top_bits);
+          const float scale = pow2f(-e);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) x[j] = j == i ? y : x[j];
+          for (int c = 0; c < 2; ++c) {
+            block[c] = to_e4m3x2(nan[c] > 0.f ? NAN : m[c] * scale / 6.f, 0.f) & 0xffu;
+            const float bs = e4m3_value(block[c]);
+            float z[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[i] = x[8 * c + i] * scale / bs;
+            code[c] = bs > 0.f ? codes_e2m1(z) : 0;
           }
-          __syncwarp();
-          block_max = largest(x);
-          amax = row_largest(block_max);
-          e = row_exponent(amax, top, top_bits);
-          code = encode<FMT>(x, block_max, e);
         }
-      }
-      if (FMT == FT_KV_E4M3) {
-        if (put && has0) *reinterpret_cast<uint2*>(dst + c0 * 8) = make_uint2(code.w[0], code.w[1]);
-        if (put && has1) *reinterpret_cast<uint2*>(dst + c1 * 8) = make_uint2(code.w[2], code.w[3]);
-      } else if (put && has0) {  // neighbouring chunks, so that a lane holds one block of 16
-        *reinterpret_cast<uint2*>(dst + l * 8) = make_uint2(code.w[0], code.w[1]);
-        a.kv.block[w][static_cast<uint64_t>(row) * (a.D / 16) + l] = static_cast<uint8_t>(code.block);
+        if (kShared) {
+          if (put && has0) *reinterpret_cast<uint32_t*>(dst + c0 * 4) = code[0];
+          if (put && has1) *reinterpret_cast<uint32_t*>(dst + c1 * 4) = code[1];
+        } else if (put && has0) {
+          *reinterpret_cast<uint2*>(dst + l * 8) = make_uint2(code[0], code[1]);
+        }
+        // of two lanes that share two blocks, each stores one scale
+        const bool second = shared && (l & 1);
+        if (put && (second ? has1 : has0))
+          a.kv.block[w][static_cast<uint64_t>(row) * (a.D / 16) + ((second ? c1 : c0) >> 1)] =
+              static_cast<uint8_t>(second ? block[1] : block[0]);
       }
       if (put && l == 0) a.kv.scale[w][row] = static_cast<uint8_t>(e + 127);
     }
@@ -694,8 +780,7 @@ bool rows_overlap_partly(const ft_rows* a, const ft_rows* b) {
 template <bool F16, int FMT>
 ft_status launch_write(WriteArgs& a, bool interleaved, const char* what, cudaStream_t s) {
   a.half = a.rot / 2;
-  constexpr bool kBlocks = FMT == FT_KV_NVFP4;  // a lane has to hold whole blocks of 16
-  const bool halves = !kBlocks && a.half % 8 == 0 && (a.D - a.rot) % 16 == 0;
+  const bool halves = a.half % (FMT == FT_KV_NVFP4 ? 16 : 8) == 0 && (a.D - a.rot) % 16 == 0;
   a.lanes_log2 = ceil_log2((a.D + 15) / 16);
   const int64_t items = static_cast<int64_t>(a.Hq + (FMT >= 0 ? 2 * a.Hkv : 0)) << a.lanes_log2;
   const int sms = device_sm_count();
@@ -730,7 +815,7 @@ ft_status launch_write(WriteArgs& a, bool interleaved, const char* what, cudaStr
   const size_t smem = static_cast<size_t>(a.batch) * 2 * ((a.half + 31) / 32 * 32) * sizeof(float);
   const auto kernel = interleaved || a.rot == 0 ? write_kernel<F16, FMT, kPairs>
                       : any                     ? write_kernel<F16, FMT, kAny>
-                                                : write_kernel<F16, FMT, kBlocks ? kAny : kHalves>;
+                                                : write_kernel<F16, FMT, kHalves>;
   return launch_pdl(kernel, dim3(grid), block, smem, s, a, what);
 }
 
