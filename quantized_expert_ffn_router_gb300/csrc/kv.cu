@@ -327,18 +327,25 @@ __global__ void __launch_bounds__(512, LAY == kAny ? 1 : 2) write_kernel(const _
   const bool vec = (a.half & 7) == 0;
   const int r_cta = (part * blockDim.x) >> a.lanes_log2;
   const int rounds = (rows - r_cta + step - 1) / step;  // the same for every thread of the CTA
-  const int r_first = r_cta + (threadIdx.x >> a.lanes_log2);
 
-  // The row of this round: what it is, and where its channels are at the
-  // present token.  Lanes past the last row, or past the last channel, load
-  // others again: valid reads, whose results are not stored.
-  int kind, h;
-  const uint16_t* src;
-  const auto turn_to = [&](int row) {
-    const int r = min(row, rows - 1);
-    kind = r < a.Hq ? 0 : r < a.Hq + a.Hkv ? 1 : 2;
-    h = kind == 0 ? r : kind == 1 ? r - a.Hq : r - a.Hq - a.Hkv;
-    src = a.in[kind] + static_cast<int64_t>(t0) * a.in_tok[kind] + h * a.in_head[kind];
+  // Of the next token's turn: the row, what it is, and where its channels are.
+  // Lanes past the last row, or past the last channel, load others again: valid
+  // reads, whose results are not stored.  4-bit keys and values take so much
+  // longer than queries that the warps change places from token to token (20000
+  // tokens, 16 + 2 x 2 heads of 128: 63.8 us, then 54.9; 8-bit rows, 32 + 2 x 8
+  // heads: 80.2, then 84.2).
+  constexpr bool kMoves = FMT == FT_KV_NVFP4;
+  const int warps = blockDim.x >> 5, sub = (threadIdx.x & 31) >> a.lanes_log2, of_warp_log2 = 5 - a.lanes_log2;
+  int place = threadIdx.x >> 5;  // the warp's place among the CTA's at this token
+  int next_kind, next_h;
+  bool next_live;
+  const uint16_t* next_src;
+  const auto turn_to = [&](int round, int tk) {
+    const int row = r_cta + round * step + (place << of_warp_log2) + sub, r = min(row, rows - 1);
+    next_live = row < rows;
+    next_kind = r < a.Hq ? 0 : r < a.Hq + a.Hkv ? 1 : 2;
+    next_h = next_kind == 0 ? r : next_kind == 1 ? r - a.Hq : r - a.Hq - a.Hkv;
+    next_src = a.in[next_kind] + static_cast<int64_t>(t0 + tk) * a.in_tok[next_kind] + next_h * a.in_head[next_kind];
   };
   const int l0 = has0 ? c0 * 8 : 0, l1 = has1 ? c1 * 8 : 0;
   const int o0 = has0 && c0 < 2 * hc ? (c0 < hc ? c0 + hc : c0 - hc) * 8 : 0;  // the other sides
@@ -361,8 +368,8 @@ __global__ void __launch_bounds__(512, LAY == kAny ? 1 : 2) write_kernel(const _
 
   pdl_wait();
   Chunks<LAY> next;
-  turn_to(r_first);
-  load(src, next);
+  turn_to(0, 0);
+  load(next_src, next);
 
   if (FMT >= 0 && threadIdx.x < tokens) {
     const int32_t place = a.pos[t0 + threadIdx.x];
@@ -420,18 +427,11 @@ __global__ void __launch_bounds__(512, LAY == kAny ? 1 : 2) write_kernel(const _
   const bool filled = a.D == (16 << a.lanes_log2);  // every lane has its channels
 
   for (int round = 0; round < rounds; ++round) {
-    if (round > 0) {
-      turn_to(r_first + round * step);
-      load(src, next);
-    }
-    const bool live = r_first + round * step < rows;
-    const bool spin = a.rot > 0 && kind < 2;
-    const bool exact = kQuant && kind == 1 && spin;
-    const int64_t stride = a.in_tok[kind];
-    const int w = kind == 2 ? 1 : 0;
-    uint16_t* dst_q = a.q_out + static_cast<int64_t>(t0) * a.out_tok + h * a.out_head;
 #pragma unroll 1
-    for (int tk = 0; tk < tokens; ++tk, src += stride, dst_q += a.out_tok) {
+    for (int tk = 0; tk < tokens; ++tk) {
+      const int kind = next_kind, h = next_h, w = kind == 2 ? 1 : 0;
+      const bool live = next_live, spin = a.rot > 0 && kind < 2, exact = kQuant && kind == 1 && spin;
+      const uint16_t* src = next_src;
       const float* cosines = turns + tk * 2 * half_up;
       const float* sines = cosines + half_up;
       float x[16];
@@ -439,7 +439,14 @@ __global__ void __launch_bounds__(512, LAY == kAny ? 1 : 2) write_kernel(const _
       unpack8<F16>(next.own[1], x + 8);
       Chunks<LAY> now;  // kAny: the other sides are still to be read
       if (LAY == kAny) now = next;
-      load(tk + 1 < tokens ? src + stride : src, next);
+      if (tk + 1 < tokens || round + 1 < rounds) {
+        if (kMoves) place = place + 1 == warps ? 0 : place + 1;
+        if (kMoves || tk + 1 == tokens)
+          turn_to(tk + 1 < tokens ? round : round + 1, tk + 1 < tokens ? tk + 1 : 0);
+        else
+          next_src += a.in_tok[kind];
+        load(next_src, next);
+      }
       if (spin) {
         if (LAY == kPairs || LAY == kHalves) {
           // 8 rotations: channels (2i, 2i + 1), or (i, i + 8)
@@ -481,6 +488,7 @@ __global__ void __launch_bounds__(512, LAY == kAny ? 1 : 2) write_kernel(const _
       }
       __syncwarp();  // in place: the row's lanes have loaded both sides before any of them stores
       if (kind == 0 || FMT < 0) {
+        uint16_t* dst_q = a.q_out + static_cast<int64_t>(t0 + tk) * a.out_tok + h * a.out_head;
         if (LAY != kHalves && live && has1) {
           store32(dst_q + c0 * 8, pack8<F16>(x), pack8<F16>(x + 8), a.wide_out != 0);
         } else {
