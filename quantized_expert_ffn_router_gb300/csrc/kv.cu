@@ -400,23 +400,23 @@ __global__ void __launch_bounds__(512, LAY == kAny ? 1 : 2) write_kernel(const _
     }
   };
   // What fp32's rotation of the lane's channels may be off by: 2^-20.5 (|u| +
-  // |v|) m; that is at most 2^-20 (|x| + |y|) of the rotated pair.
+  // |v|) m; that is at most 2^-20 (|x| + |y|) of the rotated pair.  Nothing for
+  // values, infinite ones too.
   const auto uncertainty = [&](const Chunks<LAY>& c, const uint16_t* from, bool any, const float (&x)[16], float (&d)[16]) {
     if (LAY == kAny) {
-      const float off = any ? 6.7434956e-7f * fabsf(a.mscale) : 0.f;
+      const float off = 6.7434956e-7f * fabsf(a.mscale);
       float u[16], y[16];
       unpack8<F16>(c.own[0], u);
       unpack8<F16>(c.own[1], u + 8);
       other_sides(c, from, y);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) d[i] = (i < 8 ? c0 : c1) * 8 + (i & 7) < a.rot ? (fabsf(u[i]) + fabsf(y[i])) * off : 0.f;
+      for (int i = 0; i < 16; ++i) d[i] = any && (i < 8 ? c0 : c1) * 8 + (i & 7) < a.rot ? (fabsf(u[i]) + fabsf(y[i])) * off : 0.f;
     } else {
-      const float off = any ? 0x1p-20f : 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int iu = LAY == kPairs ? 2 * i : i, iv = LAY == kPairs ? 2 * i + 1 : i + 8;
-        const bool turns_too = LAY == kPairs ? 8 * l + i < a.half : l < hc;
-        d[iu] = d[iv] = turns_too ? (fabsf(x[iu]) + fabsf(x[iv])) * off : 0.f;
+        const bool turns_too = any && (LAY == kPairs ? 8 * l + i < a.half : l < hc);
+        d[iu] = d[iv] = turns_too ? (fabsf(x[iu]) + fabsf(x[iv])) * 0x1p-20f : 0.f;
       }
     }
   };

@@ -227,3 +227,58 @@ def test_append_on_another_stream_in_a_graph(att):
             side.synchronize()
             assert (f64(ko) == quantised("e4m3", f64(k))).all()
             assert (f64(vo) == quantised("e4m3", f64(v))).all()
+
+
+@pytest.mark.parametrize("T,Hkv,D,page,rot", [(2501, 4, 128, 32, 128), (1300, 12, 256, 48, 64), (1000, 20, 64, 16, 64),
+                                              (6000, 1, 128, 64, 96)])
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3", "nvfp4"])
+@pytest.mark.parametrize("layout", ["half", "pairs"])
+def test_append_many_tokens(att, T, Hkv, D, page, rot, fmt, layout):
+    """Several tokens, and several turns of a token's rows, for each block of threads."""
+    test_append_and_gather(att, T, Hkv, D, page, rot, fmt, "bf16", layout)
+
+
+@pytest.mark.parametrize("T,h,D,rot,layout", [(4099, 40, 128, 64, "pairs"), (5001, 40, 128, 128, "half"),
+                                              (3001, 7, 256, 100, "half"), (40000, 2, 64, 64, "half")])
+def test_rope_many_tokens_in_place(att, T, h, D, rot, layout):
+    x = rows(T, h, D, "bf16", 5)
+    spin = att.Rope(rot, base=1e4, interleaved=layout == "pairs")
+    pos = torch.randint(0, 1 << 20, (T,), dtype=torch.int32, generator=torch.Generator().manual_seed(1)).to(DEV)
+    out = torch.full((T, h, D), float("nan"), dtype=torch.bfloat16, device=DEV)
+    att.rope(x, pos, spin, out)
+    want = rotated(f64(x), pos.cpu().numpy(), radians(spin), layout, 1.0)
+    assert (np.abs(f64(out) - want) <= rope_bound(x, spin, "bf16", want)).all()
+    same = x.clone()
+    att.rope(same, pos, spin, same)
+    assert torch.equal(same, out)
+
+
+@pytest.mark.parametrize("layout,rot", [("half", 64), ("half", 32), ("half", 24), ("pairs", 64)])
+@pytest.mark.parametrize("fmt", ["e4m3", "nvfp4"])
+def test_special_values_of_rotated_keys(att, fmt, layout, rot):
+    """Zeros, subnormals, infinities, NaN and ties in keys that are rotated to position 0 and to others."""
+    D, g = 64, torch.Generator().manual_seed(0)
+    x = torch.randn(12, 2, D, generator=g)
+    x[1] = 0.0
+    x[2] = -0.0
+    x[3] *= 1e-39
+    x[4, 0, 5], x[4, 1, 40] = math.inf, -math.inf
+    x[5, 0, 17], x[5, 1, 63] = math.nan, math.nan
+    x[6, :, :16] *= 1e-5  # a block scale of zero
+    x[7] = torch.arange(D) * 0.25
+    x[8] = 448.0 * torch.linspace(-1, 1, D)
+    x[9, :, 0] = 450.0
+    x[10] *= 1e30
+    x = x.to(torch.bfloat16).to(DEV)
+    spin = att.Rope(rot, base=1e4, interleaved=layout == "pairs")
+    cache = att.KvCache(FMT[fmt], 2, D, 16, 1)
+    pages, pos = torch.zeros(12, 1, dtype=torch.int32, device=DEV), torch.arange(12, dtype=torch.int32, device=DEV)
+    for at in (0, 3, 70001):
+        far = torch.full_like(pos, at)
+        att.kv_append(cache, x, -x, pages, pos, rope=spin, rope_pos=far)
+        ko, vo = torch.zeros(12, 2, D, device=DEV), torch.zeros(12, 2, D, device=DEV)
+        att.kv_gather(cache, pages, pos, ko, vo)
+        with np.errstate(invalid="ignore"):
+            want = quantised(fmt, rotated(f64(x), far.cpu().numpy(), radians(spin), layout, 1.0))
+        np.testing.assert_array_equal(f64(ko), want.astype(np.float32))
+        np.testing.assert_array_equal(f64(vo), quantised(fmt, -f64(x)).astype(np.float32))
