@@ -27,6 +27,15 @@
 // instructions for each; measured, that cost more than it saved (4-bit rows,
 // 64 rows up to 16384 tokens: 231 us against 186 us with loads into registers).
 //
+// Columns.  A warp's registers hold the sums of 16 heads of up to 128 channels,
+// or of 8 wider ones.  Where a key head has more query heads, two or four warps
+// side by side take them: they fill one ring together and meet once a step
+// (64 heads over one of 128, 128 rows up to 16384 tokens, bf16: 137 us; 241
+// with a ring for each warp).  Otherwise a CTA's four warps take different
+// tokens, each with a ring of its own, and meet at a unit's end.  Two tiles of
+// 8 heads in a warp beat two warps of one (16 heads over one of 128, E4M3: 36
+// us and 47): rows are turned into operands once.
+//
 // Order of tokens.  Place r = 0..7 of the contracted index holds token r / 2
 // (r even) or 4 + r / 2 (r odd) of its 8, so that a lane quarter's value rows
 // are q, q + 4, q + 8, q + 12 and the swizzles below keep every read of shared
@@ -47,8 +56,8 @@
 // What it measured (GPU time in a graph, inputs beyond L2; HBM at 6.70 TB/s):
 //   one row of 1000003 tokens, 32 heads over 4 of 128: bf16 306 us (the copy
 //   rate), E4M3 167 us (92% of it), NVFP4 131 us (67%);
-//   32 rows up to 8192 tokens, 32 heads over 8, bf16: 62.3 us (88%);
-//   64 rows up to 16384, 64 heads over 8, NVFP4: 100 us (63%).
+//   32 rows up to 8192 tokens, 32 heads over 8, bf16: 62.2 us (88%);
+//   64 rows up to 16384, 64 heads over 8, NVFP4: 98.8 us (64%).
 // 16-bit rows are bound by HBM, 4-bit rows by issue slots: of 370 warp
 // instructions for 16 tokens of one key head, 190 turn codes into operands
 // (conversions, bytes taken out of words, block scales), 16 are products.
@@ -150,7 +159,7 @@ constexpr int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
 // D read zeros).  Keys: piece p of a row gives lane quarter q the EK channels
 // p*4*EK + q*EK..; values: piece p gives lane group g the EV channels
 // p*8*EV + g*EV...
-// COLS: warps side by side over a block's heads (see the columns above).
+// COLS: warps side by side over a block's heads.
 template <int FMT, int DP, int NT, int COLS>
 struct Deal {
   static constexpr int kWarps = COLS == 1 ? 4 : COLS, kThreads = kWarps * 32;

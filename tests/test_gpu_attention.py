@@ -26,7 +26,7 @@ def queries(T, Hq, D, dtype, seed):
 
 
 def check(att, fmt, dtype, out_dtype, D, Hkv, G, page, lens, window=0, seed=0, order="phsd", table=None, cache=None,
-          seq=None, width=None, scale=None, status_want=0):
+          seq=None, width=None, scale=None, status_want=0, weight_step=None):
     T, Hq = len(lens), Hkv * G
     n_pages = sum(-(-int(n) // page) for n in lens) + 2 if table is None else None
     if cache is None:
@@ -46,7 +46,7 @@ def check(att, fmt, dtype, out_dtype, D, Hkv, G, page, lens, window=0, seed=0, o
     assert int(status.item()) == status_want
     scale32 = float(np.float32(scale))
     want, want_lse, parts = attention(cache, f64(q), table, lens, page, scale32, window, seq)
-    tol, tol_lse = attention_tolerance(fmt, out_dtype, D, want, want_lse, parts)
+    tol, tol_lse = attention_tolerance(fmt, out_dtype, D, want, want_lse, parts, weight_step)
     got, got_lse = f64(out), f64(lse)
     assert np.isfinite(got).all()
     bad = np.abs(got - want) > tol
@@ -285,3 +285,43 @@ def test_differences_of_the_log_sum_are_the_output(att):
         slope = (run(up)[1] - run(dn)[1]) / (2 * h)
         # third-derivative term h^2/6 * (0.125 * |k|)^3 < 2^-8/6 * 0.13, fp32 lse 2^-20 / h
         assert abs(slope - 0.125 * float(o2[0, 0, d])) <= 2.0 ** -8 / 6 * 0.2 + 2.0 ** -15
+
+
+def weight_step(fmt, out):
+    """The largest relative error of a weight: half a step of its type (bf16 2^-8, f16 2^-11), squared where it is two
+    terms (16-bit caches, and fp32 outputs)."""
+    return 2.0 ** -16 if fmt == "bf16" else 2.0 ** -22 if fmt == "f16" or out == "f32" else 2.0 ** -11
+
+
+@pytest.mark.parametrize("fmt,out", [("bf16", "bf16"), ("f16", "f16"), ("e4m3", "bf16"), ("nvfp4", "f32")])
+@pytest.mark.parametrize("D,Hkv,G", [(64, 3, 17), (64, 1, 64), (80, 1, 36), (96, 2, 20), (128, 1, 33), (128, 2, 48),
+                                     (160, 1, 11), (192, 2, 16), (192, 1, 32), (256, 1, 24), (224, 2, 9)])
+def test_heads_over_several_warps(att, fmt, out, D, Hkv, G):
+    if fmt == "nvfp4" and D % 32:
+        D += 16
+    dtype = "f16" if fmt == "f16" else "bf16"
+    kw = dict(seed=D + G, weight_step=weight_step(fmt, out))
+    check(att, fmt, dtype, out, D, Hkv, G, 24, [0, 1, 15, 16, 17, 65, 0, 401, 1290], **kw)
+    check(att, fmt, dtype, out, D, Hkv, G, 7, [5, 0, 700, 3, 99], window=61, **kw)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "nvfp4"])
+@pytest.mark.parametrize("G", [24, 64])
+def test_many_rows_of_heads_over_several_warps(att, fmt, G):
+    r = np.random.default_rng(4)
+    lens = [int(n) for n in np.exp(r.uniform(0, np.log(400), 90))] + [9001]
+    lens[40:60] = [0] * 20
+    check(att, fmt, "bf16", "bf16", 128, 2, G, 16, lens, seed=12, weight_step=weight_step(fmt, "bf16"))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_bad_pages_and_sequences_with_heads_over_several_warps(att, fmt):
+    page = 16
+    cache = Cache(fmt, 1, 128, page, 40, 9)
+    table = random_table([100, 200, 60], page, 40, 9)
+    table[0, 2], table[1, 0], table[1, 11] = 40, -7, 2 ** 30
+    for G in (20, 50):
+        check(att, fmt, "bf16", "bf16", 128, 1, G, page, [100, 200, 60, 60], table=table, cache=cache, seq=[0, 1, 2, 3],
+              status_want=5, weight_step=weight_step(fmt, "bf16"))
+        check(att, fmt, "bf16", "bf16", 128, 1, G, page, [60, 60, 100], table=table, cache=cache, seq=[2, -1, 1],
+              status_want=5, weight_step=weight_step(fmt, "bf16"))
