@@ -234,7 +234,8 @@ struct Deal {
   static constexpr int kRing = kRings * S * kSlot;
   static_assert(S >= kFewestSlots && 3 * S <= 32 && kBox >= 1 && NT % kBox == 0, "");
   static constexpr int kEarly = kHeads / kWarps < 4 ? kHeads / kWarps : 4;  // queries that a warp loads at a time
-  static_assert(kSlot % 128 == 0 && kNotes % 16 == 0, "");
+  // slots, notes and queries are read and written 16 bytes at a time
+  static_assert(kSlot % 128 == 0 && kNotes % 16 == 0 && kWarps * (H * 8 + 8) % 16 == 0 && kQuery % 16 == 0, "");
 };
 
 // Two output values in one word.
