@@ -42,6 +42,7 @@ template <int kThreads>
 __device__ __forceinline__ LineSums line_sums(const AttnArgs& a, int row) {
   __shared__ int2 part_s[kThreads / 32];
   int before = 0, total = 0;
+#pragma unroll 1
   for (int t = threadIdx.x; t < a.T; t += kThreads) {
     const int n = numbers_of(a, t);
     total += n;

@@ -153,6 +153,7 @@ __device__ __forceinline__ void copy16_or_zero(uint32_t dst, const uint8_t* src,
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
+constexpr int log2_of(int n) { return n == 1 ? 0 : 1 + log2_of(n / 2); }
 constexpr int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
 
 // How a format's rows are cut, for heads padded to DP channels (channels past
@@ -269,6 +270,7 @@ struct Walk {
     do {
       if (left == 0) return false;
       s = span_of(a, t);
+#pragma unroll 1
       while (at >= row_numbers(s.tiles, a.lead, a.units)) {
         at -= row_numbers(s.tiles, a.lead, a.units);
         s = span_of(a, ++t);
@@ -279,8 +281,8 @@ struct Walk {
     } while (part.tiles == 0);
     seq = kv_seq(a.kv, t);
     first = s.first;
-    base = s.begin + part.tile0 * a.tile + offset;
-    stop = min(s.len, s.begin + (part.tile0 + part.tiles) * a.tile);
+    base = s.begin + (part.tile0 << a.tile_log2) + offset;
+    stop = min(s.len, s.begin + ((part.tile0 + part.tiles) << a.tile_log2));
     if (static_cast<uint32_t>(seq) >= a.kv.n_seqs) {
       record_status(a.status, FT_ERR_BAD_ID);
       stop = 0;
@@ -549,6 +551,7 @@ __device__ __forceinline__ void add_values(uint32_t at, uint32_t vnotes, int u, 
 // A row that sees nothing: zeros and -inf.
 __device__ __noinline__ void empty_row(const AttnArgs& a, int t) {
   const bool f32 = a.out_f32 != 0;
+#pragma unroll 1
   for (int i = threadIdx.x; i < a.Hq * (a.kv.D / 2); i += blockDim.x) {
     const int h = i / (a.kv.D / 2), d = 2 * (i - h * (a.kv.D / 2));
     const int64_t to = static_cast<int64_t>(t) * a.out_tok + static_cast<int64_t>(h) * a.out_head + d;
@@ -592,6 +595,7 @@ __global__ void __launch_bounds__(Deal<FMT, DP, NT, COLS>::kThreads, Deal<FMT, D
   Walk walk;
   {
     // rows that see nothing
+#pragma unroll 1
     for (int t = blockIdx.x; t < a.T; t += gridDim.x)
       if (span_of(a, t).tiles == 0) empty_row(a, t);
     const Begin begin = begin_of<X::kThreads>(a, blockIdx.x);
@@ -609,7 +613,6 @@ __global__ void __launch_bounds__(Deal<FMT, DP, NT, COLS>::kThreads, Deal<FMT, D
   feed.walk = walk;
   feed.init(a, ring, wh, lane);
   feed.enter(a, lane);
-  feed.prepare(a, offset, step, lane);
 
   // places of the lane's pieces in a step's rows
   uint32_t koff[X::KP];
@@ -635,9 +638,10 @@ __global__ void __launch_bounds__(Deal<FMT, DP, NT, COLS>::kThreads, Deal<FMT, D
     for (int i = 0; i < X::kEarly; ++i) early[i] = query(warp + i * kWarps);
   };
   enter();
+  feed.more = true;
 #pragma unroll 1
-  for (int i = 0; i < S - 1; ++i) {
-    feed.issue(a, ring, wh, lane);
+  for (int i = 0; i < S; ++i) {
+    if (i > 0) feed.issue(a, ring, wh, lane);
     if (feed.more) feed.prepare(a, offset, step, lane);
   }
 
@@ -1015,10 +1019,11 @@ ft_status launch(AttnArgs& a, cudaStream_t s) {
       return fail(FT_ERR_CUDA, "attn_decode: %s", cudaGetErrorString(cudaGetLastError()));
     held.store(r, std::memory_order_relaxed);
   }
-  a.tile = X::TS * X::kWarpsT;
+  constexpr int tile = X::TS * X::kWarpsT;
+  a.tile_log2 = log2_of(tile);
   a.lead = X::kLead;
   const int64_t longest = a.window > 0 && a.window < a.most ? a.window + 15 : a.most;
-  const int64_t most_tiles = ((longest + a.tile - 1) / a.tile + a.lead) * a.units * a.T;
+  const int64_t most_tiles = ((longest + tile - 1) / tile + a.lead) * a.units * a.T;
   // the line's numbers are 32-bit in the kernel
   if (most_tiles >= (1ll << 31) - kMaxWorkers) return fail(FT_ERR_UNSUPPORTED, "attn_decode: rows times pages too large");
   int64_t workers = static_cast<int64_t>(device_sm_count()) * r;

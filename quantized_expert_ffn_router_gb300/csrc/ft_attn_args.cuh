@@ -23,7 +23,7 @@ struct AttnArgs {
   int32_t units;         // head blocks of a row: Hkv * blocks
   int32_t blocks;        // head blocks of a key head
   int32_t block_heads;   // heads of a block
-  int32_t tile;          // tokens of a CTA's tile
+  int32_t tile_log2;     // tokens of a CTA's tile: a power of two, because kernels divide by them in many places
   int32_t lead;          // numbers of a unit in the line before those of its tiles
   int32_t most;          // max_pages * page_size
   int32_t q_f16, out_f32;
@@ -32,7 +32,8 @@ struct AttnArgs {
 };
 
 __device__ __forceinline__ RowSpan span_of(const AttnArgs& a, int t) {
-  return row_span(a.lens[t], a.window, a.most, a.tile);
+  const int log2 = a.tile_log2;
+  return row_span_by(a.lens[t], a.window, a.most, [log2](int n) { return (n + (1 << log2) - 1) >> log2; });
 }
 
 __device__ __forceinline__ int numbers_of(const AttnArgs& a, int t) {
@@ -69,12 +70,14 @@ __device__ __forceinline__ Begin begin_of(const AttnArgs& a, int c) {
     __shared__ int2 begin;
     const int each = (a.T + kThreads - 1) / kThreads, first = threadIdx.x * each;
     int own = 0;
+#pragma unroll 1
     for (int t = first; t < min(first + each, a.T); ++t) own += numbers_of(a, t);
     int before = block_excl_scan(own, scratch, &r.total);
     r.share = split_share(r.total, a.workers);
     const int from = c * r.share;
     if (before <= from && from < before + own) {
       int t = first;
+#pragma unroll 1
       for (int n = numbers_of(a, t); before + n <= from; n = numbers_of(a, ++t)) before += n;
       begin = make_int2(t, from - before);
     }

@@ -68,15 +68,21 @@ struct RowSpan {
   int32_t tiles;
 };
 
-FT_HD RowSpan row_span(int32_t len, int32_t window, int64_t most, int32_t tile) {
+// `tiles_of` gives the tiles that so many tokens take.
+template <typename TilesOf>
+FT_HD RowSpan row_span_by(int32_t len, int32_t window, int32_t most, TilesOf tiles_of) {
   RowSpan r;
-  if (len > most) len = static_cast<int32_t>(most);
+  if (len > most) len = most;
   if (len < 0) len = 0;
   r.len = len;
   r.first = (window > 0 && len > window) ? len - window : 0;
   r.begin = r.first & ~15;
-  r.tiles = (len - r.begin + tile - 1) / tile;
+  r.tiles = tiles_of(len - r.begin);
   return r;
+}
+
+FT_HD RowSpan row_span(int32_t len, int32_t window, int32_t most, int32_t tile) {
+  return row_span_by(len, window, most, [tile](int32_t tokens) { return (tokens + tile - 1) / tile; });
 }
 
 FT_HD int32_t split_share(int32_t total, int32_t workers) { return total > workers ? (total + workers - 1) / workers : 1; }
