@@ -56,8 +56,8 @@
 // What it measured (GPU time in a graph, inputs beyond L2; HBM at 6.70 TB/s):
 //   one row of 1000003 tokens, 32 heads over 4 of 128: bf16 306 us (the copy
 //   rate), E4M3 167 us (92% of it), NVFP4 131 us (67%);
-//   32 rows up to 8192 tokens, 32 heads over 8, bf16: 62.2 us (88%);
-//   64 rows up to 16384, 64 heads over 8, NVFP4: 98.8 us (64%).
+//   32 rows up to 8192 tokens, 32 heads over 8, bf16: 61.8 us (88%);
+//   64 rows up to 16384, 64 heads over 8, NVFP4: 99 us (64%).
 // 16-bit rows are bound by HBM, 4-bit rows by issue slots: of 370 warp
 // instructions for 16 tokens of one key head, 190 turn codes into operands
 // (conversions, bytes taken out of words, block scales), 16 are products.
@@ -343,6 +343,11 @@ struct Feeder {
       }
       enter(a, lane);
     }
+    look_up(a, step, lane);
+  }
+
+  // The page of the lane's token of the step that the walk has come to.
+  __device__ __forceinline__ void look_up(const AttnArgs& a, int step, int lane) {
     more = true;
     const int tok = walk.base + lane;
     live = lane < X::TS && tok >= walk.first && tok < walk.stop;
@@ -611,8 +616,13 @@ __global__ void __launch_bounds__(Deal<FMT, DP, NT, COLS>::kThreads, Deal<FMT, D
   if (!walk.next(a, offset)) return;  // the share is the lead of a unit that begins in the next
   Feeder<X> feed;
   feed.walk = walk;
-  feed.init(a, ring, wh, lane);
+  feed.more = true;
   feed.enter(a, lane);
+  // The first page is on its way while the rest is set up (777 tokens bf16 7.1 us
+  // and 7.4; NVFP4, whose registers are short, 64 rows up to 16384: 101.5 and 98.8).
+  const bool early_page = !X::kBlocks && walk.base < walk.stop;
+  if (early_page) feed.look_up(a, step, lane);
+  feed.init(a, ring, wh, lane);
 
   // places of the lane's pieces in a step's rows
   uint32_t koff[X::KP];
@@ -638,11 +648,10 @@ __global__ void __launch_bounds__(Deal<FMT, DP, NT, COLS>::kThreads, Deal<FMT, D
     for (int i = 0; i < X::kEarly; ++i) early[i] = query(warp + i * kWarps);
   };
   enter();
-  feed.more = true;
 #pragma unroll 1
   for (int i = 0; i < S; ++i) {
     if (i > 0) feed.issue(a, ring, wh, lane);
-    if (feed.more) feed.prepare(a, offset, step, lane);
+    if (feed.more && !(i == 0 && early_page)) feed.prepare(a, offset, step, lane);
   }
 
   uint32_t at = ring;  // the slot to read next
@@ -889,10 +898,9 @@ __global__ void __launch_bounds__(Deal<FMT, DP, NT, COLS>::kThreads, Deal<FMT, D
       return whole ? static_cast<int64_t>(t) * a.out_tok + static_cast<int64_t>(hq0 + h) * a.out_head
                    : (static_cast<int64_t>(part) * X::kHeads + h) * DP;
     };
-    // maxima and sums of the heads h and h + 1; gives what their outputs are multiplied by
-    const auto write_sums = [&](int h, const float (&M)[2], const float (&L)[2], float (&norm)[2]) {
-      norm[0] = !whole ? 1.f : L[0] == 0.f ? 0.f : 1.f / L[0];
-      norm[1] = !whole ? 1.f : L[1] == 0.f ? 0.f : 1.f / L[1];
+    const auto norm_of = [&](float L) { return !whole ? 1.f : L == 0.f ? 0.f : 1.f / L; };
+    // maxima and sums of the heads h and h + 1
+    const auto write_sums = [&](int h, const float (&M)[2], const float (&L)[2]) {
       if (g < 2 && wt == 0 && h + g < heads) {
         const float mg = g ? M[1] : M[0], lg = g ? L[1] : L[0];
         if (whole)
@@ -919,11 +927,11 @@ __global__ void __launch_bounds__(Deal<FMT, DP, NT, COLS>::kThreads, Deal<FMT, D
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const int h = wh * H + n * 8 + 2 * q;  // in the block
-        float norm[2];
-        write_sums(h, m[n], l[n], norm);
+        const float norm[2] = {norm_of(l[n][0]), norm_of(l[n][1])};
         const int64_t to = place_of_head(h);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) write(h, to, mt, acc[mt][n], norm);
+        write_sums(h, m[n], l[n]);
       }
     } else {
       // The warps' sums meet in shared memory, and each warp joins and writes a
@@ -976,26 +984,36 @@ __global__ void __launch_bounds__(Deal<FMT, DP, NT, COLS>::kThreads, Deal<FMT, D
               L[i] = fmaf(o[w].y, y[w][i], L[i]);
             }
           }
+          norm[0] = norm_of(L[0]);
+          norm[1] = norm_of(L[1]);
+          // The sums of all the warp's tiles are read at once: one wait for shared
+          // memory (NVFP4, whose registers are short: of one tile at a time).
+          constexpr int kTiles = X::kBlocks ? 1 : MT / kWarps;
           const int h = n * 8 + 2 * q;  // in the block
-          write_sums(h, M, L, norm);
           const int64_t to = place_of_head(h);
-#pragma unroll 2
-          for (int mt = wt; mt < MT; mt += kWarps) {
-            float c[4] = {0.f, 0.f, 0.f, 0.f};
-            if (first != 0) {
-              float o[kWarps][4];
+#pragma unroll 1
+          for (int mt = wt; mt < MT; mt += kTiles * kWarps) {
+            float o[kTiles][kWarps][4];
+#pragma unroll
+            for (int j = 0; j < kTiles; ++j)
 #pragma unroll
               for (int w = 0; w < kWarps; ++w)
                 asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                             : "=f"(o[w][0]), "=f"(o[w][1]), "=f"(o[w][2]), "=f"(o[w][3])
-                             : "r"(box[w] + ((n - n0) * MT + mt) * 512));
+                             : "=f"(o[j][w][0]), "=f"(o[j][w][1]), "=f"(o[j][w][2]), "=f"(o[j][w][3])
+                             : "r"(box[w] + ((n - n0) * MT + mt + j * kWarps) * 512));
+#pragma unroll
+            for (int j = 0; j < kTiles; ++j) {
+              float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
               for (int w = 0; w < kWarps; ++w)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) c[i] = fmaf(o[w][i], y[w][i & 1], c[i]);
+                for (int i = 0; i < 4; ++i) c[i] = fmaf(o[j][w][i], y[w][i & 1], c[i]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) c[i] = first != 0 ? c[i] : 0.f;
+              write(h, to, mt + j * kWarps, c, norm);
             }
-            write(h, to, mt, c, norm);
           }
+          write_sums(h, M, L);
         }
       }
     }
