@@ -956,13 +956,14 @@ __global__ void __launch_bounds__(Deal<FMT, DP, NT, COLS>::kThreads, Deal<FMT, D
         }
         __syncthreads();
         // where the warps' sums are; the first's in the place of one that has
-        // none (whose weight is 0, or all that there is is zeros)
-        const uint32_t first = box_of[0];
+        // none (whose weight is 0); where none has any, the ring's start is read
+        // and not used
+        const uint32_t first = box_of[0], other = first != 0 ? first : smem_u32(smem);
         uint32_t box[kWarps];
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
           const uint32_t own = box_of[w];
-          box[w] = (own != 0 ? own : first) + lane * 16;
+          box[w] = (own != 0 ? own : other) + lane * 16;
         }
 #pragma unroll
         for (int n = n0; n < n0 + X::kBox; ++n) {
