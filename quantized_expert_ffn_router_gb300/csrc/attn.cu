@@ -10,28 +10,6 @@
 namespace ft {
 namespace {
 
-// A maximum over nothing, as the attention kernels leave it.
-constexpr float kLowest = -3.0e38f;
-
-__device__ __forceinline__ float weight_of(float m, float M) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(m - M));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t pack_out(const AttnArgs& a, float x, float y) {
-  uint32_t d;
-  if (a.q_f16)
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(y), "f"(x));
-  else
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(y), "f"(x));
-  return d;
-}
-
-__device__ __forceinline__ void store_lse(const AttnArgs& a, int t, int h, float m, float l) {
-  if (a.lse) a.lse[static_cast<int64_t>(t) * a.Hq + h] = l > 0.f || l != l ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
-}
-
 // Numbers of the line that the rows before `row` take, and all rows, by the
 // whole block.
 struct LineSums {

@@ -44,7 +44,7 @@
 //
 // 8- and 4-bit rows: a key's power-of-two scale multiplies its score; a
 // value's enters the running maximum, so that the weight that is rounded to
-// f16 is p_j = 2^(x_j + ev_j - m) <= 2^4 whatever the scales are, and the sum
+// f16 is p_j = 2^(x_j + ev_j - m) <= 2^15 whatever the scales are, and the sum
 // of the softmax takes p_j 2^-ev_j in fp32.
 //
 // Split.  The tiles of all rows and key heads are numbered in one line and cut
@@ -97,12 +97,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
-}
-
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
@@ -169,6 +163,11 @@ struct Deal {
   static constexpr bool kQuant = FMT == FT_KV_E4M3 || FMT == FT_KV_NVFP4;
   static constexpr bool kBlocks = FMT == FT_KV_NVFP4;
   static constexpr bool kF16 = FMT != FT_KV_BF16;  // operand type of the products
+  // How far the reference lies below the greatest score.  f16 weights reach
+  // 2^(11 + kSlack), the top of its range, so that what rounds to nothing (f16's
+  // steps end at 2^-24) is 2^-36 of the heaviest: with the heaviest at 1, a
+  // token 18 nats above 16384 others took 6% of the norm from them.
+  static constexpr int kLift = kF16 ? 11 : 0;
   static constexpr int EK = !kQuant ? 8 : !kBlocks ? 16 : DP % 128 == 0 ? 32 : 16;
   static constexpr int EV = !kQuant ? 8 : !kBlocks ? (DP % 128 == 0 ? 16 : 8) : DP % 256 == 0 ? 32 : DP % 128 == 0 ? 16 : 8;
   static constexpr int NK = DP / (4 * EK), NV = DP / (8 * EV);
@@ -238,19 +237,6 @@ struct Deal {
   // slots, notes and queries are read and written 16 bytes at a time
   static_assert(kSlot % 128 == 0 && kNotes % 16 == 0 && kWarps * (H * 8 + 8) % 16 == 0 && kQuery % 16 == 0, "");
 };
-
-// Two output values in one word.
-__device__ __forceinline__ uint32_t pack_out(const AttnArgs& a, float x, float y) {
-  return a.q_f16 ? pack16<true>(x, y) : pack16<false>(x, y);
-}
-
-__device__ __forceinline__ void store_lse(const AttnArgs& a, int t, int h, float m, float l) {
-  if (a.lse) a.lse[static_cast<int64_t>(t) * a.Hq + h] = l > 0.f || l != l ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
-}
-
-// A maximum over nothing: finite, so that 2^(-inf - kLowest) and 2^(kLowest - m) are 0 and not NaN.
-constexpr float kLowest = -3.0e38f;
-__device__ __forceinline__ float weight_of(float m, float M) { return exp2_approx(m - M); }
 
 // The place of a token among its step's (see the order of tokens above), and the token of a place.
 __device__ __forceinline__ constexpr int place_of(int t) { return (t & ~7) + 2 * (t & 3) + ((t >> 2) & 1); }
@@ -493,8 +479,8 @@ struct Feeder {
   }
 };
 
-// The weights are rescaled when a score exceeds the running reference by this
-// much (in powers of two), not at every new maximum: 2^4 leaves p far inside f16.
+// The weights are rescaled when the greatest score exceeds the one that set the
+// reference by this much (in powers of two), not at every new maximum.
 constexpr float kSlack = 4.f;
 
 template <typename X, bool TWO, int NT>
@@ -817,7 +803,7 @@ __global__ void __launch_bounds__(Deal<FMT, DP, NT, COLS>::kThreads, Deal<FMT, D
               float& x = s[u][n][2 * r + i];
               x = X::kQuant ? fmaf(x * ks, mul[n][i], ev) : x * mul[n][i];
               if (part) x = ok ? x : -INFINITY;
-              more |= x > m[n][i] + kSlack;
+              more |= x > m[n][i] + (kSlack + X::kLift);
             }
         }
       if (__any_sync(kAll, more)) {
@@ -825,12 +811,13 @@ __global__ void __launch_bounds__(Deal<FMT, DP, NT, COLS>::kThreads, Deal<FMT, D
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float top = m[n][i];
+            float top = -INFINITY;
 #pragma unroll
             for (int u = 0; u < U; ++u) top = fmaxf(top, fmaxf(s[u][n][i], s[u][n][2 + i]));
             top = fmaxf(top, __shfl_xor_sync(kAll, top, 4));
             top = fmaxf(top, __shfl_xor_sync(kAll, top, 8));
             top = fmaxf(top, __shfl_xor_sync(kAll, top, 16));
+            top = fmaxf(m[n][i], top - X::kLift);
             const float c = weight_of(m[n][i], top);
             m[n][i] = top;
             l[n][i] *= c;
@@ -1041,6 +1028,7 @@ ft_status launch(AttnArgs& a, cudaStream_t s) {
   constexpr int tile = X::TS * X::kWarpsT;
   a.tile_log2 = log2_of(tile);
   a.lead = X::kLead;
+  a.lift = X::kLift;
   const int64_t longest = a.window > 0 && a.window < a.most ? a.window + 15 : a.most;
   const int64_t most_tiles = ((longest + tile - 1) / tile + a.lead) * a.units * a.T;
   // the line's numbers are 32-bit in the kernel

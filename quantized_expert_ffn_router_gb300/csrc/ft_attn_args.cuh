@@ -28,6 +28,7 @@ struct AttnArgs {
   int32_t most;          // max_pages * page_size
   int32_t q_f16, out_f32;
   int32_t workers;
+  int32_t lift;          // weights' reference lies this many powers of two below the greatest score
   int32_t* status;
 };
 
@@ -88,12 +89,44 @@ __device__ __forceinline__ Begin begin_of(const AttnArgs& a, int c) {
   return r;
 }
 
+// Softmax weights are taken in powers of two, 2^(x - m), with a reference m
+// that is `lift` below (about) the greatest score.  A maximum over nothing is
+// kLowest: finite, so that 2^(-inf - kLowest) and 2^(kLowest - m) are 0 and not
+// NaN.
+constexpr float kLowest = -3.0e38f;
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float weight_of(float m, float M) { return exp2_approx(m - M); }
+
+// The logarithm of a head's sum l of weights with the reference m.  The lift is
+// taken off both: exactly, and without it log2(l) and m cancel to fewer bits.
+__device__ __forceinline__ void store_lse(const AttnArgs& a, int t, int h, float m, float l) {
+  if (a.lse == nullptr) return;
+  const float sum = l * __uint_as_float((127 - a.lift) << 23);
+  a.lse[static_cast<int64_t>(t) * a.Hq + h] =
+      l > 0.f || l != l ? (m + static_cast<float>(a.lift) + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+}
+
+// Two output values in one word.
+__device__ __forceinline__ uint32_t pack_out(const AttnArgs& a, float x, float y) {
+  uint32_t d;
+  if (a.q_f16)
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(y), "f"(x));
+  else
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(y), "f"(x));
+  return d;
+}
+
 struct AttnShape {
   int DP, NT;        // channels padded to 64s; 8-head column tiles of a warp
   int columns, block_heads, blocks;  // warps side by side over a block's heads
 };
 
-// The kernel of each cache format; sets a.tile and a.workers.
+// The kernel of each cache format; sets a.tile_log2, a.lead, a.lift and a.workers.
 ft_status attend_bf16(AttnArgs& a, const AttnShape& sh, cudaStream_t s);
 ft_status attend_f16(AttnArgs& a, const AttnShape& sh, cudaStream_t s);
 ft_status attend_e4m3(AttnArgs& a, const AttnShape& sh, cudaStream_t s);

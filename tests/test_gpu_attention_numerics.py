@@ -1,0 +1,110 @@
+"""ft_attn_decode where rounding to fewer bits, or a number's range, could show:
+light weights beside heavy ones, 16-bit outputs of 8- and 4-bit caches, small
+query elements, keys and scores at the ends of fp32, infinities that count.
+Rows are written by kv_append and compared as kv_gather reads them back."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from attn_helpers import DT, FMT, f64
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module")
+def att(cuda_lib):
+    from quantized_expert_ffn_router_gb300 import attention
+
+    return attention
+
+
+class Rows:
+    """One sequence's k and v [n, Hkv, D] in a cache of its own, and what they stand for."""
+
+    def __init__(self, att, fmt, dtype, k, v, page=16):
+        n, self.Hkv, self.D = k.shape
+        pages = -(-n // page) + 2
+        self.att, self.n = att, n
+        self.cache = att.KvCache(FMT[fmt], self.Hkv, self.D, page, pages)
+        order = np.random.default_rng(n).permutation(pages)[:-(-n // page)].astype(np.int32)
+        self.table = torch.from_numpy(order[None]).to(DEV)
+        pos, seq = torch.arange(n, dtype=torch.int32, device=DEV), torch.zeros(n, dtype=torch.int32, device=DEV)
+        att.kv_append(self.cache, k.to(DT[dtype]).to(DEV), v.to(DT[dtype]).to(DEV), self.table, pos, seq=seq)
+        ko, vo = (torch.empty(n, self.Hkv, self.D, device=DEV) for _ in "kv")
+        att.kv_gather(self.cache, self.table, pos, ko, vo, seq=seq)
+        self.k, self.v = f64(ko), f64(vo)
+        self.ev = np.zeros((n, self.Hkv))  # exponents of the value rows
+        if self.cache.v_scale is not None:
+            at = np.arange(n)
+            self.ev = f64(self.cache.v_scale)[order[at // page], :, at % page] - 127
+
+    def attend(self, q, out_dtype, scale):
+        att, (_, Hq, D) = self.att, q.shape
+        out = torch.full((1, Hq, D), float("nan"), dtype=DT[out_dtype], device=DEV)
+        lse = torch.full((1, Hq), float("nan"), device=DEV)
+        ws = torch.full((att.attn_decode_workspace(1, Hq, self.Hkv, D),), 0xFF, dtype=torch.uint8, device=DEV)
+        lens = torch.tensor([self.n], dtype=torch.int32, device=DEV)
+        att.attn_decode(self.cache, q, self.table, lens, out, ws, scale=scale, lse=lse)
+        return out, lse
+
+    def exact(self, q, scale):
+        """(output, log-sum, weights [Hq, n], scores' reach) in 64 bits."""
+        q, scale = f64(q)[0], float(np.float32(scale))
+        G = q.shape[0] // self.Hkv
+        out, lse, w, reach = np.zeros_like(q), np.zeros(len(q)), np.zeros((len(q), self.n)), np.zeros(len(q))
+        for h in range(len(q)):
+            x = scale * (self.k[:, h // G] @ q[h])
+            e = np.exp(x - x.max())
+            w[h] = e / e.sum()
+            out[h], lse[h] = w[h] @ self.v[:, h // G], x.max() + np.log(e.sum())
+            reach[h] = (abs(scale) * np.abs(self.k[:, h // G]) @ np.abs(q[h])).max()
+        return out, lse, w, reach
+
+
+def bound(rows, fmt, out_dtype, out, w, reach):
+    """What the output may be off by.  The weights: scores are fp32 sums of D / 16 steps (2^-23 of their reach each) and
+    their scaling, the exponential 2^-22, a step of 16 tokens 2^-23, two terms of f16 2^-22 or of bf16 2^-16, and with
+    f16 2^-36 of the heaviest weight (times its value's exponent) for each token.  Then the output's own half step."""
+    G = len(w) // rows.Hkv
+    v = np.repeat(rows.v.transpose(1, 0, 2), G, 0)                 # [Hq, n, D]
+    ev = np.repeat(rows.ev.T, G, 0)                                # [Hq, n]
+    mass = np.einsum("hn,hnd->hd", w, np.abs(v))
+    heavy = (w * 2.0 ** ev).max(-1)
+    floor = 0.0 if fmt == "bf16" else 2.0 ** -36 * heavy[:, None] * (np.abs(v) * 2.0 ** -ev[..., None]).sum(1)
+    each = 2 * (rows.D / 16 + 6) * 2.0 ** -23 * reach + (rows.n / 16 + 16) * 2.0 ** -23 + 2.0 ** -21
+    each = each + (2.0 ** -16 if fmt == "bf16" else 2.0 ** -22)
+    half = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11, "f32": 2.0 ** -24}[out_dtype]
+    return half * np.abs(out) + mass * each[:, None] + floor + 2.0 ** -25 * (out_dtype == "f16")
+
+
+def lse_bound(D, lse, reach):
+    return (D / 16 + 6) * 2.0 ** -23 * reach + 2.0 ** -20 * (1 + np.abs(lse))
+
+
+@pytest.mark.parametrize("fmt,dtype,out_dtype", [("bf16", "bf16", "bf16"), ("bf16", "bf16", "f32"), ("f16", "f16", "f16"),
+                                                 ("f16", "f16", "f32"), ("e4m3", "bf16", "bf16"), ("e4m3", "f16", "f32"),
+                                                 ("nvfp4", "bf16", "f32"), ("nvfp4", "bf16", "bf16")])
+@pytest.mark.parametrize("gap", [8, 20, 26, 30])
+@pytest.mark.parametrize("G", [4, 20])
+def test_light_weights_beside_heavy_ones(att, fmt, dtype, out_dtype, gap, G):
+    """Every 16th token weighs 2^gap times what the others do, and only the others have values outside channel 0."""
+    n, D, g = 1003, 128, torch.Generator().manual_seed(gap)
+    dirn = torch.randn(D, generator=g)
+    q = dirn.repeat(1, G, 1).to(DT[dtype])
+    k = torch.randn(n, 1, D, generator=g) * 0.05
+    v = (torch.randn(n, 1, D, generator=g) + 1.0).clamp(-4, 6) * 256
+    heavy = torch.arange(n) % 16 == 3
+    scale = D ** -0.5
+    k[heavy, 0] = dirn * (gap * math.log(2.0) / (scale * float(dirn.square().sum())))
+    v[heavy] = 0.0
+    v[heavy, 0, 0] = 256.0
+    rows = Rows(att, fmt, dtype, k, v)
+    out, lse = rows.attend(q.to(DEV), out_dtype, scale)
+    want, want_lse, w, reach = rows.exact(q, scale)
+    err = np.abs(f64(out)[0] - want)
+    assert (err <= bound(rows, fmt, out_dtype, want, w, reach)).all(), (err / np.abs(want))[:, 1:].max()
+    assert (np.abs(f64(lse)[0] - want_lse) <= lse_bound(D, want_lse, reach)).all()
