@@ -178,9 +178,9 @@ FT_API ft_status ft_kv_gather(const ft_kv_cache* cache_host, const ft_page_table
  * natural logarithm of sum_j exp(scale * q . k_j).
  * q: dtype bf16 or f16, equal to the cache's where that is 16-bit; out:
  * out_dtype of q's or FT_DT_F32.  Scores, statistics and sums are fp32; the
- * weights enter the value product as two 16-bit terms (16-bit caches and
- * fp32 outputs) or one f16 term; f16 terms end 2^36 below the heaviest weight
- * (of 8- and 4-bit rows: weight times 2^value exponent).
+ * weights enter the value product as two 16-bit terms (bf16 for bf16 caches,
+ * f16 otherwise: f16 terms end 2^36 below the heaviest weight, of 8- and 4-bit
+ * rows weight times 2^value exponent).  A 16-bit output is the fp32 one rounded.
  * ws: device scratch of ft_attn_decode_workspace bytes, 256-byte aligned, of
  * any content; calls that may overlap need separate ones.
  * Limits: Hq a multiple of Hkv, T * Hq < 2^31, T <= 65535.  Work is numbered

@@ -3,6 +3,6 @@
 
 namespace ft {
 ft_status attend_bf16(AttnArgs& a, const AttnShape& sh, cudaStream_t s) {
-  return launch_shape<FT_KV_BF16, true>(a, sh, s);
+  return launch_shape<FT_KV_BF16>(a, sh, s);
 }
 }  // namespace ft

@@ -3,6 +3,6 @@
 
 namespace ft {
 ft_status attend_e4m3(AttnArgs& a, const AttnShape& sh, cudaStream_t s) {
-  return a.out_f32 ? launch_shape<FT_KV_E4M3, true>(a, sh, s) : launch_shape<FT_KV_E4M3, false>(a, sh, s);
+  return launch_shape<FT_KV_E4M3>(a, sh, s);
 }
 }  // namespace ft

@@ -3,6 +3,6 @@
 
 namespace ft {
 ft_status attend_f16(AttnArgs& a, const AttnShape& sh, cudaStream_t s) {
-  return launch_shape<FT_KV_F16, true>(a, sh, s);
+  return launch_shape<FT_KV_F16>(a, sh, s);
 }
 }  // namespace ft

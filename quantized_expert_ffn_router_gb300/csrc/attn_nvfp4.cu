@@ -3,6 +3,6 @@
 
 namespace ft {
 ft_status attend_nvfp4(AttnArgs& a, const AttnShape& sh, cudaStream_t s) {
-  return a.out_f32 ? launch_shape<FT_KV_NVFP4, true>(a, sh, s) : launch_shape<FT_KV_NVFP4, false>(a, sh, s);
+  return launch_shape<FT_KV_NVFP4>(a, sh, s);
 }
 }  // namespace ft

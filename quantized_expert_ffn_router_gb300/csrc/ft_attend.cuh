@@ -483,7 +483,7 @@ struct Feeder {
 // reference by this much (in powers of two), not at every new maximum.
 constexpr float kSlack = 4.f;
 
-template <typename X, bool TWO, int NT>
+template <typename X, int NT>
 __device__ __forceinline__ void add_values(uint32_t at, uint32_t vnotes, int u, int g, int q,
                                            const uint32_t (&hi)[NT][2], const uint32_t (&lo)[NT][2],
                                            float (&acc)[X::MT][NT][4]) {
@@ -491,7 +491,7 @@ __device__ __forceinline__ void add_values(uint32_t at, uint32_t vnotes, int u, 
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       mma<X::kF16>(acc[mt][n], a0, a1, a2, a3, hi[n][0], hi[n][1]);
-      if (TWO) mma<X::kF16>(acc[mt][n], a0, a1, a2, a3, lo[n][0], lo[n][1]);
+      mma<X::kF16>(acc[mt][n], a0, a1, a2, a3, lo[n][0], lo[n][1]);
     }
   };
 #pragma unroll
@@ -554,13 +554,10 @@ __device__ __noinline__ void empty_row(const AttnArgs& a, int t) {
   }
 }
 
-// TWO: weights as two 16-bit terms.  16-bit caches always: one term would add
-// its rounding to the output's own (f16: 2.4e-4 of the norm where two leave
-// 2.0e-4), and two cost 1% where HBM is the bound (f16, 32 rows up to 8192:
-// 62.5 us against 61.7).  8- and 4-bit caches where the output is fp32: their
-// values are f16 products whose weights, in f16, are eight times finer than a
-// bf16 output.
-template <int FMT, int DP, int NT, int COLS, bool TWO>
+// Weights enter the value product as two 16-bit terms, so that an output is
+// that of fp32 weights (one f16 term added 2^-12 of each weight: of 16-bit
+// outputs one in twenty was rounded the other way).
+template <int FMT, int DP, int NT, int COLS>
 __global__ void __launch_bounds__(Deal<FMT, DP, NT, COLS>::kThreads, Deal<FMT, DP, NT, COLS>::kCtas)
     attend_kernel(const __grid_constant__ AttnArgs a) {
   using X = Deal<FMT, DP, NT, COLS>;
@@ -845,15 +842,12 @@ __global__ void __launch_bounds__(Deal<FMT, DP, NT, COLS>::kThreads, Deal<FMT, D
             }
             const uint32_t h = pack16<X::kF16>(p0, p1);
             hi[n][r] = transpose8x8(h);
-            lo[n][r] = 0;
-            if (TWO) {
-              const float2 back = unpack16<X::kF16>(h);
-              lo[n][r] = transpose8x8(pack16<X::kF16>(p0 - back.x, p1 - back.y));
-            }
+            const float2 back = unpack16<X::kF16>(h);
+            lo[n][r] = transpose8x8(pack16<X::kF16>(p0 - back.x, p1 - back.y));
           }
         }
         const uint32_t vnotes = note + X::kTok + X::kKeyBlk;
-        add_values<X, TWO, NT>(at + X::kSide + voff, vnotes, u, g, q, hi, lo, acc);
+        add_values<X, NT>(at + X::kSide + voff, vnotes, u, g, q, hi, lo, acc);
       }
 
       last = at;
@@ -879,7 +873,7 @@ __global__ void __launch_bounds__(Deal<FMT, DP, NT, COLS>::kThreads, Deal<FMT, D
       }
     const bool whole = unit.rest == 0 && unit.tile0 == 0;
     const int part = blockIdx.x * 2 + (unit.tile0 == 0 ? 1 : 0);
-    const bool f32 = !whole || (X::kQuant ? TWO : a.out_f32 != 0);
+    const bool f32 = !whole || a.out_f32 != 0;
     const int64_t on = whole ? a.out_head : DP;  // to the next head
     const auto place_of_head = [&](int h) {
       return whole ? static_cast<int64_t>(t) * a.out_tok + static_cast<int64_t>(hq0 + h) * a.out_head
@@ -1011,10 +1005,10 @@ __global__ void __launch_bounds__(Deal<FMT, DP, NT, COLS>::kThreads, Deal<FMT, D
 }
 
 // ------------------------------------------------------------------ host side ---
-template <int FMT, int DP, int NT, int COLS, bool TWO>
+template <int FMT, int DP, int NT, int COLS>
 ft_status launch(AttnArgs& a, cudaStream_t s) {
   using X = Deal<FMT, DP, NT, COLS>;
-  const auto kernel = attend_kernel<FMT, DP, NT, COLS, TWO>;
+  const auto kernel = attend_kernel<FMT, DP, NT, COLS>;
   constexpr int smem = X::kRing + X::kRest;
   ft_status st = ensure_dyn_smem(reinterpret_cast<const void*>(kernel), smem, "attn_decode");
   if (st != FT_OK) return st;
@@ -1040,20 +1034,20 @@ ft_status launch(AttnArgs& a, cudaStream_t s) {
   return launch_pdl(kernel, dim3(a.workers), X::kThreads, smem, s, a, "attn_decode");
 }
 
-template <int FMT, int DP, int NT, bool TWO>
+template <int FMT, int DP, int NT>
 ft_status launch_columns(AttnArgs& a, const AttnShape& sh, cudaStream_t s) {
-  if (sh.columns == 4) return launch<FMT, DP, NT, 4, TWO>(a, s);
-  if (sh.columns == 2) return launch<FMT, DP, NT, 2, TWO>(a, s);
-  return launch<FMT, DP, NT, 1, TWO>(a, s);
+  if (sh.columns == 4) return launch<FMT, DP, NT, 4>(a, s);
+  if (sh.columns == 2) return launch<FMT, DP, NT, 2>(a, s);
+  return launch<FMT, DP, NT, 1>(a, s);
 }
 
-template <int FMT, bool TWO>
+template <int FMT>
 ft_status launch_shape(AttnArgs& a, const AttnShape& sh, cudaStream_t s) {
   switch (sh.DP) {
-    case 64: return sh.NT == 2 ? launch_columns<FMT, 64, 2, TWO>(a, sh, s) : launch<FMT, 64, 1, 1, TWO>(a, s);
-    case 128: return sh.NT == 2 ? launch_columns<FMT, 128, 2, TWO>(a, sh, s) : launch<FMT, 128, 1, 1, TWO>(a, s);
-    case 192: return launch_columns<FMT, 192, 1, TWO>(a, sh, s);
-    default: return launch_columns<FMT, 256, 1, TWO>(a, sh, s);
+    case 64: return sh.NT == 2 ? launch_columns<FMT, 64, 2>(a, sh, s) : launch<FMT, 64, 1, 1>(a, s);
+    case 128: return sh.NT == 2 ? launch_columns<FMT, 128, 2>(a, sh, s) : launch<FMT, 128, 1, 1>(a, s);
+    case 192: return launch_columns<FMT, 192, 1>(a, sh, s);
+    default: return launch_columns<FMT, 256, 1>(a, sh, s);
   }
 }
 

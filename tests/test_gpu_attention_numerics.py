@@ -108,3 +108,21 @@ def test_light_weights_beside_heavy_ones(att, fmt, dtype, out_dtype, gap, G):
     err = np.abs(f64(out)[0] - want)
     assert (err <= bound(rows, fmt, out_dtype, want, w, reach)).all(), (err / np.abs(want))[:, 1:].max()
     assert (np.abs(f64(lse)[0] - want_lse) <= lse_bound(D, want_lse, reach)).all()
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "nvfp4", "bf16", "f16"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D,Hkv,G,n", [(128, 2, 4, 3000), (64, 1, 40, 700), (256, 3, 1, 90), (192, 2, 16, 1)])
+def test_sixteen_bit_outputs_are_the_fp32_ones_rounded(att, fmt, dtype, D, Hkv, G, n):
+    """The output's type decides the last rounding and nothing before it."""
+    if fmt in ("bf16", "f16") and fmt != dtype:
+        pytest.skip("a 16-bit cache takes queries of its own type")
+    g = torch.Generator().manual_seed(D + n)
+    k, v = torch.randn(n, Hkv, D, generator=g), torch.randn(n, Hkv, D, generator=g)
+    q = torch.randn(1, Hkv * G, D, generator=g).to(DT[dtype]).to(DEV)
+    rows = Rows(att, fmt, dtype, k, v)
+    short, lse = rows.attend(q, dtype, D ** -0.5)
+    full, full_lse = rows.attend(q, "f32", D ** -0.5)
+    assert torch.equal(short, full.to(DT[dtype])) and torch.equal(lse, full_lse)
+    want, _, w, reach = rows.exact(q, D ** -0.5)
+    assert (np.abs(f64(full)[0] - want) <= bound(rows, fmt, "f32", want, w, reach)).all()
