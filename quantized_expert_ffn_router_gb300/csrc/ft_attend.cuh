@@ -798,7 +798,8 @@ __global__ void __launch_bounds__(Deal<FMT, DP, NT, COLS>::kThreads, Deal<FMT, D
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               float& x = s[u][n][2 * r + i];
-              x = X::kQuant ? fmaf(x * ks, mul[n][i], ev) : x * mul[n][i];
+              // the key's exponent last: q.k of codes stays in range, and so does every finite score
+              x = X::kQuant ? fmaf(x * mul[n][i], ks, ev) : x * mul[n][i];
               if (part) x = ok ? x : -INFINITY;
               more |= x > m[n][i] + (kSlack + X::kLift);
             }

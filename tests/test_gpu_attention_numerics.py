@@ -126,3 +126,17 @@ def test_sixteen_bit_outputs_are_the_fp32_ones_rounded(att, fmt, dtype, D, Hkv, 
     assert torch.equal(short, full.to(DT[dtype])) and torch.equal(lse, full_lse)
     want, _, w, reach = rows.exact(q, D ** -0.5)
     assert (np.abs(f64(full)[0] - want) <= bound(rows, fmt, "f32", want, w, reach)).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3", "nvfp4"])
+def test_keys_near_the_end_of_the_range(att, fmt):
+    """Scores of 2^121: far apart, but finite, so the largest takes all."""
+    n, D, g = 9, 64, torch.Generator().manual_seed(2)
+    u = torch.randn(D, generator=g).bfloat16().float()
+    k = (torch.arange(n) - 4).view(n, 1, 1) * 2.0 ** 116 * u
+    rows = Rows(att, fmt, "bf16", k, torch.randn(n, 1, D, generator=g))
+    q = torch.stack([u, -u])[None].bfloat16().to(DEV)
+    out, lse = rows.attend(q, "f32", 0.125)
+    assert (np.abs(f64(out)[0] - rows.v[[n - 1, 0], 0]) <= 2.0 ** -20 * np.abs(rows.v[[n - 1, 0], 0])).all()
+    top = 0.125 * (rows.k[:, 0] @ f64(q)[0].T).max(0)
+    assert (np.abs(f64(lse)[0] - top) <= 2.0 ** -20 * top).all()
