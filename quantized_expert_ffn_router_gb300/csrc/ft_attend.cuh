@@ -643,8 +643,9 @@ __global__ void __launch_bounds__(Deal<FMT, DP, NT, COLS>::kThreads, Deal<FMT, D
 #pragma unroll 1
   while (true) {
     // Queries as B operands.  Where the products are f16, a head's row is
-    // scaled by a power of two, its largest element to [128, 256): exact,
-    // undone in the scores' factor.
+    // scaled by a power of two, undone in the scores' factor: its largest
+    // element to [2^14, 2^15), so that bf16's eight bits are kept down to 2^31
+    // below it (f16's steps end at 2^-24), and f16's eleven down to 2^28.
     const auto place = [&](int h, uint4 raw) {
       if (X::kF16) {
         float x[8];
@@ -659,7 +660,7 @@ __global__ void __launch_bounds__(Deal<FMT, DP, NT, COLS>::kThreads, Deal<FMT, D
         }
         // positive floats order as their bits do
         amax = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(amax)));
-        int e = 134 - static_cast<int>(__float_as_uint(amax) >> 23);
+        int e = 141 - static_cast<int>(__float_as_uint(amax) >> 23);
         e = amax > 0.f && amax <= 3.4028235e38f ? min(max(e, -120), 120) : 0;
         const float up = __uint_as_float((127 + e) << 23);
         raw = make_uint4(pack16<true>(x[0] * up, x[1] * up), pack16<true>(x[2] * up, x[3] * up),

@@ -128,6 +128,24 @@ def test_sixteen_bit_outputs_are_the_fp32_ones_rounded(att, fmt, dtype, D, Hkv, 
     assert (np.abs(f64(full)[0] - want) <= bound(rows, fmt, "f32", want, w, reach)).all()
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "nvfp4"])
+@pytest.mark.parametrize("small", [-12, -20, -28])
+def test_query_elements_far_below_the_largest(att, fmt, small):
+    """bf16 queries keep their eight bits 2^28 below the head's largest element: keys are zero where that one is."""
+    n, D, g = 200, 64, torch.Generator().manual_seed(1)
+    q = torch.zeros(1, 4, D)
+    q[..., 0] = 1.9921875
+    q[0, :, 1] = torch.tensor([1.9921875, 1.7578125, -1.1796875, 1.0078125]) * 2.0 ** small
+    k = torch.zeros(n, 1, D)
+    k[:, 0, 1] = (torch.randint(-16, 17, (n,), generator=g) / 4.0) * 2.0 ** -small
+    rows = Rows(att, fmt, "bf16", k, torch.randn(n, 1, D, generator=g))
+    q = q.bfloat16().to(DEV)
+    out, lse = rows.attend(q, "f32", 1.0)
+    want, want_lse, w, reach = rows.exact(q, 1.0)
+    assert (np.abs(f64(out)[0] - want) <= bound(rows, fmt, "f32", want, w, reach)).all()
+    assert (np.abs(f64(lse)[0] - want_lse) <= lse_bound(D, want_lse, reach)).all()
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3", "nvfp4"])
 def test_keys_near_the_end_of_the_range(att, fmt):
     """Scores of 2^121: far apart, but finite, so the largest takes all."""
