@@ -158,3 +158,16 @@ def test_keys_near_the_end_of_the_range(att, fmt):
     assert (np.abs(f64(out)[0] - rows.v[[n - 1, 0], 0]) <= 2.0 ** -20 * np.abs(rows.v[[n - 1, 0], 0])).all()
     top = 0.125 * (rows.k[:, 0] @ f64(q)[0].T).max(0)
     assert (np.abs(f64(lse)[0] - top) <= 2.0 ** -20 * top).all()
+
+
+def test_a_score_near_the_lowest_number(att):
+    """A lone token takes all the weight, whatever its score."""
+    D = 64
+    k, v = torch.zeros(1, 1, D), torch.randn(1, 1, D, generator=torch.Generator().manual_seed(3))
+    k[0, 0, 0] = 2.0 ** 64
+    q = torch.zeros(1, 2, D)
+    q[..., 0] = -1.3046875 * 2.0 ** 63  # -2.2e38, -3.2e38 in powers of two
+    rows = Rows(att, "bf16", "bf16", k, v)
+    out, lse = rows.attend(q.bfloat16().to(DEV), "f32", 1.0)
+    assert (np.abs(f64(out)[0] - rows.v[0]) <= 2.0 ** -20 * np.abs(rows.v[0])).all()
+    assert (np.abs(f64(lse)[0] + 1.3046875 * 2.0 ** 127) <= 2.0 ** 127 * 2.0 ** -20).all()
