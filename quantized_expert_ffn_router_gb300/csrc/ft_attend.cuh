@@ -166,8 +166,10 @@ struct Deal {
   // How far the reference lies below the greatest score.  f16 weights reach
   // 2^(11 + kSlack), the top of its range, so that what rounds to nothing (f16's
   // steps end at 2^-24) is 2^-36 of the heaviest: with the heaviest at 1, a
-  // token 18 nats above 16384 others took 6% of the norm from them.
-  static constexpr int kLift = kF16 ? 11 : 0;
+  // token 18 nats above 16384 others took 6% of the norm from them.  bf16 has
+  // fp32's range, in its values too: weights of 2^-24 keep the sums of 2^24
+  // tokens of the largest values inside it.
+  static constexpr int kLift = kF16 ? 11 : -24;
   static constexpr int EK = !kQuant ? 8 : !kBlocks ? 16 : DP % 128 == 0 ? 32 : 16;
   static constexpr int EV = !kQuant ? 8 : !kBlocks ? (DP % 128 == 0 ? 16 : 8) : DP % 256 == 0 ? 32 : DP % 128 == 0 ? 16 : 8;
   static constexpr int NK = DP / (4 * EK), NV = DP / (8 * EV);

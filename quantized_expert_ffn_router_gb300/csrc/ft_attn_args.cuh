@@ -90,9 +90,9 @@ __device__ __forceinline__ Begin begin_of(const AttnArgs& a, int c) {
 }
 
 // Softmax weights are taken in powers of two, 2^(x - m), with a reference m
-// that is `lift` below (about) the greatest score.  A maximum over nothing is
-// kLowest: finite, so that 2^(-inf - kLowest) and 2^(kLowest - m) are 0 and not
-// NaN.
+// that is `lift` below (about) the greatest score, above it where negative.  A
+// maximum over nothing is kLowest: finite, so that 2^(-inf - kLowest) and
+// 2^(kLowest - m) are 0 and not NaN.
 constexpr float kLowest = -3.4028235e38f;  // the lowest fp32
 
 __device__ __forceinline__ float exp2_approx(float x) {

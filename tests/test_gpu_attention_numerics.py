@@ -171,3 +171,22 @@ def test_a_score_near_the_lowest_number(att):
     out, lse = rows.attend(q.bfloat16().to(DEV), "f32", 1.0)
     assert (np.abs(f64(out)[0] - rows.v[0]) <= 2.0 ** -20 * np.abs(rows.v[0])).all()
     assert (np.abs(f64(lse)[0] + 1.3046875 * 2.0 ** 127) <= 2.0 ** 127 * 2.0 ** -20).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "f16", "e4m3", "nvfp4"])
+@pytest.mark.parametrize("G", [2, 20])
+def test_sums_of_the_largest_values(att, fmt, G):
+    """A mean of values at the end of the type's range is inside it, of whichever number of tokens."""
+    n, D, g = 1501, 64, torch.Generator().manual_seed(6)
+    dtype = "f16" if fmt == "f16" else "bf16"
+    most = {"bf16": 3.3895313892515355e38, "f16": 65504.0}.get(fmt, 2.0 ** 126)  # 8- and 4-bit: read back below 2^128
+    v = torch.full((n, 1, D), most)
+    v[..., 1] *= torch.randn(n, 1, generator=g).sign()
+    v[..., 2:] *= torch.rand(n, 1, D - 2, generator=g) * 2 - 1
+    rows = Rows(att, fmt, dtype, torch.randn(n, 1, D, generator=g) * 0.3, v)
+    q = torch.randn(1, G, D, generator=g).to(DT[dtype]).to(DEV)
+    for out_dtype in (dtype, "f32"):
+        out, _ = rows.attend(q, out_dtype, D ** -0.5)
+        want, _, w, reach = rows.exact(q, D ** -0.5)
+        assert torch.isfinite(out).all()
+        assert (np.abs(f64(out)[0] - want) <= bound(rows, fmt, out_dtype, want, w, reach)).all()
