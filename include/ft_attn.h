@@ -174,7 +174,8 @@ FT_API ft_status ft_kv_gather(const ft_kv_cache* cache_host, const ft_page_table
  * max(0, lens[t] - window) <= j < lens[t] (window 0: all), key and value head
  * h / (Hq / Hkv).  lens[t] counts the new token, whose row the caller has
  * appended; it is held to max_pages * page_size.  A row that sees nothing
- * gives zeros and lse = -inf.  lse [T, Hq] fp32 (NULL: not written) is the
+ * gives zeros and lse = -inf.  An infinity or NaN among the values of a 16-bit
+ * cache that count gives NaN in its channel.  lse [T, Hq] fp32 (NULL: not written) is the
  * natural logarithm of sum_j exp(scale * q . k_j).
  * q: dtype bf16 or f16, equal to the cache's where that is 16-bit; out:
  * out_dtype of q's or FT_DT_F32.  Scores, statistics and sums are fp32; the

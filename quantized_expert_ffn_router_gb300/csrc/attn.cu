@@ -155,14 +155,17 @@ __global__ void __launch_bounds__(kJoinThreads<kHeads>) join_kernel(const __grid
   if (!live) return;
   const int hq = kv_head * a.G + hg;
   const float inv = l == 0.f ? 0.f : 1.f / l;
+  const bool rows16 = a.kv.row_bytes == 2 * a.kv.D;
 #pragma unroll
   for (int i = 0; i < N; ++i)
     if (2 * lane + 64 * i < a.kv.D) {
       const int64_t to = static_cast<int64_t>(t) * a.out_tok + static_cast<int64_t>(hq) * a.out_head + 2 * lane + 64 * i;
+      float x = acc[i].x * inv, y = acc[i].y * inv;
+      if (rows16) x = finite_or_nan(x), y = finite_or_nan(y);
       if (a.out_f32)
-        *reinterpret_cast<float2*>(static_cast<float*>(a.out) + to) = make_float2(acc[i].x * inv, acc[i].y * inv);
+        *reinterpret_cast<float2*>(static_cast<float*>(a.out) + to) = make_float2(x, y);
       else
-        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + to) = pack_out(a, acc[i].x * inv, acc[i].y * inv);
+        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + to) = pack_out(a, x, y);
     }
   if (lane == 0) store_lse(a, t, hq, m, l);
 }

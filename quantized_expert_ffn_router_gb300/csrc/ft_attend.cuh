@@ -901,11 +901,12 @@ __global__ void __launch_bounds__(Deal<FMT, DP, NT, COLS>::kThreads, Deal<FMT, D
       for (int i = 0; i < 2; ++i) {
         if (h + i >= heads) continue;
         const int64_t at_d = to + i * on + d;
+        float x = c[i] * norm[i], y = c[2 + i] * norm[i];
+        if (!X::kQuant && whole) x = finite_or_nan(x), y = finite_or_nan(y);
         if (f32)
-          *reinterpret_cast<float2*>((whole ? static_cast<float*>(a.out) : a.part_o) + at_d) =
-              make_float2(c[i] * norm[i], c[2 + i] * norm[i]);
+          *reinterpret_cast<float2*>((whole ? static_cast<float*>(a.out) : a.part_o) + at_d) = make_float2(x, y);
         else
-          *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at_d) = pack_out(a, c[i] * norm[i], c[2 + i] * norm[i]);
+          *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at_d) = pack_out(a, x, y);
       }
     };
     if constexpr (COLS > 1) {  // a warp has its heads' sums

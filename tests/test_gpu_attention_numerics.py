@@ -190,3 +190,18 @@ def test_sums_of_the_largest_values(att, fmt, G):
         want, _, w, reach = rows.exact(q, D ** -0.5)
         assert torch.isfinite(out).all()
         assert (np.abs(f64(out)[0] - want) <= bound(rows, fmt, out_dtype, want, w, reach)).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "f16"])
+@pytest.mark.parametrize("G", [4, 40])
+@pytest.mark.parametrize("n", [20, 300])
+def test_an_infinite_value_that_counts_is_nan_in_its_channel_only(att, fmt, G, n):
+    D, g = 64, torch.Generator().manual_seed(4)
+    k, v = torch.randn(n, 2, D, generator=g), torch.randn(n, 2, D, generator=g)
+    q = torch.randn(1, 2 * G, D, generator=g).to(DT[fmt]).to(DEV)
+    plain, lse = Rows(att, fmt, fmt, k, v).attend(q, fmt, 0.125)
+    v[n // 4, 1, 5] = math.inf
+    out, inf_lse = Rows(att, fmt, fmt, k, v).attend(q, fmt, 0.125)
+    assert torch.isnan(out[0, G:, 5]).all() and torch.equal(lse, inf_lse)
+    out[0, G:, 5] = plain[0, G:, 5]
+    assert torch.equal(out, plain)
