@@ -41,7 +41,9 @@ enum { FT_DT_BF16 = 0, FT_DT_F16 = 1, FT_DT_F32 = 2 };
  *     the smallest integer >= -64 with max|x| <= 6 * 448 * 2^e; b the nearest
  *     E4M3 value of max|block| * 2^-e / 6; code the nearest E2M1 value of
  *     x * 2^-e / b (0 where b is 0).
- * Exponents are stored as one byte e + 127 a row.  Infinities count as the
+ * Exponents are stored as one byte e + 127 a row; bytes that no row is written
+ * with (e below -64, above 120, with FT_KV_NVFP4 above 117) are read as the
+ * nearest that one is.  Infinities count as the
  * largest finite value that the row's exponent can hold and do not raise it;
  * a NaN stays NaN (with NVFP4, its whole block of 16).
  */

@@ -157,6 +157,7 @@ constexpr int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
 // COLS: warps side by side over a block's heads.
 template <int FMT, int DP, int NT, int COLS>
 struct Deal {
+  static constexpr int kFmt = FMT;
   static constexpr int kWarps = COLS == 1 ? 4 : COLS, kThreads = kWarps * 32;
   static constexpr int kWarpsT = COLS == 1 ? 4 : 1;  // warps side by side over tokens
   static constexpr int kRings = kWarpsT, kFill = 32 * COLS;  // threads that fill a ring
@@ -386,8 +387,7 @@ struct Feeder {
         uint32_t kw, vw;
         asm volatile("ld.shared.u32 %0, [%1];" : "=r"(kw) : "r"(raw + lane * 4));
         asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vw) : "r"(raw + X::TS * 4 + lane * 4));
-        // exponent bytes as writers store them; others are held to 2^-100 .. 2^123
-        const uint32_t kb = min(max((kw >> sh) & 0xffu, 27u), 250u), vb = min(max((vw >> sh) & 0xffu, 27u), 250u);
+        const uint32_t kb = held_exponent<X::kFmt>((kw >> sh) & 0xffu), vb = held_exponent<X::kFmt>((vw >> sh) & 0xffu);
         const float ks = ok ? __uint_as_float(kb << 23) : 0.f;
         const float ev = ok ? static_cast<float>(static_cast<int>(vb) - 127) : -INFINITY;
         const float iv = ok ? __uint_as_float((254u - vb) << 23) : 0.f;

@@ -11,7 +11,16 @@
 
 namespace ft {
 
-constexpr int kMinExponent = -64;  // of a row's power-of-two scale
+// A row's power-of-two scale: the least by definition, and the greatest that
+// fp32 rows need (448 * 2^119, 6 * 448 * 2^116 < 2^128).  Exponent bytes outside,
+// which no row is written with, are read as the nearer of the two.
+constexpr int kMinExponent = -64;
+constexpr int max_exponent(int fmt) { return fmt == FT_KV_NVFP4 ? 117 : 120; }
+
+template <int FMT>
+__device__ __forceinline__ uint32_t held_exponent(uint32_t byte) {
+  return min(max(byte, 127u + kMinExponent), 127u + max_exponent(FMT));
+}
 
 // Cache and page table as kernel arguments.
 struct KvView {

@@ -205,3 +205,40 @@ def test_an_infinite_value_that_counts_is_nan_in_its_channel_only(att, fmt, G, n
     assert torch.isnan(out[0, G:, 5]).all() and torch.equal(lse, inf_lse)
     out[0, G:, 5] = plain[0, G:, 5]
     assert torch.equal(out, plain)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "nvfp4"])
+def test_exponent_bytes_outside_the_format(att, fmt):
+    """Bytes that no row is written with: reading back and attending take them for the nearest that one is (2^-64, and
+    2^120 or, with block scales, 2^117)."""
+    D, g = 64, torch.Generator().manual_seed(5)
+    byte = torch.tensor([0, 1, 40, 62, 63, 64, 127, 243, 244, 245, 247, 248, 250, 254, 255], dtype=torch.uint8)
+    n = len(byte)
+    x = torch.randint(-6, 7, (n, 1, D), generator=g).float()
+    x[..., ::16] = 6.0  # every block's largest
+    rows = Rows(att, fmt, "bf16", x * 448 / 6 if fmt == "e4m3" else x, x * 0.5, page=16)
+    cache, at = rows.cache, int(rows.table[0, 0])
+    was = {w: f64(getattr(cache, w + "_scale"))[at, 0, :n] for w in "kv"}
+    held = np.clip(byte.numpy().astype(np.float64), 63, 247 if fmt == "e4m3" else 244)
+    for w in "kv":
+        getattr(cache, w + "_scale")[at, 0, :n] = byte.to(DEV)
+        setattr(rows, w, getattr(rows, w) * 2.0 ** (held - was[w])[:, None, None])
+    ko, vo = torch.empty(n, 1, D, device=DEV), torch.empty(n, 1, D, device=DEV)
+    pos, seq = torch.arange(n, dtype=torch.int32, device=DEV), torch.zeros(n, dtype=torch.int32, device=DEV)
+    att.kv_gather(cache, rows.table, pos, ko, vo, seq=seq)
+    with np.errstate(over="ignore"):
+        assert (f64(ko) == rows.k.astype(np.float32)).all() and (f64(vo) == rows.v.astype(np.float32)).all()
+    # one token at a time: its value is the output, its key the score
+    q = torch.zeros(1, 1, D, dtype=torch.bfloat16, device=DEV)
+    q[..., 0] = 2.0 ** -30
+    for j in range(n):
+        one = torch.tensor([j + 1], dtype=torch.int32, device=DEV)
+        out, lse = torch.zeros(1, 1, D, device=DEV), torch.zeros(1, 1, device=DEV)
+        ws = torch.zeros(att.attn_decode_workspace(1, 1, 1, D), dtype=torch.uint8, device=DEV)
+        att.attn_decode(cache, q, rows.table, one, out, ws, scale=2.0 ** -30, window=1, lse=lse)
+        with np.errstate(over="ignore"):
+            want = rows.v[j, 0].astype(np.float32)
+        got, score = f64(out)[0, 0], rows.k[j, 0, 0] * 2.0 ** -60
+        fin = np.isfinite(want)
+        assert (np.abs(got - want)[fin] <= 2.0 ** -20 * np.abs(want)[fin]).all() and (got[~fin] == want[~fin]).all()
+        assert abs(float(lse) - score) <= 2.0 ** -20 * (1 + abs(score))
