@@ -610,6 +610,8 @@ __global__ void __launch_bounds__(512, LAY == kAny ? 1 : 2) write_kernel(const _
         const float amax = row_largest(fmaxf(m[0], m[1])), part = amax * 0x1p-19f;
         e = row_exponent(amax, top, top_bits);
         const float inv = pow2f(-e);
+        // An infinity anywhere in a rotated row leaves all of its lanes in doubt: amax - part is NaN there, whose
+        // exponent is one more than infinity's.
         bool all = odd || (exact && row_exponent(amax - part, top, top_bits) != row_exponent(amax + part, top, top_bits));
         uint32_t code[2], differ[2], block[2];
         float per = 0.f;
