@@ -701,7 +701,8 @@ template <int FMT, int DT>
 __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadArgs a) {
   constexpr int W = FMT == FT_KV_NVFP4 ? 2 : FMT == FT_KV_E4M3 ? 4 : 8;  // words of 16 elements
   const int l = threadIdx.x & ((1 << a.lanes_log2) - 1);
-  const uint32_t at = (blockIdx.x * 256u + threadIdx.x) >> a.lanes_log2;
+  // the launch has up to 2^35 threads, of up to 2^31 rows
+  const uint32_t at = static_cast<uint32_t>((uint64_t{blockIdx.x} * 256 + threadIdx.x) >> a.lanes_log2);
   pdl_wait();
   if (at >= a.rows || l * 16 >= a.kv.D) return;
   const uint32_t token = fast_div(at, a.by_heads), head = at - token * a.kv.Hkv;

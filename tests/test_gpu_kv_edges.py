@@ -1,5 +1,6 @@
 """The paged cache's rows where numbers or sizes are out of the ordinary:
-infinities beside rotated keys that lie next to a border between codes."""
+infinities, keys next to a border between codes, and more threads than 32 bits
+number."""
 
 import math
 
@@ -76,3 +77,18 @@ def test_rotated_rows_next_to_borders(att, fmt, layout, D, rot, infinite):
     want = quantised(fmt, rotated(f64(k), [far] * T, turn, layout, 1.0))
     assert (f64(ko) == want).all(), int((f64(ko) != want).sum())
     assert (f64(vo) == quantised(fmt, -f64(k))).all()
+
+
+def test_gather_of_more_threads_than_32_bits_number(att):
+    """2^28 + 64 rows of 256 channels, 16 threads a row: the last row is read (its page is a bad one, which is
+    recorded).  The others are padding, and the output's rows are one place."""
+    T, D = (1 << 28) + 64, 256
+    cache = att.KvCache(att.FT_KV_E4M3, 1, D, 16, 1)
+    pos = torch.full((T,), -1, dtype=torch.int32, device=DEV)
+    pos[-1] = 3
+    seq = torch.zeros(1, dtype=torch.int32, device=DEV).expand(T).contiguous()
+    table = torch.full((1, 1), 7, dtype=torch.int32, device=DEV)
+    out = torch.full((1, 1, D), 5.0, dtype=torch.bfloat16, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    att.kv_gather(cache, table, pos, out.expand(T, 1, D), None, seq=seq, dev_status=status)
+    assert int(status.item()) == 5 and not out.any()
