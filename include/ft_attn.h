@@ -43,9 +43,10 @@ enum { FT_DT_BF16 = 0, FT_DT_F16 = 1, FT_DT_F32 = 2 };
  *     x * 2^-e / b (0 where b is 0).
  * Exponents are stored as one byte e + 127 a row; bytes that no row is written
  * with (e below -64, above 120, with FT_KV_NVFP4 above 117) are read as the
- * nearest that one is.  Infinities count as the
- * largest finite value that the row's exponent can hold and do not raise it;
- * a NaN stays NaN (with NVFP4, its whole block of 16).
+ * nearest that one is.  The maxima are those of the finite elements.  An
+ * infinity has the largest code: with FT_KV_E4M3 448 * 2^e, with FT_KV_NVFP4
+ * 6 * b * 2^e of its block, 0 where the block's finite elements are all 0.  A
+ * NaN stays NaN (with NVFP4, its whole block of 16).
  */
 enum { FT_KV_BF16 = 0, FT_KV_F16 = 1, FT_KV_E4M3 = 2, FT_KV_NVFP4 = 3 };
 
@@ -177,8 +178,8 @@ FT_API ft_status ft_kv_gather(const ft_kv_cache* cache_host, const ft_page_table
  * h / (Hq / Hkv).  lens[t] counts the new token, whose row the caller has
  * appended; it is held to max_pages * page_size.  A row that sees nothing
  * gives zeros and lse = -inf.  An infinity or NaN among the values of a 16-bit
- * cache that count gives NaN in its channel.  lse [T, Hq] fp32 (NULL: not written) is the
- * natural logarithm of sum_j exp(scale * q . k_j).
+ * cache that count gives NaN in its channel.  lse [T, Hq] fp32 (NULL: not
+ * written) is the natural logarithm of sum_j exp(scale * q . k_j).
  * q: dtype bf16 or f16, equal to the cache's where that is 16-bit; out:
  * out_dtype of q's or FT_DT_F32.  Scores, statistics and sums are fp32; the
  * weights enter the value product as two 16-bit terms (bf16 for bf16 caches,

@@ -92,3 +92,25 @@ def test_gather_of_more_threads_than_32_bits_number(att):
     status = torch.zeros(1, dtype=torch.int32, device=DEV)
     att.kv_gather(cache, table, pos, out.expand(T, 1, D), None, seq=seq, dev_status=status)
     assert int(status.item()) == 5 and not out.any()
+
+
+def test_infinities_in_nvfp4_blocks(att):
+    """An infinity takes the block's largest code, 6 times its scale: the scale is that of the finite values, so 0 where
+    there are none but zeros."""
+    D = 64
+    x = torch.zeros(3, 1, D)
+    x[0, 0, :4] = torch.tensor([math.inf, 3.0, -math.inf, -1.5])
+    x[0, 0, 20] = math.inf                      # alone in its block
+    x[0, 0, 32] = 768.0                         # decides the row's exponent, not the first block's scale
+    x[1, 0, 5] = -math.inf                      # alone in its row
+    x[2, 0, :16], x[2, 0, 16:32] = 6.0, math.inf
+    cache = att.KvCache(att.FT_KV_NVFP4, 1, D, 16, 1)
+    pages, pos = torch.zeros(3, 1, dtype=torch.int32, device=DEV), torch.arange(3, dtype=torch.int32, device=DEV)
+    att.kv_append(cache, x.bfloat16().to(DEV), -x.bfloat16().to(DEV), pages, pos)
+    ko, vo = torch.ones(3, 1, D, device=DEV), torch.ones(3, 1, D, device=DEV)
+    att.kv_gather(cache, pages, pos, ko, vo)
+    want = torch.zeros(3, 1, D)
+    want[0, 0, :4] = torch.tensor([3.0, 3.0, -3.0, -1.5])
+    want[0, 0, 32] = 768.0
+    want[2, 0, :16] = 6.0
+    assert torch.equal(ko.cpu(), want) and torch.equal(vo.cpu(), -want)
