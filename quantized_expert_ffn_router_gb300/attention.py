@@ -73,29 +73,36 @@ def _need(ok, message):
         raise FtError(FT_ERR_INVALID, message)
 
 
-def _check(status):
-    if status != FT_OK:
-        raise FtError(status, _lib.ft_last_error().decode())
-
-
-def _stream(t, stream):
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(t.device.index)
-    return stream if isinstance(stream, int) else stream.cuda_stream
-
-
 def _bad(message):
     raise FtError(FT_ERR_INVALID, message)
 
 
+def _check(status, elsewhere=False):
+    if status != FT_OK:
+        more = " (for the tensors are not all on one GPU)" if elsewhere else ""
+        raise FtError(status, _lib.ft_last_error().decode() + more)
+
+
+def _stream(dev, stream):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev) if dev >= 0 else 0
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
 # The checks below build their messages only when they fail: a decode step calls these functions once a layer, and
-# formatting them costs more than the launch.
+# formatting them costs more than the launch.  Where the tensors are not all on one GPU, a kernel may not use their
+# addresses: the call is made without its positions (or lengths) then, which the library refuses after its own checks.
 def _rows(t, name, shape, dtype):
     """A tensor of this [T, heads, D] and type as an ft_rows."""
     if t.shape != shape:
         _bad(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype is not dtype:
         _bad(f"{name}: dtype {t.dtype}, expected {dtype}")
+    return _rows_of(t, name, shape)
+
+
+def _rows_of(t, name, shape):
+    """The same of a tensor whose shape and type have been looked at."""
     s0, s1, s2 = t.stride()
     if s2 != 1:
         _bad(f"{name}: channels must be contiguous")
@@ -117,6 +124,14 @@ def _table(pages):
         _bad("pages: an int32 [sequences, pages] is needed")
     n, most = pages.shape
     return _TABLE.pack(pages.data_ptr(), s0, most, n)
+
+
+def _status(t):
+    if t is None:
+        return None
+    if t.dtype is not torch.int32 or t.numel() < 1:
+        _bad("dev_status: an int32 tensor is needed")
+    return t.data_ptr()
 
 
 def _ptr(t):
@@ -162,6 +177,7 @@ class KvCache:
         _need(width is not None, f"cache format {fmt}")
         k = arrays["k"]
         _need(k.dim() == 4, "cache arrays are [pages, heads, slots, ...]")
+        self.dev = k.get_device()
         n_pages, Hkv, page_size = k.shape[:3]
         strides = None
         for name in ("k", "v", "k_scale", "v_scale", "k_block", "v_block"):
@@ -173,6 +189,7 @@ class KvCache:
             shape = (n_pages, Hkv, page_size) + (() if name.endswith("_scale") else (w,))
             size = 2 if fmt in (FT_KV_BF16, FT_KV_F16) and name in ("k", "v") else 1
             _need(tuple(t.shape) == shape and t.element_size() == size, f"cache {name}: {tuple(t.shape)} {t.dtype}")
+            _need(t.get_device() == self.dev, f"cache {name}: on {t.device}, the keys are on {k.device}")
             _need(t.dim() == 3 or t.stride(3) == 1, f"cache {name}: rows must be contiguous")
             _need(all(s % w == 0 for s in t.stride()[:3]), f"cache {name}: strides must be whole rows")
             # a dimension of one place has no stride of its own
@@ -196,6 +213,7 @@ class Rope:
         _check(lib.ft_rope_freqs(rot_dim, base, scaling, factor, low, high, orig_len, host.data_ptr()))
         self.rot_dim, self.interleaved, self.mscale = rot_dim, bool(interleaved), float(mscale)
         self.freqs = host.to(device)
+        self.dev = self.freqs.get_device()
         self.desc = FtRopeTable(self.freqs.data_ptr(), rot_dim, int(self.interleaved), self.mscale)
         self._ref = ctypes.addressof(self.desc)
 
@@ -211,12 +229,14 @@ def _shape3(t, name, heads, D):
 def rope(x, pos, table: Rope, out, stream=None):
     """out[t, h] = x[t, h] rotated to pos[t] (ft_rope); out may be x."""
     lib = _lib or _bind()
-    dtype = x.dtype
+    dtype, dev = x.dtype, x.get_device()
     T, heads, D = shape = _shape3(x, "x", None, None)
-    status = lib.ft_rope(_rows(x, "x", shape, dtype), T, heads, D, _DT.get(dtype, -1), _ints(pos, "pos", T),
-                         table._ref, _rows(out, "out", shape, dtype), _stream(x, stream))
+    at = _ints(pos, "pos", T)
+    elsewhere = dev < 0 or table.dev != dev or (at is not None and pos.get_device() != dev) or out.get_device() != dev
+    status = lib.ft_rope(_rows_of(x, "x", shape), T, heads, D, _DT.get(dtype, -1), None if elsewhere else at,
+                         table._ref, _rows(out, "out", shape, dtype), _stream(dev, stream))
     if status:
-        _check(status)
+        _check(status, elsewhere)
 
 
 def kv_append(cache: KvCache, k, v, pages, pos, seq=None, rope: Rope | None = None, rope_pos=None, q=None, q_out=None,
@@ -224,23 +244,31 @@ def kv_append(cache: KvCache, k, v, pages, pos, seq=None, rope: Rope | None = No
     """Write k and v [T, Hkv, D] to position pos[t] of sequence seq[t] (default t); with `rope`, k is rotated first
     and q into q_out in the same launch (ft_kv_append)."""
     lib = _lib or _bind()
-    dtype = k.dtype
+    dtype, dev = k.dtype, k.get_device()
     shape = _shape3(k, "k", cache.Hkv, cache.D)
     T = shape[0]
+    at = _ints(pos, "pos", T)
+    elsewhere = (dev < 0 or cache.dev != dev or v.get_device() != dev or pages.get_device() != dev
+                 or (at is not None and pos.get_device() != dev) or (seq is not None and seq.get_device() != dev)
+                 or (dev_status is not None and dev_status.get_device() != dev)
+                 or (rope is not None and (rope.dev != dev or (rope_pos is not None and rope_pos.get_device() != dev))))
     Hq, q_rows, q_out_rows = 0, None, None
     if q is not None:
         q_shape = _shape3(q, "q", None, cache.D)
         Hq = q_shape[1]
         if q_shape[0] != T or q_out is None:
             _bad("kv_append: q has k's tokens, and needs q_out")
-        q_rows, q_out_rows = _rows(q, "q", q_shape, dtype), _rows(q_out, "q_out", q_shape, dtype)
+        if q.dtype is not dtype:
+            _bad(f"q: dtype {q.dtype}, expected {dtype}")
+        q_rows, q_out_rows = _rows_of(q, "q", q_shape), _rows(q_out, "q_out", q_shape, dtype)
+        elsewhere = elsewhere or q.get_device() != dev or q_out.get_device() != dev
     status = lib.ft_kv_append(
-        cache._ref, _rows(k, "k", shape, dtype), _rows(v, "v", shape, dtype), T, _DT.get(dtype, -1), _table(pages),
-        None if seq is None else _ints(seq, "seq", T), _ints(pos, "pos", T), None if rope is None else rope._ref,
-        None if rope_pos is None else _ints(rope_pos, "rope_pos", T), q_rows, Hq, q_out_rows,
-        None if dev_status is None else dev_status.data_ptr(), _stream(k, stream))
+        cache._ref, _rows_of(k, "k", shape), _rows(v, "v", shape, dtype), T, _DT.get(dtype, -1), _table(pages),
+        None if seq is None else _ints(seq, "seq", T), None if elsewhere else at, None if rope is None else rope._ref,
+        None if rope_pos is None else _ints(rope_pos, "rope_pos", T), q_rows, Hq, q_out_rows, _status(dev_status),
+        _stream(dev, stream))
     if status:
-        _check(status)
+        _check(status, elsewhere)
 
 
 def kv_gather(cache: KvCache, pages, pos, k_out, v_out, seq=None, dev_status=None, stream=None):
@@ -250,16 +278,21 @@ def kv_gather(cache: KvCache, pages, pos, k_out, v_out, seq=None, dev_status=Non
     some = k_out if k_out is not None else v_out
     if some is None:
         _bad("kv_gather: no output")
-    dtype = some.dtype
+    dtype, dev = some.dtype, some.get_device()
     shape = _shape3(some, "output", cache.Hkv, cache.D)
     T = shape[0]
+    at = _ints(pos, "pos", T)
+    elsewhere = (dev < 0 or cache.dev != dev or (v_out is not None and v_out.get_device() != dev)
+                 or pages.get_device() != dev or (at is not None and pos.get_device() != dev)
+                 or (seq is not None and seq.get_device() != dev)
+                 or (dev_status is not None and dev_status.get_device() != dev))
     status = lib.ft_kv_gather(
-        cache._ref, _table(pages), None if seq is None else _ints(seq, "seq", T), _ints(pos, "pos", T), T,
-        None if k_out is None else _rows(k_out, "k_out", shape, dtype),
-        None if v_out is None else _rows(v_out, "v_out", shape, dtype), _DT.get(dtype, -1),
-        None if dev_status is None else dev_status.data_ptr(), _stream(some, stream))
+        cache._ref, _table(pages), None if seq is None else _ints(seq, "seq", T), None if elsewhere else at, T,
+        None if k_out is None else _rows_of(k_out, "k_out", shape),
+        None if v_out is None else _rows(v_out, "v_out", shape, dtype), _DT.get(dtype, -1), _status(dev_status),
+        _stream(dev, stream))
     if status:
-        _check(status)
+        _check(status, elsewhere)
 
 
 def attn_decode_workspace(T: int, Hq: int, Hkv: int, D: int) -> int:
@@ -272,13 +305,20 @@ def attn_decode(cache: KvCache, q, pages, lens, out, ws, seq=None, scale: float 
     cached tokens of sequence seq[t] (ft_attn_decode).  scale defaults to 1 / sqrt(D)."""
     lib = _lib or _bind()
     T, Hq, D = shape = _shape3(q, "q", None, cache.D)
-    dtype, out_dtype = q.dtype, out.dtype
+    dtype, out_dtype, dev = q.dtype, out.dtype, q.get_device()
     if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (T, Hq) or not lse.is_contiguous()):
         _bad("attn_decode: lse must be a contiguous float32 [T, Hq]")
+    if not ws.is_contiguous():
+        _bad("attn_decode: ws must be contiguous")
+    at = _ints(lens, "lens", T)
+    elsewhere = (dev < 0 or cache.dev != dev or out.get_device() != dev or pages.get_device() != dev
+                 or (at is not None and lens.get_device() != dev) or ws.get_device() != dev
+                 or (seq is not None and seq.get_device() != dev) or (lse is not None and lse.get_device() != dev)
+                 or (dev_status is not None and dev_status.get_device() != dev))
     status = lib.ft_attn_decode(
-        cache._ref, _rows(q, "q", shape, dtype), T, Hq, _DT.get(dtype, -1), _table(pages),
-        None if seq is None else _ints(seq, "seq", T), _ints(lens, "lens", T), D ** -0.5 if scale is None else scale,
+        cache._ref, _rows_of(q, "q", shape), T, Hq, _DT.get(dtype, -1), _table(pages),
+        None if seq is None else _ints(seq, "seq", T), None if elsewhere else at, D ** -0.5 if scale is None else scale,
         window, _rows(out, "out", shape, out_dtype), _DT.get(out_dtype, -1), None if lse is None else lse.data_ptr(),
-        ws.data_ptr(), ws.nbytes, None if dev_status is None else dev_status.data_ptr(), _stream(q, stream))
+        ws.data_ptr(), ws.nbytes, _status(dev_status), _stream(dev, stream))
     if status:
-        _check(status)
+        _check(status, elsewhere)
