@@ -119,10 +119,11 @@ def _ints(t, name, T):
 
 
 def _table(pages):
-    s0, s1 = pages.stride() if pages.dim() == 2 else (0, 0)
-    if pages.dtype != torch.int32 or s1 != 1:
+    if pages.dim() != 2 or pages.dtype is not torch.int32:
         _bad("pages: an int32 [sequences, pages] is needed")
-    n, most = pages.shape
+    (s0, s1), (n, most) = pages.stride(), pages.shape
+    if s1 != 1 and most > 1:  # a dimension of one place may carry any stride
+        _bad("pages: a sequence's pages must be contiguous")
     return _TABLE.pack(pages.data_ptr(), s0, most, n)
 
 

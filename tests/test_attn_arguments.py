@@ -108,3 +108,31 @@ def test_one_tensor_elsewhere_is_refused(cuda_lib, att):
     k = gpu["cache"].k
     assert "the keys are on" in refused(att.KvCache.over, att.FT_KV_BF16, 64, k, k.cpu())
     torch.cuda.synchronize()
+
+
+def test_page_tables_of_one_page(att):
+    """A transposed [1, n] table is contiguous as [n, 1] and keeps its strides (1, n)."""
+    x = cpu_call(att, T=4)
+    x["pages"] = torch.arange(4, dtype=torch.int32).view(1, 4).t().contiguous()
+    assert x["pages"].stride() == (1, 4)
+    message = refused(att.kv_gather, x["cache"], x["pages"], x["pos"], x["k"], None)
+    assert "GPU" in message and "pages" not in message
+    for bad in (torch.zeros(2, 8, dtype=torch.int32)[:, ::2], torch.zeros(8, dtype=torch.int32)):
+        assert "pages" in refused(att.kv_gather, x["cache"], bad, x["pos"], x["k"], None)
+
+
+@pytest.mark.gpu
+def test_a_decoder_block_of_one_page_a_sequence(cuda_lib):
+    """The example with sequences that end inside their first page."""
+    import sys
+
+    sys.path.insert(0, os.path.join(ROOT, "examples"))
+    import decoder_block
+
+    block = decoder_block.DecoderBlock("bf16", longest=10, page_size=16)
+    x = torch.randn(block.T, block.cfg.H, device="cuda").to(torch.bfloat16)
+    for _ in range(10):
+        y = block.step(x)
+    assert int(block.attention.status.item()) == 0 and torch.isfinite(y.float()).all()
+    assert block.cache.k[:block.T, :, :10].float().abs().sum((1, 3)).min() > 0  # every sequence's ten places are written
+    assert not block.cache.k[:, :, 10:].any()
