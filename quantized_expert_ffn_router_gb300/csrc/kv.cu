@@ -895,7 +895,9 @@ ft_status kv_view(const char* what, const ft_kv_cache* c, const ft_page_table* p
                         static_cast<const void*>(c->k_scale), static_cast<const void*>(c->v_scale),
                         static_cast<const void*>(c->k_block), static_cast<const void*>(c->v_block)})
     FT_REQUIRE(reinterpret_cast<uintptr_t>(q) % 16 == 0, "%s: cache arrays must be 16-byte aligned", what);
-  FT_REQUIRE(p->pages != nullptr && p->max_pages > 0 && p->n_seqs > 0 && p->stride >= 0, "%s: bad page table", what);
+  // calls of no tokens look nothing up, and may have a table of no sequences
+  FT_REQUIRE(T == 0 || (p->pages != nullptr && p->max_pages > 0 && p->n_seqs > 0 && p->stride >= 0), "%s: bad page table",
+             what);
   FT_REQUIRE(seq != nullptr || T <= p->n_seqs, "%s: %d rows but a page table of %d sequences", what, T, p->n_seqs);
   KvView v;
   v.data[0] = static_cast<uint8_t*>(c->k);

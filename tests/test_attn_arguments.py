@@ -136,3 +136,13 @@ def test_a_decoder_block_of_one_page_a_sequence(cuda_lib):
     assert int(block.attention.status.item()) == 0 and torch.isfinite(y.float()).all()
     assert block.cache.k[:block.T, :, :10].float().abs().sum((1, 3)).min() > 0  # every sequence's ten places are written
     assert not block.cache.k[:, :, 10:].any()
+
+
+@pytest.mark.parametrize("shape", [(0, 3), (0, 0), (2, 0)])
+def test_no_tokens_need_no_page_table(att, shape):
+    x, pages = cpu_call(att, T=0), torch.zeros(shape, dtype=torch.int32)
+    att.kv_append(x["cache"], x["k"], x["v"], pages, x["pos"], stream=0)
+    att.kv_gather(x["cache"], pages, x["pos"], x["k"], x["v"], stream=0)
+    att.attn_decode(x["cache"], x["q"], pages, x["pos"], x["out"], x["ws"], stream=0)
+    x = cpu_call(att)
+    assert "bad page table" in refused(att.kv_append, x["cache"], x["k"], x["v"], pages, x["pos"], stream=0)
