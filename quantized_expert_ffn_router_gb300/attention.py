@@ -180,6 +180,9 @@ class KvCache:
         _need(k.dim() == 4, "cache arrays are [pages, heads, slots, ...]")
         self.dev = k.get_device()
         n_pages, Hkv, page_size = k.shape[:3]
+        # each array's own floating type; integers of its size are taken for its bits
+        own = {"": {FT_KV_BF16: torch.bfloat16, FT_KV_F16: torch.float16, FT_KV_E4M3: torch.float8_e4m3fn,
+                    FT_KV_NVFP4: torch.float4_e2m1fn_x2}[fmt], "_scale": torch.float8_e8m0fnu, "_block": torch.float8_e4m3fn}
         strides = None
         for name in ("k", "v", "k_scale", "v_scale", "k_block", "v_block"):
             t = arrays.get(name)
@@ -190,6 +193,7 @@ class KvCache:
             shape = (n_pages, Hkv, page_size) + (() if name.endswith("_scale") else (w,))
             size = 2 if fmt in (FT_KV_BF16, FT_KV_F16) and name in ("k", "v") else 1
             _need(tuple(t.shape) == shape and t.element_size() == size, f"cache {name}: {tuple(t.shape)} {t.dtype}")
+            _need(not t.dtype.is_floating_point or t.dtype is own[name[1:]], f"cache {name}: {t.dtype}")
             _need(t.get_device() == self.dev, f"cache {name}: on {t.device}, the keys are on {k.device}")
             _need(t.dim() == 3 or t.stride(3) == 1, f"cache {name}: rows must be contiguous")
             _need(all(s % w == 0 for s in t.stride()[:3]), f"cache {name}: strides must be whole rows")

@@ -146,3 +146,23 @@ def test_no_tokens_need_no_page_table(att, shape):
     att.attn_decode(x["cache"], x["q"], pages, x["pos"], x["out"], x["ws"], stream=0)
     x = cpu_call(att)
     assert "bad page table" in refused(att.kv_append, x["cache"], x["k"], x["v"], pages, x["pos"], stream=0)
+
+
+def test_cache_arrays_of_another_floating_type_are_refused(att):
+    z = lambda dtype, *s: torch.zeros(*s, dtype=torch.uint8).to(dtype) if dtype.itemsize > 1 else torch.zeros(
+        *s, dtype=torch.uint8).view(dtype)
+    rows = lambda dtype: dict(k=z(dtype, 2, 1, 4, 32), v=z(dtype, 2, 1, 4, 32))
+    scales = lambda dtype: dict(k_scale=z(dtype, 2, 1, 4), v_scale=z(dtype, 2, 1, 4))
+    blocks = lambda dtype: dict(k_block=z(dtype, 2, 1, 4, 4), v_block=z(dtype, 2, 1, 4, 4))
+    e4, e5, e8, u8 = torch.float8_e4m3fn, torch.float8_e5m2, torch.float8_e8m0fnu, torch.uint8
+    for fmt, dtype, other in ((att.FT_KV_BF16, torch.bfloat16, torch.float16), (att.FT_KV_F16, torch.float16, torch.bfloat16)):
+        for fine in (dtype, torch.int16, torch.uint16):
+            att.KvCache.over(fmt, 32, **rows(fine))
+        assert "cache k" in refused(att.KvCache.over, fmt, 32, **rows(other))
+    for codes, scale in ((e4, u8), (u8, e8), (torch.int8, u8)):
+        att.KvCache.over(att.FT_KV_E4M3, 32, **rows(codes), **scales(scale))
+    assert "cache k" in refused(att.KvCache.over, att.FT_KV_E4M3, 32, **rows(e5), **scales(u8))
+    assert "cache k_scale" in refused(att.KvCache.over, att.FT_KV_E4M3, 32, **rows(e4), **scales(e4))
+    for codes, block in ((u8, u8), (torch.float4_e2m1fn_x2, e4)):
+        att.KvCache.over(att.FT_KV_NVFP4, 64, **rows(codes), **scales(u8), **blocks(block))
+    assert "cache k_block" in refused(att.KvCache.over, att.FT_KV_NVFP4, 64, **rows(u8), **scales(u8), **blocks(e5))
