@@ -1028,8 +1028,8 @@ ft_status launch(AttnArgs& a, cudaStream_t s) {
   a.tile_log2 = log2_of(tile);
   a.lead = X::kLead;
   a.lift = X::kLift;
-  const int64_t longest = a.window > 0 && a.window < a.most ? a.window + 15 : a.most;
-  const int64_t most_tiles = ((longest + tile - 1) / tile + a.lead) * a.units * a.T;
+  const int32_t longest = a.window > 0 && a.window < a.most - 15 ? a.window + 15 : a.most;
+  const int64_t most_tiles = (int64_t{row_span(longest, 0, longest, tile).tiles} + a.lead) * a.units * a.T;
   // the line's numbers are 32-bit in the kernel
   if (most_tiles >= (1ll << 31) - kMaxWorkers) return fail(FT_ERR_UNSUPPORTED, "attn_decode: rows times pages too large");
   int64_t workers = static_cast<int64_t>(device_sm_count()) * r;

@@ -33,8 +33,7 @@ struct AttnArgs {
 };
 
 __device__ __forceinline__ RowSpan span_of(const AttnArgs& a, int t) {
-  const int log2 = a.tile_log2;
-  return row_span_by(a.lens[t], a.window, a.most, [log2](int n) { return (n + (1 << log2) - 1) >> log2; });
+  return row_span_log2(a.lens[t], a.window, a.most, a.tile_log2);
 }
 
 __device__ __forceinline__ int numbers_of(const AttnArgs& a, int t) {

@@ -68,21 +68,23 @@ struct RowSpan {
   int32_t tiles;
 };
 
-// `tiles_of` gives the tiles that so many tokens take.
-template <typename TilesOf>
-FT_HD RowSpan row_span_by(int32_t len, int32_t window, int32_t most, TilesOf tiles_of) {
+// Of tiles of 2^log2 tokens.
+FT_HD RowSpan row_span_log2(int32_t len, int32_t window, int32_t most, int32_t log2) {
   RowSpan r;
   if (len > most) len = most;
   if (len < 0) len = 0;
   r.len = len;
   r.first = (window > 0 && len > window) ? len - window : 0;
   r.begin = r.first & ~15;
-  r.tiles = tiles_of(len - r.begin);
+  r.tiles = (len - r.begin + (1 << log2) - 1) >> log2;
   return r;
 }
 
+// The same of tiles of `tile` tokens, a power of two.
 FT_HD RowSpan row_span(int32_t len, int32_t window, int32_t most, int32_t tile) {
-  return row_span_by(len, window, most, [tile](int32_t tokens) { return (tokens + tile - 1) / tile; });
+  int32_t log2 = 0;
+  while ((1 << log2) < tile) ++log2;
+  return row_span_log2(len, window, most, log2);
 }
 
 FT_HD int32_t split_share(int32_t total, int32_t workers) { return total > workers ? (total + workers - 1) / workers : 1; }
