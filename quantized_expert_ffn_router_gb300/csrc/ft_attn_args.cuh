@@ -113,7 +113,7 @@ __device__ __forceinline__ void store_lse(const AttnArgs& a, int t, int h, float
 // An output of a 16-bit cache.  Its weighted mean is finite unless a value that
 // counts is not, and with an infinity the two terms of a weight, or a weight
 // that rounds to 0, may give an infinity or NaN: it is NaN throughout.
-__device__ __forceinline__ float finite_or_nan(float x) { return x - x == 0.f ? x : __uint_as_float(0x7fffffffu); }
+__device__ __forceinline__ float finite_or_nan(float x) { return __fmaf_rn(x, 0.f, x); }
 
 // Two output values in one word.
 __device__ __forceinline__ uint32_t pack_out(const AttnArgs& a, float x, float y) {

@@ -732,7 +732,7 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadA
       w[j][0] = v.x, w[j][1] = v.y, w[j][2] = v.z, w[j][3] = v.w;
       if constexpr (W == 8) w[j][4] = u.x, w[j][5] = u.y, w[j][6] = u.z, w[j][7] = u.w;
     }
-    if (W < 8) e[j] = held_exponent<FMT>(a.kv.scale[j][r]);
+    if (W < 8) e[j] = a.kv.scale[j][r];
   }
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
@@ -747,7 +747,8 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadA
       }
     } else {
       uint32_t f[8];  // f16 pairs; code * block scale is exact in fp32
-      float scale = pow2f(static_cast<int>(e[j]) - 127);
+      // held here, not where it is read: the values' loads must not wait for the keys' (0.3 us of one token's read)
+      float scale = pow2f(static_cast<int>(held_exponent<FMT>(e[j])) - 127);
       if constexpr (W == 4) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
