@@ -42,8 +42,9 @@ __device__ __forceinline__ LineSums line_sums(const AttnArgs& a, int row) {
 // Adds the partial sums of the unit that crosses the end of worker blockIdx.x's
 // share and has its first tile in that share, in the workers' order.  A CTA
 // takes kHeads heads of the block: one head with 16 warps (each every 16th
-// partial) where few units have many partials each (one row of 130999 E4M3:
-// 31.6 us in all, with 8 warps 33.1), eight heads with a warp each otherwise.
+// partial) where few units have many partials each (one row of 130999 E4M3, one
+// term a weight: 31.6 us in all, with 8 warps 33.1), eight heads with a warp each
+// otherwise.
 // Where there are fewer units than workers, CTA
 // (x, y) takes unit x instead: most shares' ends are inside units that began
 // before.

@@ -33,8 +33,9 @@
 // (64 heads over one of 128, 128 rows up to 16384 tokens, bf16: 137 us; 241
 // with a ring for each warp).  Otherwise a CTA's four warps take different
 // tokens, each with a ring of its own, and meet at a unit's end.  Two tiles of
-// 8 heads in a warp beat two warps of one (16 heads over one of 128, E4M3: 36
-// us and 47): rows are turned into operands once.
+// 8 heads in a warp beat two warps of one (16 rows up to 16384, 16 heads over
+// each of 4 of 128, E4M3, one term a weight: 36 us and 47): rows are turned into
+// operands once.
 //
 // Order of tokens.  Place r = 0..7 of the contracted index holds token r / 2
 // (r even) or 4 + r / 2 (r odd) of its 8, so that a lane quarter's value rows
@@ -54,15 +55,18 @@
 // join_kernel adds in order.
 //
 // What it measured (GPU time in a graph, inputs beyond L2; HBM at 6.70 TB/s):
-//   one row of 1000003 tokens, 32 heads over 4 of 128: bf16 306 us (the copy
-//   rate), E4M3 167 us (92% of it), NVFP4 131 us (67%);
-//   32 rows up to 8192 tokens, 32 heads over 8, bf16: 61.8 us (88%);
-//   64 rows up to 16384, 64 heads over 8, NVFP4: 99 us (64%).
-// 16-bit rows are bound by HBM, 4-bit rows by issue slots: of 370 warp
-// instructions for 16 tokens of one key head, 190 turn codes into operands
-// (conversions, bytes taken out of words, block scales), 16 are products.
+//   one row of 1000003 tokens, 32 heads over 4 of 128: bf16 299-302 us (the copy
+//   rate), E4M3 168 us (92% of it), NVFP4 141 us (62%);
+//   32 rows up to 8192 tokens, 32 heads over 8, bf16: 62.2 us (88%), E4M3 42
+//   (66%), NVFP4 39 (40%);
+//   64 rows up to 16384, 64 heads over 8, NVFP4: 109 us (58%).
+// 16-bit rows are bound by HBM, 4-bit rows by instructions and their latency (60%
+// of the issue slots, four warps a scheduler): of 403 warp instructions for 16
+// tokens of one key head, 190 turn codes into operands (conversions, bytes taken
+// out of words, block scales), 24 are products, and 20 or so are the weights'
+// second term.
 // Short work is bound by latency: about 4 us from the launch to the first rows
-// in shared memory, 1.5 us for a unit's merge, 3 us for the join.
+// in shared memory, 1.5-2 us for a unit's merge, 3 us for the join.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -191,9 +195,8 @@ struct Deal {
   static constexpr int U = TS / 16;
   // What a unit costs beside its tiles (queries, merge, output: about 2 us of a
   // CTA), in tiles.  Without it, shares of many short rows finish last: 64 rows
-  // up to 16384 tokens NVFP4 122 us, with 1, 2, 3, 4 tiles 118, 102, 102, 104
-  // (the last three after other steps); 32 rows up to 8192 bf16 with 1, 2, 3:
-  // 63.7, 63.5, 63.2.
+  // up to 16384 tokens NVFP4 with 0, 1, 2, 3 tiles 116.8 us, 113.5, 109.3, 110.9;
+  // 17 rows with a window, f16, with 1, 2, 3: 18.1, 17.6, 17.5.
   static constexpr int kLead = kQuant ? 2 : 3;
   static constexpr int kSide = TS * RB;          // keys, or values, of a step
   // The copies of a step: chunk i = kFill c + filler of a side is row i / CPR, bytes 16 (i % CPR)..;
@@ -557,8 +560,11 @@ __device__ __noinline__ void empty_row(const AttnArgs& a, int t) {
 }
 
 // Weights enter the value product as two 16-bit terms, so that an output is
-// that of fp32 weights (one f16 term added 2^-12 of each weight: of 16-bit
-// outputs one in twenty was rounded the other way).
+// that of fp32 weights (3e-7 of the norm from the 64-bit one, as far as plain
+// fp32 is).  With one f16 term each weight is up to 2^-11 off, and a few in a
+// hundred of 16-bit outputs were rounded the other way (5e-4 of the norm); it took
+// one row of 130999 E4M3 31.5 us and 64 rows up to 16384 NVFP4 99.8, the two terms
+// 33.0 and 109.3.
 template <int FMT, int DP, int NT, int COLS>
 __global__ void __launch_bounds__(Deal<FMT, DP, NT, COLS>::kThreads, Deal<FMT, DP, NT, COLS>::kCtas)
     attend_kernel(const __grid_constant__ AttnArgs a) {
@@ -603,9 +609,9 @@ __global__ void __launch_bounds__(Deal<FMT, DP, NT, COLS>::kThreads, Deal<FMT, D
   feed.walk = walk;
   feed.more = true;
   feed.enter(a, lane);
-  // The first page is on its way while the rest is set up (777 tokens bf16 7.1 us
-  // and 7.4; NVFP4, whose registers are short, 64 rows up to 16384: 101.5 and 98.8).
-  const bool early_page = !X::kBlocks && walk.base < walk.stop;
+  // The first page is on its way while the rest is set up (777 tokens bf16 7.4 us
+  // and 7.7).
+  const bool early_page = walk.base < walk.stop;
   if (early_page) feed.look_up(a, step, lane);
   feed.init(a, ring, wh, lane);
 

@@ -8,10 +8,11 @@
 // access is a 16- or 32-byte one.
 //
 // What they measured (GPU time in a graph, inputs beyond L2; of 6.70 TB/s):
-//   4099 tokens x 40 heads of 128 rotated, half of each head: 15.6 us (80%), 20000 tokens 67 us (91%);
-//   8192 tokens, 32 + 2 x 8 heads of 128, rotated, into E4M3: 35.6 us (77%), 20000 tokens 80.5 us (84%);
-//   20000 tokens, 16 + 2 x 2 heads of 128, rotated, into NVFP4: 55 us (52%, bound by instructions);
-//   16384 tokens x 2 x 8 heads of 128 read back, E4M3 to bf16: 18.3 us (82%).
+//   4099 tokens x 40 heads of 128 rotated, half of each head: 15.6 us (80%), 20000 tokens 66.7 us (92%);
+//   8192 tokens, 32 + 2 x 8 heads of 128, rotated, into E4M3: 35.4 us (78%), 20000 tokens 81.2 us (83%);
+//   the same into bf16: 35.1 us (86%), 80.7 us (91%);
+//   20000 tokens, 16 + 2 x 2 heads of 128, rotated, into NVFP4: 54.3 us (52%);
+//   16384 tokens x 2 x 8 heads of 128 read back as bf16: E4M3 18.4 us (82%), bf16 22.4 (89%), NVFP4 17.5 (74%).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
