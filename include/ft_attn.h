@@ -7,6 +7,9 @@
  *
  *   ft_rope_freqs   rotary frequencies, scaled for long contexts (host)
  *   ft_rope         rotate the heads of q or k
+ *   ft_rope_by_axes, ft_kv_append_by_axes
+ *                   the same, and the cache write, with several positions a
+ *                   token (time, height, width), one for each channel pair
  *   ft_kv_append    write new key and value rows into a paged cache, quantised
  *                   as they are written; rotates k (and q) in the same launch
  *   ft_kv_gather    read cached rows back as dense rows
@@ -143,6 +146,34 @@ FT_API ft_status ft_rope_freqs(int32_t rot_dim, double base, int32_t scaling, do
 FT_API ft_status ft_rope(const ft_rows* x_host, int32_t T, int32_t heads, int32_t D, int32_t dtype,
                          const int32_t* pos, const ft_rope_table* rope_host, const ft_rows* out_host, void* stream);
 
+/*
+ * Several axes: a token has a position on each, and channel pair i turns by that
+ * on axis[i].  Axis a's positions are pos[a * pos_stride + t], t < T (pos_stride
+ * at least T).  axis: a device array of rot_dim / 2 bytes; one past n_axes - 1
+ * counts as n_axes - 1.
+ */
+enum { FT_ROPE_MAX_AXES = 8 };
+typedef struct {
+  const uint8_t* axis;
+  int32_t n_axes;
+  int64_t pos_stride;
+} ft_rope_axes;
+
+/*
+ * ft_rope_sections -- axis_host[i], i < rot_dim / 2, from the number of pairs
+ * that turn by each of n axes (together rot_dim / 2): one run after the other, or
+ * (weave) the axes taking turns, pair i on axis i % n as long as that one has
+ * pairs left, else on axis 0.  Woven sections of axes past 0 hold at most as many
+ * as their turns.
+ */
+FT_API ft_status ft_rope_sections(int32_t rot_dim, const int32_t* sections_host, int32_t n, int32_t weave,
+                                  uint8_t* axis_host);
+
+/* ft_rope_by_axes -- ft_rope with several axes: pos [n_axes][T] as ft_rope_axes. */
+FT_API ft_status ft_rope_by_axes(const ft_rows* x_host, int32_t T, int32_t heads, int32_t D, int32_t dtype,
+                                 const int32_t* pos, const ft_rope_table* rope_host, const ft_rope_axes* axes_host,
+                                 const ft_rows* out_host, void* stream);
+
 /* Bytes of one cached row's codes; 0 for an unsupported (fmt, D). */
 FT_API uint64_t ft_kv_row_bytes(int32_t fmt, int32_t D);
 
@@ -161,6 +192,13 @@ FT_API ft_status ft_kv_append(const ft_kv_cache* cache_host, const ft_rows* k_ho
                               int32_t dtype, const ft_page_table* table_host, const int32_t* seq, const int32_t* pos,
                               const ft_rope_table* rope_host, const int32_t* rope_pos, const ft_rows* q_host,
                               int32_t Hq, const ft_rows* q_out_host, int32_t* dev_status, void* stream);
+
+/* ft_kv_append_by_axes -- ft_kv_append with several axes: rope_pos [n_axes][T] as ft_rope_axes, not NULL. */
+FT_API ft_status ft_kv_append_by_axes(const ft_kv_cache* cache_host, const ft_rows* k_host, const ft_rows* v_host,
+                                      int32_t T, int32_t dtype, const ft_page_table* table_host, const int32_t* seq,
+                                      const int32_t* pos, const ft_rope_table* rope_host,
+                                      const ft_rope_axes* axes_host, const int32_t* rope_pos, const ft_rows* q_host,
+                                      int32_t Hq, const ft_rows* q_out_host, int32_t* dev_status, void* stream);
 
 /*
  * ft_kv_gather -- the inverse: k_out and v_out [T, Hkv, D] (dtype bf16, f16 or

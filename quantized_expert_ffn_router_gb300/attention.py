@@ -33,8 +33,11 @@ _V, _I32, _F, _D, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.
 _SIGS = {
     "ft_rope_freqs": (_I32, [_I32, _D, _I32, _D, _D, _D, _I32, _V]),
     "ft_rope": (_I32, [_V, _I32, _I32, _I32, _I32, _V, _V, _V, _V]),
+    "ft_rope_sections": (_I32, [_I32, _V, _I32, _I32, _V]),
+    "ft_rope_by_axes": (_I32, [_V, _I32, _I32, _I32, _I32, _V, _V, _V, _V, _V]),
     "ft_kv_row_bytes": (ctypes.c_uint64, [_I32, _I32]),
     "ft_kv_append": (_I32, [_V, _V, _V, _I32, _I32, _V, _V, _V, _V, _V, _V, _I32, _V, _V, _V]),
+    "ft_kv_append_by_axes": (_I32, [_V, _V, _V, _I32, _I32, _V, _V, _V, _V, _V, _V, _V, _I32, _V, _V, _V]),
     "ft_kv_gather": (_I32, [_V, _V, _V, _V, _I32, _V, _V, _I32, _V, _V]),
     "ft_attn_decode_workspace": (_SZ, [_I32, _I32, _I32, _I32]),
     "ft_attn_decode": (_I32, [_V, _V, _I32, _I32, _I32, _V, _V, _V, _F, _I32, _V, _I32, _V, _V, _SZ, _V, _V]),
@@ -44,6 +47,7 @@ _lib = None
 # The descriptors of ft_attn.h as packed bytes (cheaper to build for each call than ctypes structures).
 _ROWS = struct.Struct("=Qqq")
 _TABLE = struct.Struct("=Qqii")
+_AXES = struct.Struct("=Qiiq")
 
 
 class FtKvCache(ctypes.Structure):
@@ -208,11 +212,14 @@ class KvCache:
 
 
 class Rope:
-    """A rotary table (ft_rope_freqs on the host, kept on the device)."""
+    """A rotary table (ft_rope_freqs on the host, kept on the device).
+
+    sections: how many channel pairs turn by each of several axes (time, height, width), in runs or, with `weave`,
+    taking turns (ft_rope_sections).  Positions are then [axes, T]."""
 
     def __init__(self, rot_dim: int, base: float = 10000.0, interleaved: bool = False, scaling: int = FT_ROPE_PLAIN,
                  factor: float = 1.0, low: float = 1.0, high: float = 32.0, orig_len: int = 8192,
-                 mscale: float = 1.0, device="cuda"):
+                 mscale: float = 1.0, device="cuda", sections=None, weave: bool = False):
         host = torch.empty(max(rot_dim, 0) // 2, dtype=torch.int64)
         lib = _bind()
         _check(lib.ft_rope_freqs(rot_dim, base, scaling, factor, low, high, orig_len, host.data_ptr()))
@@ -221,6 +228,26 @@ class Rope:
         self.dev = self.freqs.get_device()
         self.desc = FtRopeTable(self.freqs.data_ptr(), rot_dim, int(self.interleaved), self.mscale)
         self._ref = ctypes.addressof(self.desc)
+        self.n_axes, self.axis = 1, None
+        if sections is None:
+            _need(not weave, "Rope: weave is for sections")
+            return
+        counts = torch.tensor(list(sections), dtype=torch.int32)
+        axis = torch.empty(rot_dim // 2, dtype=torch.uint8)
+        _check(lib.ft_rope_sections(rot_dim, counts.data_ptr(), counts.numel(), int(weave), axis.data_ptr()))
+        self.n_axes, self.axis = counts.numel(), axis.to(device)
+
+    def _positions(self, pos, name, T):
+        """(address of the positions, an ft_rope_axes or None)."""
+        if self.axis is None:
+            return _ints(pos, name, T), None
+        n = self.n_axes
+        if pos.dtype is not torch.int32 or pos.shape != (n, T):
+            _bad(f"{name}: an int32 [{n}, {T}] is needed, a row for each axis")
+        stride, step = pos.stride()
+        if step != 1 and T > 1:
+            _bad(f"{name}: an axis's positions must be contiguous")
+        return pos.data_ptr(), _AXES.pack(self.axis.data_ptr(), n, 0, stride if n > 1 else T)
 
 
 def _shape3(t, name, heads, D):
@@ -232,14 +259,18 @@ def _shape3(t, name, heads, D):
 
 
 def rope(x, pos, table: Rope, out, stream=None):
-    """out[t, h] = x[t, h] rotated to pos[t] (ft_rope); out may be x."""
+    """out[t, h] = x[t, h] rotated to pos[t], or by several axes to pos[:, t] (ft_rope, ft_rope_by_axes); out may be x."""
     lib = _lib or _bind()
     dtype, dev = x.dtype, x.get_device()
     T, heads, D = shape = _shape3(x, "x", None, None)
-    at = _ints(pos, "pos", T)
+    at, axes = table._positions(pos, "pos", T)
     elsewhere = dev < 0 or table.dev != dev or (at is not None and pos.get_device() != dev) or out.get_device() != dev
-    status = lib.ft_rope(_rows_of(x, "x", shape), T, heads, D, _DT.get(dtype, -1), None if elsewhere else at,
-                         table._ref, _rows(out, "out", shape, dtype), _stream(dev, stream))
+    if axes is None:
+        status = lib.ft_rope(_rows_of(x, "x", shape), T, heads, D, _DT.get(dtype, -1), None if elsewhere else at,
+                             table._ref, _rows(out, "out", shape, dtype), _stream(dev, stream))
+    else:
+        status = lib.ft_rope_by_axes(_rows_of(x, "x", shape), T, heads, D, _DT.get(dtype, -1), None if elsewhere else at,
+                                     table._ref, axes, _rows(out, "out", shape, dtype), _stream(dev, stream))
     if status:
         _check(status, elsewhere)
 
@@ -247,7 +278,8 @@ def rope(x, pos, table: Rope, out, stream=None):
 def kv_append(cache: KvCache, k, v, pages, pos, seq=None, rope: Rope | None = None, rope_pos=None, q=None, q_out=None,
               dev_status=None, stream=None):
     """Write k and v [T, Hkv, D] to position pos[t] of sequence seq[t] (default t); with `rope`, k is rotated first
-    and q into q_out in the same launch (ft_kv_append)."""
+    and q into q_out in the same launch (ft_kv_append).  Of several axes, rope_pos [axes, T] has to be given
+    (ft_kv_append_by_axes)."""
     lib = _lib or _bind()
     dtype, dev = k.dtype, k.get_device()
     shape = _shape3(k, "k", cache.Hkv, cache.D)
@@ -267,11 +299,20 @@ def kv_append(cache: KvCache, k, v, pages, pos, seq=None, rope: Rope | None = No
             _bad(f"q: dtype {q.dtype}, expected {dtype}")
         q_rows, q_out_rows = _rows_of(q, "q", q_shape), _rows(q_out, "q_out", q_shape, dtype)
         elsewhere = elsewhere or q.get_device() != dev or q_out.get_device() != dev
-    status = lib.ft_kv_append(
-        cache._ref, _rows_of(k, "k", shape), _rows(v, "v", shape, dtype), T, _DT.get(dtype, -1), _table(pages),
-        None if seq is None else _ints(seq, "seq", T), None if elsewhere else at, None if rope is None else rope._ref,
-        None if rope_pos is None else _ints(rope_pos, "rope_pos", T), q_rows, Hq, q_out_rows, _status(dev_status),
-        _stream(dev, stream))
+    if rope is None or rope.axis is None:
+        status = lib.ft_kv_append(
+            cache._ref, _rows_of(k, "k", shape), _rows(v, "v", shape, dtype), T, _DT.get(dtype, -1), _table(pages),
+            None if seq is None else _ints(seq, "seq", T), None if elsewhere else at, None if rope is None else rope._ref,
+            None if rope_pos is None else _ints(rope_pos, "rope_pos", T), q_rows, Hq, q_out_rows, _status(dev_status),
+            _stream(dev, stream))
+    else:
+        if rope_pos is None:
+            _bad("kv_append: several axes need rope_pos")
+        turns, axes = rope._positions(rope_pos, "rope_pos", T)
+        status = lib.ft_kv_append_by_axes(
+            cache._ref, _rows_of(k, "k", shape), _rows(v, "v", shape, dtype), T, _DT.get(dtype, -1), _table(pages),
+            None if seq is None else _ints(seq, "seq", T), None if elsewhere else at, rope._ref, axes, turns, q_rows, Hq,
+            q_out_rows, _status(dev_status), _stream(dev, stream))
     if status:
         _check(status, elsewhere)
 

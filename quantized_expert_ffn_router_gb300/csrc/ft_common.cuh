@@ -55,6 +55,9 @@ ft_status ensure_dyn_smem(const void* kernel, int bytes, const char* what);
     if (!(cond)) return ::ft::fail(FT_ERR_INVALID, __VA_ARGS__); \
   } while (0)
 
+// The least exponent of a quantised row's power-of-two scale.
+constexpr int kMinExponent = -64;
+
 // ---------------------------------------------------------------- device ---
 __device__ __forceinline__ void record_status(int32_t* st, int32_t code) {
   if (st != nullptr) atomicCAS(st, 0, code);

@@ -11,10 +11,9 @@
 
 namespace ft {
 
-// A row's power-of-two scale: the least by definition, and the greatest that
-// fp32 rows need (448 * 2^119, 6 * 448 * 2^116 < 2^128).  Exponent bytes outside,
-// which no row is written with, are read as the nearer of the two.
-constexpr int kMinExponent = -64;
+// The greatest power-of-two scale that fp32 rows need (448 * 2^119, 6 * 448 *
+// 2^116 < 2^128); kMinExponent is the least, by definition.  Exponent bytes
+// outside, which no row is written with, are read as the nearer of the two.
 constexpr int max_exponent(int fmt) { return fmt == FT_KV_NVFP4 ? 117 : 120; }
 
 template <int FMT>
@@ -56,23 +55,5 @@ ft_status kv_view(const char* what, const ft_kv_cache* c, const ft_page_table* p
                   KvView* out);
 // Strides multiples of `grain` elements, base 16-byte aligned.
 ft_status check_rows(const char* what, const char* name, const ft_rows* r, int64_t grain);
-
-// A launch whose grid may start while the one before it on the stream drains;
-// the kernel waits (pdl_wait) before it touches memory.
-template <typename Kernel, typename Args>
-ft_status launch_pdl(Kernel kernel, dim3 grid, int block, size_t smem, cudaStream_t s, const Args& a, const char* what) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, kernel, a);
-  return launch_check(what);
-}
 
 }  // namespace ft

@@ -13,11 +13,10 @@
 //   the same into bf16: 35.1 us (86%), 80.7 us (91%);
 //   20000 tokens, 16 + 2 x 2 heads of 128, rotated, into NVFP4: 54.3 us (52%);
 //   16384 tokens x 2 x 8 heads of 128 read back as bf16: E4M3 18.4 us (82%), bf16 22.4 (89%), NVFP4 17.5 (74%).
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <math.h>
 
 #include "ft_kv.cuh"
+#include "ft_narrow.cuh"
 
 namespace ft {
 namespace {
@@ -116,101 +115,6 @@ __device__ __forceinline__ float rotate_odd(float x, float y, float c, float cl,
   return __uint_as_float(b);
 }
 
-// ----------------------------------------------------------- 16-bit pairs ---
-template <bool F16>
-__device__ __forceinline__ float2 unpack2(uint32_t w) {
-  if (F16) {
-    const __half2 h = *reinterpret_cast<const __half2*>(&w);
-    return __half22float2(h);
-  }
-  return make_float2(bf16_lo(w), bf16_hi(w));
-}
-
-template <bool F16>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  if (F16) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-template <bool F16>
-__device__ __forceinline__ float load_one(const uint16_t* p) {
-  return F16 ? __half2float(__ushort_as_half(*p)) : bf16_val(*p);
-}
-
-template <bool F16>
-__device__ __forceinline__ void unpack8(const uint4& v, float* f) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 t = unpack2<F16>(w[i]);
-    f[2 * i] = t.x;
-    f[2 * i + 1] = t.y;
-  }
-}
-
-template <bool F16>
-__device__ __forceinline__ uint4 pack8(const float* f) {
-  return make_uint4(pack2<F16>(f[0], f[1]), pack2<F16>(f[2], f[3]), pack2<F16>(f[4], f[5]), pack2<F16>(f[6], f[7]));
-}
-
-// 32 bytes to or from two places of 16, in one access where they are one
-// 32-byte place: two would each touch half of every sector.
-__device__ __forceinline__ void store32(void* p, uint4 a, uint4 b, bool whole) {
-  if (whole) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z),
-                 "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
-                 : "memory");
-  } else {
-    static_cast<uint4*>(p)[0] = a;
-    static_cast<uint4*>(p)[1] = b;
-  }
-}
-
-__device__ __forceinline__ void load32(const void* p, uint4& a, uint4& b, bool whole) {
-  if (whole) {
-    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
-                 : "l"(p));
-  } else {
-    a = static_cast<const uint4*>(p)[0];
-    b = static_cast<const uint4*>(p)[1];
-  }
-}
-
-// --------------------------------------------------------------- quantising ---
-// The smallest e >= kMinExponent with amax <= top * 2^e, where top = 1.t * 2^x
-// and t_bits are top's fraction bits: exact, from the bits of amax.
-__device__ __forceinline__ int row_exponent(float amax, int x, uint32_t t_bits) {
-  const uint32_t b = __float_as_uint(amax);
-  const int e = static_cast<int>(b >> 23) - 127 - x + ((b & 0x7fffffu) > t_bits ? 1 : 0);
-  return max(e, kMinExponent);
-}
-
-__device__ __forceinline__ float pow2f(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
-
-// Two E4M3 codes, `a` in the low byte; |x| > 448 gives 448, NaN stays NaN.
-__device__ __forceinline__ uint32_t to_e4m3x2(float a, float b) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
-  return r;
-}
-
-// Two E2M1 codes in a byte, `a` in the low nibble.
-__device__ __forceinline__ uint32_t to_e2m1x2(float a, float b) {
-  uint32_t r;
-  asm("{\n .reg .b8 c;\n cvt.rn.satfinite.e2m1x2.f32 c, %1, %2;\n cvt.u32.u8 %0, c;\n}" : "=r"(r) : "f"(b), "f"(a));
-  return r;
-}
-
-__device__ __forceinline__ float finite_abs(float x) {
-  const float a = fabsf(x);
-  return a <= 3.4028235e38f ? a : 0.f;
-}
-
 // ------------------------------------------------------------ rotate, write ---
 enum { kPairs, kHalves, kAny };
 constexpr int kMaxBatch = 16;
@@ -221,7 +125,10 @@ struct WriteArgs {
   uint16_t* q_out;
   int64_t out_tok, out_head;
   const int32_t* pos;       // places in the cache (NULL: rotation only)
-  const int32_t* rope_pos;  // positions of the rotation
+  const int32_t* rope_pos;  // positions of the rotation: [axis][token] where there are several axes
+  int64_t pos_stride;       // from one axis to the next
+  const uint8_t* axis;      // each frequency's axis; NULL: one axis
+  int32_t last_axis;
   const int64_t* freqs;
   float mscale;
   int32_t rot, half;        // rotated channels, half of them; 0: no rotation
@@ -232,6 +139,11 @@ struct WriteArgs {
   int32_t wide_in, wide_out;  // inputs, q_out: every 16 channels are a 32-byte place
   int32_t* status;
 };
+
+// The position by which token t's channel pair f turns.
+__device__ __forceinline__ int32_t position_of(const WriteArgs& a, int t, int f) {
+  return a.rope_pos[(a.axis != nullptr ? min(int{a.axis[f]}, a.last_axis) * a.pos_stride : 0) + t];
+}
 
 // Where frequency f's cosine (or sine) lies among `half`: 16-byte chunks in an
 // order that lets 8 lanes read every other chunk without a bank conflict.
@@ -256,18 +168,6 @@ __device__ __forceinline__ uint4 codes_e4m3(const float (&x)[16], int e) {
   for (int i = 0; i < 4; ++i)
     w[i] = to_e4m3x2(x[4 * i] * inv, x[4 * i + 1] * inv) | (to_e4m3x2(x[4 * i + 2] * inv, x[4 * i + 3] * inv) << 16);
   return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// Half a block's E2M1 codes from values that are scaled already.
-__device__ __forceinline__ uint32_t codes_e2m1(const float (&z)[8]) {
-  uint32_t w = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w |= to_e2m1x2(z[2 * i], z[2 * i + 1]) << (8 * i);
-  return w;
-}
-
-__device__ __forceinline__ float e4m3_value(uint32_t code) {
-  return __half2float(__ushort_as_half(static_cast<uint16_t>(cvt_e4m3x2(code))));
 }
 
 // The largest finite magnitude of x[16].
@@ -380,7 +280,7 @@ __global__ void __launch_bounds__(512, LAY == kAny ? 1 : 2) write_kernel(const _
   if (a.rot > 0) {
     for (int i = threadIdx.x; i < tokens * a.half; i += blockDim.x) {
       const int token = i / a.half, f = i - token * a.half;
-      const int64_t p = a.rope_pos[t0 + token];
+      const int64_t p = position_of(a, t0 + token, f);
       const float2 cs = turn_f32(static_cast<int64_t>(static_cast<uint64_t>(p) * static_cast<uint64_t>(a.freqs[f])), a.mscale);
       turns[token * 2 * half_up + turn_at(f)] = cs.x;
       turns[token * 2 * half_up + half_up + turn_at(f)] = cs.y;
@@ -521,7 +421,6 @@ __global__ void __launch_bounds__(512, LAY == kAny ? 1 : 2) write_kernel(const _
       }
       // What the exact rotation of the elements in `unsure` (a bit each) gives.
       const auto rotate_again = [&](uint32_t unsure) {
-        const int64_t p = a.rope_pos[t0 + tk];
         while (unsure != 0) {
           const int i = __ffs(unsure) - 1;
           unsure &= unsure - 1;
@@ -530,6 +429,7 @@ __global__ void __launch_bounds__(512, LAY == kAny ? 1 : 2) write_kernel(const _
           const bool left = LAY == kPairs ? (c & 1) == 0 : c < a.half;
           const int f = LAY == kPairs ? c >> 1 : left ? c : c - a.half;
           const int o = LAY == kPairs ? c ^ 1 : left ? c + a.half : c - a.half;
+          const int64_t p = position_of(a, t0 + tk, f);
           float2 hi, lo;
           turn_pair(static_cast<int64_t>(static_cast<uint64_t>(p) * static_cast<uint64_t>(a.freqs[f])), a.mscale, &hi, &lo);
           const float u = load_one<F16>(src + c), v = load_one<F16>(src + o);
@@ -847,6 +747,20 @@ bool wide(const ft_rows* r) {
   return reinterpret_cast<uintptr_t>(r->base) % 32 == 0 && r->token_stride % 16 == 0 && r->head_stride % 16 == 0;
 }
 
+// The axes of a rotation (NULL: one) and its positions, of T tokens, as kernel arguments.
+ft_status rope_positions(const char* what, const ft_rope_axes* x, const int32_t* pos, int32_t T, WriteArgs* a) {
+  a->rope_pos = pos;
+  if (x == nullptr) return FT_OK;
+  FT_REQUIRE(x->axis != nullptr, "%s: axes without their channel pairs' axis", what);
+  FT_REQUIRE(x->n_axes >= 1 && x->n_axes <= FT_ROPE_MAX_AXES, "%s: n_axes %d must be 1..%d", what, x->n_axes, FT_ROPE_MAX_AXES);
+  FT_REQUIRE(x->pos_stride >= T, "%s: an axis's positions are %lld after the last one's, for %d tokens", what,
+             static_cast<long long>(x->pos_stride), T);
+  a->axis = x->axis;
+  a->last_axis = x->n_axes - 1;
+  a->pos_stride = x->pos_stride;
+  return FT_OK;
+}
+
 ft_status check_rope(const char* what, const ft_rope_table* r, int32_t D) {
   FT_REQUIRE(r->freqs != nullptr, "%s: freqs is NULL", what);
   FT_REQUIRE(r->rot_dim >= 2 && r->rot_dim % 2 == 0 && r->rot_dim <= D, "%s: rot_dim %d must be even, 2..%d", what,
@@ -926,6 +840,106 @@ ft_status kv_view(const char* what, const ft_kv_cache* c, const ft_page_table* p
   return FT_OK;
 }
 
+namespace {
+
+ft_status rope_call(const ft_rows* x_host, int32_t T, int32_t heads, int32_t D, int32_t dtype, const int32_t* pos,
+                    const ft_rope_table* rope_host, const ft_rope_axes* axes_host, const ft_rows* out_host, void* stream) {
+  FT_REQUIRE(T >= 0 && heads >= 0, "rope: T %d, heads %d", T, heads);
+  FT_REQUIRE(D >= 8 && D <= 256 && D % 8 == 0, "rope: D %d must be a multiple of 8, at most 256", D);
+  FT_REQUIRE(dtype == FT_DT_BF16 || dtype == FT_DT_F16, "rope: dtype %d", dtype);
+  if (T == 0 || heads == 0) return FT_OK;
+  FT_REQUIRE(pos != nullptr && rope_host != nullptr, "rope: NULL pointer");
+  ft_status st;
+  if ((st = check_rope("rope", rope_host, D)) != FT_OK) return st;
+  if ((st = check_rows("rope", "x", x_host, 8)) != FT_OK) return st;
+  if ((st = check_rows("rope", "out", out_host, 8)) != FT_OK) return st;
+  FT_REQUIRE(!rows_overlap_partly(x_host, out_host), "rope: in place needs the same strides");
+  WriteArgs a = {};
+  a.in[0] = static_cast<const uint16_t*>(x_host->base);
+  a.in_tok[0] = x_host->token_stride;
+  a.in_head[0] = x_host->head_stride;
+  a.q_out = static_cast<uint16_t*>(out_host->base);
+  a.out_tok = out_host->token_stride;
+  a.out_head = out_host->head_stride;
+  if ((st = rope_positions("rope", axes_host, pos, T, &a)) != FT_OK) return st;
+  a.freqs = rope_host->freqs;
+  a.mscale = rope_host->mscale;
+  a.rot = rope_host->rot_dim;
+  a.T = T;
+  a.Hq = heads;
+  a.D = D;
+  a.wide_in = wide(x_host) && D % 16 == 0;
+  a.wide_out = wide(out_host);
+  const bool pairs = rope_host->interleaved != 0;
+  if (dtype == FT_DT_F16) return launch_write<true, -1>(a, pairs, "rope", as_stream(stream));
+  return launch_write<false, -1>(a, pairs, "rope", as_stream(stream));
+}
+
+ft_status append_call(const ft_kv_cache* cache_host, const ft_rows* k_host, const ft_rows* v_host, int32_t T,
+                      int32_t dtype, const ft_page_table* table_host, const int32_t* seq, const int32_t* pos,
+                      const ft_rope_table* rope_host, const ft_rope_axes* axes_host, const int32_t* rope_pos,
+                      const ft_rows* q_host, int32_t Hq, const ft_rows* q_out_host, int32_t* dev_status, void* stream) {
+  FT_REQUIRE(T >= 0, "kv_append: T %d", T);
+  WriteArgs a = {};
+  ft_status st;
+  if ((st = kv_view("kv_append", cache_host, table_host, seq, T, &a.kv)) != FT_OK) return st;
+  const int32_t fmt = cache_host->fmt;
+  FT_REQUIRE(dtype == FT_DT_BF16 || dtype == FT_DT_F16, "kv_append: dtype %d", dtype);
+  FT_REQUIRE(!(fmt == FT_KV_BF16 && dtype != FT_DT_BF16) && !(fmt == FT_KV_F16 && dtype != FT_DT_F16),
+             "kv_append: a 16-bit cache takes rows of its own type");
+  const bool with_q = q_host != nullptr || q_out_host != nullptr;
+  FT_REQUIRE(!with_q || (rope_host != nullptr && Hq > 0), "kv_append: q needs a rotation and Hq > 0");
+  if (T == 0) return FT_OK;
+  FT_REQUIRE(pos != nullptr, "kv_append: pos is NULL");
+  if ((st = check_rows("kv_append", "k", k_host, 8)) != FT_OK) return st;
+  if ((st = check_rows("kv_append", "v", v_host, 8)) != FT_OK) return st;
+  if (with_q) {
+    if ((st = check_rows("kv_append", "q", q_host, 8)) != FT_OK) return st;
+    if ((st = check_rows("kv_append", "q_out", q_out_host, 8)) != FT_OK) return st;
+    FT_REQUIRE(!rows_overlap_partly(q_host, q_out_host), "kv_append: q in place needs the same strides");
+    a.Hq = Hq;
+    a.q_out = static_cast<uint16_t*>(q_out_host->base);
+    a.out_tok = q_out_host->token_stride;
+    a.out_head = q_out_host->head_stride;
+  }
+  const ft_rows* in[3] = {q_host, k_host, v_host};
+  for (int i = with_q ? 0 : 1; i < 3; ++i) {
+    a.in[i] = static_cast<const uint16_t*>(in[i]->base);
+    a.in_tok[i] = in[i]->token_stride;
+    a.in_head[i] = in[i]->head_stride;
+  }
+  a.wide_in = wide(k_host) && wide(v_host) && (!with_q || wide(q_host));
+  a.wide_out = with_q && wide(q_out_host);
+  bool pairs = false;
+  if (rope_host != nullptr) {
+    if ((st = check_rope("kv_append", rope_host, cache_host->D)) != FT_OK) return st;
+    a.freqs = rope_host->freqs;
+    a.mscale = rope_host->mscale;
+    a.rot = rope_host->rot_dim;
+    FT_REQUIRE(axes_host == nullptr || rope_pos != nullptr, "kv_append: several axes need rope_pos");
+    if ((st = rope_positions("kv_append", axes_host, rope_pos ? rope_pos : pos, T, &a)) != FT_OK) return st;
+    pairs = rope_host->interleaved != 0;
+  }
+  a.pos = pos;
+  a.T = T;
+  a.Hkv = cache_host->Hkv;
+  a.D = cache_host->D;
+  a.status = dev_status;
+  cudaStream_t s = as_stream(stream);
+  const char* what = "kv_append";
+  switch (fmt) {
+    case FT_KV_BF16: return launch_write<false, FT_KV_BF16>(a, pairs, what, s);
+    case FT_KV_F16: return launch_write<true, FT_KV_F16>(a, pairs, what, s);
+    case FT_KV_E4M3:
+      return dtype == FT_DT_F16 ? launch_write<true, FT_KV_E4M3>(a, pairs, what, s)
+                                : launch_write<false, FT_KV_E4M3>(a, pairs, what, s);
+    default:
+      return dtype == FT_DT_F16 ? launch_write<true, FT_KV_NVFP4>(a, pairs, what, s)
+                                : launch_write<false, FT_KV_NVFP4>(a, pairs, what, s);
+  }
+}
+
+}  // namespace
 }  // namespace ft
 
 using namespace ft;
@@ -973,100 +987,63 @@ ft_status ft_rope_freqs(int32_t rot_dim, double base, int32_t scaling, double fa
   return FT_OK;
 }
 
+ft_status ft_rope_sections(int32_t rot_dim, const int32_t* sections_host, int32_t n, int32_t weave, uint8_t* axis_host) {
+  FT_REQUIRE(sections_host != nullptr && axis_host != nullptr, "rope_sections: NULL pointer");
+  FT_REQUIRE(rot_dim >= 2 && rot_dim % 2 == 0, "rope_sections: rot_dim %d must be even and at least 2", rot_dim);
+  FT_REQUIRE(n >= 1 && n <= FT_ROPE_MAX_AXES, "rope_sections: %d axes, expected 1..%d", n, FT_ROPE_MAX_AXES);
+  const int32_t half = rot_dim / 2;
+  int64_t sum = 0;
+  for (int i = 0; i < n; ++i) {
+    FT_REQUIRE(sections_host[i] >= 0, "rope_sections: section %d is negative", i);
+    sum += sections_host[i];
+  }
+  FT_REQUIRE(sum == half, "rope_sections: sections of %lld pairs, rot_dim %d has %d", static_cast<long long>(sum), rot_dim, half);
+  // woven: axis a > 0 has the pairs a, a + n, ...; as many as its section has to be among them
+  for (int a = 1; weave && a < n; ++a)
+    FT_REQUIRE(sections_host[a] <= (half - a + n - 1) / n, "rope_sections: section %d of %d pairs cannot be woven into %d", a,
+               sections_host[a], half);
+  int32_t section = 0, left = sections_host[0];
+  for (int i = 0; i < half; ++i) {
+    if (weave) {
+      const int a = i % n;
+      axis_host[i] = static_cast<uint8_t>(i / n < sections_host[a] ? a : 0);
+      continue;
+    }
+    while (left == 0) left = sections_host[++section];
+    axis_host[i] = static_cast<uint8_t>(section);
+    --left;
+  }
+  return FT_OK;
+}
+
 ft_status ft_rope(const ft_rows* x_host, int32_t T, int32_t heads, int32_t D, int32_t dtype, const int32_t* pos,
                   const ft_rope_table* rope_host, const ft_rows* out_host, void* stream) {
-  FT_REQUIRE(T >= 0 && heads >= 0, "rope: T %d, heads %d", T, heads);
-  FT_REQUIRE(D >= 8 && D <= 256 && D % 8 == 0, "rope: D %d must be a multiple of 8, at most 256", D);
-  FT_REQUIRE(dtype == FT_DT_BF16 || dtype == FT_DT_F16, "rope: dtype %d", dtype);
-  if (T == 0 || heads == 0) return FT_OK;
-  FT_REQUIRE(pos != nullptr && rope_host != nullptr, "rope: NULL pointer");
-  ft_status st;
-  if ((st = check_rope("rope", rope_host, D)) != FT_OK) return st;
-  if ((st = check_rows("rope", "x", x_host, 8)) != FT_OK) return st;
-  if ((st = check_rows("rope", "out", out_host, 8)) != FT_OK) return st;
-  FT_REQUIRE(!rows_overlap_partly(x_host, out_host), "rope: in place needs the same strides");
-  WriteArgs a = {};
-  a.in[0] = static_cast<const uint16_t*>(x_host->base);
-  a.in_tok[0] = x_host->token_stride;
-  a.in_head[0] = x_host->head_stride;
-  a.q_out = static_cast<uint16_t*>(out_host->base);
-  a.out_tok = out_host->token_stride;
-  a.out_head = out_host->head_stride;
-  a.rope_pos = pos;
-  a.freqs = rope_host->freqs;
-  a.mscale = rope_host->mscale;
-  a.rot = rope_host->rot_dim;
-  a.T = T;
-  a.Hq = heads;
-  a.D = D;
-  a.wide_in = wide(x_host) && D % 16 == 0;
-  a.wide_out = wide(out_host);
-  const bool pairs = rope_host->interleaved != 0;
-  if (dtype == FT_DT_F16) return launch_write<true, -1>(a, pairs, "rope", as_stream(stream));
-  return launch_write<false, -1>(a, pairs, "rope", as_stream(stream));
+  return rope_call(x_host, T, heads, D, dtype, pos, rope_host, nullptr, out_host, stream);
+}
+
+ft_status ft_rope_by_axes(const ft_rows* x_host, int32_t T, int32_t heads, int32_t D, int32_t dtype, const int32_t* pos,
+                          const ft_rope_table* rope_host, const ft_rope_axes* axes_host, const ft_rows* out_host,
+                          void* stream) {
+  FT_REQUIRE(axes_host != nullptr, "rope: axes are NULL");
+  return rope_call(x_host, T, heads, D, dtype, pos, rope_host, axes_host, out_host, stream);
 }
 
 ft_status ft_kv_append(const ft_kv_cache* cache_host, const ft_rows* k_host, const ft_rows* v_host, int32_t T,
                        int32_t dtype, const ft_page_table* table_host, const int32_t* seq, const int32_t* pos,
                        const ft_rope_table* rope_host, const int32_t* rope_pos, const ft_rows* q_host, int32_t Hq,
                        const ft_rows* q_out_host, int32_t* dev_status, void* stream) {
-  FT_REQUIRE(T >= 0, "kv_append: T %d", T);
-  WriteArgs a = {};
-  ft_status st;
-  if ((st = kv_view("kv_append", cache_host, table_host, seq, T, &a.kv)) != FT_OK) return st;
-  const int32_t fmt = cache_host->fmt;
-  FT_REQUIRE(dtype == FT_DT_BF16 || dtype == FT_DT_F16, "kv_append: dtype %d", dtype);
-  FT_REQUIRE(!(fmt == FT_KV_BF16 && dtype != FT_DT_BF16) && !(fmt == FT_KV_F16 && dtype != FT_DT_F16),
-             "kv_append: a 16-bit cache takes rows of its own type");
-  const bool with_q = q_host != nullptr || q_out_host != nullptr;
-  FT_REQUIRE(!with_q || (rope_host != nullptr && Hq > 0), "kv_append: q needs a rotation and Hq > 0");
-  if (T == 0) return FT_OK;
-  FT_REQUIRE(pos != nullptr, "kv_append: pos is NULL");
-  if ((st = check_rows("kv_append", "k", k_host, 8)) != FT_OK) return st;
-  if ((st = check_rows("kv_append", "v", v_host, 8)) != FT_OK) return st;
-  if (with_q) {
-    if ((st = check_rows("kv_append", "q", q_host, 8)) != FT_OK) return st;
-    if ((st = check_rows("kv_append", "q_out", q_out_host, 8)) != FT_OK) return st;
-    FT_REQUIRE(!rows_overlap_partly(q_host, q_out_host), "kv_append: q in place needs the same strides");
-    a.Hq = Hq;
-    a.q_out = static_cast<uint16_t*>(q_out_host->base);
-    a.out_tok = q_out_host->token_stride;
-    a.out_head = q_out_host->head_stride;
-  }
-  const ft_rows* in[3] = {q_host, k_host, v_host};
-  for (int i = with_q ? 0 : 1; i < 3; ++i) {
-    a.in[i] = static_cast<const uint16_t*>(in[i]->base);
-    a.in_tok[i] = in[i]->token_stride;
-    a.in_head[i] = in[i]->head_stride;
-  }
-  a.wide_in = wide(k_host) && wide(v_host) && (!with_q || wide(q_host));
-  a.wide_out = with_q && wide(q_out_host);
-  bool pairs = false;
-  if (rope_host != nullptr) {
-    if ((st = check_rope("kv_append", rope_host, cache_host->D)) != FT_OK) return st;
-    a.freqs = rope_host->freqs;
-    a.mscale = rope_host->mscale;
-    a.rot = rope_host->rot_dim;
-    a.rope_pos = rope_pos ? rope_pos : pos;
-    pairs = rope_host->interleaved != 0;
-  }
-  a.pos = pos;
-  a.T = T;
-  a.Hkv = cache_host->Hkv;
-  a.D = cache_host->D;
-  a.status = dev_status;
-  cudaStream_t s = as_stream(stream);
-  const char* what = "kv_append";
-  switch (fmt) {
-    case FT_KV_BF16: return launch_write<false, FT_KV_BF16>(a, pairs, what, s);
-    case FT_KV_F16: return launch_write<true, FT_KV_F16>(a, pairs, what, s);
-    case FT_KV_E4M3:
-      return dtype == FT_DT_F16 ? launch_write<true, FT_KV_E4M3>(a, pairs, what, s)
-                                : launch_write<false, FT_KV_E4M3>(a, pairs, what, s);
-    default:
-      return dtype == FT_DT_F16 ? launch_write<true, FT_KV_NVFP4>(a, pairs, what, s)
-                                : launch_write<false, FT_KV_NVFP4>(a, pairs, what, s);
-  }
+  return append_call(cache_host, k_host, v_host, T, dtype, table_host, seq, pos, rope_host, nullptr, rope_pos, q_host, Hq,
+                     q_out_host, dev_status, stream);
+}
+
+ft_status ft_kv_append_by_axes(const ft_kv_cache* cache_host, const ft_rows* k_host, const ft_rows* v_host, int32_t T,
+                               int32_t dtype, const ft_page_table* table_host, const int32_t* seq, const int32_t* pos,
+                               const ft_rope_table* rope_host, const ft_rope_axes* axes_host, const int32_t* rope_pos,
+                               const ft_rows* q_host, int32_t Hq, const ft_rows* q_out_host, int32_t* dev_status,
+                               void* stream) {
+  FT_REQUIRE(rope_host != nullptr && axes_host != nullptr, "kv_append: rope or axes are NULL");
+  return append_call(cache_host, k_host, v_host, T, dtype, table_host, seq, pos, rope_host, axes_host, rope_pos, q_host,
+                     Hq, q_out_host, dev_status, stream);
 }
 
 ft_status ft_kv_gather(const ft_kv_cache* cache_host, const ft_page_table* table_host, const int32_t* seq,
