@@ -24,9 +24,12 @@ namespace {
 
 constexpr int kM = 128;          // weight rows of a tile
 constexpr int kStep = 256;       // values of K in a step: four products of 64
-constexpr int kThreads = 192;    // TMA, MMA, four warps of the epilogue
+constexpr int kEpilogueWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpilogueWarps;  // TMA, MMA, epilogue
 constexpr int kMaxStages = 8;
 constexpr int kMaxWidth = 256;
+constexpr int kScaleColumn = 256;  // of TMEM: accumulators before it, each stage's scales from it
+constexpr int kChunks = kMaxWidth / 32 / 2;  // of 32 columns that a warp of the epilogue takes, at most
 constexpr int kSmem = 225 * 1024;
 
 template <int FMT>
@@ -39,17 +42,22 @@ struct MmArgs {
   const float* sx;
   const float* sw;
   int64_t sx_stride, sw_stride;
-  const uint8_t* x_scales;
-  const uint8_t* w_scales;
   int32_t T, N, K;
   int32_t steps;    // of K
-  int32_t ktiles;   // scale tiles of a row of tiles
-  int32_t w_tiles;  // of 128 rows
+  int32_t tiles;
+  int32_t inner;    // tiles that follow one another share the outer matrix's rows: this many, ...
+  int32_t x_inner;  // ... of tokens (the smaller matrix goes round inside)
   int32_t width;    // tokens of a tile
-  int32_t split;    // CTAs of a cluster, slices of K
+  int32_t x_tiles;  // scale tiles that a tile's tokens lie in, at most
+  int32_t buffers;  // accumulators
+  int32_t split;    // slices of K, one a CTA of a cluster (pairs of CTAs: 1)
   int32_t stages, stage_bytes;
-  int32_t dtype;
+  int32_t pairs;    // out and add hold words of two neighbours
   int32_t* status;
+};
+
+struct Maps {
+  CUtensorMap w, x, w_scales, x_scales;
 };
 
 template <int DT>
@@ -68,155 +76,296 @@ __device__ __forceinline__ void store_out(void* p, int64_t at, float x) {
     static_cast<__nv_bfloat16*>(p)[at] = __float2bfloat16_rn(x);
 }
 
-template <int FMT, int DT>
-__global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_constant__ CUtensorMap wmap,
-                                                             const __grid_constant__ CUtensorMap xmap,
+// Where a tile lies: its tile of weight rows, its first token, how many it has.
+struct Place {
+  int w, t0, tokens;
+};
+__device__ __forceinline__ Place place_of(const MmArgs& a, int tile) {
+  const int outer = tile / a.inner, in = tile - outer * a.inner;
+  Place p;
+  p.w = a.x_inner ? outer : in;
+  p.t0 = (a.x_inner ? in : outer) * a.width;
+  p.tokens = min(a.width, a.T - p.t0);
+  return p;
+}
+
+// Columns of a product over these tokens: whole 16s of each CTA's.
+template <int CG>
+__device__ __forceinline__ int columns_of(int tokens) { return (tokens + 16 * CG - 1) & ~(16 * CG - 1); }
+
+// 32 columns of sums, tokens t.. (`count` of them) by the lane's row n, scaled
+// and written: 32 neighbours of one token a store.
+template <int DT>
+__device__ __forceinline__ void put_each(const MmArgs& a, const uint32_t (&v)[32], int64_t t, int count, int n, float sw,
+                                         float sx_of_lane) {
+#pragma unroll
+  for (int i0 = 0; i0 < 32; i0 += 8) {
+    float more[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      more[i] = a.add != nullptr && i0 + i < count && n < a.N ? load_out<DT>(a.add, (t + i0 + i) * a.add_stride + n) : 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float y = __uint_as_float(v[i0 + i]) * sw * __shfl_sync(0xffffffffu, sx_of_lane, i0 + i);
+      if (i0 + i < count && n < a.N)
+        store_out<DT>(a.out, (t + i0 + i) * a.out_stride + n, a.add != nullptr ? y + more[i] : y);
+    }
+  }
+}
+
+// The same where two neighbours share a 4-byte word (16-bit types): lanes trade
+// every second token's sum with their neighbour, and store a word of one token.
+template <int DT>
+__device__ __forceinline__ void put_pairs(const MmArgs& a, const uint32_t (&v)[32], int64_t t, int count, int n, float sw,
+                                          float sx_of_lane) {
+  const int odd = threadIdx.x & 1;
+  const bool in = n < a.N;
+  uint16_t* const out = static_cast<uint16_t*>(a.out) + (t + odd) * a.out_stride + (n & ~1);
+  const uint16_t* const add = static_cast<const uint16_t*>(a.add) + (t + odd) * a.add_stride + (n & ~1);
+#pragma unroll
+  for (int i0 = 0; i0 < 16; i0 += 8) {
+    uint32_t more[8];
+    if (a.add != nullptr) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        more[i] = 2 * (i0 + i) + odd < count && in ? *reinterpret_cast<const uint32_t*>(add + 2 * (i0 + i) * a.add_stride) : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = 2 * (i0 + i);
+      const float y0 = __uint_as_float(v[c]) * sw * __shfl_sync(0xffffffffu, sx_of_lane, c);
+      const float y1 = __uint_as_float(v[c + 1]) * sw * __shfl_sync(0xffffffffu, sx_of_lane, c + 1);
+      const float other = __shfl_xor_sync(0xffffffffu, odd ? y0 : y1, 1);
+      float lo = odd ? other : y0, hi = odd ? y1 : other;
+      if (a.add != nullptr) {
+        const float2 m = unpack2<DT == FT_DT_F16>(more[i]);
+        lo += m.x;
+        hi += m.y;
+      }
+      if (c + odd < count && in) *reinterpret_cast<uint32_t*>(out + c * a.out_stride) = pack2<DT == FT_DT_F16>(lo, hi);
+    }
+  }
+}
+
+template <int FMT, int DT, int CG>
+__global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_constant__ Maps maps,
                                                              const __grid_constant__ MmArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full;
+  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
   __shared__ uint32_t s_tmem;
+  __shared__ int s_bad;
   constexpr int kTiles = step_tiles<FMT>();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = a.split > 1 ? static_cast<int>(blockIdx.x) % a.split : 0;
-  const int tile = blockIdx.x / a.split;
-  const int wt = tile % a.w_tiles, n0 = wt * kM;
-  const int t0 = tile / a.w_tiles * a.width;
-  const int tokens = min(a.width, a.T - t0);
-  const int s0 = static_cast<int>(static_cast<int64_t>(a.steps) * rank / a.split);
-  const int s1 = static_cast<int>(static_cast<int64_t>(a.steps) * (rank + 1) / a.split);
-  const int x_tile0 = t0 / 128, x_tiles = (t0 + tokens + 127) / 128 - x_tile0;  // scale tiles of the tokens
-  constexpr int kWBytes = kM * 128;
-  const int x_bytes = a.width * 128;
-  const uint32_t kAcc = kMaxWidth;  // TMEM columns: accumulators, then each stage's scales
-  constexpr int kScaleCols = kTiles * 4 * 3;
+  constexpr int kRows = kM * CG;  // weight rows of a tile
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int rank = CG == 2 || a.split > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int slice = CG == 2 ? 0 : rank;
+  const int s0 = static_cast<int>(static_cast<int64_t>(a.steps) * slice / a.split);
+  const int s1 = static_cast<int>(static_cast<int64_t>(a.steps) * (slice + 1) / a.split);
+  const int first = blockIdx.x / (CG * a.split), stride = gridDim.x / (CG * a.split);
+  const int x_rows = a.width / CG;  // tokens that a CTA loads of a tile
+  const int x_at = kM * 128, scales_at = x_at + x_rows * 128;
+  constexpr int kWScales = kTiles * 512;
 
   if (threadIdx.x == 0) {
-    prefetch_map(&wmap);
-    prefetch_map(&xmap);
+    prefetch_map(&maps.w);
+    prefetch_map(&maps.x);
+    prefetch_map(&maps.w_scales);
+    prefetch_map(&maps.x_scales);
     for (int i = 0; i < a.stages; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
-    mbar_init(&acc_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], kEpilogueWarps * CG);
+    }
+    s_bad = 0;
     fence_barrier_init();
   }
-  if (warp == 1) tmem_alloc(&s_tmem, 512);
+  if (warp == 1) tmem_alloc<CG>(&s_tmem, 512);
   tc_fence_before();
-  __syncthreads();
+  if (CG == 2) cluster_sync();
+  else __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
   pdl_wait();
-  const bool skip = prior_timeout(a.status);
-  bool ok = !skip;
 
-  if (ok && warp == 0) {
-    if (lane == 0) {
-      int st = 0;
-      uint32_t ph = 1;
+  if (warp == 0) {
+    int st = 0;
+    uint32_t ph = 1;
+    bool ok = true;
+    const uint32_t bytes = CG * (kM * 128 + x_rows * 128 + kWScales * (1 + a.x_tiles));
+    for (int tile = first; tile < a.tiles && ok; tile += stride) {
+      const Place p = place_of(a, tile);
+      const int n0 = p.w * kRows + (CG == 2 ? rank * kM : 0);
+      const int x0 = p.t0 + (CG == 2 ? rank * (columns_of<CG>(p.tokens) / 2) : 0);
       for (int s = s0; s < s1; ++s) {
-        if (!mbar_wait(&empty[st], ph, a.status)) break;
-        uint8_t* const at = smem + st * a.stage_bytes;
-        const int nk = min(kTiles, a.ktiles - s * kTiles);
-        mbar_arrive_expect_tx(&full[st], kWBytes + x_bytes + 512 * nk * (1 + x_tiles));
-        tma_load_2d(at, &wmap, s * 128, n0, &full[st]);
-        tma_load_2d(at + kWBytes, &xmap, s * 128, t0, &full[st]);
-        uint8_t* const sc = at + kWBytes + x_bytes;
-        bulk_g2s(sc, a.w_scales + (static_cast<int64_t>(wt) * a.ktiles + s * kTiles) * 512, 512 * nk, &full[st]);
-        for (int i = 0; i < x_tiles; ++i)
-          bulk_g2s(sc + (1 + i) * kTiles * 512, a.x_scales + (static_cast<int64_t>(x_tile0 + i) * a.ktiles + s * kTiles) * 512,
-                   512 * nk, &full[st]);
+        if (!mbar_wait_warp(&empty[st], ph, a.status)) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
+          uint8_t* const at = smem + st * a.stage_bytes;
+          if (CG == 2) {
+            const uint32_t bar = map_cluster(smem_u32(&full[st]), 0);
+            if (rank == 0) mbar_arrive_expect_tx(&full[st], bytes);
+            tma_load_2d_pair(at, &maps.w, s * 128, n0, bar);
+            tma_load_2d_pair(at + x_at, &maps.x, s * 128, x0, bar);
+            tma_load_2d_pair(at + scales_at, &maps.w_scales, s * kTiles * 64, n0 / 128, bar);
+            tma_load_2d_pair(at + scales_at + kWScales, &maps.x_scales, s * kTiles * 64, p.t0 / 128, bar);
+          } else {
+            mbar_arrive_expect_tx(&full[st], bytes);
+            tma_load_2d(at, &maps.w, s * 128, n0, &full[st]);
+            tma_load_2d(at + x_at, &maps.x, s * 128, x0, &full[st]);
+            tma_load_2d(at + scales_at, &maps.w_scales, s * kTiles * 64, n0 / 128, &full[st]);
+            tma_load_2d(at + scales_at + kWScales, &maps.x_scales, s * kTiles * 64, p.t0 / 128, &full[st]);
+          }
+        }
+        __syncwarp();
         if (++st == a.stages) st = 0, ph ^= 1;
       }
     }
-  } else if (ok && warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = idesc_fp4(FMT == FT_FP4_MXFP4, (tokens + 15) & ~15);
-      int st = 0;
-      uint32_t ph = 0;
-      bool good = true;
-      for (int s = s0; s < s1; ++s) {
-        if (!mbar_wait(&full[st], ph, a.status)) {
-          good = false;
+    if (!ok && lane == 0) s_bad = 1;
+  } else if (warp == 1 && (CG == 1 || rank == 0)) {
+    int st = 0, it = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    const int per = (1 + a.x_tiles) * 4;  // TMEM columns of the scales of one tile of K
+    for (int tile = first; tile < a.tiles && ok; tile += stride, ++it) {
+      const Place p = place_of(a, tile);
+      const uint32_t idesc = idesc_fp4<CG>(FMT == FT_FP4_MXFP4, columns_of<CG>(p.tokens));
+      const int buf = a.buffers == 2 ? it & 1 : 0;
+      const uint32_t acc = tmem + buf * (kScaleColumn / 2);
+      if (it >= a.buffers) {
+        if (!mbar_wait_warp(&acc_empty[buf], (it / a.buffers - 1) & 1, a.status)) {
+          ok = false;
           break;
         }
         tc_fence_after();
-        uint8_t* const at = smem + st * a.stage_bytes;
-        const int nk = min(kTiles, a.ktiles - s * kTiles);
-        const uint8_t* const sc = at + kWBytes + x_bytes;
-        const uint32_t cols = tmem + kAcc + st * kScaleCols;  // [tile of K][weights, tokens 0.., tokens 128..][4]
-        for (int i = 0; i < nk; ++i)
-          for (int j = 0; j <= x_tiles; ++j)
-            scales_to_tmem(cols + i * 12 + j * 4, sc + (j * kTiles + i) * 512);
-        const uint64_t wdesc = sw128_desc(at), xdesc = sw128_desc(at + kWBytes);
-        const int n = min(4, (a.K - s * kStep + 63) / 64);
-        for (int j = 0; j < n; ++j) {
-          const uint32_t c = cols + (FMT == FT_FP4_MXFP4 ? j >> 1 : j) * 12;
-          mma_fp4<FMT == FT_FP4_MXFP4>(tmem, wdesc + 2 * j, xdesc + 2 * j,
-                                       FMT == FT_FP4_MXFP4 ? idesc_scales(idesc, (j & 1) * 2) : idesc, c,
-                                       c + 4 + ((t0 & 127) >> 5), s > s0 || j > 0);
+      }
+      const uint32_t shift = (p.t0 & 127) >> 5;
+      for (int s = s0; s < s1; ++s) {
+        if (!mbar_wait_warp(&full[st], ph, a.status)) {
+          ok = false;
+          break;
         }
-        mma_commit(&empty[st]);
+        tc_fence_after();
+        if (elect_one()) {
+          const uint8_t* const at = smem + st * a.stage_bytes;
+          const uint32_t cols = tmem + kScaleColumn + st * kTiles * per;  // [tile of K][weights, tokens 0.., tokens 128..][4]
+          const uint64_t sc = scales_desc(at + scales_at);
+#pragma unroll
+          for (int i = 0; i < kTiles; ++i) {
+            scales_to_tmem<CG>(cols + i * per, sc + i * 32);
+            scales_to_tmem<CG>(cols + i * per + 4, sc + (kTiles + i) * 32);
+            if (a.x_tiles == 2) scales_to_tmem<CG>(cols + i * per + 8, sc + (2 * kTiles + i) * 32);
+          }
+          const uint64_t wdesc = sw128_desc(at), xdesc = sw128_desc(at + x_at);
+          const int n = min(4, (a.K - s * kStep + 63) / 64);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (j >= n) break;
+            const uint32_t c = cols + (FMT == FT_FP4_MXFP4 ? j >> 1 : j) * per;
+            mma_fp4<CG, FMT == FT_FP4_MXFP4>(acc, wdesc + 2 * j, xdesc + 2 * j,
+                                             FMT == FT_FP4_MXFP4 ? idesc_scales(idesc, (j & 1) * 2) : idesc, c, c + 4 + shift,
+                                             s > s0 || j > 0);
+          }
+          mma_commit<CG>(&empty[st]);
+          if (s + 1 == s1) mma_commit<CG>(&acc_full[buf]);
+        }
+        __syncwarp();
         if (++st == a.stages) st = 0, ph ^= 1;
       }
-      if (good) mma_commit(&acc_full);
     }
-  } else if (ok) {
-    const int q = warp & 3;  // the lanes that the warp may read
-    if (!mbar_wait_warp(&acc_full, 0, a.status)) ok = false;
-    if (ok) {
-      tc_fence_after();
-      const int row = q * 32 + lane, n = n0 + row;
-      const uint32_t from = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    if (!ok && lane == 0) s_bad = 1;
+  } else if (warp >= 2) {
+    const int q = warp & 3, h = (warp - 2) >> 2;  // the lanes that the warp may read; which chunks of 32 columns it takes
+    const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
+    const uint32_t empty_bar = CG == 2 ? map_cluster(smem_u32(&acc_empty[0]), 0) : smem_u32(&acc_empty[0]);
+    int it = 0;
+    for (int tile = first; tile < a.tiles; tile += stride, ++it) {
+      const Place p = place_of(a, tile);
+      const int row = q * 32 + lane, n = p.w * kRows + (CG == 2 ? rank * kM : 0) + row;
+      const int buf = a.buffers == 2 ? it & 1 : 0;
       const float sw = a.sw != nullptr && n < a.N ? a.sw[n * a.sw_stride] : 1.f;
-      float* const part = reinterpret_cast<float*>(smem);  // [token][128]
-      for (int c0 = 0; c0 < tokens; c0 += 32) {
-        float v[32];
-        tmem_ld32(from + c0, v);
-        if (a.split > 1) {
+      float sx[kChunks];
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        const int t = (2 * c + h) * 32 + lane;
+        sx[c] = a.sx != nullptr && t < p.tokens ? a.sx[(p.t0 + t) * a.sx_stride] : 1.f;
+      }
+      if (!mbar_wait_warp(&acc_full[buf], (it / a.buffers) & 1, a.status)) {
+        if (lane == 0) s_bad = 1;
+        break;
+      }
+      tc_fence_after();
+      uint32_t v[kChunks][32];
+      const uint32_t from = tmem + buf * (kScaleColumn / 2) + lanes;
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c)
+        if ((2 * c + h) * 32 < p.tokens) tmem_ld32(from + (2 * c + h) * 32, v[c]);
+      tmem_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (CG == 2) mbar_arrive_cluster(empty_bar + buf * 8);
+        else mbar_arrive(&acc_empty[buf]);
+      }
+      if (CG == 1 && a.split > 1) {
+        float* const part = reinterpret_cast<float*>(smem);  // [token][128]
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            if (c0 + i < tokens) part[(c0 + i) * kM + row] = v[i];
-          continue;
-        }
-        const int t = t0 + c0 + lane;
-        const float sx_l = a.sx != nullptr && t < a.T ? a.sx[t * a.sx_stride] : 1.f;
+            if ((2 * c + h) * 32 + i < p.tokens) part[((2 * c + h) * 32 + i) * kM + row] = __uint_as_float(v[c][i]);
+        break;
+      }
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float sx = __shfl_sync(0xffffffffu, sx_l, i);
-          if (c0 + i >= tokens || n >= a.N) continue;
-          float y = v[i] * sw * sx;
-          const int64_t t_at = t0 + c0 + i;
-          if (a.add != nullptr) y += load_out<DT>(a.add, t_at * a.add_stride + n);
-          store_out<DT>(a.out, t_at * a.out_stride + n, y);
-        }
+      for (int c = 0; c < kChunks; ++c) {
+        const int c0 = (2 * c + h) * 32;
+        if (c0 >= p.tokens) break;
+        if (DT != FT_DT_F32 && a.pairs)
+          put_pairs<DT>(a, v[c], p.t0 + c0, min(32, p.tokens - c0), n, sw, sx[c]);
+        else
+          put_each<DT>(a, v[c], p.t0 + c0, min(32, p.tokens - c0), n, sw, sx[c]);
       }
     }
-    tc_fence_before();
   }
-  if (a.split > 1) {
-    // the slices' partial sums: CTA `rank` joins its share of the elements
+  if (CG == 1 && a.split > 1) {
+    // the slices' partial sums: CTA `slice` joins its share of the elements
     __syncwarp();
     cluster_sync();
-    const int total = tokens * kM, share = (total + a.split - 1) / a.split;
+    const Place p = place_of(a, first);
+    const int total = p.tokens * kM, share = (total + a.split - 1) / a.split;
     const uint32_t mine = smem_u32(smem);
-    for (int e = rank * share + threadIdx.x; e < min(total, (rank + 1) * share); e += kThreads) {
+    for (int e = slice * share + threadIdx.x; e < min(total, (slice + 1) * share); e += kThreads) {
       float y = 0.f;
-      for (int r = 0; r < a.split; ++r) y += ld_cluster_f32(mine + e * 4, r);
-      const int n = n0 + e % kM;
-      const int64_t t = t0 + e / kM;
+      for (int r = 0; r < a.split; ++r) y += ld_cluster_f32(map_cluster(mine + e * 4, r));
+      const int n = p.w * kM + e % kM;
+      const int64_t t = p.t0 + e / kM;
       if (n >= a.N) continue;
       y *= a.sw != nullptr ? a.sw[n * a.sw_stride] : 1.f;
       y *= a.sx != nullptr ? a.sx[t * a.sx_stride] : 1.f;
       if (a.add != nullptr) y += load_out<DT>(a.add, t * a.add_stride + n);
       store_out<DT>(a.out, t * a.out_stride + n, y);
     }
-    cluster_sync();
   }
-  drain_after_timeout(a.status);
+  // A wait that gave up ends its role's loop with copies or products possibly
+  // still in flight: let them land (a bounded 200 us) before TMEM is freed and
+  // the CTA exits.
+  tc_fence_before();
+  __syncthreads();
+  if (s_bad != 0) {
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 200000ull) {
+    }
+  }
+  __syncwarp();
+  if (CG == 2 || a.split > 1) cluster_sync();  // nobody leaves while its memory or barriers are in use
   if (warp == 1) {
     tc_fence_after();
-    tmem_free(tmem, 512);
+    tmem_free<CG>(tmem, 512);
   }
 }
 
@@ -231,13 +380,26 @@ bool map_codes(CUtensorMap* map, const ft_fp4_matrix* m, int rows) {
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int FMT, int DT>
-ft_status launch(const CUtensorMap& wmap, const CUtensorMap& xmap, const MmArgs& a, int64_t tiles, cudaStream_t s) {
-  const auto kernel = matmul_kernel<FMT, DT>;
+// Its scale tiles: a row of tiles in 8-byte words, in boxes of a step by so many rows of tiles.
+bool map_scales(CUtensorMap* map, const ft_fp4_matrix* m, int64_t ktiles, int step, int rows) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(ktiles * 64),
+                              static_cast<cuuint64_t>((m->rows + kScaleTileRows - 1) / kScaleTileRows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ktiles * 512)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(step * 64), static_cast<cuuint32_t>(rows)};
+  const cuuint32_t es[2] = {1, 1};
+  return encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_INT64, 2, m->scales, dims, strides, box, es,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int FMT, int DT, int CG>
+ft_status launch(const Maps& maps, const MmArgs& a, cudaStream_t s) {
+  const auto kernel = matmul_kernel<FMT, DT, CG>;
   ft_status st = ensure_dyn_smem(reinterpret_cast<const void*>(kernel), kSmem, "fp4_matmul");
   if (st != FT_OK) return st;
+  const int cluster = CG * a.split;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * a.split));
+  cfg.gridDim = dim3(std::min(a.tiles, device_sm_count() / cluster) * cluster);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = s;
@@ -245,20 +407,20 @@ ft_status launch(const CUtensorMap& wmap, const CUtensorMap& xmap, const MmArgs&
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = a.split;
+  at[1].val.clusterDim.x = cluster;
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 2;
-  cudaLaunchKernelEx(&cfg, kernel, wmap, xmap, a);
+  cudaLaunchKernelEx(&cfg, kernel, maps, a);
   return launch_check("fp4_matmul");
 }
 
-template <int FMT>
-ft_status launch_typed(const CUtensorMap& w, const CUtensorMap& x, const MmArgs& a, int64_t tiles, cudaStream_t s) {
-  switch (a.dtype) {
-    case FT_DT_BF16: return launch<FMT, FT_DT_BF16>(w, x, a, tiles, s);
-    case FT_DT_F16: return launch<FMT, FT_DT_F16>(w, x, a, tiles, s);
-    default: return launch<FMT, FT_DT_F32>(w, x, a, tiles, s);
+template <int FMT, int CG>
+ft_status launch_typed(const Maps& maps, const MmArgs& a, int32_t dtype, cudaStream_t s) {
+  switch (dtype) {
+    case FT_DT_BF16: return launch<FMT, FT_DT_BF16, CG>(maps, a, s);
+    case FT_DT_F16: return launch<FMT, FT_DT_F16, CG>(maps, a, s);
+    default: return launch<FMT, FT_DT_F32, CG>(maps, a, s);
   }
 }
 
@@ -297,40 +459,51 @@ ft_status ft_fp4_matmul(const ft_fp4_matrix* x_host, const ft_fp4_matrix* w_host
   a.sw = w_host->scale;
   a.sx_stride = x_host->scale_stride;
   a.sw_stride = w_host->scale_stride;
-  a.x_scales = x_host->scales;
-  a.w_scales = w_host->scales;
   a.T = static_cast<int32_t>(x_host->rows);
   a.N = static_cast<int32_t>(w_host->rows);
   a.K = static_cast<int32_t>(x_host->K);
   a.steps = static_cast<int32_t>((x_host->K + kStep - 1) / kStep);
-  a.ktiles = static_cast<int32_t>((x_host->K / fp4_block(x_host->fmt) + 3) / 4);
-  a.w_tiles = (a.N - 1) / kM + 1;
-  a.dtype = dtype;
   a.status = dev_status;
-  const int sms = device_sm_count();
-  const auto tiles_of = [&](int width) { return static_cast<int64_t>(a.w_tiles) * ((a.T - 1) / width + 1); };
+  const auto even = [](const void* p, int64_t stride) { return reinterpret_cast<uintptr_t>(p) % 4 == 0 && stride % 2 == 0; };
+  a.pairs = dtype != FT_DT_F32 && a.N % 2 == 0 && even(out, out_stride) && (add == nullptr || even(add, add_stride));
+  const bool nv = x_host->fmt == FT_FP4_NVFP4;
+  const int sms = device_sm_count(), step = nv ? step_tiles<FT_FP4_NVFP4>() : step_tiles<FT_FP4_MXFP4>();
+  const auto tiles_of = [&](int width, int cg) {
+    return (static_cast<int64_t>(a.N - 1) / (kM * cg) + 1) * ((static_cast<int64_t>(a.T) - 1) / width + 1);
+  };
   a.split = 1;
+  int cg = 1;
   if (a.T <= 64) {
     a.width = (a.T + 15) / 16 * 16;
   } else {
     // waves of the SMs times what a tile takes
     double best = 0;
-    for (int w = 64; w <= kMaxWidth; w += 64) {
-      const double cost = static_cast<double>((tiles_of(w) + sms - 1) / sms) * (w + 64);
-      if (w == 64 || cost <= best) best = cost, a.width = w;
-    }
+    for (int c = 1; c <= 2; ++c)
+      for (int w = 64; w <= kMaxWidth; w += 64) {
+        const double cost = static_cast<double>((tiles_of(w, c) + sms / c - 1) / (sms / c)) * (w + 64);
+        if (best == 0 || cost <= best) best = cost, a.width = w, cg = c;
+      }
   }
-  const int64_t tiles = tiles_of(a.width);
-  while (a.split < 8 && tiles * a.split * 2 <= sms && a.split * 2 <= a.steps) a.split *= 2;
-  FT_REQUIRE(tiles * a.split < (1ll << 31), "%s: too many tiles", what);
-  a.stage_bytes = kM * 128 + a.width * 128 + (x_host->fmt == FT_FP4_NVFP4 ? 2048 : 1024) * 3;
-  a.stages = std::min((kSmem - 1024) / a.stage_bytes, std::min(kMaxStages, 256 / (x_host->fmt == FT_FP4_NVFP4 ? 48 : 24)));
-  CUtensorMap wmap, xmap;
-  if (!map_codes(&wmap, w_host, kM) || !map_codes(&xmap, x_host, a.width))
-    return fail(FT_ERR_INVALID, "%s: a tensor map of the codes was rejected", what);
+  const int64_t tiles = tiles_of(a.width, cg);
+  FT_REQUIRE(tiles < (1ll << 31), "%s: too many tiles", what);
+  a.tiles = static_cast<int32_t>(tiles);
+  while (cg == 1 && a.split < 8 && tiles * a.split * 2 <= sms && a.split * 2 <= a.steps) a.split *= 2;
+  a.x_inner = a.T <= a.N;
+  a.inner = a.x_inner ? (a.T - 1) / a.width + 1 : (a.N - 1) / (kM * cg) + 1;
+  a.x_tiles = a.width > 128 ? 2 : 1;
+  a.buffers = a.width > 128 ? 1 : 2;
+  a.stage_bytes = kM * 128 + a.width / cg * 128 + step * 512 * (1 + a.x_tiles);
+  a.stage_bytes = (a.stage_bytes + 1023) & ~1023;
+  a.stages = std::min({(kSmem - 1024) / a.stage_bytes, kMaxStages, (512 - kScaleColumn) / (step * 4 * (1 + a.x_tiles))});
+  const int64_t ktiles = (x_host->K / fp4_block(x_host->fmt) + 3) / 4;
+  Maps maps;
+  if (!map_codes(&maps.w, w_host, kM) || !map_codes(&maps.x, x_host, a.width / cg) ||
+      !map_scales(&maps.w_scales, w_host, ktiles, step, 1) || !map_scales(&maps.x_scales, x_host, ktiles, step, a.x_tiles))
+    return fail(FT_ERR_INVALID, "%s: a tensor map of the codes or scales was rejected", what);
   cudaStream_t s = as_stream(stream);
-  return x_host->fmt == FT_FP4_NVFP4 ? launch_typed<FT_FP4_NVFP4>(wmap, xmap, a, tiles, s)
-                                     : launch_typed<FT_FP4_MXFP4>(wmap, xmap, a, tiles, s);
+  if (nv)
+    return cg == 2 ? launch_typed<FT_FP4_NVFP4, 2>(maps, a, dtype, s) : launch_typed<FT_FP4_NVFP4, 1>(maps, a, dtype, s);
+  return cg == 2 ? launch_typed<FT_FP4_MXFP4, 2>(maps, a, dtype, s) : launch_typed<FT_FP4_MXFP4, 1>(maps, a, dtype, s);
 }
 
 }  // extern "C"

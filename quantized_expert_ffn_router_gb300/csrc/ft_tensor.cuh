@@ -22,35 +22,59 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
+// The same by a CTA of a pair, counted on the barrier of either (a shared::cluster address).
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+
+// One lane of a warp that runs together.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(is));
+  return is != 0;
+}
+
 // -------------------------------------------------------------------- TMEM ---
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// By one whole warp.
+// By one whole warp; CG 2: of each CTA of a pair.
+template <int CG>
 __device__ __forceinline__ void tmem_alloc(uint32_t* where, uint32_t columns) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(where)), "r"(columns)
-               : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  if (CG == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(where)), "r"(columns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(where)), "r"(columns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
 }
+template <int CG>
 __device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t columns) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(columns) : "memory");
+  if (CG == 2)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(columns) : "memory");
+  else
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(columns) : "memory");
 }
 
 #define FT_R8(b) "=r"(r[b]), "=r"(r[b + 1]), "=r"(r[b + 2]), "=r"(r[b + 3]), "=r"(r[b + 4]), "=r"(r[b + 5]), "=r"(r[b + 6]), "=r"(r[b + 7])
-// 32 columns of the warp's 32 lanes.
-__device__ __forceinline__ void tmem_ld32(uint32_t from, float (&v)[32]) {
-  uint32_t r[32];
+// 32 columns of the warp's 32 lanes, in flight until tmem_wait.
+__device__ __forceinline__ void tmem_ld32(uint32_t from, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
-      "tcgen05.wait::ld.sync.aligned;"
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
       : FT_R8(0), FT_R8(8), FT_R8(16), FT_R8(24)
       : "r"(from)
       : "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 #undef FT_R8
+__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // ---------------------------------------------------------------- products ---
 // K-major operand in the 128-byte swizzle: rows of 128 bytes, groups of 8 rows
@@ -60,40 +84,58 @@ __device__ __forceinline__ uint64_t sw128_desc(const void* tile) {
 }
 
 // A scale tile: 32 rows of 16 bytes without swizzle, groups of 8 rows 128 bytes
-// apart, copied to 32 lanes x 4 columns of each quarter of TMEM.
-__device__ __forceinline__ void scales_to_tmem(uint32_t to, const void* tile) {
-  const uint64_t d = ((smem_u32(tile) >> 4) & 0x3FFFull) | (uint64_t{128 >> 4} << 32) | (1ull << 46);
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(to), "l"(d) : "memory");
+// apart, copied to 32 lanes x 4 columns of each quarter of TMEM (CG 2: by each
+// CTA of the pair from its own shared memory to its own TMEM).
+__device__ __forceinline__ uint64_t scales_desc(const void* tile) {
+  return ((smem_u32(tile) >> 4) & 0x3FFFull) | (uint64_t{128 >> 4} << 32) | (1ull << 46);
+}
+template <int CG>
+__device__ __forceinline__ void scales_to_tmem(uint32_t to, uint64_t desc) {
+  if (CG == 2)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(to), "l"(desc) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(to), "l"(desc) : "memory");
 }
 
-// E2M1 by E2M1, both K-major, M = 128, N = n: scales E4M3, or powers of two.
+// E2M1 by E2M1, both K-major, M = 128 (CG 2: 256), N = n: scales E4M3, or powers of two.
+template <int CG>
 __device__ __forceinline__ uint32_t idesc_fp4(bool pow2, int n) {
-  return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (pow2 ? 1u << 23 : 0u) | (1u << 27);
+  return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (pow2 ? 1u << 23 : 0u) | (uint32_t{CG} << 27);
 }
 // ... with the scales of a row from byte `id` of its word (powers of two: two of the four).
 __device__ __forceinline__ uint32_t idesc_scales(uint32_t idesc, uint32_t id) { return idesc | (id << 4) | (id << 29); }
 
+#define FT_MMA(GROUP, KIND)                                                                                            \
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n tcgen05.mma." GROUP "." KIND                               \
+               " [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),                                                         \
+               "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(static_cast<uint32_t>(accumulate))                      \
+               : "memory")
 // 64 values of K.
-template <bool POW2>
+template <int CG, bool POW2>
 __device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
                                         bool accumulate) {
-  if (POW2)
+  if (CG == 2) {
+    if (POW2) FT_MMA("cta_group::2", "kind::mxf4.block_scale.scale_vec::2X");
+    else FT_MMA("cta_group::2", "kind::mxf4nvf4.block_scale.scale_vec::4X");
+  } else {
+    if (POW2) FT_MMA("cta_group::1", "kind::mxf4.block_scale.scale_vec::2X");
+    else FT_MMA("cta_group::1", "kind::mxf4nvf4.block_scale.scale_vec::4X");
+  }
+}
+#undef FT_MMA
+
+// The barrier (of both CTAs of a pair) is arrived at once the products issued so far are done.
+template <int CG>
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  if (CG == 2)
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(static_cast<uint32_t>(accumulate))
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"(static_cast<uint16_t>(3))
         : "memory");
   else
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(static_cast<uint32_t>(accumulate))
-        : "memory");
-}
-
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-               : "memory");
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
 }
 
 // ---------------------------------------------------------------- clusters ---
@@ -102,32 +144,27 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// The float at a shared memory address of CTA `rank`.
-__device__ __forceinline__ float ld_cluster_f32(uint32_t address, int rank) {
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+// A shared memory address in CTA `rank`.
+__device__ __forceinline__ uint32_t map_cluster(uint32_t address, uint32_t rank) {
   uint32_t at;
-  float v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(address), "r"(rank));
+  return at;
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t at) {
+  float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
   return v;
 }
 
-// ----------------------------------------------------------- after a timeout ---
-// A wait that gave up ends its role's loop with copies or products possibly
-// still in flight: let them land (a bounded 200 us) before TMEM is freed and the
-// CTA exits.  By the whole block.
-__device__ __forceinline__ void drain_after_timeout(const int32_t* status) {
-  __shared__ int s_drain;
-  tc_fence_before();
-  __syncthreads();
-  if (threadIdx.x == 0)
-    s_drain = status != nullptr && *reinterpret_cast<const volatile int32_t*>(status) == FT_ERR_TIMEOUT;
-  __syncthreads();
-  if (s_drain) {
-    const uint64_t t0 = global_timer_ns();
-    while (global_timer_ns() - t0 < 200000ull) {
-    }
-    __syncthreads();
-  }
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // ------------------------------------------------------------ tensor maps ---
