@@ -30,6 +30,7 @@ constexpr int kMaxStages = 8;
 constexpr int kMaxWidth = 256;
 constexpr int kScaleColumn = 256;  // of TMEM: accumulators before it, each stage's scales from it
 constexpr int kChunks = kMaxWidth / 32 / 2;  // of 32 columns that a warp of the epilogue takes, at most
+constexpr int kPartPitch = kM + 4;  // floats of a token's partial sums: fragments are stored without bank conflicts
 constexpr int kSmem = 225 * 1024;
 
 template <int FMT>
@@ -52,12 +53,13 @@ struct MmArgs {
   int32_t buffers;  // accumulators
   int32_t split;    // slices of K, one a CTA of a cluster (pairs of CTAs: 1)
   int32_t stages, stage_bytes;
-  int32_t pairs;    // out and add hold words of two neighbours
+  int32_t chunks;   // of 32 tokens that a warp of the epilogue takes of a tile, at most
+  int32_t tma;      // out and add are reached by tensor maps (16-bit types)
   int32_t* status;
 };
 
 struct Maps {
-  CUtensorMap w, x, w_scales, x_scales;
+  CUtensorMap w, x, w_scales, x_scales, out, add;
 };
 
 template <int DT>
@@ -93,58 +95,11 @@ __device__ __forceinline__ Place place_of(const MmArgs& a, int tile) {
 template <int CG>
 __device__ __forceinline__ int columns_of(int tokens) { return (tokens + 16 * CG - 1) & ~(16 * CG - 1); }
 
-// 32 columns of sums, tokens t.. (`count` of them) by the lane's row n, scaled
-// and written: 32 neighbours of one token a store.
-template <int DT>
-__device__ __forceinline__ void put_each(const MmArgs& a, const uint32_t (&v)[32], int64_t t, int count, int n, float sw,
-                                         float sx_of_lane) {
-#pragma unroll
-  for (int i0 = 0; i0 < 32; i0 += 8) {
-    float more[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      more[i] = a.add != nullptr && i0 + i < count && n < a.N ? load_out<DT>(a.add, (t + i0 + i) * a.add_stride + n) : 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float y = __uint_as_float(v[i0 + i]) * sw * __shfl_sync(0xffffffffu, sx_of_lane, i0 + i);
-      if (i0 + i < count && n < a.N)
-        store_out<DT>(a.out, (t + i0 + i) * a.out_stride + n, a.add != nullptr ? y + more[i] : y);
-    }
-  }
-}
-
-// The same where two neighbours share a 4-byte word (16-bit types): lanes trade
-// every second token's sum with their neighbour, and store a word of one token.
-template <int DT>
-__device__ __forceinline__ void put_pairs(const MmArgs& a, const uint32_t (&v)[32], int64_t t, int count, int n, float sw,
-                                          float sx_of_lane) {
-  const int odd = threadIdx.x & 1;
-  const bool in = n < a.N;
-  uint16_t* const out = static_cast<uint16_t*>(a.out) + (t + odd) * a.out_stride + (n & ~1);
-  const uint16_t* const add = static_cast<const uint16_t*>(a.add) + (t + odd) * a.add_stride + (n & ~1);
-#pragma unroll
-  for (int i0 = 0; i0 < 16; i0 += 8) {
-    uint32_t more[8];
-    if (a.add != nullptr) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        more[i] = 2 * (i0 + i) + odd < count && in ? *reinterpret_cast<const uint32_t*>(add + 2 * (i0 + i) * a.add_stride) : 0;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = 2 * (i0 + i);
-      const float y0 = __uint_as_float(v[c]) * sw * __shfl_sync(0xffffffffu, sx_of_lane, c);
-      const float y1 = __uint_as_float(v[c + 1]) * sw * __shfl_sync(0xffffffffu, sx_of_lane, c + 1);
-      const float other = __shfl_xor_sync(0xffffffffu, odd ? y0 : y1, 1);
-      float lo = odd ? other : y0, hi = odd ? y1 : other;
-      if (a.add != nullptr) {
-        const float2 m = unpack2<DT == FT_DT_F16>(more[i]);
-        lo += m.x;
-        hi += m.y;
-      }
-      if (c + odd < count && in) *reinterpret_cast<uint32_t*>(out + c * a.out_stride) = pack2<DT == FT_DT_F16>(lo, hi);
-    }
-  }
+// A warp's 32 tokens x 32 rows of 16-bit outputs in shared memory: 64 bytes a
+// token, in the 64-byte swizzle.
+constexpr int kBoxBytes = 32 * 64;
+__device__ __forceinline__ uint32_t box_at(uint32_t box, int token, int chunk) {
+  return box + token * 64 + ((chunk ^ ((token >> 1) & 3)) << 4);
 }
 
 template <int FMT, int DT, int CG>
@@ -155,6 +110,9 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
   __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
   __shared__ uint32_t s_tmem;
   __shared__ int s_bad;
+  __shared__ __align__(8) uint64_t add_full[kEpilogueWarps];
+  constexpr bool kNarrow = DT != FT_DT_F32;
+  uint32_t add_phase = 0;
   constexpr int kTiles = step_tiles<FMT>();
   constexpr int kRows = kM * CG;  // weight rows of a tile
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -180,6 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
       mbar_init(&acc_full[i], 1);
       mbar_init(&acc_empty[i], kEpilogueWarps * CG);
     }
+    for (int i = 0; i < kEpilogueWarps; ++i) mbar_init(&add_full[i], 1);
     s_bad = 0;
     fence_barrier_init();
   }
@@ -280,16 +239,49 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
     }
     if (!ok && lane == 0) s_bad = 1;
   } else if (warp >= 2) {
-    const int q = warp & 3, h = (warp - 2) >> 2;  // the lanes that the warp may read; which chunks of 32 columns it takes
-    const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
+    const int e = warp - 2, q = warp & 3, h = e >> 2;  // the lanes that the warp may read; which chunks of 32 columns it takes
     const uint32_t empty_bar = CG == 2 ? map_cluster(smem_u32(&acc_empty[0]), 0) : smem_u32(&acc_empty[0]);
+    uint8_t* const boxes = smem + a.stages * a.stage_bytes + (q * 2 + h) * (a.chunks * kBoxBytes);
+    const uint32_t box0 = smem_u32(boxes);
+    const int row = lane >> 2, col = 2 * (lane & 3);        // of a fragment
+    const int box_token = (lane >> 4) * 8 + (lane & 7), box_chunk = (lane >> 3) & 1;  // the lane's rows of transposed matrices
     int it = 0;
     for (int tile = first; tile < a.tiles; tile += stride, ++it) {
       const Place p = place_of(a, tile);
-      const int row = q * 32 + lane, n = p.w * kRows + (CG == 2 ? rank * kM : 0) + row;
+      const int n0 = p.w * kRows + (CG == 2 ? rank * kM : 0) + q * 32;  // the warp's rows
       const int buf = a.buffers == 2 ? it & 1 : 0;
-      const float sw = a.sw != nullptr && n < a.N ? a.sw[n * a.sw_stride] : 1.f;
-      float sx[kChunks];
+      const int mine = min(kChunks, (p.tokens - h * 32 + 63) / 64);  // chunks
+      if (kNarrow && a.split == 1) {
+        if (lane == 0 && a.tma) bulk_wait_read();  // the boxes are free
+        __syncwarp();
+        if (a.add != nullptr) {
+          if (a.tma) {
+            if (lane == 0 && mine > 0 && n0 < a.N) {
+              mbar_arrive_expect_tx(&add_full[e], mine * kBoxBytes);
+              for (int c = 0; c < mine; ++c)
+                tma_load_2d(boxes + c * kBoxBytes, &maps.add, n0, p.t0 + (2 * c + h) * 32, &add_full[e]);
+            }
+          } else {
+            for (int c = 0; c < mine; ++c) {
+              const int t = p.t0 + (2 * c + h) * 32;
+              const uint16_t* const from = static_cast<const uint16_t*>(a.add) + t * a.add_stride + n0 + lane;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const uint16_t x = t + i < a.T && n0 + lane < a.N ? from[i * a.add_stride] : 0;
+                asm volatile("st.shared.u16 [%0], %1;" ::"r"(box_at(box0 + c * kBoxBytes, i, lane >> 3) + (lane & 7) * 2), "h"(x)
+                             : "memory");
+              }
+            }
+            __syncwarp();
+          }
+        }
+      }
+      float sw[4], sx[kChunks];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int n = n0 + row + 8 * i;
+        sw[i] = a.sw != nullptr && n < a.N ? a.sw[n * a.sw_stride] : 1.f;
+      }
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
         const int t = (2 * c + h) * 32 + lane;
@@ -300,11 +292,15 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
         break;
       }
       tc_fence_after();
-      uint32_t v[kChunks][32];
-      const uint32_t from = tmem + buf * (kScaleColumn / 2) + lanes;
+      uint32_t v[kChunks][32];  // [16 rows][columns of 8][...]
+      const uint32_t from = tmem + buf * (kScaleColumn / 2) + (static_cast<uint32_t>(q * 32) << 16);
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c)
-        if ((2 * c + h) * 32 < p.tokens) tmem_ld32(from + (2 * c + h) * 32, v[c]);
+      for (int c = 0; c < kChunks; ++c) {
+        if (c < mine) {
+          tmem_ld16x32(from + (2 * c + h) * 32, v[c]);
+          tmem_ld16x32(from + (2 * c + h) * 32 + (16u << 16), v[c] + 16);
+        }
+      }
       tmem_wait();
       tc_fence_before();
       __syncwarp();
@@ -313,24 +309,89 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
         else mbar_arrive(&acc_empty[buf]);
       }
       if (CG == 1 && a.split > 1) {
-        float* const part = reinterpret_cast<float*>(smem);  // [token][128]
+        float* const part = reinterpret_cast<float*>(smem);  // [token][kPartPitch]
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c)
+        for (int c = 0; c < kChunks; ++c) {
+          if (c >= mine) break;
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if ((2 * c + h) * 32 + i < p.tokens) part[((2 * c + h) * 32 + i) * kM + row] = __uint_as_float(v[c][i]);
+          for (int i = 0; i < 32; ++i) {
+            const int t = (2 * c + h) * 32 + (i >> 2 & 3) * 8 + col + (i & 1);
+            part[t * kPartPitch + q * 32 + row + (i >> 4) * 16 + (i >> 1 & 1) * 8] = __uint_as_float(v[c][i]);
+          }
+        }
         break;
       }
+      if (kNarrow && a.add != nullptr && a.tma && mine > 0 && n0 < a.N && !mbar_wait_warp(&add_full[e], add_phase, a.status)) {
+        if (lane == 0) s_bad = 1;
+        break;
+      }
+      if (mine > 0 && n0 < a.N) add_phase ^= 1;
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
-        const int c0 = (2 * c + h) * 32;
-        if (c0 >= p.tokens) break;
-        if (DT != FT_DT_F32 && a.pairs)
-          put_pairs<DT>(a, v[c], p.t0 + c0, min(32, p.tokens - c0), n, sw, sx[c]);
-        else
-          put_each<DT>(a, v[c], p.t0 + c0, min(32, p.tokens - c0), n, sw, sx[c]);
+        if (c >= mine) break;
+        const int t0 = p.t0 + (2 * c + h) * 32;
+        const uint32_t box = box0 + c * kBoxBytes;
+#pragma unroll
+        for (int k = 0; k < 4; k += 2) {  // 16 tokens
+          float s[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[i] = __shfl_sync(0xffffffffu, sx[c], (k + (i >> 1)) * 8 + col + (i & 1));
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {  // 16 rows
+            float y[8];  // [token group][8 rows][token]
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              y[i] = __uint_as_float(v[c][16 * half + 4 * k + i]) * sw[2 * half + (i >> 1 & 1)] * s[2 * (i >> 2) + (i & 1)];
+            if constexpr (kNarrow) {
+              const uint32_t at = box_at(box, k * 8 + box_token, 2 * half + box_chunk);
+              uint32_t r[4];
+              if (a.add != nullptr) {
+                load_transposed(at, r);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float2 m = unpack2<DT == FT_DT_F16>(r[i]);
+                  y[2 * i] += m.x;
+                  y[2 * i + 1] += m.y;
+                }
+              }
+#pragma unroll
+              for (int i = 0; i < 4; ++i) r[i] = pack2<DT == FT_DT_F16>(y[2 * i], y[2 * i + 1]);
+              store_transposed(at, r);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int n = n0 + row + 16 * half + 8 * (i >> 1 & 1);
+                const int64_t t = t0 + (k + (i >> 2)) * 8 + col + (i & 1);
+                if (t >= a.T || n >= a.N) continue;
+                if (a.add != nullptr) y[i] += static_cast<const float*>(a.add)[t * a.add_stride + n];
+                static_cast<float*>(a.out)[t * a.out_stride + n] = y[i];
+              }
+            }
+          }
+        }
+        if constexpr (kNarrow) {
+          if (a.tma) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && n0 < a.N) {
+              tma_store_2d(&maps.out, n0, t0, boxes + c * kBoxBytes);
+              bulk_commit();
+            }
+          } else {
+            __syncwarp();
+            uint16_t* const to = static_cast<uint16_t*>(a.out) + t0 * a.out_stride + n0 + lane;
+#pragma unroll 8
+            for (int i = 0; i < 32; ++i) {
+              uint16_t x;
+              asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(box_at(box, i, lane >> 3) + (lane & 7) * 2) : "memory");
+              if (t0 + i < a.T && n0 + lane < a.N) to[i * a.out_stride] = x;
+            }
+            __syncwarp();
+          }
+        }
       }
     }
+    if (lane == 0) bulk_wait();
   }
   if (CG == 1 && a.split > 1) {
     // the slices' partial sums: CTA `slice` joins its share of the elements
@@ -338,13 +399,19 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
     cluster_sync();
     const Place p = place_of(a, first);
     const int total = p.tokens * kM, share = (total + a.split - 1) / a.split;
-    const uint32_t mine = smem_u32(smem);
+    uint32_t part[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) part[r] = map_cluster(smem_u32(smem), min(r, a.split - 1));
     for (int e = slice * share + threadIdx.x; e < min(total, (slice + 1) * share); e += kThreads) {
-      float y = 0.f;
-      for (int r = 0; r < a.split; ++r) y += ld_cluster_f32(map_cluster(mine + e * 4, r));
       const int n = p.w * kM + e % kM;
       const int64_t t = p.t0 + e / kM;
       if (n >= a.N) continue;
+      const uint32_t at = ((e / kM) * kPartPitch + e % kM) * 4;
+      float x[8], y = 0.f;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) x[r] = r < a.split ? ld_cluster_f32(part[r] + at) : 0.f;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) y += x[r];
       y *= a.sw != nullptr ? a.sw[n * a.sw_stride] : 1.f;
       y *= a.sx != nullptr ? a.sx[t * a.sx_stride] : 1.f;
       if (a.add != nullptr) y += load_out<DT>(a.add, t * a.add_stride + n);
@@ -389,6 +456,18 @@ bool map_scales(CUtensorMap* map, const ft_fp4_matrix* m, int64_t ktiles, int st
   const cuuint32_t es[2] = {1, 1};
   return encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_INT64, 2, m->scales, dims, strides, box, es,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Rows of 16-bit outputs, in boxes of 32 by 32 tokens.
+bool map_rows(CUtensorMap* map, const void* p, int64_t N, int64_t T, int64_t stride) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(T)};
+  // one row may have any stride
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(T > 1 ? stride * 2 : (N + 7) / 8 * 16)};
+  const cuuint32_t box[2] = {32, 32};
+  const cuuint32_t es[2] = {1, 1};
+  return encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(p), dims, strides, box, es,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -464,8 +543,8 @@ ft_status ft_fp4_matmul(const ft_fp4_matrix* x_host, const ft_fp4_matrix* w_host
   a.K = static_cast<int32_t>(x_host->K);
   a.steps = static_cast<int32_t>((x_host->K + kStep - 1) / kStep);
   a.status = dev_status;
-  const auto even = [](const void* p, int64_t stride) { return reinterpret_cast<uintptr_t>(p) % 4 == 0 && stride % 2 == 0; };
-  a.pairs = dtype != FT_DT_F32 && a.N % 2 == 0 && even(out, out_stride) && (add == nullptr || even(add, add_stride));
+  const auto whole = [](const void* p, int64_t stride) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % 8 == 0; };
+  a.tma = dtype != FT_DT_F32 && whole(out, out_stride) && (add == nullptr || whole(add, add_stride));
   const bool nv = x_host->fmt == FT_FP4_NVFP4;
   const int sms = device_sm_count(), step = nv ? step_tiles<FT_FP4_NVFP4>() : step_tiles<FT_FP4_MXFP4>();
   const auto tiles_of = [&](int width, int cg) {
@@ -494,12 +573,16 @@ ft_status ft_fp4_matmul(const ft_fp4_matrix* x_host, const ft_fp4_matrix* w_host
   a.buffers = a.width > 128 ? 1 : 2;
   a.stage_bytes = kM * 128 + a.width / cg * 128 + step * 512 * (1 + a.x_tiles);
   a.stage_bytes = (a.stage_bytes + 1023) & ~1023;
-  a.stages = std::min({(kSmem - 1024) / a.stage_bytes, kMaxStages, (512 - kScaleColumn) / (step * 4 * (1 + a.x_tiles))});
+  a.chunks = (a.width + 63) / 64;
+  const int boxes = dtype == FT_DT_F32 ? 0 : kEpilogueWarps * a.chunks * kBoxBytes;
+  a.stages = std::min({(kSmem - 1024 - boxes) / a.stage_bytes, kMaxStages, (512 - kScaleColumn) / (step * 4 * (1 + a.x_tiles))});
   const int64_t ktiles = (x_host->K / fp4_block(x_host->fmt) + 3) / 4;
   Maps maps;
   if (!map_codes(&maps.w, w_host, kM) || !map_codes(&maps.x, x_host, a.width / cg) ||
       !map_scales(&maps.w_scales, w_host, ktiles, step, 1) || !map_scales(&maps.x_scales, x_host, ktiles, step, a.x_tiles))
     return fail(FT_ERR_INVALID, "%s: a tensor map of the codes or scales was rejected", what);
+  if (a.tma && (!map_rows(&maps.out, out, a.N, a.T, out_stride) || (add != nullptr && !map_rows(&maps.add, add, a.N, a.T, add_stride))))
+    a.tma = 0;
   cudaStream_t s = as_stream(stream);
   if (nv)
     return cg == 2 ? launch_typed<FT_FP4_NVFP4, 2>(maps, a, dtype, s) : launch_typed<FT_FP4_NVFP4, 1>(maps, a, dtype, s);

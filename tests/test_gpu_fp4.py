@@ -172,10 +172,12 @@ def test_products_are_exact_where_32_bits_hold_them(fp4, T, N, K, fmt):
     assert (got == multiplied(x, w, fmt)).all()
 
 
-@pytest.mark.parametrize("T,N,K", [(1, 100, 1040), (7, 4096, 4096), (64, 300, 528), (200, 130, 784), (600, 1111, 1040)])
+@pytest.mark.parametrize("T,N,K", [(1, 100, 1040), (7, 4096, 4096), (64, 300, 528), (200, 130, 784), (600, 1111, 1040),
+                                   (1000, 2048, 272)])
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("scale", ["rows", "one", "none"])
-def test_scales_and_a_sum(fp4, T, N, K, dtype, scale):
+@pytest.mark.parametrize("aligned", [False, True])
+def test_scales_and_a_sum(fp4, T, N, K, dtype, scale, aligned):
     """Sums are exact before the row scales: two products, the sum and the output's rounding are left."""
     x, w = random_matrix("nvfp4", T, K, 3, plain=False, scale=scale), random_matrix("nvfp4", N, K, 4, plain=False, scale=scale)
     lift = 2.0 ** -6  # inside f16's range
@@ -183,10 +185,13 @@ def test_scales_and_a_sum(fp4, T, N, K, dtype, scale):
         w.scale.mul_(lift).clamp_(max=4 * lift)
         x.scale.clamp_(max=2.0)
     y = multiplied(x, w, "nvfp4")
-    add = torch.randn(T, N + 3, generator=torch.Generator().manual_seed(0)).mul_(30).to(DT[dtype]).to(DEV)[:, 1:N + 1]
+    # rows on 16-byte boundaries, which are written by whole boxes, or one element off them
+    pad, offset = (-N % 8 + 8, 8) if aligned else (3, 1)
+    add = torch.randn(T, offset + N + pad, generator=torch.Generator().manual_seed(0)).mul_(30).to(DT[dtype]).to(DEV)
+    add = add[:, offset:offset + N]
     for more in (None, add):
         z = y if more is None else y + f64(more)
-        got = product(fp4, x, w, "nvfp4", dtype, add=more, pad=3, offset=1)
+        got = product(fp4, x, w, "nvfp4", dtype, add=more, pad=pad, offset=offset)
         bound = 3 * 2.0 ** -24 * (np.abs(y) + np.abs(z))
         if dtype != "f32":
             bound = bound + HALF[dtype] * np.abs(z) * (1 + 2.0 ** -10) + LEAST[dtype]
@@ -197,10 +202,12 @@ def test_scales_and_a_sum(fp4, T, N, K, dtype, scale):
         assert ok.all()
 
 
-def test_onto_itself_and_repeated(fp4):
+@pytest.mark.parametrize("N", [296, 300])
+@pytest.mark.parametrize("T", [5, 400])
+def test_onto_itself_and_repeated(fp4, T, N):
     """add may be out; two runs give the same bits (slices of K are added in one order)."""
-    x, w = random_matrix("nvfp4", 5, 8192, 1, plain=False), random_matrix("nvfp4", 300, 8192, 2, plain=False)
-    res = torch.randn(5, 300, device=DEV).to(torch.bfloat16)
+    x, w = random_matrix("nvfp4", T, 8192, 1, plain=False), random_matrix("nvfp4", N, 8192, 2, plain=False)
+    res = torch.randn(T, N, device=DEV).to(torch.bfloat16)
     outs = []
     for _ in range(3):
         out = res.clone()
