@@ -53,7 +53,7 @@ struct MmArgs {
   int32_t buffers;  // accumulators
   int32_t split;    // slices of K, one a CTA of a cluster (pairs of CTAs: 1)
   int32_t stages, stage_bytes;
-  int32_t chunks;   // of 32 tokens that a warp of the epilogue takes of a tile, at most
+  int32_t boxes;    // of 32 tokens that each warp of the epilogue has in shared memory, a power of two
   int32_t tma;      // out and add are reached by tensor maps (16-bit types)
   int32_t* status;
 };
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
   } else if (warp >= 2) {
     const int e = warp - 2, q = warp & 3, h = e >> 2;  // the lanes that the warp may read; which chunks of 32 columns it takes
     const uint32_t empty_bar = CG == 2 ? map_cluster(smem_u32(&acc_empty[0]), 0) : smem_u32(&acc_empty[0]);
-    uint8_t* const boxes = smem + a.stages * a.stage_bytes + (q * 2 + h) * (a.chunks * kBoxBytes);
+    uint8_t* const boxes = smem + a.stages * a.stage_bytes + (q * 2 + h) * (a.boxes * kBoxBytes);
     const uint32_t box0 = smem_u32(boxes);
     const int row = lane >> 2, col = 2 * (lane & 3);        // of a fragment
     const int box_token = (lane >> 4) * 8 + (lane & 7), box_chunk = (lane >> 3) & 1;  // the lane's rows of transposed matrices
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
       const int buf = a.buffers == 2 ? it & 1 : 0;
       const int mine = min(kChunks, (p.tokens - h * 32 + 63) / 64);  // chunks
       if (kNarrow && a.split == 1) {
-        if (lane == 0 && a.tma) bulk_wait_read();  // the boxes are free
+        if (lane == 0 && a.tma) bulk_wait_read<0>();  // the boxes are free
         __syncwarp();
         if (a.add != nullptr) {
           if (a.tma) {
@@ -330,7 +330,12 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
       for (int c = 0; c < kChunks; ++c) {
         if (c >= mine) break;
         const int t0 = p.t0 + (2 * c + h) * 32;
-        const uint32_t box = box0 + c * kBoxBytes;
+        const int b = c & (a.boxes - 1);
+        const uint32_t box = box0 + b * kBoxBytes;
+        if (kNarrow && a.tma && c >= a.boxes) {  // (no add: it has a box for each chunk)
+          if (lane == 0) bulk_wait_read<1>();
+          __syncwarp();
+        }
 #pragma unroll
         for (int k = 0; k < 4; k += 2) {  // 16 tokens
           float s[4];
@@ -374,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0 && n0 < a.N) {
-              tma_store_2d(&maps.out, n0, t0, boxes + c * kBoxBytes);
+              tma_store_2d(&maps.out, n0, t0, boxes + b * kBoxBytes);
               bulk_commit();
             }
           } else {
@@ -573,8 +578,10 @@ ft_status ft_fp4_matmul(const ft_fp4_matrix* x_host, const ft_fp4_matrix* w_host
   a.buffers = a.width > 128 ? 1 : 2;
   a.stage_bytes = kM * 128 + a.width / cg * 128 + step * 512 * (1 + a.x_tiles);
   a.stage_bytes = (a.stage_bytes + 1023) & ~1023;
-  a.chunks = (a.width + 63) / 64;
-  const int boxes = dtype == FT_DT_F32 ? 0 : kEpilogueWarps * a.chunks * kBoxBytes;
+  // two boxes a warp; add is loaded ahead, into one for each chunk
+  const int chunks = (a.width + 63) / 64;
+  a.boxes = add == nullptr ? std::min(chunks, 2) : chunks > 2 ? 4 : chunks;
+  const int boxes = dtype == FT_DT_F32 ? 0 : kEpilogueWarps * a.boxes * kBoxBytes;
   a.stages = std::min({(kSmem - 1024 - boxes) / a.stage_bytes, kMaxStages, (512 - kScaleColumn) / (step * 4 * (1 + a.x_tiles))});
   const int64_t ktiles = (x_host->K / fp4_block(x_host->fmt) + 3) / 4;
   Maps maps;
