@@ -6,6 +6,9 @@
 // block's maximum stays in one or two lanes, loads are of 32 bytes and codes of
 // 8; a row's maximum is a few shuffles, and a word a warp in shared memory where
 // a row has several warps.
+#include <algorithm>
+#include <type_traits>
+
 #include "ft_fp4.cuh"
 #include "ft_narrow.cuh"
 
@@ -23,7 +26,8 @@ struct RowArgs {
   uint32_t rows;
   int32_t chunks;   // of 16 values in a row
   int32_t blocks;   // block scales of a row
-  int32_t group_log2;  // threads of a row
+  int32_t group_log2;  // values: threads of a row
+  int32_t group, block_rows;  // quantise: threads of a row, rows of a block
   int32_t tiles;    // order FT_FP4_TILES
   int32_t wide;     // every 16 elements are a 32-byte place
 };
@@ -62,20 +66,28 @@ __device__ __forceinline__ void values_of(const Chunk<DT>& c, float (&x)[16]) {
 
 constexpr float kLargest = 3.4028235e38f;
 
-// The largest magnitude of 16 values, NaN where one is NaN.  Magnitudes of the
-// same type order as their bits do, and NaN come last.
+// The largest magnitude of 16 values, NaN where one is NaN.
 template <int DT>
 __device__ __forceinline__ float chunk_max(const Chunk<DT>& c) {
-  uint32_t m = 0;
+  if constexpr (DT == FT_DT_F32) {  // magnitudes order as their bits do, and NaN come last
+    uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < (DT == FT_DT_F32 ? 4 : 2); ++i) {
-    const uint32_t w[4] = {c.w[i].x, c.w[i].y, c.w[i].z, c.w[i].w};
+    for (int i = 0; i < 4; ++i)
+      m = max(max(m, max(c.w[i].x & 0x7fffffffu, c.w[i].y & 0x7fffffffu)), max(c.w[i].z & 0x7fffffffu, c.w[i].w & 0x7fffffffu));
+    return __uint_as_float(m);
+  } else {
+    using T2 = std::conditional_t<DT == FT_DT_F16, __half2, __nv_bfloat162>;
+    const auto at = [&](int i) {
+      const uint4& v = c.w[i >> 2];
+      const uint32_t w = (i & 3) == 0 ? v.x : (i & 3) == 1 ? v.y : (i & 3) == 2 ? v.z : v.w;
+      return __habs2(*reinterpret_cast<const T2*>(&w));
+    };
+    T2 m = __hmax2_nan(at(0), at(1));
 #pragma unroll
-    for (int j = 0; j < 4; ++j) m = DT == FT_DT_F32 ? max(m, w[j] & 0x7fffffffu) : __vmaxu2(m, w[j] & 0x7fff7fffu);
+    for (int i = 2; i < 8; ++i) m = __hmax2_nan(m, at(i));
+    if constexpr (DT == FT_DT_F16) return __half2float(__hmax_nan(__low2half(m), __high2half(m)));
+    else return __bfloat162float(__hmax_nan(__low2bfloat16(m), __high2bfloat16(m)));
   }
-  if constexpr (DT == FT_DT_F32) return __uint_as_float(m);
-  const uint32_t top = max(m >> 16, m & 0xffffu);
-  return DT == FT_DT_F16 ? __half2float(__ushort_as_half(static_cast<uint16_t>(top))) : __uint_as_float(top << 16);
 }
 
 // The same of finite values alone.
@@ -93,154 +105,242 @@ __device__ __forceinline__ bool any_nan(const float (&x)[16]) {
   return n;
 }
 
-// Codes of 16 values.
-__device__ __forceinline__ uint2 codes16(const float (&q)[16]) {
-  uint32_t w[2] = {0, 0};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w[i >> 2] |= to_e2m1x2(q[2 * i], q[2 * i + 1]) << (8 * (i & 3));
-  return make_uint2(w[0], w[1]);
+// Two floats as one operand of the packed fp32 instructions.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  return static_cast<uint64_t>(__float_as_uint(b)) << 32 | __float_as_uint(a);
+}
+__device__ __forceinline__ float2 unpair(uint64_t p) {
+  return make_float2(__uint_as_float(static_cast<uint32_t>(p)), __uint_as_float(static_cast<uint32_t>(p >> 32)));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
 }
 
-// Codes of x / d for a d of few bits, with r = fl(1 / d): a product with the
-// reciprocal and one correction step (Markstein).  q = fl(x r) is within 2 ulp;
-// x - q d is exact in an fma, because d has 4 bits; so the corrected quotient is
-// that of x / d + 2^-46 of it, rounded.  A border between two codes has at most
-// 4 bits, its product with d at most 8: x is that product, and the quotient
-// comes out as the border, or differs by an ulp of x at least, which is more than
-// 0.53 ulp of the quotient.  Either way the code is that of x / d.
-__device__ __forceinline__ uint2 codes_over(const float (&x)[16], float r, float d, bool odd) {
+// Codes of 8 values.
+__device__ __forceinline__ uint32_t codes8(const float* q) {
+  uint32_t w;
+  asm("{\n .reg .b8 c0, c1, c2, c3;\n cvt.rn.satfinite.e2m1x2.f32 c0, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 c1, %4, %3;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 c2, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 c3, %8, %7;\n mov.b32 %0, {c0, c1, c2, c3};\n}"
+      : "=r"(w)
+      : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
+  return w;
+}
+__device__ __forceinline__ uint2 codes16(const float (&q)[16]) { return make_uint2(codes8(q), codes8(q + 8)); }
+
+// x / d for a d of at most 4 bits, as far as borders between codes of at most 4
+// bits go, with an r of 1 / d (1 + 2^-22 or less): a product with the reciprocal
+// and one correction step (Markstein).  y = fl(x r) is within 2^-21 of x / d; x -
+// y d is exact in an fma, because d has few bits; so y + (x - y d) r is x / d
+// within 2^-43 of it, and is rounded once.  A border times d has at most 8
+// bits.  Where x is that product, the quotient is the border itself; else x is an
+// ulp of x away at least, which is more than 0.53 ulp of the quotient, and does not
+// round to the border.  So codes are those of x / d.  (Divisions took 23.1 us for
+// 8192 x 4096 bf16, this 15.4.)
+__device__ __forceinline__ float over(float x, float r, float d) {
+  const float y = x * r;
+  return fmaf(fmaf(-y, d, x), r, y);
+}
+
+__device__ __forceinline__ uint2 codes_over(const float (&x)[16], float r, float d) {
   float q[16];
+  const uint64_t rr = pair(r, r), dd = pair(-d, -d);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float y = x[i] * r;
-    q[i] = fmaf(fmaf(-y, d, x[i]), r, y);
-  }
-  if (odd) {  // infinities have no remainder
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (!(fabsf(x[i] * r) <= kLargest)) q[i] = x[i] * r;
+  for (int i = 0; i < 8; ++i) {
+    const uint64_t v = pair(x[2 * i], x[2 * i + 1]), y = mul2(v, rr);
+    const float2 z = unpair(fma2(fma2(y, dd, v), rr, y));
+    q[2 * i] = z.x;
+    q[2 * i + 1] = z.y;
   }
   return codes16(q);
+}
+
+__device__ __forceinline__ float reciprocal(float x) {  // to 1 ulp
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// What a chunk becomes: its codes and its block's scale.
+struct Coded {
+  uint2 code;
+  uint32_t byte;
+};
+
+// A chunk of NVFP4 whose largest finite magnitude is m: x is scaled by 1 / up =
+// down where FOUND (powers of two), else x is scaled already.
+template <bool FOUND>
+__device__ __forceinline__ Coded code_nvfp4(const float (&x)[16], float m, float up, float down) {
+  Coded c;
+  c.byte = to_e4m3x2(over(FOUND ? m * down : m, 1.f / 6.f, 6.f), 0.f) & 0xffu;
+  const float b = e4m3_value(c.byte);
+  // without a block scale all codes are 0: the quotients, not their remainders, are NaN else
+  const float r = b > 0.f ? reciprocal(b) : 0.f;
+  c.code = codes_over(x, FOUND ? r * down : r, FOUND ? b * up : b);
+  if (b == 0.f) c.code = make_uint2(0, 0);
+  return c;
+}
+
+// The same of a chunk that holds infinities or NaN, not scaled yet.  (Out of
+// line, and by values: as a reference, x would be in memory for every chunk.)
+template <int DT, bool FOUND>
+__device__ __noinline__ Coded code_odd(Chunk<DT> chunk, float up, float down) {
+  Coded c;
+  float x[16];
+  values_of(chunk, x);
+  if (!FOUND) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] *= down;
+  }
+  const float m = finite_max(x);
+  if (any_nan(x)) return Coded{make_uint2(0, 0), 0x7fu};
+  c.byte = to_e4m3x2(over(FOUND ? m * down : m, 1.f / 6.f, 6.f), 0.f) & 0xffu;
+  const float b = e4m3_value(c.byte);
+  if (b == 0.f) return Coded{make_uint2(0, 0), c.byte};
+  const float r = FOUND ? reciprocal(b) * down : reciprocal(b), d = FOUND ? b * up : b;
+  float q[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) q[i] = fabsf(x[i] * r) <= kLargest ? over(x[i], r, d) : x[i] * r;
+  c.code = codes16(q);
+  return c;
 }
 
 // FMT, DT as named; CH: chunks that a thread holds from the row's maximum to
 // the codes.  0: rows longer than the block's threads hold are read twice.
 // ROW: the row's scale is found (NVFP4); otherwise it is given.
+//
+// A block walks the rows, the next one's chunks on their way while it works on
+// this one's.  Lanes past a row's last chunk, or past the last row, work on the
+// last one again, and store nothing.
 template <int FMT, int DT, int CH, bool ROW>
-__global__ void __launch_bounds__(1024) quantize_kernel(const __grid_constant__ RowArgs a) {
-  __shared__ float warp_max[32];
-  const int group = 1 << a.group_log2;
-  const int l = threadIdx.x & (group - 1);
-  // the launch has up to 2^31 rows of up to 2^10 threads
-  const uint32_t row = blockIdx.x * (blockDim.x >> a.group_log2) + (threadIdx.x >> a.group_log2);
-  const bool live = row < a.rows;
-  const uint32_t r = live ? row : a.rows - 1;
+__global__ void __launch_bounds__(CH > 0 ? 512 : 1024, CH > 0 ? 2 : 1) quantize_kernel(const __grid_constant__ RowArgs a) {
+  __shared__ float warp_max[2][32];
+  // threads of a row: a power of two of one warp's, or whole warps
+  const int group = a.group, in_block = static_cast<int>(threadIdx.x) / group;
+  const int l = threadIdx.x - in_block * group;
+  const uint32_t step = gridDim.x * a.block_rows;
+  const int last = a.chunks - 1;
   pdl_wait();
   constexpr int kHeld = CH > 0 ? CH : 1;
-  Chunk<DT> held[kHeld];
-  const int rounds = CH > 0 ? CH : (a.chunks + group - 1) >> a.group_log2;
-  const auto load = [&](int i, Chunk<DT>& c) {
-    const int at = l + (i << a.group_log2);
-    if (at < a.chunks) {
-      c = load_chunk<DT>(a, r, at);
-    } else {
-#pragma unroll
-      for (auto& w : c.w) w = make_uint4(0, 0, 0, 0);
-    }
+  Chunk<DT> next[kHeld];
+  const int rounds = CH > 0 ? CH : (a.chunks + group - 1) / group;
+  const auto load = [&](uint32_t row, int i) {
+    return load_chunk<DT>(a, min(row, a.rows - 1), min(l + i * group, last));
   };
+  uint32_t base = blockIdx.x * a.block_rows;
   if (CH > 0) {
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) load(i, held[i]);
+    for (int i = 0; i < kHeld; ++i) next[i] = load(base + in_block, i);
   }
-  int e = 0;
-  float inv = 1.f;
-  if constexpr (ROW) {
-    float m = 0.f;
+  int flip = 0;
+  for (; base < a.rows; base += step) {  // below 2^31 + 2^20: no overflow
+    const uint32_t row = base + in_block;
+    const bool live = row < a.rows;
+    Chunk<DT> held[kHeld];
+    if (CH > 0) {
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) held[i] = next[i];
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) next[i] = load(row + step, i);
+    }
+    float most[kHeld];
+    float up = 1.f, down = 1.f;  // 2^e, 2^-e; given: down is fl(1 / s)
+    if constexpr (ROW) {
+      float m = 0.f;
+#pragma unroll(CH > 0 ? CH : 1)
+      for (int i = 0; i < rounds; ++i) {
+        Chunk<DT> c;
+        if (CH > 0) c = held[CH > 0 ? i : 0];
+        else c = load(row, i);
+        float mine = chunk_max(c);
+        if (CH > 0) most[CH > 0 ? i : 0] = mine;
+        if (!(mine <= kLargest)) {
+          float x[16];
+          values_of(c, x);
+          mine = finite_max(x);
+        }
+        m = fmaxf(m, mine);
+      }
+      // magnitudes order as their bits do
+      uint32_t bits = __float_as_uint(m);
+      if (group >= 32) {
+        bits = __reduce_max_sync(0xffffffffu, bits);
+      } else {
+        for (int o = group >> 1; o > 0; o >>= 1) bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, o));
+      }
+      if (group > 32) {
+        const int warps = group >> 5, lane = threadIdx.x & 31;
+        if (lane == 0) warp_max[flip][threadIdx.x >> 5] = __uint_as_float(bits);
+        __syncthreads();
+        bits = __reduce_max_sync(0xffffffffu, __float_as_uint(warp_max[flip][in_block * warps + min(lane, warps - 1)]));
+        flip ^= 1;
+      }
+      const int e = row_exponent(__uint_as_float(bits), 11, 0x280000u);  // 6 * 448 = 1.3125 * 2^11
+      up = pow2f(e);
+      down = pow2f(-e);
+      if (live && l == 0) a.scale[row * a.scale_stride] = up;
+    } else if (FMT == FT_FP4_NVFP4 && a.scale != nullptr) {
+      down = __frcp_rn(a.scale[(live ? row : 0) * a.scale_stride]);
+    }
+    uint8_t* const codes = a.codes + row * a.pitch;
+    const uint32_t r7 = row & 127;
+    uint8_t* const scales = a.scales + (a.tiles ? int64_t{row >> 7} * ((a.blocks + 3) >> 2) * 512 + (r7 & 31) * 16 + (r7 >> 5) * 4
+                                                : int64_t{row} * a.blocks);
+    constexpr int kPer = FMT == FT_FP4_NVFP4 ? 1 : 2;  // chunks of a block
 #pragma unroll(CH > 0 ? CH : 1)
     for (int i = 0; i < rounds; ++i) {
       Chunk<DT> c;
       if (CH > 0) c = held[CH > 0 ? i : 0];
-      else load(i, c);
-      float mine = chunk_max(c);
-      if (!(mine <= kLargest)) {
-        float x[16];
-        values_of(c, x);
-        mine = finite_max(x);
-      }
-      m = fmaxf(m, mine);
-    }
-    for (int o = min(group, 32) >> 1; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (group > 32) {
-      const int warp = threadIdx.x >> 5, warps = group >> 5;
-      if ((threadIdx.x & 31) == 0) warp_max[warp] = m;
-      __syncthreads();
-      m = warp_max[(warp & ~(warps - 1)) | (threadIdx.x & (warps - 1))];
-      for (int o = warps >> 1; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    }
-    e = row_exponent(m, 11, 0x280000u);  // 6 * 448 = 1.3125 * 2^11
-    if (live && l == 0) a.scale[static_cast<int64_t>(row) * a.scale_stride] = pow2f(e);
-  } else if (FMT == FT_FP4_NVFP4 && a.scale != nullptr) {
-    inv = __frcp_rn(a.scale[static_cast<int64_t>(r) * a.scale_stride]);
-  }
-  uint8_t* const codes = a.codes + static_cast<int64_t>(r) * a.pitch;
-  constexpr int kPer = FMT == FT_FP4_NVFP4 ? 1 : 2;  // chunks of a block
-#pragma unroll(CH > 0 ? CH : 1)
-  for (int i = 0; i < rounds; ++i) {
-    Chunk<DT> c;
-    if (CH > 0) c = held[CH > 0 ? i : 0];
-    else load(i, c);
-    const int at = l + (i << a.group_log2);
-    float x[16];
-    values_of(c, x);
-    float m;
-    if (FMT == FT_FP4_NVFP4 && !ROW) {
-      m = 0.f;
+      else c = load(row, i);
+      const int at = l + i * group;
+      float x[16];
+      values_of(c, x);
+      float m = ROW && CH > 0 ? most[CH > 0 ? i : 0] : chunk_max(c);
+      Coded out;
+      if constexpr (FMT == FT_FP4_NVFP4) {
+        if (!ROW) {
+          m *= fabsf(down);  // the greatest value's product is the greatest
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        x[j] *= inv;
-        m = fmaxf(m, fabsf(x[j]));
-        if (isnan(x[j])) m = INFINITY;  // sorted out below
-      }
-    } else {
-      m = chunk_max(c);
-    }
-    bool odd = !(m <= kLargest), nan = false;
-    if (odd) {
-      m = finite_max(x);
-      nan = any_nan(x);
-    }
-    uint32_t byte;
-    uint2 code;
-    if constexpr (FMT == FT_FP4_NVFP4) {
-      byte = to_e4m3x2(nan ? NAN : __fdiv_rn(m * pow2f(-e), 6.f), 0.f) & 0xffu;
-      const float b = e4m3_value(byte);
-      code = make_uint2(0, 0);
-      if (b > 0.f) code = codes_over(x, __frcp_rn(b) * pow2f(-e), b * pow2f(e), odd);
-    } else {
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      nan |= __shfl_xor_sync(0xffffffffu, nan ? 1 : 0, 1) != 0;
-      const int top = max(static_cast<int>(__float_as_uint(m) >> 23) - 129, -127);  // floor(log2 m) - 2
-      byte = nan ? 0xffu : static_cast<uint32_t>(top + 127);
-      const float per = __uint_as_float(static_cast<uint32_t>(127 - top) << 23);  // 2^-top: an exact product
+          for (int j = 0; j < 16; ++j) x[j] *= down;
+        }
+        if (__any_sync(0xffffffffu, !(m <= kLargest)))
+          out = code_odd<DT, ROW>(c, up, down);
+        else
+          out = code_nvfp4<ROW>(x, m, up, down);
+      } else {
+        bool nan = false;
+        if (!(m <= kLargest)) {
+          m = finite_max(x);
+          nan = any_nan(x);
+        }
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        nan |= __shfl_xor_sync(0xffffffffu, nan ? 1 : 0, 1) != 0;
+        const int top = max(static_cast<int>(__float_as_uint(m) >> 23) - 129, -127);  // floor(log2 m) - 2
+        out.byte = nan ? 0xffu : static_cast<uint32_t>(top + 127);
+        const float per = __uint_as_float(static_cast<uint32_t>(127 - top) << 23);  // 2^-top: an exact product
 #pragma unroll
-      for (int j = 0; j < 16; ++j) x[j] *= per;
-      code = codes16(x);
-      if (nan) code = make_uint2(0, 0);
-    }
-    const bool in = live && at < a.chunks;
-    if (in) *reinterpret_cast<uint2*>(codes + static_cast<int64_t>(at) * 8) = code;
-    const int block = at / kPer;
-    if (a.tiles) {
-      // four scales a word, by one lane of four (or eight); 0 past the row's last
-      uint32_t word = in && at % kPer == 0 ? byte << (8 * (block & 3)) : 0;
-      word |= __shfl_xor_sync(0xffffffffu, word, kPer);
-      word |= __shfl_xor_sync(0xffffffffu, word, 2 * kPer);
-      if (in && at % (4 * kPer) == 0) {
-        const int64_t tile = static_cast<int64_t>(row >> 7) * ((a.blocks + 3) >> 2) + (block >> 2);
-        *reinterpret_cast<uint32_t*>(a.scales + tile * 512 + (row & 31) * 16 + ((row & 127) >> 5) * 4) = word;
+        for (int j = 0; j < 16; ++j) x[j] *= per;
+        out.code = codes16(x);
+        if (nan) out.code = make_uint2(0, 0);
       }
-    } else if (in && at % kPer == 0) {
-      a.scales[static_cast<int64_t>(row) * a.blocks + block] = static_cast<uint8_t>(byte);
+      const bool in = live && at <= last;
+      if (in) *reinterpret_cast<uint2*>(codes + at * int64_t{8}) = out.code;
+      const int block = at / kPer;
+      if (a.tiles) {
+        // four scales a word, by one lane of four (or eight); 0 past the row's last
+        uint32_t word = at <= last && at % kPer == 0 ? out.byte << (8 * (block & 3)) : 0;
+        word |= __shfl_xor_sync(0xffffffffu, word, kPer);
+        word |= __shfl_xor_sync(0xffffffffu, word, 2 * kPer);
+        if (in && at % (4 * kPer) == 0) *reinterpret_cast<uint32_t*>(scales + (block >> 2) * int64_t{512}) = word;
+      } else if (in && at % kPer == 0) {
+        scales[block] = static_cast<uint8_t>(out.byte);
+      }
     }
   }
 }
@@ -300,21 +400,28 @@ int ceil_log2(int64_t n) {
 
 template <int FMT, int DT, bool ROW>
 ft_status launch_quantize(RowArgs& a, cudaStream_t s) {
-  // Long calls: two chunks a thread, so that loads overlap and a row's maximum
-  // costs fewer steps.  Short ones: one, so that more threads share the row.
-  const int64_t work = static_cast<int64_t>(a.rows) * a.chunks;
-  const int per = work > static_cast<int64_t>(device_sm_count()) * 2048 ? 2 : 1;
-  int log2 = ceil_log2((a.chunks + per - 1) / per);
-  if (log2 < 3) log2 = 3;  // an MXFP4 word of scales is of 8 lanes
-  int ch = per;
-  if (log2 > 10) {
-    ch = (a.chunks + 1023) / 1024;
-    log2 = 10;
+  // Long calls: two chunks a thread where that leaves fewer lanes idle, or as
+  // many, so that a row's maximum costs fewer steps; short ones: one, so that more
+  // threads share the row.
+  const int sms = device_sm_count();
+  const int warps1 = (a.chunks + 31) / 32, warps2 = (a.chunks + 63) / 64;
+  int ch = 1;
+  if (DT != FT_DT_F32 && static_cast<int64_t>(a.rows) * a.chunks > static_cast<int64_t>(sms) * 2048 && warps2 * 2 <= warps1) ch = 2;
+  if (warps1 > 16) ch = warps2 <= 16 ? 2 : 0;
+  int block;
+  if (ch == 0) {
+    a.group = block = 1024;
+  } else if (warps1 == 1) {
+    a.group = std::max(8, 1 << ceil_log2(a.chunks));  // an MXFP4 word of scales is of 8 lanes
+    block = 256;
+  } else {
+    a.group = 32 * (ch == 2 ? warps2 : warps1);
+    block = a.group * std::max(1, 256 / a.group);
   }
-  a.group_log2 = log2;
-  const int block = log2 > 8 ? 1 << log2 : 256;
-  const uint32_t per_block = static_cast<uint32_t>(block) >> log2;
-  const dim3 grid((a.rows + per_block - 1) / per_block);
+  a.block_rows = block / a.group;
+  const int64_t blocks = (static_cast<int64_t>(a.rows) + a.block_rows - 1) / a.block_rows;
+  const int64_t resident = static_cast<int64_t>(sms) * std::max(1, (ch == 0 ? 1024 : 1024 / block * block) / block);
+  const dim3 grid(static_cast<unsigned>(std::min(blocks, resident)));
   const auto kernel = ch == 1   ? quantize_kernel<FMT, DT, 1, ROW>
                       : ch == 2 ? quantize_kernel<FMT, DT, 2, ROW>
                                 : quantize_kernel<FMT, DT, 0, ROW>;
