@@ -54,7 +54,6 @@ struct MmArgs {
   int32_t split;    // slices of K, one a CTA of a cluster (pairs of CTAs: 1)
   int32_t stages, stage_bytes;
   int32_t boxes;    // of 32 tokens that each warp of the epilogue has in shared memory, a power of two
-  int32_t tma;      // out and add are reached by tensor maps (16-bit types)
   int32_t* status;
 };
 
@@ -95,6 +94,36 @@ __device__ __forceinline__ Place place_of(const MmArgs& a, int tile) {
 template <int CG>
 __device__ __forceinline__ int columns_of(int tokens) { return (tokens + 16 * CG - 1) & ~(16 * CG - 1); }
 
+// A chunk of sums, 32 rows (TMEM lanes) x 32 tokens, as a warp's lanes hold it:
+// value i is of row row_of(i) and token token(i).
+struct Fragment {
+  int row, col;               // of value 0
+  int box_token, box_chunk;   // the lane's row of four 8 x 8 matrices in a box, and its 16-byte place there
+  __device__ __forceinline__ int row_of(int i) const { return row + (i >> 4) * 16 + (i >> 1 & 1) * 8; }
+  __device__ __forceinline__ int token(int i) const { return (i >> 2 & 3) * 8 + col + (i & 1); }
+};
+__device__ __forceinline__ Fragment fragment_of(int lane) {
+  return Fragment{lane >> 2, 2 * (lane & 3), (lane >> 4) * 8 + (lane & 7), (lane >> 3) & 1};
+}
+
+// Its loads, in flight until tmem_wait.
+__device__ __forceinline__ void tmem_ld32x32(uint32_t from, uint32_t (&v)[32]) {
+  tmem_ld16x32(from, v);
+  tmem_ld16x32(from + (16u << 16), v + 16);
+}
+
+// The 8 values of 16 tokens (from 8 k) x 16 rows (from 16 half), scaled.
+__device__ __forceinline__ void scaled(const uint32_t (&v)[32], const float (&sw)[4], const float (&s)[4], int k, int half,
+                                       float (&y)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    y[i] = __uint_as_float(v[16 * half + 4 * k + i]) * sw[2 * half + (i >> 1 & 1)] * s[2 * (i >> 2) + (i & 1)];
+}
+__device__ __forceinline__ void scales_of(float sx_of_lane, const Fragment& f, int k, float (&s)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s[i] = __shfl_sync(0xffffffffu, sx_of_lane, (k + (i >> 1)) * 8 + f.col + (i & 1));
+}
+
 // A warp's 32 tokens x 32 rows of 16-bit outputs in shared memory: 64 bytes a
 // token, in the 64-byte swizzle.
 constexpr int kBoxBytes = 32 * 64;
@@ -102,7 +131,93 @@ __device__ __forceinline__ uint32_t box_at(uint32_t box, int token, int chunk) {
   return box + token * 64 + ((chunk ^ ((token >> 1) & 3)) << 4);
 }
 
-template <int FMT, int DT, int CG>
+// A chunk scaled, rounded and put into a box, which holds what is added to it before.
+template <int DT>
+__device__ __forceinline__ void chunk_to_box(const uint32_t (&v)[32], const float (&sw)[4], float sx_of_lane,
+                                             const Fragment& f, uint32_t box, bool added) {
+#pragma unroll
+  for (int k = 0; k < 4; k += 2) {
+    float s[4];
+    scales_of(sx_of_lane, f, k, s);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      float y[8];
+      scaled(v, sw, s, k, half, y);
+      const uint32_t at = box_at(box, k * 8 + f.box_token, 2 * half + f.box_chunk);
+      uint32_t r[4];
+      if (added) {
+        load_transposed(at, r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 m = unpack2<DT == FT_DT_F16>(r[i]);
+          y[2 * i] += m.x;
+          y[2 * i + 1] += m.y;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r[i] = pack2<DT == FT_DT_F16>(y[2 * i], y[2 * i + 1]);
+      store_transposed(at, r);
+    }
+  }
+}
+
+// What is added to a chunk, as it lies in memory (16-bit types two to a register).
+template <int DT>
+struct Added {
+  uint32_t x[DT == FT_DT_F32 ? 32 : 16];
+};
+template <int DT>
+__device__ __forceinline__ void load_added(const MmArgs& a, int t, int n, const Fragment& f, Added<DT>& to) {
+  // Past the last token or row, the last one again: branches would have each load wait for the one before.
+  const auto at = [&](int i) {
+    return static_cast<int64_t>(min(t + f.token(i), a.T - 1)) * a.add_stride + min(n + f.row_of(i), a.N - 1);
+  };
+  if constexpr (DT == FT_DT_F32) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) to.x[i] = static_cast<const uint32_t*>(a.add)[at(i)];
+  } else {
+    uint16_t x[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = static_cast<const uint16_t*>(a.add)[at(i)];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) to.x[i] = x[2 * i] | static_cast<uint32_t>(x[2 * i + 1]) << 16;
+  }
+}
+
+// A chunk scaled, added to and written where rows are not on 16-byte boundaries
+// (or of fp32): 8 neighbouring rows of 4 tokens a store.  WHOLE: nothing of it is
+// past the last row or token, so that stores need no branches.
+template <int DT, bool WHOLE>
+__device__ __forceinline__ void chunk_to_rows(const MmArgs& a, const uint32_t (&v)[32], const float (&sw)[4], float sx_of_lane,
+                                              const Fragment& f, int t, int n, const Added<DT>& add) {
+#pragma unroll
+  for (int k = 0; k < 4; k += 2) {
+    float s[4];
+    scales_of(sx_of_lane, f, k, s);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      float y[8];
+      scaled(v, sw, s, k, half, y);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int i = 16 * half + 4 * k + j;
+        if (a.add != nullptr) {
+          if (DT == FT_DT_F32) {
+            y[j] += __uint_as_float(add.x[i]);
+          } else {
+            const float2 m = unpack2<DT == FT_DT_F16>(add.x[DT == FT_DT_F32 ? 0 : i >> 1]);
+            y[j] += i & 1 ? m.y : m.x;
+          }
+        }
+        if (WHOLE || (t + f.token(i) < a.T && n + f.row_of(i) < a.N))
+          store_out<DT>(a.out, (t + f.token(i)) * a.out_stride + n + f.row_of(i), y[j]);
+      }
+    }
+  }
+}
+
+// BOXES: 16-bit rows of out (and add) on 16-byte boundaries, moved by whole boxes.
+template <int FMT, int DT, int CG, bool BOXES>
 __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_constant__ Maps maps,
                                                              const __grid_constant__ MmArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -111,7 +226,6 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
   __shared__ uint32_t s_tmem;
   __shared__ int s_bad;
   __shared__ __align__(8) uint64_t add_full[kEpilogueWarps];
-  constexpr bool kNarrow = DT != FT_DT_F32;
   uint32_t add_phase = 0;
   constexpr int kTiles = step_tiles<FMT>();
   constexpr int kRows = kM * CG;  // weight rows of a tile
@@ -130,6 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
     prefetch_map(&maps.x);
     prefetch_map(&maps.w_scales);
     prefetch_map(&maps.x_scales);
+    if (BOXES) prefetch_map(&maps.out);
     for (int i = 0; i < a.stages; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
@@ -241,45 +356,40 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
   } else if (warp >= 2) {
     const int e = warp - 2, q = warp & 3, h = e >> 2;  // the lanes that the warp may read; which chunks of 32 columns it takes
     const uint32_t empty_bar = CG == 2 ? map_cluster(smem_u32(&acc_empty[0]), 0) : smem_u32(&acc_empty[0]);
+    const Fragment f = fragment_of(lane);
     uint8_t* const boxes = smem + a.stages * a.stage_bytes + (q * 2 + h) * (a.boxes * kBoxBytes);
     const uint32_t box0 = smem_u32(boxes);
-    const int row = lane >> 2, col = 2 * (lane & 3);        // of a fragment
-    const int box_token = (lane >> 4) * 8 + (lane & 7), box_chunk = (lane >> 3) & 1;  // the lane's rows of transposed matrices
+    bool ok = true;
     int it = 0;
-    for (int tile = first; tile < a.tiles; tile += stride, ++it) {
+    for (int tile = first; tile < a.tiles && ok; tile += stride, ++it) {
       const Place p = place_of(a, tile);
       const int n0 = p.w * kRows + (CG == 2 ? rank * kM : 0) + q * 32;  // the warp's rows
       const int buf = a.buffers == 2 ? it & 1 : 0;
       const int mine = min(kChunks, (p.tokens - h * 32 + 63) / 64);  // chunks
-      if (kNarrow && a.split == 1) {
-        if (lane == 0 && a.tma) bulk_wait_read<0>();  // the boxes are free
+      const uint32_t from = tmem + buf * (kScaleColumn / 2) + (static_cast<uint32_t>(q * 32) << 16) + h * 32;
+      const auto release = [&] {  // the accumulator
+        tc_fence_before();
         __syncwarp();
-        if (a.add != nullptr) {
-          if (a.tma) {
-            if (lane == 0 && mine > 0 && n0 < a.N) {
-              mbar_arrive_expect_tx(&add_full[e], mine * kBoxBytes);
-              for (int c = 0; c < mine; ++c)
-                tma_load_2d(boxes + c * kBoxBytes, &maps.add, n0, p.t0 + (2 * c + h) * 32, &add_full[e]);
-            }
-          } else {
-            for (int c = 0; c < mine; ++c) {
-              const int t = p.t0 + (2 * c + h) * 32;
-              const uint16_t* const from = static_cast<const uint16_t*>(a.add) + t * a.add_stride + n0 + lane;
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const uint16_t x = t + i < a.T && n0 + lane < a.N ? from[i * a.add_stride] : 0;
-                asm volatile("st.shared.u16 [%0], %1;" ::"r"(box_at(box0 + c * kBoxBytes, i, lane >> 3) + (lane & 7) * 2), "h"(x)
-                             : "memory");
-              }
-            }
-            __syncwarp();
+        if (lane == 0) {
+          if (CG == 2) mbar_arrive_cluster(empty_bar + buf * 8);
+          else mbar_arrive(&acc_empty[buf]);
+        }
+      };
+      if constexpr (BOXES) {
+        if (lane == 0) {
+          bulk_wait_read<0>();  // the boxes are free
+          if (a.add != nullptr && mine > 0 && n0 < a.N) {
+            mbar_arrive_expect_tx(&add_full[e], mine * kBoxBytes);
+            for (int c = 0; c < mine; ++c)
+              tma_load_2d(boxes + c * kBoxBytes, &maps.add, n0, p.t0 + (2 * c + h) * 32, &add_full[e]);
           }
         }
+        __syncwarp();
       }
       float sw[4], sx[kChunks];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int n = n0 + row + 8 * i;
+        const int n = n0 + f.row + 8 * i;
         sw[i] = a.sw != nullptr && n < a.N ? a.sw[n * a.sw_stride] : 1.f;
       }
 #pragma unroll
@@ -287,116 +397,71 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
         const int t = (2 * c + h) * 32 + lane;
         sx[c] = a.sx != nullptr && t < p.tokens ? a.sx[(p.t0 + t) * a.sx_stride] : 1.f;
       }
-      if (!mbar_wait_warp(&acc_full[buf], (it / a.buffers) & 1, a.status)) {
-        if (lane == 0) s_bad = 1;
-        break;
-      }
-      tc_fence_after();
-      uint32_t v[kChunks][32];  // [16 rows][columns of 8][...]
-      const uint32_t from = tmem + buf * (kScaleColumn / 2) + (static_cast<uint32_t>(q * 32) << 16);
+      if constexpr (BOXES) {
+        ok = mbar_wait_warp(&acc_full[buf], (it / a.buffers) & 1, a.status);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t v[kChunks][32];
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        if (c < mine) {
-          tmem_ld16x32(from + (2 * c + h) * 32, v[c]);
-          tmem_ld16x32(from + (2 * c + h) * 32 + (16u << 16), v[c] + 16);
+        for (int c = 0; c < kChunks; ++c)
+          if (c < mine) tmem_ld32x32(from + c * 64, v[c]);
+        tmem_wait();
+        release();
+        if (a.add != nullptr && mine > 0 && n0 < a.N) {
+          ok = mbar_wait_warp(&add_full[e], add_phase, a.status);
+          if (!ok) break;
+          add_phase ^= 1;
         }
-      }
-      tmem_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (CG == 2) mbar_arrive_cluster(empty_bar + buf * 8);
-        else mbar_arrive(&acc_empty[buf]);
-      }
-      if (CG == 1 && a.split > 1) {
-        float* const part = reinterpret_cast<float*>(smem);  // [token][kPartPitch]
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
           if (c >= mine) break;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int t = (2 * c + h) * 32 + (i >> 2 & 3) * 8 + col + (i & 1);
-            part[t * kPartPitch + q * 32 + row + (i >> 4) * 16 + (i >> 1 & 1) * 8] = __uint_as_float(v[c][i]);
+          const int b = c & (a.boxes - 1);
+          if (c >= a.boxes) {  // (no add: it has a box for each chunk)
+            if (lane == 0) bulk_wait_read<1>();
+            __syncwarp();
           }
-        }
-        break;
-      }
-      if (kNarrow && a.add != nullptr && a.tma && mine > 0 && n0 < a.N && !mbar_wait_warp(&add_full[e], add_phase, a.status)) {
-        if (lane == 0) s_bad = 1;
-        break;
-      }
-      if (mine > 0 && n0 < a.N) add_phase ^= 1;
-#pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        if (c >= mine) break;
-        const int t0 = p.t0 + (2 * c + h) * 32;
-        const int b = c & (a.boxes - 1);
-        const uint32_t box = box0 + b * kBoxBytes;
-        if (kNarrow && a.tma && c >= a.boxes) {  // (no add: it has a box for each chunk)
-          if (lane == 0) bulk_wait_read<1>();
+          chunk_to_box<DT>(v[c], sw, sx[c], f, box0 + b * kBoxBytes, a.add != nullptr);
+          fence_proxy_async_smem();
           __syncwarp();
-        }
-#pragma unroll
-        for (int k = 0; k < 4; k += 2) {  // 16 tokens
-          float s[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[i] = __shfl_sync(0xffffffffu, sx[c], (k + (i >> 1)) * 8 + col + (i & 1));
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {  // 16 rows
-            float y[8];  // [token group][8 rows][token]
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              y[i] = __uint_as_float(v[c][16 * half + 4 * k + i]) * sw[2 * half + (i >> 1 & 1)] * s[2 * (i >> 2) + (i & 1)];
-            if constexpr (kNarrow) {
-              const uint32_t at = box_at(box, k * 8 + box_token, 2 * half + box_chunk);
-              uint32_t r[4];
-              if (a.add != nullptr) {
-                load_transposed(at, r);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const float2 m = unpack2<DT == FT_DT_F16>(r[i]);
-                  y[2 * i] += m.x;
-                  y[2 * i + 1] += m.y;
-                }
-              }
-#pragma unroll
-              for (int i = 0; i < 4; ++i) r[i] = pack2<DT == FT_DT_F16>(y[2 * i], y[2 * i + 1]);
-              store_transposed(at, r);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const int n = n0 + row + 16 * half + 8 * (i >> 1 & 1);
-                const int64_t t = t0 + (k + (i >> 2)) * 8 + col + (i & 1);
-                if (t >= a.T || n >= a.N) continue;
-                if (a.add != nullptr) y[i] += static_cast<const float*>(a.add)[t * a.add_stride + n];
-                static_cast<float*>(a.out)[t * a.out_stride + n] = y[i];
-              }
-            }
+          if (lane == 0 && n0 < a.N) {
+            tma_store_2d(&maps.out, n0, p.t0 + (2 * c + h) * 32, boxes + b * kBoxBytes);
+            bulk_commit();
           }
         }
-        if constexpr (kNarrow) {
-          if (a.tma) {
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0 && n0 < a.N) {
-              tma_store_2d(&maps.out, n0, t0, boxes + b * kBoxBytes);
-              bulk_commit();
-            }
+      } else {
+        // A chunk at a time, the next one's add on its way; the first one's while the products run.
+        Added<DT> add[2];
+        const int t0 = p.t0 + h * 32;
+        if (a.add != nullptr && mine > 0 && a.split == 1) load_added(a, t0, n0, f, add[0]);
+        ok = mbar_wait_warp(&acc_full[buf], (it / a.buffers) & 1, a.status);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          if (c >= mine) break;
+          uint32_t v[32];
+          tmem_ld32x32(from + c * 64, v);
+          if (a.add != nullptr && c + 1 < mine && a.split == 1) load_added(a, t0 + (c + 1) * 64, n0, f, add[(c + 1) & 1]);
+          tmem_wait();
+          if (c + 1 == mine) release();
+          if (CG == 1 && a.split > 1) {
+            float* const part = reinterpret_cast<float*>(smem);  // [token][kPartPitch]
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              part[((2 * c + h) * 32 + f.token(i)) * kPartPitch + q * 32 + f.row_of(i)] = __uint_as_float(v[i]);
+          } else if (n0 + 32 <= a.N && t0 + c * 64 + 32 <= a.T) {
+            chunk_to_rows<DT, true>(a, v, sw, sx[c], f, t0 + c * 64, n0, add[c & 1]);
           } else {
-            __syncwarp();
-            uint16_t* const to = static_cast<uint16_t*>(a.out) + t0 * a.out_stride + n0 + lane;
-#pragma unroll 8
-            for (int i = 0; i < 32; ++i) {
-              uint16_t x;
-              asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(box_at(box, i, lane >> 3) + (lane & 7) * 2) : "memory");
-              if (t0 + i < a.T && n0 + lane < a.N) to[i * a.out_stride] = x;
-            }
-            __syncwarp();
+            chunk_to_rows<DT, false>(a, v, sw, sx[c], f, t0 + c * 64, n0, add[c & 1]);
           }
         }
+        if (mine <= 0) release();
       }
     }
-    if (lane == 0) bulk_wait();
+    if (lane == 0) {
+      bulk_wait();
+      if (!ok) s_bad = 1;
+    }
   }
   if (CG == 1 && a.split > 1) {
     // the slices' partial sums: CTA `slice` joins its share of the elements
@@ -476,9 +541,9 @@ bool map_rows(CUtensorMap* map, const void* p, int64_t N, int64_t T, int64_t str
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int FMT, int DT, int CG>
+template <int FMT, int DT, int CG, bool BOXES>
 ft_status launch(const Maps& maps, const MmArgs& a, cudaStream_t s) {
-  const auto kernel = matmul_kernel<FMT, DT, CG>;
+  const auto kernel = matmul_kernel<FMT, DT, CG, BOXES>;
   ft_status st = ensure_dyn_smem(reinterpret_cast<const void*>(kernel), kSmem, "fp4_matmul");
   if (st != FT_OK) return st;
   const int cluster = CG * a.split;
@@ -500,11 +565,13 @@ ft_status launch(const Maps& maps, const MmArgs& a, cudaStream_t s) {
 }
 
 template <int FMT, int CG>
-ft_status launch_typed(const Maps& maps, const MmArgs& a, int32_t dtype, cudaStream_t s) {
+ft_status launch_typed(const Maps& maps, const MmArgs& a, int32_t dtype, bool by_boxes, cudaStream_t s) {
   switch (dtype) {
-    case FT_DT_BF16: return launch<FMT, FT_DT_BF16, CG>(maps, a, s);
-    case FT_DT_F16: return launch<FMT, FT_DT_F16, CG>(maps, a, s);
-    default: return launch<FMT, FT_DT_F32, CG>(maps, a, s);
+    case FT_DT_BF16:
+      return by_boxes ? launch<FMT, FT_DT_BF16, CG, true>(maps, a, s) : launch<FMT, FT_DT_BF16, CG, false>(maps, a, s);
+    case FT_DT_F16:
+      return by_boxes ? launch<FMT, FT_DT_F16, CG, true>(maps, a, s) : launch<FMT, FT_DT_F16, CG, false>(maps, a, s);
+    default: return launch<FMT, FT_DT_F32, CG, false>(maps, a, s);
   }
 }
 
@@ -549,7 +616,7 @@ ft_status ft_fp4_matmul(const ft_fp4_matrix* x_host, const ft_fp4_matrix* w_host
   a.steps = static_cast<int32_t>((x_host->K + kStep - 1) / kStep);
   a.status = dev_status;
   const auto whole = [](const void* p, int64_t stride) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % 8 == 0; };
-  a.tma = dtype != FT_DT_F32 && whole(out, out_stride) && (add == nullptr || whole(add, add_stride));
+  bool by_boxes = dtype != FT_DT_F32 && whole(out, out_stride) && (add == nullptr || whole(add, add_stride));
   const bool nv = x_host->fmt == FT_FP4_NVFP4;
   const int sms = device_sm_count(), step = nv ? step_tiles<FT_FP4_NVFP4>() : step_tiles<FT_FP4_MXFP4>();
   const auto tiles_of = [&](int width, int cg) {
@@ -572,6 +639,7 @@ ft_status ft_fp4_matmul(const ft_fp4_matrix* x_host, const ft_fp4_matrix* w_host
   FT_REQUIRE(tiles < (1ll << 31), "%s: too many tiles", what);
   a.tiles = static_cast<int32_t>(tiles);
   while (cg == 1 && a.split < 8 && tiles * a.split * 2 <= sms && a.split * 2 <= a.steps) a.split *= 2;
+  by_boxes = by_boxes && a.split == 1;  // the slices' sums are joined and written otherwise
   a.x_inner = a.T <= a.N;
   a.inner = a.x_inner ? (a.T - 1) / a.width + 1 : (a.N - 1) / (kM * cg) + 1;
   a.x_tiles = a.width > 128 ? 2 : 1;
@@ -581,19 +649,20 @@ ft_status ft_fp4_matmul(const ft_fp4_matrix* x_host, const ft_fp4_matrix* w_host
   // two boxes a warp; add is loaded ahead, into one for each chunk
   const int chunks = (a.width + 63) / 64;
   a.boxes = add == nullptr ? std::min(chunks, 2) : chunks > 2 ? 4 : chunks;
-  const int boxes = dtype == FT_DT_F32 ? 0 : kEpilogueWarps * a.boxes * kBoxBytes;
+  const int boxes = !by_boxes ? 0 : kEpilogueWarps * a.boxes * kBoxBytes;
   a.stages = std::min({(kSmem - 1024 - boxes) / a.stage_bytes, kMaxStages, (512 - kScaleColumn) / (step * 4 * (1 + a.x_tiles))});
   const int64_t ktiles = (x_host->K / fp4_block(x_host->fmt) + 3) / 4;
   Maps maps;
   if (!map_codes(&maps.w, w_host, kM) || !map_codes(&maps.x, x_host, a.width / cg) ||
       !map_scales(&maps.w_scales, w_host, ktiles, step, 1) || !map_scales(&maps.x_scales, x_host, ktiles, step, a.x_tiles))
     return fail(FT_ERR_INVALID, "%s: a tensor map of the codes or scales was rejected", what);
-  if (a.tma && (!map_rows(&maps.out, out, a.N, a.T, out_stride) || (add != nullptr && !map_rows(&maps.add, add, a.N, a.T, add_stride))))
-    a.tma = 0;
+  if (by_boxes && (!map_rows(&maps.out, out, a.N, a.T, out_stride) ||
+                   (add != nullptr && !map_rows(&maps.add, add, a.N, a.T, add_stride))))
+    return fail(FT_ERR_INVALID, "%s: a tensor map of out or add was rejected", what);
   cudaStream_t s = as_stream(stream);
   if (nv)
-    return cg == 2 ? launch_typed<FT_FP4_NVFP4, 2>(maps, a, dtype, s) : launch_typed<FT_FP4_NVFP4, 1>(maps, a, dtype, s);
-  return cg == 2 ? launch_typed<FT_FP4_MXFP4, 2>(maps, a, dtype, s) : launch_typed<FT_FP4_MXFP4, 1>(maps, a, dtype, s);
+    return cg == 2 ? launch_typed<FT_FP4_NVFP4, 2>(maps, a, dtype, by_boxes, s) : launch_typed<FT_FP4_NVFP4, 1>(maps, a, dtype, by_boxes, s);
+  return cg == 2 ? launch_typed<FT_FP4_MXFP4, 2>(maps, a, dtype, by_boxes, s) : launch_typed<FT_FP4_MXFP4, 1>(maps, a, dtype, by_boxes, s);
 }
 
 }  // extern "C"
