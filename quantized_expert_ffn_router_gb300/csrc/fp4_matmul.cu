@@ -468,24 +468,33 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
     __syncwarp();
     cluster_sync();
     const Place p = place_of(a, first);
-    const int total = p.tokens * kM, share = (total + a.split - 1) / a.split;
+    const int n = p.w * kM + lane * 4;
+    float sw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sw[i] = a.sw != nullptr && n + i < a.N ? a.sw[(n + i) * a.sw_stride] : 1.f;
     uint32_t part[8];
 #pragma unroll
-    for (int r = 0; r < 8; ++r) part[r] = map_cluster(smem_u32(smem), min(r, a.split - 1));
-    for (int e = slice * share + threadIdx.x; e < min(total, (slice + 1) * share); e += kThreads) {
-      const int n = p.w * kM + e % kM;
-      const int64_t t = p.t0 + e / kM;
-      if (n >= a.N) continue;
-      const uint32_t at = ((e / kM) * kPartPitch + e % kM) * 4;
-      float x[8], y = 0.f;
+    for (int r = 0; r < 8; ++r) part[r] = map_cluster(smem_u32(smem) + lane * 16, min(r, a.split - 1));
+    // a token a warp: its 128 rows, four a lane
+#pragma unroll 2
+    for (int t = slice + a.split * warp; t < p.tokens; t += a.split * (kThreads / 32)) {
+      const float sx = a.sx != nullptr ? a.sx[(p.t0 + t) * a.sx_stride] : 1.f;
+      float4 x[8];
 #pragma unroll
-      for (int r = 0; r < 8; ++r) x[r] = r < a.split ? ld_cluster_f32(part[r] + at) : 0.f;
+      for (int r = 0; r < 8; ++r) x[r] = r < a.split ? ld_cluster_f32x4(part[r] + t * (kPartPitch * 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      float y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int r = 0; r < 8; ++r) y += x[r];
-      y *= a.sw != nullptr ? a.sw[n * a.sw_stride] : 1.f;
-      y *= a.sx != nullptr ? a.sx[t * a.sx_stride] : 1.f;
-      if (a.add != nullptr) y += load_out<DT>(a.add, t * a.add_stride + n);
-      store_out<DT>(a.out, t * a.out_stride + n, y);
+      for (int r = 0; r < 8; ++r) y[0] += x[r].x, y[1] += x[r].y, y[2] += x[r].z, y[3] += x[r].w;
+      float more[4];
+      const int64_t to = (p.t0 + t) * a.out_stride + n, from = (p.t0 + t) * a.add_stride;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) more[i] = a.add != nullptr ? load_out<DT>(a.add, from + min(n + i, a.N - 1)) : 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        y[i] = y[i] * sw[i] * sx;
+        if (a.add != nullptr) y[i] += more[i];
+        if (n + i < a.N) store_out<DT>(a.out, to + i, y[i]);
+      }
     }
   }
   // A wait that gave up ends its role's loop with copies or products possibly
@@ -622,23 +631,40 @@ ft_status ft_fp4_matmul(const ft_fp4_matrix* x_host, const ft_fp4_matrix* w_host
   const auto tiles_of = [&](int width, int cg) {
     return (static_cast<int64_t>(a.N - 1) / (kM * cg) + 1) * ((static_cast<int64_t>(a.T) - 1) / width + 1);
   };
-  a.split = 1;
+  // Tiles, and slices of K, by what they take together (us, measured; what all of
+  // them take, 3.5 and the bytes from HBM, left out).  A step: issuing its copies
+  // and products, or the products themselves where they are wide.  After the last
+  // step the tile's sums are drained and written, 0.7 for 64 tokens, under the
+  // next tile's steps where there are two accumulators.  A pair of CTAs meets
+  // first; slices meet before and after their sums are joined.  E.g. 2048 x 4096 x
+  // 4096: pairs of 256 tokens 18.6, alone 20.7, of 128 24.3; 777 x 2560 x 2560:
+  // alone of 128 7.7, of 64 10.2, pairs 8.9; 300 x 300 x 8192: 8 slices of 64 7.5,
+  // whole 13.2; 64 x 2560 x 2048: whole 6.5, 4 slices 7.1.
+  static const double kStepUs[2][4] = {{0.255, 0.285, 0.32, 0.365}, {0.255, 0.28, 0.29, 0.303}};
   int cg = 1;
-  if (a.T <= 64) {
-    a.width = (a.T + 15) / 16 * 16;
-  } else {
-    // waves of the SMs times what a tile takes
-    double best = 0;
-    for (int c = 1; c <= 2; ++c)
-      for (int w = 64; w <= kMaxWidth; w += 64) {
-        const double cost = static_cast<double>((tiles_of(w, c) + sms / c - 1) / (sms / c)) * (w + 64);
-        if (best == 0 || cost <= best) best = cost, a.width = w, cg = c;
-      }
+  double best = 0;
+  const auto consider = [&](int c, int w, int slices) {
+    const int64_t tiles = tiles_of(w, c), places = sms / (c * slices);
+    if (slices > 1 && (tiles > places || slices > a.steps)) return;
+    const int64_t waves = (tiles + places - 1) / places;
+    const double tokens = w / 64.0, steps = (a.steps + slices - 1) / slices * kStepUs[c - 1][w > 64 ? w / 64 - 1 : 0];
+    const double drain = 0.7 * tokens, wait = std::max(w > 128 ? 0.6 : 0.0, drain - steps);
+    const double cost = (c == 2 ? 1.1 : 0) + waves * steps + drain + (waves - 1) * wait + (slices > 1 ? 1.1 + 1.1 * tokens : 0);
+    if (best == 0 || cost < best) best = cost, cg = c, a.width = w, a.split = slices;
+  };
+  for (int slices = 1; slices <= 8; slices *= 2) {
+    if (a.T <= 64) {
+      consider(1, (a.T + 15) / 16 * 16, slices);
+      continue;
+    }
+    for (int w = 64; w <= kMaxWidth; w += 64) {
+      consider(1, w, slices);
+      if (slices == 1) consider(2, w, 1);
+    }
   }
   const int64_t tiles = tiles_of(a.width, cg);
   FT_REQUIRE(tiles < (1ll << 31), "%s: too many tiles", what);
   a.tiles = static_cast<int32_t>(tiles);
-  while (cg == 1 && a.split < 8 && tiles * a.split * 2 <= sms && a.split * 2 <= a.steps) a.split *= 2;
   by_boxes = by_boxes && a.split == 1;  // the slices' sums are joined and written otherwise
   a.x_inner = a.T <= a.N;
   a.inner = a.x_inner ? (a.T - 1) / a.width + 1 : (a.N - 1) / (kM * cg) + 1;

@@ -187,9 +187,12 @@ __device__ __forceinline__ uint32_t map_cluster(uint32_t address, uint32_t rank)
   return at;
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t at) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(at)
+               : "memory");
   return v;
 }
 
