@@ -2,7 +2,7 @@
 cache, then the routed, quantised expert layer, captured into one CUDA graph
 that serves the sequences as they grow.
 
-    python examples/decoder_block.py [--cache bf16|e4m3|nvfp4] [--steps N]
+    python examples/decoder_block.py [--cache bf16|e4m3|nvfp4] [--weights bf16|nvfp4|mxfp4] [--steps N]
 
 Sizes are those of the tiny expert layer (synth.TINY) with 8 query heads over
 2 key heads of 64 channels; weights and inputs are random.
@@ -23,10 +23,11 @@ if ROOT not in sys.path:
 
 import quantized_expert_ffn_router_gb300 as ft  # noqa: E402
 import synth  # noqa: E402
-from quantized_expert_ffn_router_gb300 import attention as att  # noqa: E402
-from quantized_expert_ffn_router_gb300.pipeline import DecodeAttention, DecodeLayer  # noqa: E402
+from quantized_expert_ffn_router_gb300 import attention as att, fp4  # noqa: E402
+from quantized_expert_ffn_router_gb300.pipeline import DecodeAttention, DecodeLayer, Projection  # noqa: E402
 
 FORMATS = {"bf16": att.FT_KV_BF16, "e4m3": att.FT_KV_E4M3, "nvfp4": att.FT_KV_NVFP4}
+WEIGHTS = {"bf16": None, "nvfp4": fp4.FT_FP4_NVFP4, "mxfp4": fp4.FT_FP4_MXFP4}
 
 
 def rms_norm(x):
@@ -35,15 +36,20 @@ def rms_norm(x):
 
 
 class DecoderBlock:
-    """One block for T sequences of up to `longest` tokens, its weights random from `seed`."""
+    """One block for T sequences of up to `longest` tokens, its weights random from `seed`; the projections around the
+    attention in bf16, or in 4 bits (with the rows in front of them quantised each step)."""
 
-    def __init__(self, cache_format="e4m3", longest=4096, page_size=64, Hq=8, Hkv=2, D=64, seed=0, device="cuda"):
+    def __init__(self, cache_format="e4m3", longest=4096, page_size=64, Hq=8, Hkv=2, D=64, seed=0, device="cuda",
+                 weights="bf16"):
         cfg = synth.get_config("tiny")
         self.cfg, T, H = cfg, cfg.tokens[0], cfg.H
         self.T, self.Hq, self.Hkv, self.D = T, Hq, Hkv, D
         g = torch.Generator(device=device).manual_seed(seed)
         weight = lambda n, m: (torch.randn(n, m, generator=g, device=device) / m ** 0.5).to(torch.bfloat16)
         self.w_qkv, self.w_out = weight((Hq + 2 * Hkv) * D, H), weight(H, Hq * D)
+        self.qkv = self.project = None
+        if WEIGHTS[weights] is not None:
+            self.qkv, self.project = (Projection(w, T, WEIGHTS[weights]) for w in (self.w_qkv, self.w_out))
         # attention: a cache whose pages are handed out to the sequences in turn
         per = -(-longest // page_size)
         self.cache = att.KvCache(FORMATS[cache_format], Hkv, D, page_size, T * per, device=device)
@@ -64,8 +70,11 @@ class DecoderBlock:
 
     def step(self, x):
         """x [T, H] bf16 -> [T, H]: attention, then experts, each around a residual; the sequences grow by a token."""
-        qkv = rms_norm(x) @ self.w_qkv.t()
-        x = x + self.attention(qkv, self.pages, self.pos) @ self.w_out.t()
+        if self.qkv is None:
+            qkv = rms_norm(x) @ self.w_qkv.t()
+            x = x + self.attention(qkv, self.pages, self.pos) @ self.w_out.t()
+        else:
+            x = self.project(self.attention(self.qkv(rms_norm(x)), self.pages, self.pos), add=x)
         # the library reads bf16 as bit patterns
         self.moe(0, rms_norm(x).view(torch.int16), self.router, self.cfg.phis[0], self.moe_out.view(torch.int16),
                  overlapped=False)
@@ -76,9 +85,10 @@ class DecoderBlock:
 def main():
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--cache", choices=sorted(FORMATS), default="e4m3")
+    ap.add_argument("--weights", choices=sorted(WEIGHTS), default="bf16")
     ap.add_argument("--steps", type=int, default=1000)
     a = ap.parse_args()
-    block = DecoderBlock(a.cache, longest=a.steps + 8)
+    block = DecoderBlock(a.cache, longest=a.steps + 8, weights=a.weights)
     x = torch.randn(block.T, block.cfg.H, device="cuda").to(torch.bfloat16)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
@@ -95,7 +105,10 @@ def main():
         side.synchronize()
         seconds = time.perf_counter() - t0
     bad = int(block.attention.status.item()) or int(block.moe.status.item())
-    print(f"{block.T} sequences to {int(block.pos[0].item())} tokens, {a.cache} cache: {a.steps / seconds:.0f} steps/s, "
+    if block.qkv is not None:
+        bad = bad or int(block.qkv.status.item()) or int(block.project.status.item())
+    print(f"{block.T} sequences to {int(block.pos[0].item())} tokens, {a.cache} cache, {a.weights} projections: "
+          f"{a.steps / seconds:.0f} steps/s, "
           f"status {bad}, |y| {float(y.float().norm()):.3f}")
     return 1 if bad else 0
 

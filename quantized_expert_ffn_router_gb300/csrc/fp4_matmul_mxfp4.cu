@@ -1,0 +1,10 @@
+// fp4_matmul_mxfp4.cu -- the products' kernels of the format FT_FP4_MXFP4.
+#include "ft_fp4_matmul.cuh"
+
+namespace ft {
+
+ft_status multiply_mxfp4(const Maps& maps, const MmArgs& a, int cg, int32_t dtype, bool by_boxes, cudaStream_t s) {
+  return multiply<FT_FP4_MXFP4>(maps, a, cg, dtype, by_boxes, s);
+}
+
+}  // namespace ft

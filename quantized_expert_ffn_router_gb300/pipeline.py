@@ -153,9 +153,10 @@ class DecodeAttention:
         self.ws = torch.empty(att.attn_decode_workspace(T, Hq, cache.Hkv, D), dtype=torch.uint8, device=device)
         self.status = torch.zeros(1, dtype=torch.int32, device=device)
 
-    def __call__(self, qkv, pages, pos, seq=None):
+    def __call__(self, qkv, pages, pos, seq=None, rope_pos=None):
         """qkv [T, (Hq + 2 Hkv) D]: one projection's row of queries, keys, values; pos [T] int32: the new tokens'
-        positions, that is the tokens cached before them -> [T, Hq D], on the current stream."""
+        positions, that is the tokens cached before them -> [T, Hq D], on the current stream.  rope_pos: the positions
+        of the rotation where those are others (of several axes: [axes, T])."""
         from . import attention as att
 
         T, Hq, Hkv, D = self.T, self.Hq, self.cache.Hkv, self.cache.D
@@ -164,13 +165,40 @@ class DecodeAttention:
         if self.rope is None:
             att.kv_append(self.cache, k, v, pages, pos, seq=seq, dev_status=self.status)
         else:
-            att.kv_append(self.cache, k, v, pages, pos, seq=seq, rope=self.rope, q=q, q_out=self.q,
+            att.kv_append(self.cache, k, v, pages, pos, seq=seq, rope=self.rope, rope_pos=rope_pos, q=q, q_out=self.q,
                           dev_status=self.status)
             q = self.q
         self.lens.copy_(pos).add_(1)
         att.attn_decode(self.cache, q, pages, self.lens, self.out, self.ws, seq=seq, scale=self.scale,
                         window=self.window, dev_status=self.status)
         return self.out.view(T, Hq * D)
+
+
+class Projection:
+    """A dense projection of T rows a step with its weight [N, K] in 4 bits: the weight is quantised once, the rows in
+    front of each product (allocated once, so that steps can be captured in a CUDA graph)."""
+
+    def __init__(self, weight, T: int, fmt: int = 0, dtype=None):
+        import torch
+
+        from . import fp4
+
+        N, K = weight.shape
+        device = weight.device
+        self.w, self.x = fp4.Fp4Matrix(fmt, N, K, device=device), fp4.Fp4Matrix(fmt, T, K, device=device)
+        fp4.fp4_quantize(weight, self.w)
+        self.out = torch.empty((T, N), dtype=dtype or weight.dtype, device=device)
+        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+
+    def __call__(self, x, add=None, out=None):
+        """x [T, K] -> x weight^T (+ add [T, N], which may be `out`) in `out` (default: the same buffer every step), on
+        the current stream."""
+        from . import fp4
+
+        out = self.out if out is None else out
+        fp4.fp4_quantize(x, self.x)
+        fp4.fp4_matmul(self.x, self.w, out, add=add, dev_status=self.status)
+        return out
 
 
 class SpeculativeDecode:
