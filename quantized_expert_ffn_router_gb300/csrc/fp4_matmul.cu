@@ -85,6 +85,8 @@ ft_status ft_fp4_matmul(const ft_fp4_matrix* x_host, const ft_fp4_matrix* w_host
   a.status = dev_status;
   const auto whole = [](const void* p, int64_t stride) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % 8 == 0; };
   bool by_boxes = dtype != FT_DT_F32 && whole(out, out_stride) && (add == nullptr || whole(add, add_stride));
+  const auto even = [](const void* p, int64_t stride) { return reinterpret_cast<uintptr_t>(p) % 4 == 0 && stride % 2 == 0; };
+  a.words = dtype != FT_DT_F32 && a.N % 2 == 0 && even(out, out_stride) && (add == nullptr || even(add, add_stride));
   const bool nv = x_host->fmt == FT_FP4_NVFP4;
   const int sms = device_sm_count(), step = nv ? step_tiles<FT_FP4_NVFP4>() : step_tiles<FT_FP4_MXFP4>();
   const auto tiles_of = [&](int width, int cg) {
@@ -131,10 +133,10 @@ ft_status ft_fp4_matmul(const ft_fp4_matrix* x_host, const ft_fp4_matrix* w_host
   a.buffers = a.width > 128 ? 1 : 2;
   a.stage_bytes = kM * 128 + a.width / cg * 128 + step * 512 * (1 + a.x_tiles);
   a.stage_bytes = (a.stage_bytes + 1023) & ~1023;
-  // two boxes a warp; add is loaded ahead, into one for each chunk
+  // two boxes a warp (row by row: one); add is loaded ahead, into one for each chunk
   const int chunks = (a.width + 63) / 64;
-  a.boxes = add == nullptr ? std::min(chunks, 2) : chunks > 2 ? 4 : chunks;
-  const int boxes = !by_boxes ? 0 : kEpilogueWarps * a.boxes * kBoxBytes;
+  a.boxes = !by_boxes ? 1 : add == nullptr ? std::min(chunks, 2) : chunks > 2 ? 4 : chunks;
+  const int boxes = dtype == FT_DT_F32 ? 0 : kEpilogueWarps * a.boxes * kBoxBytes;
   a.stages = std::min({(kSmem - 1024 - boxes) / a.stage_bytes, kMaxStages, (512 - kScaleColumn) / (step * 4 * (1 + a.x_tiles))});
   const int64_t ktiles = (x_host->K / fp4_block(x_host->fmt) + 3) / 4;
   Maps maps;

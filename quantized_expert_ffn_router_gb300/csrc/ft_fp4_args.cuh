@@ -41,6 +41,7 @@ struct MmArgs {
   int32_t split;    // slices of K, one a CTA of a cluster (pairs of CTAs: 1)
   int32_t stages, stage_bytes;
   int32_t boxes;    // of 32 tokens that each warp of the epilogue has in shared memory, a power of two
+  int32_t words;    // row by row: out and add hold whole words of two rows
   int32_t* status;
 };
 

@@ -121,58 +121,98 @@ __device__ __forceinline__ void chunk_to_box(const uint32_t (&v)[32], const floa
   }
 }
 
-// What is added to a chunk, as it lies in memory (16-bit types two to a register).
+// What is added to a chunk, on its way: fp32 as the sums lie; 16-bit rows a
+// token's 32 over the lanes, or (`words`) two tokens', two rows a lane.  Past the last token or row it is the last one again: branches would have
+// each load wait for the one before (1237 x 5003 x 2592: 44.7 us so).
 template <int DT>
 struct Added {
-  uint32_t x[DT == FT_DT_F32 ? 32 : 16];
+  uint32_t x[32];
 };
 template <int DT>
 __device__ __forceinline__ void load_added(const MmArgs& a, int t, int n, const Fragment& f, Added<DT>& to) {
-  // Past the last token or row, the last one again: branches would have each load wait for the one before.
-  const auto at = [&](int i) {
-    return static_cast<int64_t>(min(t + f.token(i), a.T - 1)) * a.add_stride + min(n + f.row_of(i), a.N - 1);
-  };
+  const int lane = threadIdx.x & 31;
+  const auto at = [&](int token, int row) { return static_cast<int64_t>(min(token, a.T - 1)) * a.add_stride + row; };
   if constexpr (DT == FT_DT_F32) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) to.x[i] = static_cast<const uint32_t*>(a.add)[at(i)];
+    for (int i = 0; i < 32; ++i) to.x[i] = static_cast<const uint32_t*>(a.add)[at(t + f.token(i), min(n + f.row_of(i), a.N - 1))];
+  } else if (a.words) {
+    const int i = lane >> 4, m = min(n + 2 * (lane & 15), a.N - 2);
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      to.x[j] = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.add) + at(t + 2 * j + i, m));
   } else {
-    uint16_t x[32];
+    const int m = min(n + lane, a.N - 1);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = static_cast<const uint16_t*>(a.add)[at(i)];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) to.x[i] = x[2 * i] | static_cast<uint32_t>(x[2 * i + 1]) << 16;
+    for (int j = 0; j < 32; ++j) to.x[j] = static_cast<const uint16_t*>(a.add)[at(t + j, m)];
   }
 }
 
-// A chunk scaled, added to and written where rows are not on 16-byte boundaries
-// (or of fp32): 8 neighbouring rows of 4 tokens a store.  WHOLE: nothing of it is
-// past the last row or token, so that stores need no branches.
+// 16-bit rows from there into the warp's box.
+__device__ __forceinline__ void added_to_box(const MmArgs& a, const uint32_t (&x)[32], uint32_t box) {
+  const int lane = threadIdx.x & 31;
+  if (a.words) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) st_shared_u32(box_at(box, 2 * j + (lane >> 4), (lane & 15) >> 2) + (lane & 3) * 4, x[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      st_shared_u16(box_at(box, j, lane >> 3) + (lane & 7) * 2, static_cast<uint16_t>(x[j]));
+  }
+  __syncwarp();
+}
+
+// A chunk scaled, added to and written where rows are not on 16-byte boundaries:
+// through the warp's box, so that a store is of one token's 32 rows, or (`words`)
+// of two tokens', two rows a lane.  fp32: as the sums lie, 8 rows of 4 tokens a
+// store.  WHOLE: nothing of it is past the last row or token, so that stores need
+// no branches.
 template <int DT, bool WHOLE>
 __device__ __forceinline__ void chunk_to_rows(const MmArgs& a, const uint32_t (&v)[32], const float (&sw)[4], float sx_of_lane,
-                                              const Fragment& f, int t, int n, const Added<DT>& add) {
+                                              const Fragment& f, int t, int n, const Added<DT>& add, uint32_t box) {
+  const int lane = threadIdx.x & 31;
+  if constexpr (DT != FT_DT_F32) {
+    if (a.add != nullptr) added_to_box(a, add.x, box);
+    chunk_to_box<DT>(v, sw, sx_of_lane, f, box, a.add != nullptr);
+  } else {
 #pragma unroll
-  for (int k = 0; k < 4; k += 2) {
-    float s[4];
-    scales_of(sx_of_lane, f, k, s);
+    for (int k = 0; k < 4; k += 2) {
+      float s[4];
+      scales_of(sx_of_lane, f, k, s);
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      float y[8];
-      scaled(v, sw, s, k, half, y);
+      for (int half = 0; half < 2; ++half) {
+        float y[8];
+        scaled(v, sw, s, k, half, y);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int i = 16 * half + 4 * k + j;
-        if (a.add != nullptr) {
-          if (DT == FT_DT_F32) {
-            y[j] += __uint_as_float(add.x[i]);
-          } else {
-            const float2 m = unpack2<DT == FT_DT_F16>(add.x[DT == FT_DT_F32 ? 0 : i >> 1]);
-            y[j] += i & 1 ? m.y : m.x;
-          }
+        for (int j = 0; j < 8; ++j) {
+          const int i = 16 * half + 4 * k + j;
+          if (a.add != nullptr) y[j] += __uint_as_float(add.x[i]);
+          if (WHOLE || (t + f.token(i) < a.T && n + f.row_of(i) < a.N))
+            store_out<DT>(a.out, (t + f.token(i)) * a.out_stride + n + f.row_of(i), y[j]);
         }
-        if (WHOLE || (t + f.token(i) < a.T && n + f.row_of(i) < a.N))
-          store_out<DT>(a.out, (t + f.token(i)) * a.out_stride + n + f.row_of(i), y[j]);
       }
     }
+  }
+  if constexpr (DT != FT_DT_F32) {
+    __syncwarp();
+    if (a.words) {
+      const int i = lane >> 4, m = n + 2 * (lane & 15);
+      uint16_t* const to = static_cast<uint16_t*>(a.out) + (t + i) * a.out_stride + m;
+      uint32_t x[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) x[j] = ld_shared_u32(box_at(box, 2 * j + i, (lane & 15) >> 2) + (lane & 3) * 4);
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (WHOLE || (t + 2 * j + i < a.T && m < a.N)) *reinterpret_cast<uint32_t*>(to + 2 * j * a.out_stride) = x[j];
+    } else {
+      uint16_t* const to = static_cast<uint16_t*>(a.out) + t * a.out_stride + n + lane;
+      uint16_t x[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) x[j] = ld_shared_u16(box_at(box, j, lane >> 3) + (lane & 7) * 2);
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (WHOLE || (t + j < a.T && n + lane < a.N)) to[j * a.out_stride] = x[j];
+    }
+    __syncwarp();
   }
 }
 
@@ -410,9 +450,9 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
             for (int i = 0; i < 32; ++i)
               part[((2 * c + h) * 32 + f.token(i)) * kPartPitch + q * 32 + f.row_of(i)] = __uint_as_float(v[i]);
           } else if (n0 + 32 <= a.N && t0 + c * 64 + 32 <= a.T) {
-            chunk_to_rows<DT, true>(a, v, sw, sx[c], f, t0 + c * 64, n0, add[c & 1]);
+            chunk_to_rows<DT, true>(a, v, sw, sx[c], f, t0 + c * 64, n0, add[c & 1], box0);
           } else {
-            chunk_to_rows<DT, false>(a, v, sw, sx[c], f, t0 + c * 64, n0, add[c & 1]);
+            chunk_to_rows<DT, false>(a, v, sw, sx[c], f, t0 + c * 64, n0, add[c & 1], box0);
           }
         }
         if (mine <= 0) release();

@@ -60,6 +60,25 @@ __device__ __forceinline__ void load_transposed(uint32_t at, uint32_t (&r)[4]) {
                : "memory");
 }
 
+// Not to be moved over stores of shared memory, but over those of global memory.
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t at) {
+  uint32_t x;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(at));
+  return x;
+}
+__device__ __forceinline__ uint16_t ld_shared_u16(uint32_t at) {
+  uint16_t x;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(at));
+  return x;
+}
+
+__device__ __forceinline__ void st_shared_u32(uint32_t at, uint32_t x) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(x) : "memory");
+}
+__device__ __forceinline__ void st_shared_u16(uint32_t at, uint16_t x) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(x) : "memory");
+}
+
 // One lane of a warp that runs together.
 __device__ __forceinline__ bool elect_one() {
   uint32_t is;
