@@ -8,6 +8,8 @@
 namespace ft {
 namespace {
 
+constexpr int64_t kMostRows = (1ll << 31) - 1024;
+
 // A matrix's codes, in boxes of 128 bytes by so many rows.
 bool map_codes(CUtensorMap* map, const ft_fp4_matrix* m, int rows) {
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(m->K / 2), static_cast<cuuint64_t>(m->rows)};
@@ -61,6 +63,9 @@ ft_status ft_fp4_matmul(const ft_fp4_matrix* x_host, const ft_fp4_matrix* w_host
              static_cast<long long>(w_host->K));
   if (x_host->order != FT_FP4_TILES || w_host->order != FT_FP4_TILES)
     return fail(FT_ERR_UNSUPPORTED, "%s: block scales must be in the order FT_FP4_TILES", what);
+  // rows are numbered in 32 bits, up to the end of the last tile
+  if (x_host->rows > kMostRows || w_host->rows > kMostRows)
+    return fail(FT_ERR_UNSUPPORTED, "%s: more than %lld rows", what, static_cast<long long>(kMostRows));
   FT_REQUIRE(dtype >= FT_DT_BF16 && dtype <= FT_DT_F32, "%s: dtype %d", what, dtype);
   if (x_host->rows == 0 || w_host->rows == 0) return FT_OK;
   const uintptr_t size = dtype == FT_DT_F32 ? 4 : 2;

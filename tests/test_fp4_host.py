@@ -137,6 +137,8 @@ def test_the_library_refuses(fp4):
     for bad in (dict(out=None), dict(out=(1 << 16) + 1), dict(stride=-8), dict(dtype=4), dict(add=(1 << 17) + 1),
                 dict(add=1 << 17, add_stride=-1), dict(add=1 << 16, add_stride=16)):
         assert c.matmul(c.m(), c.m(), **bad) == 1, bad
+    for rows in ((1 << 31) - 1, (1 << 31) - 1023):
+        assert c.matmul(c.m(rows=rows), c.m()) == 2 and c.matmul(c.m(), c.m(rows=rows)) == 2
     assert c.quantize(c.m(rows=0)) == c.matmul(c.m(rows=0), c.m()) == c.matmul(c.m(), c.m(rows=0)) == 0
 
 

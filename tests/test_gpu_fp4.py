@@ -158,7 +158,7 @@ def product(fp4, x, w, fmt, dtype, add=None, pad=0, offset=0):
 
 
 SIZES = [  # T, N, K
-    (1, 1, 32), (1, 128, 256), (1, 200, 4096), (3, 130, 96), (16, 128, 2048), (17, 384, 544), (33, 5, 1024), (64, 2560, 2048),
+    (1, 1, 32), (1, 5, 16), (3, 131, 48), (70, 260, 16), (300, 300, 272), (1, 128, 256), (1, 200, 4096), (3, 130, 96), (16, 128, 2048), (17, 384, 544), (33, 5, 1024), (64, 2560, 2048),
     (65, 129, 608), (100, 333, 288), (128, 128, 512), (129, 257, 320), (191, 640, 32), (256, 256, 256), (300, 1000, 1120),
     (777, 512, 96), (1237, 200, 2592), (2048, 1024, 512), (2, 70000, 64), (5000, 17, 160)]
 
@@ -167,6 +167,7 @@ SIZES = [  # T, N, K
 @pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
 def test_products_are_exact_where_32_bits_hold_them(fp4, T, N, K, fmt):
     """Products are whole multiples of 2^-8 (2^-6), sums below 2^24 of those: nothing is rounded."""
+    K += -K % BLOCK[fmt]
     x, w = random_matrix(fmt, T, K, 1), random_matrix(fmt, N, K, 2)
     got = product(fp4, x, w, fmt, "f32")
     assert (got == multiplied(x, w, fmt)).all()
@@ -216,6 +217,33 @@ def test_onto_itself_and_repeated(fp4, T, N):
     other = torch.empty_like(res)
     fp4.fp4_matmul(x, w, other, add=res)
     assert all(torch.equal(o, other) for o in outs)
+
+
+def test_views(fp4):
+    """Codes in wider rows, row scales a step apart, x whose rows are one row, in- and outputs of one row of any stride."""
+    T, N, K = 37, 150, 96
+    x, w = random_matrix("nvfp4", T, K, 1), random_matrix("nvfp4", N, K, 2)
+    wide = lambda m: torch.cat((m.codes, torch.full((m.rows, 80), 0x77, dtype=torch.uint8, device=DEV)), 1)[:, :m.codes.shape[1]]
+    apart = lambda m: torch.stack((m.scale, torch.full_like(m.scale, float("nan"))), 1)[:, 0]
+    views = [fp4.Fp4Matrix.over(m.fmt, K, wide(m), m.scales, scale=apart(m)) for m in (x, w)]
+    assert views[0].desc.pitch == 128 and views[0].desc.scale_stride == 2
+    assert (product(fp4, *views, "nvfp4", "f32") == multiplied(x, w, "nvfp4")).all()
+    row = rows_of(1, K, "bf16", 3)
+    fp4.fp4_quantize(row.expand(T, K), views[0])
+    want = quantised("nvfp4", np.broadcast_to(f64(row), (T, K)))
+    check_quantised(views[0], "nvfp4", want, True)
+    assert torch.isnan(views[0].scale.as_strided((2 * T - 1,), (1,))[1::2]).all()
+    out = torch.empty(1, 3 * N, device=DEV)[:, ::3].as_strided((1, N), (7, 1))
+    one = fp4.Fp4Matrix(FMT["nvfp4"], 1, K)
+    fp4.fp4_quantize(row.as_strided((1, K), (5, 1)), one)
+    fp4.fp4_matmul(one, w, out)
+    want = multiplied(one, w, "nvfp4")
+    assert (np.abs(f64(out) - want) <= 2.0 ** -23 * np.abs(want)).all()
+
+
+def test_a_matrix_by_itself(fp4):
+    x = random_matrix("mxfp4", 200, 320, 1)
+    assert (product(fp4, x, x, "mxfp4", "f32") == multiplied(x, x, "mxfp4")).all()
 
 
 def test_nothing_to_do(fp4):
