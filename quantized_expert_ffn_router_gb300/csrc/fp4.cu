@@ -107,10 +107,14 @@ __device__ __forceinline__ bool any_nan(const float (&x)[16]) {
 
 // Two floats as one operand of the packed fp32 instructions.
 __device__ __forceinline__ uint64_t pair(float a, float b) {
-  return static_cast<uint64_t>(__float_as_uint(b)) << 32 | __float_as_uint(a);
+  uint64_t p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(a), "f"(b));
+  return p;
 }
 __device__ __forceinline__ float2 unpair(uint64_t p) {
-  return make_float2(__uint_as_float(static_cast<uint32_t>(p)), __uint_as_float(static_cast<uint32_t>(p >> 32)));
+  float2 v;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
+  return v;
 }
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t d;
