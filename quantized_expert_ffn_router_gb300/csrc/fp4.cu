@@ -6,6 +6,14 @@
 // block's maximum stays in one or two lanes, loads are of 32 bytes and codes of
 // 8; a row's maximum is a few shuffles, and a word a warp in shared memory where
 // a row has several warps.
+//
+// Measured (GPU time in a graph, inputs beyond L2; of 6.79 TB/s):
+//   8192 x 4096 bf16 to NVFP4 with row scales 17.6 us (72%: instructions, of which
+//     65% of the issue slots are used, and the row's maximum between loads and
+//     codes), f32 25.2 (90%), to MXFP4 15.2 (82%); 20480 x 2560 by a given scale
+//     25.0 (79%);
+//   read back as bf16: 8192 x 4096 15.4 us (82%), 20480 x 2560 24.0 (83%);
+//   one row of 2048: 1.2 and 1.0 us.
 #include <algorithm>
 #include <type_traits>
 

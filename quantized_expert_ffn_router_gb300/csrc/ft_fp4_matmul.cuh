@@ -1,16 +1,37 @@
 // ft_fp4_matmul.cuh -- the product of two microscaled 4-bit matrices, X [T, K] and
 // W [N, K], on the block-scaled tensor cores.
 //
-// A tile is 128 rows of W (the M side, TMEM's lanes) by up to 256 tokens (the N
-// side, its columns): one token's product then costs no more than the weights'
-// bytes, and outputs are stored with 32 neighbouring n a warp, whatever the
-// alignment of out.  A step is 256 values of K: 128 bytes of codes a row, by TMA
-// in the 128-byte swizzle, and the scale tiles (512 bytes for 128 rows x 4
-// scales) as they lie in memory, copied from shared memory to TMEM beside the
-// accumulator in the same thread's order as the products that read them.
+// A tile is 128 rows of W (the M side, TMEM's lanes), or 256 over a pair of CTAs,
+// by up to 256 tokens (the N side, its columns): one token's product then costs no
+// more than the weights' bytes.  A step is 256 values of K: 128 bytes of codes a
+// row, by TMA in the 128-byte swizzle, and the scale tiles (512 bytes for 128 rows x
+// 4 scales) as they lie in memory, copied from shared memory to TMEM by the thread
+// that issues the products, in front of them.  Each stage of the ring has scale
+// columns of its own, so that a stage's release covers them.
 //
-// Few tiles: K is cut into slices over the CTAs of a cluster, whose partial sums
-// meet through distributed shared memory, added in the slices' order.
+// One warp issues the copies, one the products, eight drain the sums: where out is
+// written by boxes, all of a tile's at once into registers, so that the next tile's
+// products can begin; tiles of at most 128 tokens have two accumulators besides.  A CTA, or a pair, walks
+// tiles; where there are few, K is cut into slices over the CTAs of a cluster, whose
+// partial sums meet through distributed shared memory and are added in the slices'
+// order.
+//
+// What bounds it.  64 x 131072 x 2048 reads its weights at 5.1 TB/s (30.0 us, 28.9
+// issued one after another; floor 24.8).  8192 x 6144 x 4096 takes 72.5 us, 5.7
+// PFLOP/s, 8192^3 159.5 us, 6.9 (four times the bf16 library rate is 7.8): a step of a
+// 256 x 256 pair takes 0.30 us where the products alone take 0.27, the copies of
+// scales to TMEM 0.02 more and contention in shared memory the rest (operands are
+// read at 64 bytes a clock, filled at 75); each tile adds 1 us in which its sums
+// are drained; 768 tiles on 76 pairs are 10.1 waves.  Narrower tiles are bound by
+// issuing: a step takes 0.255 us at 64 tokens, of which its barrier 0.15.  Calls of
+// a few tokens: 3.0 us for one tile and one step, 5.6 for 1 x 2560 x 2048, most of
+// them launch, first loads and the way out.
+//
+// Tried and not kept: the next step's scales copied to TMEM ahead of this step's
+// products (8192 x 6144 x 4096: 87.5 us, then 75.1); scale copies between the
+// products that need them (no change); asking for the next step's barrier while a
+// step is issued (75.2, then 76.0); the first steps' copies before the CTA has met
+// (1 x 2560 x 2048: 5.5, then 5.5).
 #pragma once
 
 #include <algorithm>
