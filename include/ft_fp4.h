@@ -96,7 +96,8 @@ FT_API ft_status ft_fp4_values(const ft_fp4_matrix* m_host, void* out, int64_t s
  * ft_fp4_matmul -- out[t, n] = sum_k X[t, k] W[n, k] (+ add[t, n]) for X
  * [T, K] and W [N, K] of the same format, both in the order FT_FP4_TILES.  out
  * and add [T, N] (dtype bf16, f16 or f32; rows at stride elements, any
- * alignment of the type); add NULL: nothing is added; add may be out itself.
+ * alignment of the type); add NULL: nothing is added; add may be out itself, or
+ * one row for all tokens (stride 0).  Rows of out must not overlap.
  * Sums are fp32, of exact products of codes and block scales; each sum is
  * multiplied by the two row scales, add is added, and the result rounded once.
  * The result of a call depends on its sizes and values alone: sums over slices

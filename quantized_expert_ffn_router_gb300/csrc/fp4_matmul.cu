@@ -72,6 +72,7 @@ ft_status ft_fp4_matmul(const ft_fp4_matrix* x_host, const ft_fp4_matrix* w_host
   FT_REQUIRE(out != nullptr && reinterpret_cast<uintptr_t>(out) % size == 0, "%s: out is NULL or not aligned", what);
   FT_REQUIRE(reinterpret_cast<uintptr_t>(add) % size == 0, "%s: add is not aligned", what);
   FT_REQUIRE(out_stride >= 0 && add_stride >= 0, "%s: negative stride", what);
+  FT_REQUIRE(x_host->rows == 1 || out_stride >= w_host->rows, "%s: rows of out overlap", what);
   FT_REQUIRE(add != out || add_stride == out_stride, "%s: in place needs the same strides", what);
   if (encode_fn() == nullptr) return fail(FT_ERR_CUDA, "%s: cuTensorMapEncodeTiled unavailable", what);
   MmArgs a = {};
@@ -89,7 +90,9 @@ ft_status ft_fp4_matmul(const ft_fp4_matrix* x_host, const ft_fp4_matrix* w_host
   a.steps = static_cast<int32_t>((x_host->K + kStep - 1) / kStep);
   a.status = dev_status;
   const auto whole = [](const void* p, int64_t stride) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % 8 == 0; };
-  bool by_boxes = dtype != FT_DT_F32 && whole(out, out_stride) && (add == nullptr || whole(add, add_stride));
+  // (a tensor map has no rows that overlap, such as one row added to all tokens)
+  bool by_boxes = dtype != FT_DT_F32 && whole(out, out_stride) &&
+                  (add == nullptr || (whole(add, add_stride) && (a.T == 1 || add_stride >= a.N)));
   const auto even = [](const void* p, int64_t stride) { return reinterpret_cast<uintptr_t>(p) % 4 == 0 && stride % 2 == 0; };
   a.words = dtype != FT_DT_F32 && a.N % 2 == 0 && even(out, out_stride) && (add == nullptr || even(add, add_stride));
   const bool nv = x_host->fmt == FT_FP4_NVFP4;
@@ -111,7 +114,7 @@ ft_status ft_fp4_matmul(const ft_fp4_matrix* x_host, const ft_fp4_matrix* w_host
   double best = 0;
   const auto consider = [&](int c, int w, int slices) {
     const int64_t tiles = tiles_of(w, c), places = sms / (c * slices);
-    if (slices > 1 && (tiles > places || slices > a.steps)) return;
+    if (places < 1 || (slices > 1 && (tiles > places || slices > a.steps))) return;
     const int64_t waves = (tiles + places - 1) / places;
     const double tokens = w / 64.0, steps = (a.steps + slices - 1) / slices * kStepUs[c - 1][w > 64 ? w / 64 - 1 : 0];
     const double drain = 0.7 * tokens, wait = std::max(w > 128 ? 0.6 : 0.0, drain - steps);

@@ -135,7 +135,7 @@ def test_the_library_refuses(fp4):
     assert c.matmul(c.m(), c.m(fmt=1, scale=None)) == 1 and c.matmul(c.m(), c.m(K=128, pitch=64)) == 1
     assert c.matmul(c.m(order=1), c.m()) == 2 and c.matmul(c.m(), c.m(order=1)) == 2
     for bad in (dict(out=None), dict(out=(1 << 16) + 1), dict(stride=-8), dict(dtype=4), dict(add=(1 << 17) + 1),
-                dict(add=1 << 17, add_stride=-1), dict(add=1 << 16, add_stride=16)):
+                dict(add=1 << 17, add_stride=-1), dict(add=1 << 16, add_stride=16), dict(stride=3), dict(stride=0)):
         assert c.matmul(c.m(), c.m(), **bad) == 1, bad
     for rows in ((1 << 31) - 1, (1 << 31) - 1023):
         assert c.matmul(c.m(rows=rows), c.m()) == 2 and c.matmul(c.m(), c.m(rows=rows)) == 2

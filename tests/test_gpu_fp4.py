@@ -219,6 +219,16 @@ def test_onto_itself_and_repeated(fp4, T, N):
     assert all(torch.equal(o, other) for o in outs)
 
 
+@pytest.mark.parametrize("T,N,K", [(3, 256, 4096), (200, 256, 128), (200, 251, 128), (900, 1024, 64)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_one_row_added_to_all(fp4, T, N, K, dtype):
+    x, w = random_matrix("mxfp4", T, K, 1), random_matrix("mxfp4", N, K, 2)
+    row = (torch.arange(N, device=DEV) - 100).to(DT[dtype])
+    got = product(fp4, x, w, "mxfp4", dtype, add=row.expand(T, N), pad=-N % 8 + 8)
+    want = multiplied(x, w, "mxfp4") + f64(row)
+    assert (np.abs(got - want) <= HALF[dtype] * np.abs(want)).all()
+
+
 def test_views(fp4):
     """Codes in wider rows, row scales a step apart, x whose rows are one row, in- and outputs of one row of any stride."""
     T, N, K = 37, 150, 96
