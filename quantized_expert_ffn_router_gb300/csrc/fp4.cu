@@ -239,6 +239,7 @@ __global__ void __launch_bounds__(CH > 0 ? 512 : 1024, CH > 0 ? 2 : 1) quantize_
   const uint32_t step = gridDim.x * a.block_rows;
   const int last = a.chunks - 1;
   pdl_wait();
+  if (a.rows <= kFewRows) pdl_launch_dependents();
   constexpr int kHeld = CH > 0 ? CH : 1;
   Chunk<DT> next[kHeld];
   const int rounds = CH > 0 ? CH : (a.chunks + group - 1) / group;
@@ -363,6 +364,7 @@ __global__ void __launch_bounds__(256) values_kernel(const __grid_constant__ Row
   const int group = 1 << a.group_log2;
   const uint32_t row = blockIdx.x * (256 >> a.group_log2) + (threadIdx.x >> a.group_log2);
   pdl_wait();
+  if (a.rows <= kFewRows) pdl_launch_dependents();
   if (row >= a.rows) return;
   float s = 1.f;
   if (FMT == FT_FP4_NVFP4 && a.scale != nullptr) s = a.scale[static_cast<int64_t>(row) * a.scale_stride];

@@ -16,16 +16,15 @@
 // partial sums meet through distributed shared memory and are added in the slices'
 // order.
 //
-// What bounds it.  64 x 131072 x 2048 reads its weights at 5.1 TB/s (30.0 us, 28.9
-// issued one after another; floor 24.8).  8192 x 6144 x 4096 takes 72.5 us, 5.7
+// What bounds it.  64 x 131072 x 2048 reads its weights at 5.2 TB/s (29.0 us; floor
+// 24.8).  8192 x 6144 x 4096 takes 72.5 us, 5.7
 // PFLOP/s, 8192^3 159.5 us, 6.9 (four times the bf16 library rate is 7.8): a step of a
 // 256 x 256 pair takes 0.30 us where the products alone take 0.27, the copies of
 // scales to TMEM 0.02 more and contention in shared memory the rest (operands are
 // read at 64 bytes a clock, filled at 75); each tile adds 1 us in which its sums
 // are drained; 768 tiles on 76 pairs are 10.1 waves.  Narrower tiles are bound by
 // issuing: a step takes 0.255 us at 64 tokens, of which its barrier 0.15.  Calls of
-// a few tokens: 3.0 us for one tile and one step, 5.6 for 1 x 2560 x 2048, most of
-// them launch, first loads and the way out.
+// a few tokens, 4.5 us for 1 x 2560 x 2048, are launch, first loads and the way out.
 //
 // Tried and not kept: the next step's scales copied to TMEM ahead of this step's
 // products (8192 x 6144 x 4096: 87.5 us, then 75.1); scale copies between the
@@ -285,6 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
   pdl_wait();
+  if (a.T <= kFewRows) pdl_launch_dependents();
 
   if (warp == 0) {
     int st = 0;
