@@ -425,7 +425,6 @@ __global__ void __launch_bounds__(512, LAY == kAny ? 1 : 2) write_kernel(const _
       }
       // What the exact rotation of the elements in `unsure` (a bit each) gives.
       const auto rotate_again = [&](uint32_t unsure) {
-        const int64_t alone = AXES ? 0 : a.rope_pos[t0 + tk];
         while (unsure != 0) {
           const int i = __ffs(unsure) - 1;
           unsure &= unsure - 1;
@@ -434,7 +433,7 @@ __global__ void __launch_bounds__(512, LAY == kAny ? 1 : 2) write_kernel(const _
           const bool left = LAY == kPairs ? (c & 1) == 0 : c < a.half;
           const int f = LAY == kPairs ? c >> 1 : left ? c : c - a.half;
           const int o = LAY == kPairs ? c ^ 1 : left ? c + a.half : c - a.half;
-          const int64_t p = AXES ? position_of<AXES>(a, t0 + tk, f) : alone;
+          const int64_t p = position_of<AXES>(a, t0 + tk, f);  // (here: without a rotation there are no positions)
           float2 hi, lo;
           turn_pair(static_cast<int64_t>(static_cast<uint64_t>(p) * static_cast<uint64_t>(a.freqs[f])), a.mscale, &hi, &lo);
           const float u = load_one<F16>(src + c), v = load_one<F16>(src + o);

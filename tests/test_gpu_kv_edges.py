@@ -114,3 +114,23 @@ def test_infinities_in_nvfp4_blocks(att):
     want[0, 0, 32] = 768.0
     want[2, 0, :16] = 6.0
     assert torch.equal(ko.cpu(), want) and torch.equal(vo.cpu(), -want)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "nvfp4"])
+@pytest.mark.parametrize("D", [64, 160])
+def test_rows_at_borders_without_a_rotation(att, fmt, D):
+    """Rows whose codes are in doubt (on borders, infinite, NaN) where nothing is rotated: there are no positions to
+    look up again."""
+    T, page = 3000, 64
+    x = torch.randint(-28, 29, (T, 1, D), generator=torch.Generator().manual_seed(D)).float() / 4
+    x[::7, 0, 3], x[1::7, 0, D - 1], x[2::7, 0, 17] = math.inf, -math.inf, math.nan
+    x = x.bfloat16().to(DEV)
+    n = -(-T // page)
+    cache = att.KvCache(att.FT_KV_E4M3 if fmt == "e4m3" else att.FT_KV_NVFP4, 1, D, page, n)
+    table = torch.arange(n, dtype=torch.int32, device=DEV)[None]
+    pos, seq = torch.arange(T, dtype=torch.int32, device=DEV), torch.zeros(T, dtype=torch.int32, device=DEV)
+    att.kv_append(cache, x, -x, table, pos, seq=seq)
+    ko, vo = torch.zeros(T, 1, D, device=DEV), torch.zeros(T, 1, D, device=DEV)
+    att.kv_gather(cache, table, pos, ko, vo, seq=seq)
+    want = quantised(fmt, f64(x))
+    assert np.array_equal(f64(ko), want, equal_nan=True) and np.array_equal(f64(vo), -want, equal_nan=True)
