@@ -88,7 +88,8 @@ FT_API ft_status ft_fp4_quantize(const void* x, int64_t stride, int32_t dtype, c
 /*
  * ft_fp4_values -- out [rows, K] (dtype bf16, f16 or f32, row r at r * stride
  * elements) = the matrix's values: fl(code * b * s) in fp32, rounded to the
- * output's type.  Strides and alignment as ft_fp4_quantize.
+ * output's type.  Strides and alignment as ft_fp4_quantize; rows of out must not
+ * overlap.
  */
 FT_API ft_status ft_fp4_values(const ft_fp4_matrix* m_host, void* out, int64_t stride, int32_t dtype, void* stream);
 

@@ -555,6 +555,7 @@ ft_status ft_fp4_values(const ft_fp4_matrix* m_host, void* out, int64_t stride, 
   RowArgs a;
   ft_status st;
   if ((st = row_args("fp4_values", "out", out, stride, dtype, m_host, &a)) != FT_OK) return st;
+  FT_REQUIRE(m_host->rows <= 1 || stride >= m_host->K, "fp4_values: rows of out overlap");
   if (m_host->rows == 0) return FT_OK;
   return m_host->fmt == FT_FP4_NVFP4 ? launch_values<FT_FP4_NVFP4>(a, dtype, as_stream(stream))
                                      : launch_values<FT_FP4_MXFP4>(a, dtype, as_stream(stream));

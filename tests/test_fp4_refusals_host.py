@@ -1,0 +1,24 @@
+"""Calls of the 4-bit matrices and of rotations by several axes that are taken or
+refused at the edge of what the headers say, without a GPU: a call that is taken
+comes as far as the launch, which fails here."""
+
+import ctypes
+
+import pytest
+import torch
+
+from test_fp4_host import C, att, fp4, refused  # noqa: F401
+
+pytestmark = pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are nobody's")
+INVALID = 1
+
+
+def test_rows_of_values_that_overlap_are_refused(fp4):  # noqa: F811
+    c = C(fp4)
+    values = lambda m, stride, dtype=0: c.lib.ft_fp4_values(ctypes.byref(m), 1 << 16, stride, dtype, None)
+    for stride in (0, 8, 56):
+        assert values(c.m(), stride) == INVALID and "overlap" in c.lib.ft_last_error().decode()
+        assert values(c.m(rows=1), stride) != INVALID  # one row may carry any stride
+        assert c.quantize(c.m(), stride=stride) != INVALID  # rows that are read may be one row
+    assert values(c.m(), 60, 2) == INVALID
+    assert values(c.m(), 64) != INVALID and values(c.m(), 72) != INVALID
