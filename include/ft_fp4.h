@@ -100,7 +100,8 @@ FT_API ft_status ft_fp4_values(const ft_fp4_matrix* m_host, void* out, int64_t s
  * alignment of the type); add NULL: nothing is added; add may be out itself, or
  * one row for all tokens (stride 0).  Rows of out must not overlap.
  * Sums are fp32, of exact products of codes and block scales; each sum is
- * multiplied by the two row scales, add is added, and the result rounded once.
+ * multiplied by the two row scales, with no infinity or lost bits between the two
+ * where the result has none, add is added, and the result rounded once.
  * The result of a call depends on its sizes and values alone: sums over slices
  * of K are joined in one order.
  * dev_status records FT_ERR_TIMEOUT where a bounded wait gave up.

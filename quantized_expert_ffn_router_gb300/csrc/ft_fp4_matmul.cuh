@@ -93,12 +93,43 @@ __device__ __forceinline__ void tmem_ld32x32(uint32_t from, uint32_t (&v)[32]) {
   tmem_ld16x32(from + (16u << 16), v + 16);
 }
 
-// The 8 values of 16 tokens (from 8 k) x 16 rows (from 16 half), scaled.
-__device__ __forceinline__ void scaled(const uint32_t (&v)[32], const float (&sw)[4], const float (&s)[4], int k, int half,
+// A weight row's scale as near * by.  Sums are 0 or 2^-20 to 2^54 in size; their
+// products with near, 0 or 2^-100 to 2^71, are neither infinite nor below the normal
+// numbers, and neither is that with the token's scale unless the whole is, since by
+// is a power of two that leads further the same way (1 unless the scale is outside
+// near's range): ((sum * near) * token's) * by rounds as sum * scale * token's does.
+struct RowScale {
+  float near, by;
+};
+__device__ __forceinline__ RowScale split_scale(float s) {
+  const float m = fabsf(s);
+  RowScale r = {s, 1.f};
+  if ((m < 0x1p-100f && m > 0.f) || (m >= 0x1p71f && m <= 0x1.fffffep127f)) {
+    const float t = m < 1.f ? s * 0x1p49f : s;  // a normal number
+    const int e = static_cast<int>(__float_as_uint(t) >> 23 & 255) - 127, to = m < 1.f ? -100 : 70;
+    r.near = __uint_as_float(__float_as_uint(t) + (static_cast<uint32_t>(to - e) << 23));
+    r.by = pow2f(e - (m < 1.f ? 49 : 0) - to);
+  }
+  return r;
+}
+
+// The 8 values of 16 tokens (from 8 k) x 16 rows (from 16 half), scaled: two
+// tokens of a row at a time.
+template <int FMT>
+__device__ __forceinline__ void scaled(const uint32_t (&v)[32], const RowScale (&sw)[4], const float (&s)[4], int k, int half,
                                        float (&y)[8]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    y[i] = __uint_as_float(v[16 * half + 4 * k + i]) * sw[2 * half + (i >> 1 & 1)] * s[2 * (i >> 2) + (i & 1)];
+  for (int i = 0; i < 8; i += 2) {
+    const int at = 16 * half + 4 * k + i;
+    float2 p = make_float2(__uint_as_float(v[at]), __uint_as_float(v[at + 1]));
+    if (FMT == FT_FP4_NVFP4) {  // MXFP4 has no scales beside its blocks'
+      const RowScale& w = sw[2 * half + (i >> 1 & 1)];
+      uint64_t q = mul2(mul2(pair(p.x, p.y), pair(w.near, w.near)), pair(s[2 * (i >> 2)], s[2 * (i >> 2) + 1]));
+      p = unpair(mul2(q, pair(w.by, w.by)));
+    }
+    y[i] = p.x;
+    y[i + 1] = p.y;
+  }
 }
 __device__ __forceinline__ void scales_of(float sx_of_lane, const Fragment& f, int k, float (&s)[4]) {
 #pragma unroll
@@ -112,8 +143,8 @@ __device__ __forceinline__ uint32_t box_at(uint32_t box, int token, int chunk) {
 }
 
 // A chunk scaled, rounded and put into a box, which holds what is added to it before.
-template <int DT>
-__device__ __forceinline__ void chunk_to_box(const uint32_t (&v)[32], const float (&sw)[4], float sx_of_lane,
+template <int FMT, int DT>
+__device__ __forceinline__ void chunk_to_box(const uint32_t (&v)[32], const RowScale (&sw)[4], float sx_of_lane,
                                              const Fragment& f, uint32_t box, bool added) {
 #pragma unroll
   for (int k = 0; k < 4; k += 2) {
@@ -122,7 +153,7 @@ __device__ __forceinline__ void chunk_to_box(const uint32_t (&v)[32], const floa
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       float y[8];
-      scaled(v, sw, s, k, half, y);
+      scaled<FMT>(v, sw, s, k, half, y);
       const uint32_t at = box_at(box, k * 8 + f.box_token, 2 * half + f.box_chunk);
       uint32_t r[4];
       if (added) {
@@ -186,13 +217,13 @@ __device__ __forceinline__ void added_to_box(const MmArgs& a, const uint32_t (&x
 // of two tokens', two rows a lane.  fp32: as the sums lie, 8 rows of 4 tokens a
 // store.  WHOLE: nothing of it is past the last row or token, so that stores need
 // no branches.
-template <int DT, bool WHOLE>
-__device__ __forceinline__ void chunk_to_rows(const MmArgs& a, const uint32_t (&v)[32], const float (&sw)[4], float sx_of_lane,
+template <int FMT, int DT, bool WHOLE>
+__device__ __forceinline__ void chunk_to_rows(const MmArgs& a, const uint32_t (&v)[32], const RowScale (&sw)[4], float sx_of_lane,
                                               const Fragment& f, int t, int n, const Added<DT>& add, uint32_t box) {
   const int lane = threadIdx.x & 31;
   if constexpr (DT != FT_DT_F32) {
     if (a.add != nullptr) added_to_box(a, add.x, box);
-    chunk_to_box<DT>(v, sw, sx_of_lane, f, box, a.add != nullptr);
+    chunk_to_box<FMT, DT>(v, sw, sx_of_lane, f, box, a.add != nullptr);
   } else {
 #pragma unroll
     for (int k = 0; k < 4; k += 2) {
@@ -201,7 +232,7 @@ __device__ __forceinline__ void chunk_to_rows(const MmArgs& a, const uint32_t (&
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         float y[8];
-        scaled(v, sw, s, k, half, y);
+        scaled<FMT>(v, sw, s, k, half, y);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int i = 16 * half + 4 * k + j;
@@ -407,18 +438,21 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
         }
         __syncwarp();
       }
-      float sw[4], sx[kChunks];
+      float w_scale[4], sx[kChunks];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int n = n0 + f.row + 8 * i;
-        sw[i] = a.sw != nullptr && n < a.N ? a.sw[n * a.sw_stride] : 1.f;
+        w_scale[i] = FMT == FT_FP4_NVFP4 && a.sw != nullptr && n < a.N ? a.sw[n * a.sw_stride] : 1.f;
       }
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
         const int t = (2 * c + h) * 32 + lane;
-        sx[c] = a.sx != nullptr && t < p.tokens ? a.sx[(p.t0 + t) * a.sx_stride] : 1.f;
+        sx[c] = FMT == FT_FP4_NVFP4 && a.sx != nullptr && t < p.tokens ? a.sx[(p.t0 + t) * a.sx_stride] : 1.f;
       }
       if constexpr (BOXES) {
+        RowScale sw[4];  // behind all loads, in front of the wait for the products
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sw[i] = split_scale(w_scale[i]);
         ok = mbar_wait_warp(&acc_full[buf], (it / a.buffers) & 1, a.status);
         if (!ok) break;
         tc_fence_after();
@@ -441,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
             if (lane == 0) bulk_wait_read<1>();
             __syncwarp();
           }
-          chunk_to_box<DT>(v[c], sw, sx[c], f, box0 + b * kBoxBytes, a.add != nullptr);
+          chunk_to_box<FMT, DT>(v[c], sw, sx[c], f, box0 + b * kBoxBytes, a.add != nullptr);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0 && n0 < a.N) {
@@ -454,6 +488,9 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
         Added<DT> add[2];
         const int t0 = p.t0 + h * 32;
         if (a.add != nullptr && mine > 0 && a.split == 1) load_added(a, t0, n0, f, add[0]);
+        RowScale sw[4];  // behind all loads, in front of the wait for the products
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sw[i] = split_scale(w_scale[i]);
         ok = mbar_wait_warp(&acc_full[buf], (it / a.buffers) & 1, a.status);
         if (!ok) break;
         tc_fence_after();
@@ -471,9 +508,9 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
             for (int i = 0; i < 32; ++i)
               part[((2 * c + h) * 32 + f.token(i)) * kPartPitch + q * 32 + f.row_of(i)] = __uint_as_float(v[i]);
           } else if (n0 + 32 <= a.N && t0 + c * 64 + 32 <= a.T) {
-            chunk_to_rows<DT, true>(a, v, sw, sx[c], f, t0 + c * 64, n0, add[c & 1], box0);
+            chunk_to_rows<FMT, DT, true>(a, v, sw, sx[c], f, t0 + c * 64, n0, add[c & 1], box0);
           } else {
-            chunk_to_rows<DT, false>(a, v, sw, sx[c], f, t0 + c * 64, n0, add[c & 1], box0);
+            chunk_to_rows<FMT, DT, false>(a, v, sw, sx[c], f, t0 + c * 64, n0, add[c & 1], box0);
           }
         }
         if (mine <= 0) release();
@@ -486,13 +523,13 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
   }
   if (CG == 1 && a.split > 1) {
     // the slices' partial sums: CTA `slice` joins its share of the elements
-    __syncwarp();
-    cluster_sync();
     const Place p = place_of(a, first);
     const int n = p.w * kM + lane * 4;
-    float sw[4];
+    __syncwarp();
+    cluster_sync();
+    float w_scale[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sw[i] = a.sw != nullptr && n + i < a.N ? a.sw[(n + i) * a.sw_stride] : 1.f;
+    for (int i = 0; i < 4; ++i) w_scale[i] = a.sw != nullptr && n + i < a.N ? a.sw[(n + i) * a.sw_stride] : 1.f;
     uint32_t part[8];
 #pragma unroll
     for (int r = 0; r < 8; ++r) part[r] = map_cluster(smem_u32(smem) + lane * 16, min(r, a.split - 1));
@@ -512,7 +549,9 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
       for (int i = 0; i < 4; ++i) more[i] = a.add != nullptr ? load_out<DT>(a.add, from + min(n + i, a.N - 1)) : 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        y[i] = y[i] * sw[i] * sx;
+        asm volatile("" : "+f"(w_scale[i]));  // not to be split, and waited for, in front of the partial sums' loads
+        const RowScale w = split_scale(w_scale[i]);
+        y[i] = y[i] * w.near * sx * w.by;
         if (a.add != nullptr) y[i] += more[i];
         if (n + i < a.N) store_out<DT>(a.out, to + i, y[i]);
       }
