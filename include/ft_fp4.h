@@ -104,7 +104,8 @@ FT_API ft_status ft_fp4_values(const ft_fp4_matrix* m_host, void* out, int64_t s
  * where the result has none, add is added, and the result rounded once.
  * The result of a call depends on its sizes and values alone: sums over slices
  * of K are joined in one order.
- * dev_status records FT_ERR_TIMEOUT where a bounded wait gave up.
+ * dev_status records FT_ERR_TIMEOUT where a bounded wait gave up; a call that
+ * finds it there writes nothing.
  * Limits: T and N at most 2^31 - 1024, and fewer than 2^31 tiles (of 128 or 256
  * rows of W by 16 to 256 of X).
  */

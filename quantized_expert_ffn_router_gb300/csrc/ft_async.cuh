@@ -50,16 +50,25 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// What the status word holds now (0 without one).
+__device__ __forceinline__ int32_t status_now(const int32_t* status) {
+  return status != nullptr ? *reinterpret_cast<const volatile int32_t*>(status) : 0;
+}
+
 // Wait for the phase with the given parity; false (and FT_ERR_TIMEOUT
-// recorded) if it has not completed within kWaitLimitNs.
+// recorded) if it has not completed within kWaitLimitNs, or as soon as another
+// wait is seen to have given up.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int32_t* status) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
   for (uint32_t i = 1;; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 255u) == 0 && global_timer_ns() - t0 > kWaitLimitNs) {
-      record_status(status, FT_ERR_TIMEOUT);
-      return false;
+    if ((i & 255u) == 0) {
+      if (status_now(status) == FT_ERR_TIMEOUT) return false;
+      if (global_timer_ns() - t0 > kWaitLimitNs) {
+        record_status(status, FT_ERR_TIMEOUT);
+        return false;
+      }
     }
   }
 }

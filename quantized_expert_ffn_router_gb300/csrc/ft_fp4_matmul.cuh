@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
   uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
   __shared__ uint32_t s_tmem;
-  __shared__ int s_bad;
+  __shared__ int s_bad, s_skip;
   __shared__ __align__(8) uint64_t add_full[kEpilogueWarps];
   uint32_t add_phase = 0;
   constexpr int kTiles = step_tiles<FMT>();
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
       mbar_init(&acc_empty[i], kEpilogueWarps * CG);
     }
     for (int i = 0; i < kEpilogueWarps; ++i) mbar_init(&add_full[i], 1);
-    s_bad = 0;
+    s_bad = s_skip = 0;
     fence_barrier_init();
   }
   if (warp == 1) tmem_alloc<CG>(&s_tmem, 512);
@@ -316,7 +316,6 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
   const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
   pdl_wait();
   if (a.T <= kFewRows) pdl_launch_dependents();
-
   if (warp == 0) {
     int st = 0;
     uint32_t ph = 1;
@@ -438,6 +437,8 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
         }
         __syncwarp();
       }
+      // Where a wait of an earlier call gave up, nothing is written (read with the scales, looked at behind the products).
+      const int32_t before = status_now(a.status);
       float w_scale[4], sx[kChunks];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -462,6 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
           if (c < mine) tmem_ld32x32(from + c * 64, v[c]);
         tmem_wait();
         release();
+        const int kept = __any_sync(0xffffffffu, before == FT_ERR_TIMEOUT) ? 0 : mine;
         if (a.add != nullptr && mine > 0 && n0 < a.N) {
           ok = mbar_wait_warp(&add_full[e], add_phase, a.status);
           if (!ok) break;
@@ -469,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
         }
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
-          if (c >= mine) break;
+          if (c >= kept) break;
           const int b = c & (a.boxes - 1);
           if (c >= a.boxes) {  // (no add: it has a box for each chunk)
             if (lane == 0) bulk_wait_read<1>();
@@ -494,14 +496,15 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
         ok = mbar_wait_warp(&acc_full[buf], (it / a.buffers) & 1, a.status);
         if (!ok) break;
         tc_fence_after();
+        const int kept = __any_sync(0xffffffffu, before == FT_ERR_TIMEOUT) ? 0 : mine;
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
-          if (c >= mine) break;
+          if (c >= kept) break;
           uint32_t v[32];
           tmem_ld32x32(from + c * 64, v);
           if (a.add != nullptr && c + 1 < mine && a.split == 1) load_added(a, t0 + (c + 1) * 64, n0, f, add[(c + 1) & 1]);
           tmem_wait();
-          if (c + 1 == mine) release();
+          if (c + 1 == kept) release();
           if (CG == 1 && a.split > 1) {
             float* const part = reinterpret_cast<float*>(smem);  // [token][kPartPitch]
 #pragma unroll
@@ -513,7 +516,8 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
             chunk_to_rows<FMT, DT, false>(a, v, sw, sx[c], f, t0 + c * 64, n0, add[c & 1], box0);
           }
         }
-        if (mine <= 0) release();
+        if (kept <= 0) release();
+        if (kept < mine && lane == 0) s_skip = 1;
       }
     }
     if (lane == 0) {
@@ -533,9 +537,10 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
     uint32_t part[8];
 #pragma unroll
     for (int r = 0; r < 8; ++r) part[r] = map_cluster(smem_u32(smem) + lane * 16, min(r, a.split - 1));
+    const int tokens = s_skip != 0 ? 0 : p.tokens;
     // a token a warp: its 128 rows, four a lane
 #pragma unroll 2
-    for (int t = slice + a.split * warp; t < p.tokens; t += a.split * (kThreads / 32)) {
+    for (int t = slice + a.split * warp; t < tokens; t += a.split * (kThreads / 32)) {
       const float sx = a.sx != nullptr ? a.sx[(p.t0 + t) * a.sx_stride] : 1.f;
       float4 x[8];
 #pragma unroll

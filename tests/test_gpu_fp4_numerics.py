@@ -90,3 +90,23 @@ def test_nan_stays_in_its_row_and_column(fp4, fmt, dtype, T, N, K):  # noqa: F81
     nan[rows], nan[:, cols] = True, True
     assert (np.isnan(got) == nan).all()
     assert rounded_once(got[~nan], want[~nan], dtype)
+
+
+@pytest.mark.parametrize("T,N,K", PATHS + [(600, 2048, 8192), (2500, 4000, 528)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("added", [False, True])
+def test_nothing_is_written_where_a_wait_gave_up_before(cuda_lib, fp4, dtype, added, T, N, K):  # noqa: F811
+    """The status word that a call finds: of a wait that gave up, or another error, or none."""
+    x, w = random_matrix("nvfp4", T, K, 1), random_matrix("nvfp4", N, K, 2)
+    place = beside(N)
+    wide = torch.full((T, place["offset"] + N + place["pad"]), 7.0, dtype=DT[dtype], device=DEV)
+    out = wide[:, place["offset"]:place["offset"] + N]
+    add = torch.full_like(wide, 8.0)[:, place["offset"]:place["offset"] + N] if added else None
+    status = torch.full((1,), cuda_lib.FT_ERR_TIMEOUT, dtype=torch.int32, device=DEV)
+    fp4.fp4_matmul(x, w, out, add=add, dev_status=status)
+    assert (wide == 7.0).all() and int(status.item()) == cuda_lib.FT_ERR_TIMEOUT
+    want = multiplied(x, w, "nvfp4") + (8.0 if added else 0.0)
+    for found in (cuda_lib.FT_ERR_BAD_ID, 0):
+        out.fill_(7.0), status.fill_(found)
+        fp4.fp4_matmul(x, w, out, add=add, dev_status=status)
+        assert rounded_once(f64(out), want, dtype) and int(status.item()) == found
