@@ -149,7 +149,7 @@ FT_API ft_status ft_rope(const ft_rows* x_host, int32_t T, int32_t heads, int32_
 /*
  * Several axes: a token has a position on each, and channel pair i turns by that
  * on axis[i].  Axis a's positions are pos[a * pos_stride + t], t < T (pos_stride
- * at least T).  axis: a device array of rot_dim / 2 bytes; one past n_axes - 1
+ * at least T, or 0: the same on every axis).  axis: a device array of rot_dim / 2 bytes; one past n_axes - 1
  * counts as n_axes - 1.
  */
 enum { FT_ROPE_MAX_AXES = 8 };

@@ -764,8 +764,8 @@ ft_status rope_positions(const char* what, const ft_rope_axes* x, const int32_t*
   if (x == nullptr) return FT_OK;
   FT_REQUIRE(x->axis != nullptr, "%s: axes without their channel pairs' axis", what);
   FT_REQUIRE(x->n_axes >= 1 && x->n_axes <= FT_ROPE_MAX_AXES, "%s: n_axes %d must be 1..%d", what, x->n_axes, FT_ROPE_MAX_AXES);
-  FT_REQUIRE(x->pos_stride >= T, "%s: an axis's positions are %lld after the last one's, for %d tokens", what,
-             static_cast<long long>(x->pos_stride), T);
+  FT_REQUIRE(x->pos_stride >= T || x->pos_stride == 0, "%s: an axis's positions are %lld after the last one's, for %d tokens",
+             what, static_cast<long long>(x->pos_stride), T);
   a->axis = x->axis;
   a->last_axis = x->n_axes - 1;
   a->pos_stride = x->pos_stride;

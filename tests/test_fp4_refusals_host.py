@@ -22,3 +22,13 @@ def test_rows_of_values_that_overlap_are_refused(fp4):  # noqa: F811
         assert c.quantize(c.m(), stride=stride) != INVALID  # rows that are read may be one row
     assert values(c.m(), 60, 2) == INVALID
     assert values(c.m(), 64) != INVALID and values(c.m(), 72) != INVALID
+
+
+def test_positions_may_be_the_same_on_every_axis(att):  # noqa: F811
+    T, D = 3, 32
+    rows, table = att._ROWS.pack(1 << 16, 64, 32), att.FtRopeTable(1 << 17, D, 0, 1.0)
+    lib = att._bind()
+    call = lambda stride, T=T: lib.ft_rope_by_axes(rows, T, 2, D, 0, 1 << 18, ctypes.addressof(table),
+                                                   att._AXES.pack(1 << 19, 2, 0, stride), rows, None)
+    assert call(0) != INVALID and call(T) != INVALID
+    assert call(T - 1) == call(1) == call(-T) == call(-1) == INVALID

@@ -124,3 +124,27 @@ def test_no_tokens(att):
     spin = att.Rope(64, sections=(16, 16))
     z = torch.zeros(0, 4, 64, dtype=torch.bfloat16, device=DEV)
     att.rope(z, torch.zeros(2, 0, dtype=torch.int32, device=DEV), spin, z)
+
+
+@pytest.mark.parametrize("T", [1, 33])
+@pytest.mark.parametrize("weave", [False, True])
+def test_the_same_position_on_every_axis(att, T, weave):
+    """Text: one row of positions expanded to all axes turns as one axis does, alone and into a cache."""
+    Hkv, D, page = 2, 64, 16
+    kw = dict(base=1e4)
+    spin, one = att.Rope(D, sections=(12, 10, 10), weave=weave, **kw), att.Rope(D, **kw)
+    pos = i32(positions(1, T, T)[0])
+    x = rows(T, 5, D, "bf16", 1)
+    a, b = torch.zeros_like(x), torch.ones_like(x)
+    att.rope(x, pos.expand(3, T), spin, a)
+    att.rope(x, pos, one, b)
+    assert torch.equal(a, b)
+    pages = -(-T // page)
+    table, at, seq = i32(np.arange(pages))[None], i32(np.arange(T)), i32(np.zeros(T))
+    k, v = rows(T, Hkv, D, "bf16", 2), rows(T, Hkv, D, "bf16", 3)
+    caches = [att.KvCache(att.FT_KV_NVFP4, Hkv, D, page, pages) for _ in range(2)]
+    att.kv_append(caches[0], k, v, table, at, seq=seq, rope=spin, rope_pos=pos.expand(3, T), q=x, q_out=a)
+    att.kv_append(caches[1], k, v, table, at, seq=seq, rope=one, rope_pos=pos, q=x, q_out=b)
+    assert torch.equal(a, b)
+    for n in ("k", "v", "k_scale", "v_scale", "k_block", "v_block"):
+        assert torch.equal(getattr(caches[0], n), getattr(caches[1], n))
