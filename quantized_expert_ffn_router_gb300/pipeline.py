@@ -159,6 +159,8 @@ class DecodeAttention:
         of the rotation where those are others (of several axes: [axes, T])."""
         from . import attention as att
 
+        if rope_pos is not None and self.rope is None:
+            att._bad("DecodeAttention: rope_pos without a rotation (rope)")
         T, Hq, Hkv, D = self.T, self.Hq, self.cache.Hkv, self.cache.D
         heads = qkv.view(T, Hq + 2 * Hkv, D)
         q, k, v = heads[:, :Hq], heads[:, Hq:Hq + Hkv], heads[:, Hq + Hkv:]

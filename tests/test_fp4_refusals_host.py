@@ -32,3 +32,16 @@ def test_positions_may_be_the_same_on_every_axis(att):  # noqa: F811
                                                    att._AXES.pack(1 << 19, 2, 0, stride), rows, None)
     assert call(0) != INVALID and call(T) != INVALID
     assert call(T - 1) == call(1) == call(-T) == call(-1) == INVALID
+
+
+def test_positions_of_a_rotation_that_is_not_there_are_refused(att):  # noqa: F811
+    from quantized_expert_ffn_router_gb300 import pipeline
+
+    T, Hq, D = 2, 4, 32
+    cache = att.KvCache(att.FT_KV_BF16, 2, D, 16, 4, device="cpu")
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    qkv = torch.zeros(T, (Hq + 4) * D, dtype=torch.bfloat16)
+    plain = pipeline.DecodeAttention(cache, Hq, T, device="cpu")
+    message = refused(plain, qkv, i(T, 1), i(T), rope_pos=i(T))
+    assert "rope" in message and "GPU" not in message
+    assert "GPU" in refused(plain, qkv, i(T, 1), i(T))  # without them it is a call of tensors that are on none
