@@ -73,7 +73,7 @@ ft_status ft_fp4_matmul(const ft_fp4_matrix* x_host, const ft_fp4_matrix* w_host
   FT_REQUIRE(reinterpret_cast<uintptr_t>(add) % size == 0, "%s: add is not aligned", what);
   FT_REQUIRE(out_stride >= 0 && add_stride >= 0, "%s: negative stride", what);
   FT_REQUIRE(x_host->rows == 1 || out_stride >= w_host->rows, "%s: rows of out overlap", what);
-  FT_REQUIRE(add != out || add_stride == out_stride, "%s: in place needs the same strides", what);
+  FT_REQUIRE(add != out || add_stride == out_stride || x_host->rows == 1, "%s: in place needs the same strides", what);
   if (encode_fn() == nullptr) return fail(FT_ERR_CUDA, "%s: cuTensorMapEncodeTiled unavailable", what);
   MmArgs a = {};
   a.out = out;

@@ -45,3 +45,9 @@ def test_positions_of_a_rotation_that_is_not_there_are_refused(att):  # noqa: F8
     message = refused(plain, qkv, i(T, 1), i(T), rope_pos=i(T))
     assert "rope" in message and "GPU" not in message
     assert "GPU" in refused(plain, qkv, i(T, 1), i(T))  # without them it is a call of tensors that are on none
+
+
+def test_one_row_in_place_may_carry_any_strides(fp4):  # noqa: F811
+    c = C(fp4)
+    assert c.matmul(c.m(rows=1), c.m(), stride=8, add=1 << 16, add_stride=16) != INVALID
+    assert c.matmul(c.m(rows=2), c.m(), stride=8, add=1 << 16, add_stride=16) == INVALID
