@@ -1,5 +1,5 @@
-// fp4_matmul.cu -- ft_fp4_matmul's entry point: checks, tensor maps, and the
-// choice of tiles.  The kernels: ft_fp4_matmul.cuh.
+// fp4_matmul.cu -- ft_fp4_matmul's entry point: checks and tensor maps.  The choice
+// of tiles: ft_fp4_tiles.h; the kernels: ft_fp4_matmul.cuh.
 #include <algorithm>
 
 #include "ft_fp4_args.cuh"
@@ -97,41 +97,11 @@ ft_status ft_fp4_matmul(const ft_fp4_matrix* x_host, const ft_fp4_matrix* w_host
   a.words = dtype != FT_DT_F32 && a.N % 2 == 0 && even(out, out_stride) && (add == nullptr || even(add, add_stride));
   const bool nv = x_host->fmt == FT_FP4_NVFP4;
   const int sms = device_sm_count(), step = nv ? step_tiles<FT_FP4_NVFP4>() : step_tiles<FT_FP4_MXFP4>();
-  const auto tiles_of = [&](int width, int cg) {
-    return (static_cast<int64_t>(a.N - 1) / (kM * cg) + 1) * ((static_cast<int64_t>(a.T) - 1) / width + 1);
-  };
-  // Tiles, and slices of K, by what they take together (us, measured; what all of
-  // them take, 3.5 and the bytes from HBM, left out).  A step: issuing its copies
-  // and products, or the products themselves where they are wide.  After the last
-  // step the tile's sums are drained and written, 0.7 for 64 tokens, under the
-  // next tile's steps where there are two accumulators.  A pair of CTAs meets
-  // first; slices meet before and after their sums are joined.  E.g. 2048 x 4096 x
-  // 4096: pairs of 256 tokens 18.6, alone 20.7, of 128 24.3; 777 x 2560 x 2560:
-  // alone of 128 7.7, of 64 10.2, pairs 8.9; 300 x 300 x 8192: 8 slices of 64 7.5,
-  // whole 13.2; 64 x 2560 x 2048: whole 6.5, 4 slices 7.1.
-  static const double kStepUs[2][4] = {{0.255, 0.285, 0.32, 0.365}, {0.255, 0.28, 0.29, 0.303}};
-  int cg = 1;
-  double best = 0;
-  const auto consider = [&](int c, int w, int slices) {
-    const int64_t tiles = tiles_of(w, c), places = sms / (c * slices);
-    if (places < 1 || (slices > 1 && (tiles > places || slices > a.steps))) return;
-    const int64_t waves = (tiles + places - 1) / places;
-    const double tokens = w / 64.0, steps = (a.steps + slices - 1) / slices * kStepUs[c - 1][w > 64 ? w / 64 - 1 : 0];
-    const double drain = 0.7 * tokens, wait = std::max(w > 128 ? 0.6 : 0.0, drain - steps);
-    const double cost = (c == 2 ? 1.1 : 0) + waves * steps + drain + (waves - 1) * wait + (slices > 1 ? 1.1 + 1.1 * tokens : 0);
-    if (best == 0 || cost < best) best = cost, cg = c, a.width = w, a.split = slices;
-  };
-  for (int slices = 1; slices <= 8; slices *= 2) {
-    if (a.T <= 64) {
-      consider(1, (a.T + 15) / 16 * 16, slices);
-      continue;
-    }
-    for (int w = 64; w <= kMaxWidth; w += 64) {
-      consider(1, w, slices);
-      if (slices == 1) consider(2, w, 1);
-    }
-  }
-  const int64_t tiles = tiles_of(a.width, cg);
+  const Tiles t = choose_tiles(a.T, a.N, a.steps, sms);
+  const int cg = t.pair;
+  a.width = t.width;
+  a.split = t.slices;
+  const int64_t tiles = tiles_of(a.T, a.N, a.width, cg);
   FT_REQUIRE(tiles < (1ll << 31), "%s: too many tiles", what);
   a.tiles = static_cast<int32_t>(tiles);
   by_boxes = by_boxes && a.split == 1;  // the slices' sums are joined and written otherwise

@@ -5,15 +5,13 @@
 #include <cuda.h>
 
 #include "ft_fp4.cuh"
+#include "ft_fp4_tiles.h"
 
 namespace ft {
 
-constexpr int kM = 128;          // weight rows of a tile
-constexpr int kStep = 256;       // values of K in a step: four products of 64
 constexpr int kEpilogueWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpilogueWarps;  // TMA, MMA, epilogue
 constexpr int kMaxStages = 8;
-constexpr int kMaxWidth = 256;
 constexpr int kScaleColumn = 256;  // of TMEM: accumulators before it, each stage's scales from it
 constexpr int kChunks = kMaxWidth / 32 / 2;  // of 32 columns that a warp of the epilogue takes, at most
 constexpr int kBoxBytes = 32 * 64;  // 32 tokens x 32 rows of 16-bit outputs
