@@ -123,6 +123,19 @@ __device__ __forceinline__ void tmem_ld16x32(uint32_t from, uint32_t* r) {
       : "memory");
 }
 #undef FT_R8
+// 8 columns of 16 lanes, likewise.
+__device__ __forceinline__ void tmem_ld16x8(uint32_t from, uint32_t (&r)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(from)
+               : "memory");
+}
+// The same the other way, in flight until tmem_wait_stores.
+__device__ __forceinline__ void tmem_st16x8(uint32_t to, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x1.b32 [%4], {%0, %1, %2, %3};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(to)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait_stores() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // ---------------------------------------------------------------- products ---
