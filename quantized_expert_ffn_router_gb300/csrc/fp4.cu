@@ -11,7 +11,8 @@
 //   8192 x 4096 bf16 to NVFP4 with row scales 17.6 us (72%: instructions, of which
 //     65% of the issue slots are used, and the row's maximum between loads and
 //     codes), f32 25.2 (90%), to MXFP4 15.2 (82%); 20480 x 2560 by a given scale
-//     25.0 (79%);
+//     25.0 (79%); rows of more than 16384 values, read twice: 4096 x 20480 f32 116.8
+//     (48%, each value counted once);
 //   read back as bf16: 8192 x 4096 15.4 us (82%), 20480 x 2560 24.0 (83%);
 //   one row of 2048: 1.2 and 1.0 us.
 #include <algorithm>
@@ -230,8 +231,12 @@ __device__ __noinline__ Coded code_odd(Chunk<DT> chunk, float up, float down) {
 // A block walks the rows, the next one's chunks on their way while it works on
 // this one's.  Lanes past a row's last chunk, or past the last row, work on the
 // last one again, and store nothing.
+//
+// Two chunks of fp32 and the next two are 64 registers: one block an SM (8192 x
+// 12288: 76 us, 89% of HBM; 128 of two, which spill).
+constexpr int blocks_of_sm(int DT, int CH) { return CH == 0 || (CH == 2 && DT == FT_DT_F32) ? 1 : 2; }
 template <int FMT, int DT, int CH, bool ROW>
-__global__ void __launch_bounds__(CH > 0 ? 512 : 1024, CH > 0 ? 2 : 1) quantize_kernel(const __grid_constant__ RowArgs a) {
+__global__ void __launch_bounds__(CH > 0 ? 512 : 1024, blocks_of_sm(DT, CH)) quantize_kernel(const __grid_constant__ RowArgs a) {
   __shared__ float warp_max[2][32];
   // threads of a row: a power of two of one warp's, or whole warps
   const int group = a.group, in_block = static_cast<int>(threadIdx.x) / group;
@@ -437,7 +442,7 @@ ft_status launch_quantize(RowArgs& a, cudaStream_t s) {
   }
   a.block_rows = block / a.group;
   const int64_t blocks = (static_cast<int64_t>(a.rows) + a.block_rows - 1) / a.block_rows;
-  const int64_t resident = static_cast<int64_t>(sms) * std::max(1, (ch == 0 ? 1024 : 1024 / block * block) / block);
+  const int64_t resident = static_cast<int64_t>(sms) * std::max(1, (ch == 0 ? 1024 : 512 * blocks_of_sm(DT, ch)) / block);
   const dim3 grid(static_cast<unsigned>(std::min(blocks, resident)));
   const auto kernel = ch == 1   ? quantize_kernel<FMT, DT, 1, ROW>
                       : ch == 2 ? quantize_kernel<FMT, DT, 2, ROW>
