@@ -16,15 +16,18 @@
 // partial sums meet through distributed shared memory and are added in the slices'
 // order.
 //
-// What bounds it.  64 x 131072 x 2048 reads its weights at 5.2 TB/s (29.0 us; floor
-// 24.8).  8192 x 6144 x 4096 takes 72.5 us, 5.7
-// PFLOP/s, 8192^3 159.5 us, 6.9 (four times the bf16 library rate is 7.8): a step of a
-// 256 x 256 pair takes 0.30 us where the products alone take 0.27, the copies of
-// scales to TMEM 0.02 more and contention in shared memory the rest (operands are
-// read at 64 bytes a clock, filled at 75); each tile adds 1 us in which its sums
-// are drained; 768 tiles on 76 pairs are 10.1 waves.  Narrower tiles are bound by
-// issuing: a step takes 0.255 us at 64 tokens, of which its barrier 0.15.  Calls of
-// a few tokens, 4.5 us for 1 x 2560 x 2048, are launch, first loads and the way out.
+// What bounds it.  64 x 131072 x 2048 reads its weights at 5.4 TB/s (28.2 us; floor
+// 24.8).  8192 x 6144 x 4096 takes 73.5 us, 5.6 PFLOP/s, 8192^3 160, 6.9: a step of a
+// 256 x 256 pair takes 0.30 us where its products alone take 0.27 (9.4 PFLOP/s), the
+// copies of scales to TMEM 0.02 more and contention in shared memory the rest
+// (operands are read at 64 bytes a clock, filled at 75); each tile adds 1 us in which
+// its sums are drained; 768 tiles on 76 pairs are 10.1 waves.  Narrower tiles are bound
+// by issuing: a step takes 0.255 us at 64 tokens, of which its barrier 0.15.  Calls of
+// a few tokens, 4.7 us for 1 x 2560 x 2048, are launch, first loads and the way out.
+// Rows of out off 16-byte boundaries are bound by their way out, which stands still
+// for the products of tiles of more than 128 tokens: 8000 x 9998 x 1024 71 us (floor
+// 25), 8000 x 9999 x 1024 onto a residual 156 (49); fp32 likewise, 2048 x 4096 x 4096
+// 21.7 us (7.0).
 //
 // Tried and not kept: the next step's scales copied to TMEM ahead of this step's
 // products (8192 x 6144 x 4096: 87.5 us, then 75.1); scale copies between the
