@@ -110,3 +110,39 @@ def test_nothing_is_written_where_a_wait_gave_up_before(cuda_lib, fp4, dtype, ad
         out.fill_(7.0), status.fill_(found)
         fp4.fp4_matmul(x, w, out, add=add, dev_status=status)
         assert rounded_once(f64(out), want, dtype) and int(status.item()) == found
+
+
+@pytest.mark.parametrize("T,N,K", [(394, 19560, 1824), (385, 15289, 2080), (130, 39674, 3200), (132, 19744, 4640), (193, 9842, 1568),
+                                   (390, 14655, 1312), (129, 32477, 544), (66, 9749, 832), (65, 19467, 32), (65, 1158, 2912),
+                                   (1217, 150, 15616), (17, 38915, 32), (2, 4894, 2848)])
+def test_far_scales_in_tiles_of_every_width(fp4, T, N, K):  # noqa: F811
+    """Rows with far scales, in both directions, among others: pairs of CTAs and single ones, several tiles each, slices;
+    out by boxes and row by row, residuals in place."""
+    from test_gpu_fp4_tiles import random_on_gpu
+
+    (x, xv), (w, wv) = random_on_gpu(fp4, "nvfp4", T, K, 1), random_on_gpu(fp4, "nvfp4", N, K, 2)
+    sums = xv @ wv.T
+    del xv, wv
+    for w_exp, x_exp in ((120, -100), (-130, 110)):
+        x.scale.fill_(2.0 ** x_exp * 1.25)
+        w.scale.fill_(1.0)
+        w.scale[5::37] = 2.0 ** w_exp
+        w.scale[-1] = 2.0 ** w_exp
+        y = sums * x.scale.double()[:, None] * w.scale.double()[None]
+        for dtype, offset, pad, added in (("f32", 1, 0, False), ("bf16", 8, -N % 8 + 8, False), ("bf16", 8, -N % 8 + 8, True),
+                                          ("bf16", 1, 2 + N % 2, True), ("bf16", 1, 3 + N % 2, False)):
+            wide = torch.full((T + 1, offset + N + pad), float("nan"), dtype=DT[dtype], device=DEV)
+            out, z = wide[:T, offset:offset + N], y
+            if added:
+                out.copy_(torch.randn(T, N, generator=torch.Generator(device=DEV).manual_seed(3), device=DEV))
+                z = y + out.double()
+            fp4.fp4_matmul(x, w, out, add=out if added else None)
+            assert wide[T:].isnan().all() and wide[:, :offset].isnan().all() and wide[:, offset + N:].isnan().all()
+            # roundings of the two products, of the sum, and of the output
+            bound = 3 * 2.0 ** -24 * (y.abs() + z.abs()) + LEAST["f32"]
+            if dtype != "f32":
+                bound = bound + HALF[dtype] * z.abs() * (1 + 2.0 ** -10) + LEAST[dtype]
+            border = 2.0 ** 128 * (1 - HALF[dtype] / 2)
+            past, under = z.abs() > border * (1 + 2.0 ** -20), z.abs() < border * (1 - 2.0 ** -20)
+            assert (out.double()[past] == torch.sign(z[past]) * float("inf")).all()
+            assert ((out.double() - z).abs() <= bound)[under].all(), (w_exp, dtype, offset, added)
