@@ -56,19 +56,19 @@ __device__ __forceinline__ int32_t status_now(const int32_t* status) {
 }
 
 // Wait for the phase with the given parity; false (and FT_ERR_TIMEOUT
-// recorded) if it has not completed within kWaitLimitNs, or as soon as another
-// wait is seen to have given up.
+// recorded) if it has not completed within kWaitLimitNs.  OTHERS: false, too,
+// as soon as another wait is seen to have given up (for kernels that do not
+// look for one before they begin).
+template <bool OTHERS = false>
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int32_t* status) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
   for (uint32_t i = 1;; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 255u) == 0) {
-      if (status_now(status) == FT_ERR_TIMEOUT) return false;
-      if (global_timer_ns() - t0 > kWaitLimitNs) {
-        record_status(status, FT_ERR_TIMEOUT);
-        return false;
-      }
+    if (OTHERS && (i & 255u) == 0 && status_now(status) == FT_ERR_TIMEOUT) return false;
+    if ((i & 255u) == 0 && global_timer_ns() - t0 > kWaitLimitNs) {
+      record_status(status, FT_ERR_TIMEOUT);
+      return false;
     }
   }
 }
@@ -76,8 +76,9 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int32_
 // mbar_wait by every lane of a warp with one verdict for the whole warp (a
 // lane that gave up makes every lane give up), for warps that run
 // warp-collective instructions (tcgen05.ld) after the wait.
+template <bool OTHERS = false>
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, int32_t* status) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, status));
+  return __all_sync(0xffffffffu, mbar_wait<OTHERS>(bar, parity, status));
 }
 
 // True (for the whole CTA) when an earlier wait of this stream's work already

@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
       const int n0 = p.w * kRows + (CG == 2 ? rank * kM : 0);
       const int x0 = p.t0 + (CG == 2 ? rank * (columns_of<CG>(p.tokens) / 2) : 0);
       for (int s = s0; s < s1; ++s) {
-        if (!mbar_wait_warp(&empty[st], ph, a.status)) {
+        if (!mbar_wait_warp<true>(&empty[st], ph, a.status)) {
           ok = false;
           break;
         }
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
       const int buf = a.buffers == 2 ? it & 1 : 0;
       const uint32_t acc = tmem + buf * (kScaleColumn / 2);
       if (it >= a.buffers) {
-        if (!mbar_wait_warp(&acc_empty[buf], (it / a.buffers - 1) & 1, a.status)) {
+        if (!mbar_wait_warp<true>(&acc_empty[buf], (it / a.buffers - 1) & 1, a.status)) {
           ok = false;
           break;
         }
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
       }
       const uint32_t shift = (p.t0 & 127) >> 5;
       for (int s = s0; s < s1; ++s) {
-        if (!mbar_wait_warp(&full[st], ph, a.status)) {
+        if (!mbar_wait_warp<true>(&full[st], ph, a.status)) {
           ok = false;
           break;
         }
@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
       };
       if constexpr (BOXES) {
         const bool odd = seldom();
-        ok = mbar_wait_warp(&acc_full[buf], (it / a.buffers) & 1, a.status);
+        ok = mbar_wait_warp<true>(&acc_full[buf], (it / a.buffers) & 1, a.status);
         if (!ok) break;
         tc_fence_after();
         if (__builtin_expect(odd, 0)) handle();
@@ -506,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
         tmem_wait();
         release();
         if (a.add != nullptr && mine > 0 && n0 < a.N) {
-          ok = mbar_wait_warp(&add_full[e], add_phase, a.status);
+          ok = mbar_wait_warp<true>(&add_full[e], add_phase, a.status);
           if (!ok) break;
           add_phase ^= 1;
         }
@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
         const int t0 = p.t0 + h * 32;
         const bool odd = seldom();
         if (a.add != nullptr && mine > 0 && a.split == 1) load_added(a, t0, n0, f, add[0]);
-        ok = mbar_wait_warp(&acc_full[buf], (it / a.buffers) & 1, a.status);
+        ok = mbar_wait_warp<true>(&acc_full[buf], (it / a.buffers) & 1, a.status);
         if (!ok) break;
         tc_fence_after();
         if (__builtin_expect(odd, 0)) handle();
