@@ -25,9 +25,9 @@
 // by issuing: a step takes 0.255 us at 64 tokens, of which its barrier 0.15.  Calls of
 // a few tokens, 4.7 us for 1 x 2560 x 2048, are launch, first loads and the way out.
 // Rows of out off 16-byte boundaries are bound by their way out, which stands still
-// for the products of tiles of more than 128 tokens: 8000 x 9998 x 1024 71 us (floor
-// 25), 8000 x 9999 x 1024 onto a residual 156 (49); fp32 likewise, 2048 x 4096 x 4096
-// 21.7 us (7.0).
+// for the products of tiles of more than 128 tokens: 8000 x 9998 x 1024 69 us (floor
+// 25), 8000 x 9999 x 1024 onto a residual 149 (49); fp32 likewise, 2048 x 4096 x 4096
+// 21.8 us (7.0).
 //
 // Tried and not kept: the next step's scales copied to TMEM ahead of this step's
 // products (8192 x 6144 x 4096: 87.5 us, then 75.1); scale copies between the
@@ -134,9 +134,9 @@ __device__ __forceinline__ RowScale split_scale(float s) {
 
 // A warp's sums of a tile, `chunks` of every other 32 columns from `from`, scaled
 // where they are: what follows then scales by 1.  In few registers and off the way of
-// the tiles without far scales, which are nearly all (a third factor for every value
-// took 8192 x 6144 x 4096 from 93.2 to 94.7 us in fp32 and 500 x 20001 x 512 onto a
-// residual from 26.3 to 30.6; so it is 93.4 and 28.0).
+// the tiles without far scales, which are nearly all (8000 x 9999 x 1024 takes 74.1 us
+// without far scales, 77.8 so, 89 with a third factor for every value; asked for with
+// the tile's own scales, not a tile ahead, 85.9).
 __device__ __forceinline__ void scale_in_tmem(uint32_t from, int chunks, const float (&sw)[4], const float* sx,
                                               int64_t sx_stride, int tokens, const Fragment& f) {
 #pragma unroll 1
@@ -434,6 +434,19 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
     const uint32_t box0 = smem_u32(boxes);
     bool ok = true;
     int it = 0;
+    // Seldom, a wait of an earlier call gave up, and nothing is written, or the warp's rows have far scales.  Those
+    // are asked for a tile ahead, so that nothing waits for the answer.
+    float own;  // the scale of row `lane` of the warp's
+    const auto ask = [&](const Place& p) {
+      const int n = p.w * kRows + (CG == 2 ? rank * kM : 0) + q * 32 + lane;
+      // (slices: where they are joined)
+      own = FMT == FT_FP4_NVFP4 && a.split == 1 && a.sw != nullptr && n < a.N ? a.sw[n * a.sw_stride] : 1.f;
+    };
+    const auto any_far = [&] { return __any_sync(0xffffffffu, far_scale(own)) != 0; };
+    const int32_t found = status_now(a.status);
+    ask(place_of(a, first));
+    const bool gone = __any_sync(0xffffffffu, found == FT_ERR_TIMEOUT) != 0;
+    bool seldom = any_far() || gone;
     for (int tile = first; tile < a.tiles && ok; tile += stride, ++it) {
       const Place p = place_of(a, tile);
       const int n0 = p.w * kRows + (CG == 2 ? rank * kM : 0) + q * 32;  // the warp's rows
@@ -459,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
         }
         __syncwarp();
       }
-      const int32_t before = status_now(a.status);
+      ask(place_of(a, min(tile + stride, a.tiles - 1)));
       float sw[4], sx[kChunks];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -471,17 +484,9 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
         const int t = (2 * c + h) * 32 + lane;
         sx[c] = a.sx != nullptr && t < p.tokens ? a.sx[(p.t0 + t) * a.sx_stride] : 1.f;
       }
-      // Seldom: a wait of an earlier call gave up, and nothing is written; or far scales.  Looked at in front of the
-      // wait for the products, under which the loads arrive.
-      const auto seldom = [&] {
-        bool is = before == FT_ERR_TIMEOUT;
-        if (FMT == FT_FP4_NVFP4 && a.split == 1)  // (slices: where they are joined)
-          is |= far_scale(sw[0]) | far_scale(sw[1]) | far_scale(sw[2]) | far_scale(sw[3]);
-        return __any_sync(0xffffffffu, is) != 0;
-      };
       int kept = mine;  // chunks that are written
       const auto handle = [&] {
-        if (__any_sync(0xffffffffu, before == FT_ERR_TIMEOUT)) {
+        if (gone) {
           kept = 0;
           if (lane == 0) s_skip = 1;
           return;
@@ -494,11 +499,10 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
         for (int c = 0; c < kChunks; ++c) sx[c] = 1.f;
       };
       if constexpr (BOXES) {
-        const bool odd = seldom();
         ok = mbar_wait_warp<true>(&acc_full[buf], (it / a.buffers) & 1, a.status);
         if (!ok) break;
         tc_fence_after();
-        if (__builtin_expect(odd, 0)) handle();
+        if (__builtin_expect(seldom, 0)) handle();
         uint32_t v[kChunks][32];
 #pragma unroll
         for (int c = 0; c < kChunks; ++c)
@@ -530,12 +534,11 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
         // A chunk at a time, the next one's add on its way; the first one's while the products run.
         Added<DT> add[2];
         const int t0 = p.t0 + h * 32;
-        const bool odd = seldom();
         if (a.add != nullptr && mine > 0 && a.split == 1) load_added(a, t0, n0, f, add[0]);
         ok = mbar_wait_warp<true>(&acc_full[buf], (it / a.buffers) & 1, a.status);
         if (!ok) break;
         tc_fence_after();
-        if (__builtin_expect(odd, 0)) handle();
+        if (__builtin_expect(seldom, 0)) handle();
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
           if (c >= kept) break;
@@ -557,6 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_kernel(const __grid_consta
         }
         if (kept <= 0) release();
       }
+      seldom = any_far() || gone;
     }
     if (lane == 0) {
       bulk_wait();
